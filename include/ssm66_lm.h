@@ -1,0 +1,97 @@
+/*
+ * ssm66_lm.h -- C ABI of the operators around a linear-attention layer, in the
+ * same library as ssm66.h and with its conventions: caller-owned device
+ * pointers, dense row-major tensors, no allocation, every call asynchronous on
+ * the caller's stream, arguments checked before any HIP call, the status codes
+ * and io dtypes of ssm66.h, float32 states and parameters in every mode.
+ *
+ *   ssm_linattn_fwd, ssm_linattn_bwd, ssm_linattn_step
+ *       linear attention with a decay for each head: prompts, gradients, one
+ *       token.
+ */
+#ifndef SSM66_LM_H
+#define SSM66_LM_H
+
+#include "ssm66.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * Linear attention with a decay for each head.  Head h of `nheads` reads the
+ * keys of key head h / (nheads / kheads), and with lam = exp(log_decay[h])
+ *   S_t = lam S_{t-1} + v_t k_t^T        (S: dv x dk),
+ *   o_t = scale S_t q_t.
+ *   q, k       : (batch, seqlen, kheads, dk), io dtype
+ *   v, o       : (batch, seqlen, nheads, dv), io dtype
+ *   log_decay  : (nheads) float32; the log of the factor per token, 0 = keep
+ *                everything, -inf = keep nothing
+ *   h0         : (batch, nheads, dv, dk) float32, the state before token 0, or
+ *                NULL (zero)
+ *   seq_lens   : (batch) int32 or NULL: as for ssm_scan_fwd_ex -- tokens at or
+ *                past a length are padding, whatever they hold: o = 0 there and
+ *                the state is the one after the last real token
+ *   reset      : (batch, seqlen) uint8 or NULL: the state is zeroed before a
+ *                flagged token (a document starts there)
+ *   last_state : (batch, nheads, dv, dk) float32, or NULL; must not overlap h0
+ * kheads divides nheads; dk and dv are multiples of 8, at most 256; q, k, v
+ * and o are 16-byte aligned, and so are h0 and last_state; nheads * dv and
+ * kheads * dk at most 2^22 (else SSM_ERR_UNSUPPORTED).  Zero batch or nheads
+ * is a no-op; seqlen == 0 copies h0 (or zero) to last_state.
+ * workspace: ssm_linattn_fwd_workspace_size(...) bytes, 256-byte aligned,
+ * contents not needed before or after (NULL where the size is 0).
+ * Values are not checked.  A NaN or infinity in a real token reaches the
+ * outputs of its own chunk of 64 tokens (tokens before it too) and of later
+ * ones.  Repeated calls give identical bits.
+ */
+size_t ssm_linattn_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads,
+                                      int64_t kheads, int64_t dk, int64_t dv, int io_dtype);
+int ssm_linattn_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                    float scale, const float* h0, const int32_t* seq_lens, const uint8_t* reset,
+                    void* o, float* last_state, void* workspace, size_t workspace_bytes,
+                    int64_t batch, int64_t seqlen, int64_t nheads, int64_t kheads, int64_t dk,
+                    int64_t dv, int io_dtype, void* stream);
+
+/*
+ * Gradients of ssm_linattn_fwd, from its inputs (the states are recomputed).
+ *   do_        : (batch, seqlen, nheads, dv), io dtype
+ *   dlast      : (batch, nheads, dv, dk) float32, the gradient of last_state,
+ *                or NULL (zero)
+ *   dq, dk_, dv_ : like q, k, v (dq and dk_ summed in float32 over the heads
+ *                that share a key head, rounded once); zero at padding
+ *   dlog_decay : (nheads) float32, or NULL
+ *   dh0        : (batch, nheads, dv, dk) float32, or NULL
+ * Outputs are overwritten.  A token sees no gradient from after the next
+ * document start.  workspace: ssm_linattn_bwd_workspace_size(...) bytes,
+ * 256-byte aligned (need_dlog_decay says whether dlog_decay is asked for).
+ * Alignment and limits as for ssm_linattn_fwd.  All sums are taken in a fixed
+ * order: repeated calls give identical bits.
+ */
+size_t ssm_linattn_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads,
+                                      int64_t kheads, int64_t dk, int64_t dv,
+                                      int need_dlog_decay, int io_dtype);
+int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                    float scale, const float* h0, const int32_t* seq_lens, const uint8_t* reset,
+                    const void* do_, const float* dlast, void* dq, void* dk_, void* dv_,
+                    float* dlog_decay, float* dh0, void* workspace, size_t workspace_bytes,
+                    int64_t batch, int64_t seqlen, int64_t nheads, int64_t kheads, int64_t dk,
+                    int64_t dv, int io_dtype, void* stream);
+
+/*
+ * One token against a state cache (batch, nheads, dv, dk) float32, updated in
+ * place: S = lam S + v k^T, o = scale S q.  q, k: (batch, kheads, dk);
+ * v, o: (batch, nheads, dv), io dtype.  dk is a multiple of 8, at most 256;
+ * dv any positive size; state, q and k are 16-byte aligned, v and o to their
+ * element size.
+ */
+int ssm_linattn_step(float* state, const void* q, const void* k, const void* v,
+                     const float* log_decay, float scale, void* o, int64_t batch,
+                     int64_t nheads, int64_t kheads, int64_t dk, int64_t dv, int io_dtype,
+                     void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SSM66_LM_H */

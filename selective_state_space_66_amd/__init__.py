@@ -18,9 +18,16 @@ missing, every call raises.
     out, window = conv1d_fwd(x, weight, bias=None, silu=True, window_in=None,
                              seq_lens=None, reset=None)
     out = conv1d_step(window, x, weight, bias=None, silu=True)   # window updated in place
+
+The operators of a linear-attention layer (lm.py) are reached from here too:
+linattn_fwd, linattn_bwd, linattn_step.
 """
 import ctypes
 import os
+
+from . import lm as _lm
+from .lm import (linattn_bwd, linattn_bwd_workspace_size, linattn_fwd,  # noqa: F401
+                 linattn_fwd_workspace_size, linattn_step)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libssm66_hip.so")
 
@@ -92,6 +99,7 @@ def load_library():
     lib.ssm_status_string.argtypes = [ci]
     lib.ssm_abi_version.restype = ci
     lib.ssm_abi_version.argtypes = []
+    _lm.declare(lib)
     _lib = lib
     return lib
 
