@@ -8,6 +8,10 @@
  *   ssm_linattn_fwd, ssm_linattn_bwd, ssm_linattn_step
  *       linear attention with a decay for each head: prompts, gradients, one
  *       token.
+ *   ssm_group_norm_fwd, ssm_group_norm_bwd
+ *       group norm, channels last, with an activation and a gate.
+ *   ssm_clip_grad_norm
+ *       the global norm of many gradients, and the gradients clipped to it.
  */
 #ifndef SSM66_LM_H
 #define SSM66_LM_H
@@ -89,6 +93,69 @@ int ssm_linattn_step(float* state, const void* q, const void* k, const void* v,
                      const float* log_decay, float scale, void* o, int64_t batch,
                      int64_t nheads, int64_t kheads, int64_t dk, int64_t dv, int io_dtype,
                      void* stream);
+
+/* activations of ssm_group_norm_fwd */
+#define SSM_ACT_NONE 0
+#define SSM_ACT_SILU 1
+
+/*
+ * Group norm over channels-last tensors.  Entry n and group g normalise over
+ * the rows and the channels / groups channels of the group together:
+ *   xh = (x - mean) / sqrt(var + eps),  u = xh weight[c] + bias[c],
+ *   y = act(u) silu(z)
+ * with the variance over the same values (not one less).  rows == 1 is the
+ * norm of each token's heads: the batch holds the tokens.
+ *   x, z, y      : (batch, rows, channels), io dtype; z may be NULL (no gate)
+ *   weight, bias : (channels) float32, or NULL (one, zero)
+ *   mean, rstd   : (batch, groups) float32, or NULL: what ssm_group_norm_bwd
+ *                  takes
+ * groups divides channels; channels at most 2^22.  Tensors are aligned to
+ * their element size (to 16 bytes, and with channels / groups a multiple of
+ * 16 bytes, is fastest).  y may be x or z.  Zero batch or rows is a no-op.
+ * workspace: ssm_group_norm_workspace_size(..., 0, ...) bytes, 256-byte
+ * aligned.  Repeated calls give identical bits.
+ */
+size_t ssm_group_norm_workspace_size(int64_t batch, int64_t rows, int64_t channels,
+                                     int64_t groups, int backward, int io_dtype);
+int ssm_group_norm_fwd(const void* x, const float* weight, const float* bias, const void* z,
+                       int act, float eps, void* y, float* mean, float* rstd, void* workspace,
+                       size_t workspace_bytes, int64_t batch, int64_t rows, int64_t channels,
+                       int64_t groups, int io_dtype, void* stream);
+
+/*
+ * Gradients of ssm_group_norm_fwd, from its inputs and the mean and rstd it
+ * wrote.
+ *   dy, dx, dz     : (batch, rows, channels), io dtype; dz is written where z
+ *                    is given
+ *   dweight, dbias : (channels) float32, or NULL
+ * Outputs are overwritten and overlap no input.  workspace:
+ * ssm_group_norm_workspace_size(..., 1, ...) bytes, 256-byte aligned.  Zero
+ * batch or rows writes zeros to dweight and dbias.
+ */
+int ssm_group_norm_bwd(const void* x, const float* weight, const float* bias, const void* z,
+                       int act, const float* mean, const float* rstd, const void* dy, void* dx,
+                       float* dweight, float* dbias, void* dz, void* workspace,
+                       size_t workspace_bytes, int64_t batch, int64_t rows, int64_t channels,
+                       int64_t groups, int io_dtype, void* stream);
+
+/*
+ * The global norm of many gradients, and the gradients clipped to it:
+ *   norm = sqrt(sum of the squares of all values of all tensors),
+ *   outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6)).
+ *   grads, outs : HOST arrays of ntensors device pointers; outs[i] may be
+ *                 grads[i] (in place), and overlaps no other tensor
+ *   counts      : HOST array of element counts (zero is fine)
+ *   io_dtypes   : HOST array, SSM_F32 or SSM_BF16 for each tensor
+ *   norm        : one float32, device memory
+ * The host arrays are read before the call returns.  Squares are added in
+ * float64.  A norm that is infinite gives a factor of 0, a NaN spreads to all
+ * outputs.  max_norm >= 0.  workspace: ssm_clip_grad_norm_workspace_size(
+ * ntensors) bytes, 256-byte aligned.  Repeated calls give identical bits.
+ */
+size_t ssm_clip_grad_norm_workspace_size(int64_t ntensors);
+int ssm_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* counts,
+                       const int32_t* io_dtypes, int64_t ntensors, float max_norm, float* norm,
+                       void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -19,14 +19,16 @@ missing, every call raises.
                              seq_lens=None, reset=None)
     out = conv1d_step(window, x, weight, bias=None, silu=True)   # window updated in place
 
-The operators of a linear-attention layer (lm.py) are reached from here too:
-linattn_fwd, linattn_bwd, linattn_step.
+The operators of a linear-attention layer and of its training step (lm.py) are
+reached from here too: linattn_fwd, linattn_bwd, linattn_step, group_norm_fwd,
+group_norm_bwd, clip_grad_norm.
 """
 import ctypes
 import os
 
 from . import lm as _lm
-from .lm import (linattn_bwd, linattn_bwd_workspace_size, linattn_fwd,  # noqa: F401
+from .lm import (clip_grad_norm, group_norm_bwd, group_norm_fwd,  # noqa: F401
+                 group_norm_workspace_size, linattn_bwd, linattn_bwd_workspace_size, linattn_fwd,
                  linattn_fwd_workspace_size, linattn_step)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libssm66_hip.so")

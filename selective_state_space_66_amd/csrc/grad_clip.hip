@@ -1,0 +1,229 @@
+// grad_clip.hip -- the global norm of many gradients, and the clipped gradients.
+//
+//   norm = sqrt(sum over all tensors of x^2),  out = x min(1, max_norm / (norm + 1e-6)).
+//
+// Two passes over the gradients, both bound by HBM (or by the Infinity Cache,
+// where the second pass finds what fits of them).  The list of tensors travels
+// in the kernel arguments, kTensors at a time, so a call needs no copy to the
+// device; a tensor is cut into chunks, and a fixed grid takes the chunks of
+// the list in turn, so a list of very different sizes loads the CUs evenly and
+// a model of a few hundred tensors costs a handful of launches.
+//
+// The squares are added in fp64: neither overflow (1e38 squared) nor the small
+// ones of fp32 gradients (1e-30 squared) are lost, and 64-bit adds cost less
+// than the loads.  Every block leaves one partial sum, and each block of the
+// second pass adds all of them itself, in the same order: one launch less than
+// a kernel of its own, and identical bits on every call.
+#include "grad_clip_launch.h"
+#include "ssm_device.h"
+
+namespace ssm66 {
+namespace grad_clip {
+
+namespace {
+
+constexpr int kTensors = 120;          // entries of one launch: under 4 KB of kernel arguments
+constexpr int kChunkBytes = 64 * 1024; // of a tensor, for one turn of a block
+constexpr int kBlocks = 1024;          // of one launch
+
+typedef __attribute__((ext_vector_type(4))) unsigned int u32x4;
+
+struct Entry {
+  const void* src;
+  void* dst;
+  int64_t count;
+  uint32_t first;    // its first chunk in the list
+  uint32_t f32;
+};
+struct List {
+  Entry e[kTensors];
+  int n;
+  uint32_t chunks;
+};
+
+// the entry that holds chunk c: the last one whose first chunk is not past it
+__device__ __forceinline__ int entry_of(const List& l, uint32_t c) {
+  int lo = 0, hi = l.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (l.e[mid].first <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double part[4];
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+template <typename T>
+__device__ __forceinline__ double piece_squares(u32x4 v) {
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      const double d = (double)__uint_as_float(v[i]);
+      s = fma(d, d, s);
+    } else {
+      const double a = (double)__uint_as_float(v[i] << 16), b = (double)__uint_as_float(v[i] & 0xffff0000u);
+      s = fma(a, a, s);
+      s = fma(b, b, s);
+    }
+  }
+  return s;
+}
+
+template <typename T>
+__device__ __forceinline__ double squares(const T* p, int64_t n) {
+  constexpr int V = 16 / sizeof(T);
+  double s = 0.0;
+  int64_t i = 0;
+  if ((uintptr_t)p % 16 == 0) {
+    const int64_t nv = n / V;
+    constexpr int U = 8;  // pieces in flight
+    int64_t k = threadIdx.x;
+    for (; k + (U - 1) * 256 < nv; k += U * 256) {
+      u32x4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = ((const u32x4*)p)[k + u * 256];
+#pragma unroll
+      for (int u = 0; u < U; ++u) s += piece_squares<T>(v[u]);
+    }
+    for (; k < nv; k += 256) s += piece_squares<T>(((const u32x4*)p)[k]);
+    i = nv * V;
+  }
+  for (i += threadIdx.x; i < n; i += 256) {
+    const double d = (double)to_f32(p[i]);
+    s = fma(d, d, s);
+  }
+  return s;
+}
+
+template <typename T>
+__device__ __forceinline__ u32x4 piece_scaled(u32x4 v, float c) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4)
+      v[i] = __float_as_uint(__uint_as_float(v[i]) * c);
+    else
+      v[i] = pack_bf16x2(__uint_as_float(v[i] << 16) * c, __uint_as_float(v[i] & 0xffff0000u) * c);
+  }
+  return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void scale(const T* p, T* q, int64_t n, float c) {
+  constexpr int V = 16 / sizeof(T);
+  int64_t i = 0;
+  if ((uintptr_t)p % 16 == 0 && (uintptr_t)q % 16 == 0) {
+    const int64_t nv = n / V;
+    constexpr int U = 8;
+    int64_t k = threadIdx.x;
+    for (; k + (U - 1) * 256 < nv; k += U * 256) {
+      u32x4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = ((const u32x4*)p)[k + u * 256];
+#pragma unroll
+      for (int u = 0; u < U; ++u) ((u32x4*)q)[k + u * 256] = piece_scaled<T>(v[u], c);
+    }
+    for (; k < nv; k += 256) ((u32x4*)q)[k] = piece_scaled<T>(((const u32x4*)p)[k], c);
+    i = nv * V;
+  }
+  for (i += threadIdx.x; i < n; i += 256) store_io(q + i, to_f32(p[i]) * c);
+}
+
+__global__ __launch_bounds__(256) void norm_kernel(const List l, double* parts) {
+  double s = 0.0;
+  for (uint32_t c = blockIdx.x; c < l.chunks; c += gridDim.x) {
+    const Entry& e = l.e[entry_of(l, c)];
+    const int64_t per = kChunkBytes / (e.f32 ? 4 : 2);
+    const int64_t at = (int64_t)(c - e.first) * per;
+    const int64_t n = e.count - at < per ? e.count - at : per;
+    s += e.f32 ? squares((const float*)e.src + at, n) : squares((const bf16_bits*)e.src + at, n);
+  }
+  s = block_sum(s);
+  if (threadIdx.x == 0) parts[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(256) void clip_kernel(const List l, const double* parts, int nparts,
+                                                   float max_norm, float* norm, int first) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < nparts; i += 256) s += parts[i];
+  const float total = (float)sqrt(block_sum(s));
+  if (first && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+  float coef = max_norm / (total + 1e-6f);
+  coef = coef > 1.0f ? 1.0f : coef;  // a NaN stays one
+  for (uint32_t c = blockIdx.x; c < l.chunks; c += gridDim.x) {
+    const Entry& e = l.e[entry_of(l, c)];
+    if (coef == 1.0f && e.src == e.dst) continue;  // in place, and every value times one
+    const int64_t per = kChunkBytes / (e.f32 ? 4 : 2);
+    const int64_t at = (int64_t)(c - e.first) * per;
+    const int64_t n = e.count - at < per ? e.count - at : per;
+    if (e.f32) scale((const float*)e.src + at, (float*)e.dst + at, n, coef);
+    else scale((const bf16_bits*)e.src + at, (bf16_bits*)e.dst + at, n, coef);
+  }
+}
+
+// the next list of a call: entries from *at on, empty tensors left out
+void next_list(const Call& c, int64_t* at, List* l) {
+  l->n = 0;
+  l->chunks = 0;
+  while (*at < c.n && l->n < kTensors) {
+    const int64_t i = (*at)++;
+    if (c.counts[i] == 0) continue;
+    const int64_t per = kChunkBytes / (c.io_dtypes[i] == 0 ? 4 : 2);
+    Entry& e = l->e[l->n++];
+    e.src = c.grads[i];
+    e.dst = c.outs[i];
+    e.count = c.counts[i];
+    e.first = l->chunks;
+    e.f32 = c.io_dtypes[i] == 0;
+    l->chunks += (uint32_t)((c.counts[i] + per - 1) / per);
+  }
+}
+
+uint32_t blocks_of(const List& l) { return l.chunks < (uint32_t)kBlocks ? l.chunks : (uint32_t)kBlocks; }
+
+}  // namespace
+
+size_t workspace_bytes(int64_t n) {
+  return (size_t)((n + kTensors - 1) / kTensors) * kBlocks * sizeof(double);
+}
+
+hipError_t run(const Call& c, hipStream_t s) {
+  double* const parts = (double*)c.ws;
+  List l;
+  int nparts = 0;
+  for (int64_t at = 0; at < c.n;) {
+    next_list(c, &at, &l);
+    const uint32_t nb = blocks_of(l);
+    if (nb == 0) continue;
+    norm_kernel<<<dim3(nb), 256, 0, s>>>(l, parts + nparts);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    nparts += (int)nb;
+  }
+  bool first = true;
+  for (int64_t at = 0; at < c.n || first;) {
+    next_list(c, &at, &l);
+    uint32_t nb = blocks_of(l);
+    if (nb == 0) {
+      if (!first || at < c.n) continue;
+      nb = 1;  // nothing but empty tensors: the norm is still written
+    }
+    clip_kernel<<<dim3(nb), 256, 0, s>>>(l, parts, nparts, c.max_norm, c.norm, first ? 1 : 0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    first = false;
+  }
+  return hipSuccess;
+}
+
+}  // namespace grad_clip
+}  // namespace ssm66

@@ -5,6 +5,8 @@
 #include <initializer_list>
 
 #include "../../include/ssm66_lm.h"
+#include "grad_clip_launch.h"
+#include "group_norm_launch.h"
 #include "linattn_launch.h"
 
 namespace {
@@ -64,9 +66,119 @@ ssm66::linattn::Problem problem(const void* q, const void* k, const void* v, con
   return p;
 }
 
+int norm_shape(int64_t batch, int64_t rows, int64_t channels, int64_t groups, int io_dtype) {
+  if (batch < 0 || rows < 0 || channels < 1 || groups < 1 || channels % groups != 0) return SSM_ERR_SHAPE;
+  if (io_dtype != SSM_F32 && io_dtype != SSM_BF16) return SSM_ERR_DTYPE;
+  int64_t t;
+  if (!product(&t, {batch, rows, channels}) || !product(&t, {batch, channels})) return SSM_ERR_SHAPE;
+  if (channels > ((int64_t)1 << 22)) return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+ssm66::group_norm::Args norm_args(int64_t batch, int64_t rows, int64_t channels, int64_t groups) {
+  ssm66::group_norm::Args a = {};
+  a.batch = batch; a.rows = rows; a.C = (int)channels; a.groups = (int)groups;
+  return a;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t ssm_group_norm_workspace_size(int64_t batch, int64_t rows, int64_t channels,
+                                     int64_t groups, int backward, int io_dtype) {
+  if (norm_shape(batch, rows, channels, groups, io_dtype) != SSM_OK) return 0;
+  ssm66::group_norm::Args a = norm_args(batch, rows, channels, groups);
+  if (!ssm66::group_norm::fits(a, io_dtype == SSM_F32, backward != 0)) return 0;
+  return ssm66::group_norm::workspace_bytes(a, io_dtype == SSM_F32, backward != 0);
+}
+
+int ssm_group_norm_fwd(const void* x, const float* weight, const float* bias, const void* z,
+                       int act, float eps, void* y, float* mean, float* rstd, void* workspace,
+                       size_t workspace_bytes, int64_t batch, int64_t rows, int64_t channels,
+                       int64_t groups, int io_dtype, void* stream) {
+  const int st = norm_shape(batch, rows, channels, groups, io_dtype);
+  if (st != SSM_OK) return st;
+  if (act != SSM_ACT_NONE && act != SSM_ACT_SILU) return SSM_ERR_FLAG;
+  if (batch == 0 || rows == 0) return SSM_OK;
+  if (!x || !y) return SSM_ERR_NULL;
+  const size_t es = io_dtype == SSM_BF16 ? 2 : 4;
+  if (!aligned(x, es) || !aligned(y, es) || !aligned(z, es)) return SSM_ERR_ALIGN;
+  const void* p4[4] = {weight, bias, mean, rstd};
+  for (const void* q : p4)
+    if (!aligned(q, 4)) return SSM_ERR_ALIGN;
+  if (!aligned(workspace, 256)) return SSM_ERR_ALIGN;
+  ssm66::group_norm::Args a = norm_args(batch, rows, channels, groups);
+  const bool f32 = io_dtype == SSM_F32;
+  if (!ssm66::group_norm::fits(a, f32, false)) return SSM_ERR_UNSUPPORTED;
+  const size_t need = ssm66::group_norm::workspace_bytes(a, f32, false);
+  if (need > 0 && !workspace) return SSM_ERR_NULL;
+  if (workspace_bytes < need) return SSM_ERR_SHAPE;
+  a.x = x; a.z = z; a.y = y; a.weight = weight; a.bias = bias; a.mean = mean; a.rstd = rstd;
+  a.silu = act == SSM_ACT_SILU; a.eps = eps; a.ws = workspace;
+  return status(ssm66::group_norm::forward(a, f32, (hipStream_t)stream));
+}
+
+int ssm_group_norm_bwd(const void* x, const float* weight, const float* bias, const void* z,
+                       int act, const float* mean, const float* rstd, const void* dy, void* dx,
+                       float* dweight, float* dbias, void* dz, void* workspace,
+                       size_t workspace_bytes, int64_t batch, int64_t rows, int64_t channels,
+                       int64_t groups, int io_dtype, void* stream) {
+  const int st = norm_shape(batch, rows, channels, groups, io_dtype);
+  if (st != SSM_OK) return st;
+  if (act != SSM_ACT_NONE && act != SSM_ACT_SILU) return SSM_ERR_FLAG;
+  if (batch > 0 && rows > 0 && (!x || !dy || !dx || !mean || !rstd || (z && !dz))) return SSM_ERR_NULL;
+  const size_t es = io_dtype == SSM_BF16 ? 2 : 4;
+  const void* io[5] = {x, z, dy, dx, dz};
+  for (const void* q : io)
+    if (!aligned(q, es)) return SSM_ERR_ALIGN;
+  const void* p4[6] = {weight, bias, mean, rstd, dweight, dbias};
+  for (const void* q : p4)
+    if (!aligned(q, 4)) return SSM_ERR_ALIGN;
+  if (!aligned(workspace, 256)) return SSM_ERR_ALIGN;
+  ssm66::group_norm::Args a = norm_args(batch, rows, channels, groups);
+  const bool f32 = io_dtype == SSM_F32;
+  if (!ssm66::group_norm::fits(a, f32, true)) return SSM_ERR_UNSUPPORTED;
+  const size_t need = ssm66::group_norm::workspace_bytes(a, f32, true);
+  if (need > 0 && !workspace) return SSM_ERR_NULL;
+  if (workspace_bytes < need) return SSM_ERR_SHAPE;
+  a.x = x; a.z = z; a.dy = dy; a.dx = dx; a.dz = dz; a.weight = weight; a.bias = bias;
+  a.mean = (float*)mean; a.rstd = (float*)rstd; a.dweight = dweight; a.dbias = dbias;
+  a.silu = act == SSM_ACT_SILU; a.ws = workspace;
+  return status(ssm66::group_norm::backward(a, f32, (hipStream_t)stream));
+}
+
+size_t ssm_clip_grad_norm_workspace_size(int64_t ntensors) {
+  if (ntensors < 0 || ntensors > ((int64_t)1 << 24)) return 0;
+  return ssm66::grad_clip::workspace_bytes(ntensors);
+}
+
+int ssm_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* counts,
+                       const int32_t* io_dtypes, int64_t ntensors, float max_norm, float* norm,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  if (ntensors < 0) return SSM_ERR_SHAPE;
+  if (ntensors > ((int64_t)1 << 24)) return SSM_ERR_UNSUPPORTED;
+  if (!(max_norm >= 0.0f)) return SSM_ERR_FLAG;
+  if (!norm || (ntensors > 0 && (!grads || !outs || !counts || !io_dtypes))) return SSM_ERR_NULL;
+  for (int64_t i = 0; i < ntensors; ++i) {
+    if (counts[i] < 0) return SSM_ERR_SHAPE;
+    if (counts[i] > ((int64_t)1 << 38)) return SSM_ERR_UNSUPPORTED;  // chunk numbers are 32-bit
+    if (io_dtypes[i] != SSM_F32 && io_dtypes[i] != SSM_BF16) return SSM_ERR_DTYPE;
+    if (counts[i] == 0) continue;
+    if (!grads[i] || !outs[i]) return SSM_ERR_NULL;
+    const size_t es = io_dtypes[i] == SSM_BF16 ? 2 : 4;
+    if (!aligned(grads[i], es) || !aligned(outs[i], es)) return SSM_ERR_ALIGN;
+  }
+  if (!aligned(norm, 4) || !aligned(workspace, 256)) return SSM_ERR_ALIGN;
+  const size_t need = ssm66::grad_clip::workspace_bytes(ntensors);
+  if (need > 0 && !workspace) return SSM_ERR_NULL;
+  if (workspace_bytes < need) return SSM_ERR_SHAPE;
+  ssm66::grad_clip::Call c;
+  c.grads = grads; c.outs = outs; c.counts = counts; c.io_dtypes = io_dtypes; c.n = ntensors;
+  c.max_norm = max_norm; c.norm = norm; c.ws = workspace;
+  return status(ssm66::grad_clip::run(c, (hipStream_t)stream));
+}
+
 
 size_t ssm_linattn_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads,
                                       int64_t kheads, int64_t dk, int64_t dv, int io_dtype) {

@@ -1,0 +1,198 @@
+"""Group norm (channels last, activation, gate) on the GPU against the formula in 64 bits.
+
+Bounds (relative RMS over a tensor): fp32 results are chains of at most about a hundred
+roundings of 2^-24 relative to the terms summed, 6e-6: 1e-5.  (dx is a difference: its terms
+are rstd dn, which in a group of two values it cancels almost wholly; a mean's terms are the
+values.)  bf16 results add one rounding,
+of at most 2^-8 of each value.
+"""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_66_amd as ssm
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TOL = {torch.float32: 1e-5, torch.bfloat16: 2.0 ** -8 + 1e-5}
+
+
+def reference(x, groups, w, b, z, act, eps, dy=None):
+    """y, mean, rstd and, with dy, the gradients, by the formula, on float64 arrays."""
+    N, S, C = x.shape
+    cg = C // groups
+    xs = x.reshape(N, S, groups, cg)
+    mean = xs.mean((1, 3), keepdims=True)
+    rstd = 1.0 / np.sqrt(((xs - mean) ** 2).mean((1, 3), keepdims=True) + eps)
+    xh = (xs - mean) * rstd
+    wf = (np.ones(C) if w is None else w).reshape(groups, cg)
+    bf = (np.zeros(C) if b is None else b).reshape(groups, cg)
+    u = (xh * wf + bf).reshape(N, S, C)
+    sg = 1 / (1 + np.exp(-u))
+    a = u * sg if act == "silu" else u
+    gate, dgate = 1.0, 0.0
+    if z is not None:
+        sz = 1 / (1 + np.exp(-z))
+        gate, dgate = z * sz, sz * (1 + z * (1 - sz))
+    out = dict(y=a * gate, mean=mean[:, 0, :, 0], rstd=rstd[:, 0, :, 0])
+    out["rms"] = np.sqrt((xs ** 2).mean((1, 3)))
+    if dy is not None:
+        du = dy * gate * (sg * (1 + u * (1 - sg)) if act == "silu" else 1.0)
+        du4 = du.reshape(N, S, groups, cg)
+        dn = du4 * wf
+        out["dx"] = (rstd * (dn - dn.mean((1, 3), keepdims=True)
+                             - xh * (dn * xh).mean((1, 3), keepdims=True))).reshape(N, S, C)
+        out["dweight"] = (du4 * xh).sum((0, 1)).reshape(C)
+        out["dbias"] = du.sum((0, 1))
+        out["dx_terms"] = (rstd * dn).reshape(N, S, C)
+        out["dz"] = dy * a * dgate
+    return out
+
+
+def close(got, ref, tol, what, terms=None):
+    got = got.detach().double().cpu().numpy()
+    assert got.shape == ref.shape, what
+    assert np.isfinite(got).all(), what
+    den = float(np.sqrt((ref * ref).sum() if terms is None else (terms * terms).sum()))
+    err = float(np.sqrt(((got - ref) ** 2).sum())) / den if den > 0 else float(np.abs(got).max(initial=0.0))
+    assert err <= tol, f"{what}: {err:.2e}"
+
+
+def tensor(rng, shape, io, offset=0.0, shift=0):
+    """A tensor on the GPU whose memory starts `shift` elements into an allocation."""
+    t = torch.from_numpy((rng.normal(size=shape) + offset).astype(np.float32)).to(DEV).to(io)
+    buf = torch.zeros(t.numel() + shift, dtype=io, device=DEV)
+    buf[shift:] = t.reshape(-1)
+    return buf[shift:].view(shape)
+
+
+def check(seed, N, S, C, groups, io, act="none", gate=False, affine=True, offset=0.0, shift=0):
+    print(f"[group norm] {N}x{S}x{C}/{groups} {io} {act} gate={gate} shift={shift}", flush=True)
+    rng = np.random.default_rng(seed)
+    x, dy = tensor(rng, (N, S, C), io, offset, shift), tensor(rng, (N, S, C), io, 0, shift)
+    z = tensor(rng, (N, S, C), io) if gate else None
+    w = tensor(rng, (C,), torch.float32, 1.0) if affine else None
+    b = tensor(rng, (C,), torch.float32) if affine else None
+    y, mean, rstd = ssm.group_norm_fwd(x, groups, weight=w, bias=b, z=z, act=act)
+    g = ssm.group_norm_bwd(x, groups, dy, mean, rstd, weight=w, bias=b, z=z, act=act)
+    torch.cuda.synchronize()
+    f = [None if t is None else t.double().cpu().numpy() for t in (x, w, b, z, dy)]
+    ref = reference(f[0], groups, f[1], f[2], f[3], act, 1e-5, f[4])
+    close(y, ref["y"], TOL[io], "y")
+    close(mean, ref["mean"], 1e-5, "mean", terms=ref["rms"])
+    close(rstd, ref["rstd"], 1e-5, "rstd")
+    close(g["dx"], ref["dx"], TOL[io], "dx", terms=ref["dx_terms"])
+    for name, given in (("dweight", affine), ("dbias", affine), ("dz", gate)):
+        if given:
+            close(g[name], ref[name], TOL[io] if name == "dz" else 1e-5, name)
+        else:
+            assert g[name] is None
+
+
+IOS = [torch.float32, torch.bfloat16]
+
+
+@pytest.mark.parametrize("io", IOS)
+@pytest.mark.parametrize("cg,groups", [(4, 1), (7, 3), (8, 5), (10, 12), (24, 2), (40, 8), (64, 24),
+                                       (100, 3), (128, 1), (255, 2), (256, 8), (257, 2), (520, 4),
+                                       (2048, 1), (2056, 1)])
+def test_one_row(cg, groups, io):
+    check(cg, 37, 1, cg * groups, groups, io, gate=True)
+
+
+@pytest.mark.parametrize("io", IOS)
+@pytest.mark.parametrize("rows", [2, 3, 15, 64, 1000])
+@pytest.mark.parametrize("cg,groups", [(1, 4), (5, 7), (10, 32), (64, 24), (1030, 1)])
+def test_many_rows(rows, cg, groups, io):
+    check(rows + cg, 3, rows, cg * groups, groups, io, act="silu")
+
+
+@pytest.mark.parametrize("io", IOS)
+@pytest.mark.parametrize("rows", [1, 50])
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("affine", [False, True])
+def test_forms(rows, act, gate, affine, io):
+    check(7, 20, rows, 96, 3, io, act=act, gate=gate, affine=affine)
+
+
+@pytest.mark.parametrize("io", IOS)
+@pytest.mark.parametrize("rows", [1, 70])
+def test_alignment(rows, io):
+    for shift in (1, 2, 4):
+        check(11, 9, rows, 128, 4, io, gate=True, shift=shift)
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+def test_common_offset(rows):
+    check(12, 8, rows, 256, 4, torch.float32, act="silu", offset=30.0)
+
+
+def test_many_entries_and_wide():
+    check(13, 5000, 1, 48, 3, torch.bfloat16, gate=True)
+    check(14, 2, 5, 6000, 2, torch.float32, act="silu")
+
+
+def test_constant_values():
+    """Nothing varies: the variance is zero, y is the bias and dx finite."""
+    x = torch.full((4, 3, 32), 2.5, device=DEV)
+    b = torch.arange(32, dtype=torch.float32, device=DEV)
+    y, mean, rstd = ssm.group_norm_fwd(x, 4, bias=b)
+    assert torch.equal(y, b.expand(4, 3, 32)) and (mean == 2.5).all()
+    g = ssm.group_norm_bwd(x, 4, torch.ones_like(x), mean, rstd, bias=b)
+    assert (g["dx"].abs() < 1e-3).all() and torch.equal(g["dbias"], torch.full_like(b, 12.0))
+
+
+def test_gradients_against_differences():
+    """Central differences of the kernel's own forward, along random directions.  An fp32 loss of
+    about 100 terms carries 1e-6; over a step of 2e-2 that is 1e-4, and the step's own error is
+    of third order, 1e-4: 1e-2 of the largest is ample."""
+    rng = np.random.default_rng(15)
+    for rows in (1, 6):
+        t = {n: tensor(rng, (2, rows, 24), torch.float32) for n in ("x", "z", "dy")}
+        p = {n: tensor(rng, (24,), torch.float32, 1.0) for n in ("weight", "bias")}
+
+        def loss(x, z, weight, bias):
+            y = ssm.group_norm_fwd(x, 3, weight=weight, bias=bias, z=z, act="silu")[0]
+            return float((y.double() * t["dy"].double()).sum())
+
+        args = dict(x=t["x"], z=t["z"], **p)
+        _, mean, rstd = ssm.group_norm_fwd(t["x"], 3, weight=p["weight"], bias=p["bias"], z=t["z"], act="silu")
+        g = ssm.group_norm_bwd(t["x"], 3, t["dy"], mean, rstd, weight=p["weight"], bias=p["bias"], z=t["z"], act="silu")
+        for n in args:
+            d = tensor(rng, args[n].shape, torch.float32)
+            e = 1e-2
+            up = loss(**{**args, n: args[n] + e * d})
+            down = loss(**{**args, n: args[n] - e * d})
+            want = float((g["d" + n].double() * d.double()).sum())
+            assert abs((up - down) / (2 * e) - want) <= 1e-2 * max(1.0, abs(want)), n
+
+
+def test_same_bits_other_stream_in_place():
+    rng = np.random.default_rng(16)
+    for rows, io in ((1, torch.bfloat16), (200, torch.float32)):
+        x, z, dy = (tensor(rng, (30, rows, 192), io) for _ in range(3))
+        w = tensor(rng, (192,), torch.float32)
+        y, mean, rstd = ssm.group_norm_fwd(x, 3, weight=w, z=z)
+        g = ssm.group_norm_bwd(x, 3, dy, mean, rstd, weight=w, z=z)
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        need = max(ssm.group_norm_workspace_size(30, rows, 192, 3, io, backward=d) for d in (False, True))
+        ws = torch.full((max(need, 1),), 255, dtype=torch.uint8, device=DEV)
+        x2 = x.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            g2 = ssm.group_norm_bwd(x2, 3, dy, mean, rstd, weight=w, z=z, workspace=ws)
+            y2 = ssm.group_norm_fwd(x2, 3, weight=w, z=z, y=x2, workspace=ws, return_stats=False)[0]
+        s.synchronize()
+        assert torch.equal(y, y2) and all(torch.equal(g[n], g2[n]) for n in ("dx", "dz", "dweight"))
+        assert g2["dbias"] is None
+
+
+def test_empty():
+    w = torch.ones(8, device=DEV)
+    for shape in ((0, 3, 8), (2, 0, 8)):
+        x = torch.empty(shape, device=DEV)
+        y, mean, rstd = ssm.group_norm_fwd(x, 2, weight=w)
+        g = ssm.group_norm_bwd(x, 2, x, mean, rstd, weight=w)
+        assert y.shape == x.shape and (g["dweight"] == 0).all()
