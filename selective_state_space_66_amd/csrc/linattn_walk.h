@@ -35,11 +35,23 @@
 // parts whose sizes matter (hi hi; hi mid, mid hi; hi lo, mid mid, lo hi).
 // fp32 tensors travel as three parts.  With bf16 tensors the weighted c of
 // the state update has three parts, so the state (an fp32 output) is exact to
-// fp32 rounding; the scores and the state that multiplies a_t have one part in
-// what is rounded to a bf16 output afterwards (their rounding of 2^-9 adds in
-// quadrature to the output's own: 2.0e-3 relative RMS against 1.7e-3), three
-// in what leads to g's gradient, which is an fp32 sum.  Everything is
-// accumulated in fp32.
+// fp32 rounding.  Where they lead to a bf16 output, the scores have two parts
+// and the state that multiplies a_t one: its rounding adds in quadrature to
+// the output's own (2.3e-3 relative RMS where the state is all there is,
+// against 1.7e-3), and a second part costs the LDS traffic of the longest
+// step twice.  Where they lead to g's gradient, an fp32 sum, both have three.
+// Everything is accumulated in fp32.
+//
+// Work split.  A block owns one entry, head, span of the tokens and VB columns
+// of c.  A chunk's steps form a chain (state, outputs, next state), and with
+// one wave of a block per SIMD its latencies add up, so a block has two groups
+// of four waves that work on a chunk at the same time.  Group A makes the
+// outputs, with the rows of a straight from memory in operand registers.  Group B keeps the state in registers,
+// updates it, and brings b and c in: it stages chunk i + 1 while chunk i is
+// worked on, from loads issued a chunk earlier, into the other of two buffers:
+// one barrier per chunk.  (Where the LDS holds one buffer only, group B waits
+// for both groups to be done with it: two barriers.)
+// Chunks of 64 tokens: the starts of documents fit one ballot.
 #pragma once
 
 #include "linattn_launch.h"
@@ -127,6 +139,14 @@ __device__ __forceinline__ constexpr int swc(int r, int col) {
   return (((col >> 3) ^ (((r >> kShift) & kMask) << 1)) << 3) | (col & 7);
 }
 
+// The contractions over kappa take it in steps of 32; lane group lk of step k
+// holds the 8 values from here on (any split that both operands share gives
+// the same sums; this one is what the loads of a deliver)
+template <int NP>
+__device__ __forceinline__ constexpr int kcol(int k, int lk) {
+  return NP == 1 ? 64 * (k / 2) + 16 * lk + 8 * (k % 2) : 32 * k + 8 * lk;
+}
+
 // Transposing reads: the operand "row l % 16, k = ..." of a matrix stored
 // k-major.  Lane i of each 16 receives, as its 4 values, element i % 4 of the
 // 8 bytes addressed by lanes 4 k + i / 4, k = 0..3, of its group.
@@ -145,20 +165,34 @@ struct Io<3> { typedef float T; };
 
 template <int NP, int KP, int VB, bool DG, bool STATE>
 struct Shape {
-  static constexpr int PS = STATE ? 0 : (NP == 3 || DG ? 3 : 1);            // parts of the state
+  static constexpr int PS = STATE ? 0 : (NP == 3 || DG ? 3 : 1);  // parts of the state
   // the fp32 form with 256-wide rows keeps two parts of T: three do not fit the LDS
   static constexpr int PT = (STATE || !DG) ? 0 : (NP == 3 && KP == 256 ? 2 : 3);
-  static constexpr int PW = 3;                                             // parts of the weighted c
-  static constexpr int NC = STATE ? 0 : NP;
-  static constexpr int NW2 = DG ? PW : 0;
-  static constexpr int kB = NP * kQ * KP;
-  static constexpr int kC = NC * kQ * VB;
+  static constexpr int PW = 3;                                    // parts of the weighted c
+  static constexpr int kB = NP * kQ * KP;                         // one buffer of b
+  static constexpr int kC = STATE ? 0 : NP * kQ * VB;             // one buffer of c
   static constexpr int kW = PW * kQ * VB;
-  static constexpr int kW2 = NW2 * kQ * VB;
+  static constexpr int kW2 = DG ? kW : 0;
   static constexpr int kS = PS * VB * KP;
   static constexpr int kT = PT * VB * KP;
+  static constexpr int kLds = 160 * 1024;                         // of a CU
   static constexpr int kElems = kB + kC + kW + kW2 + kS + kT;
-  static constexpr bool kFits = 2 * kElems + 1024 <= 160 * 1024;  // the LDS of a CU
+  static constexpr int bytes(int nbuf) { return 2 * nbuf * kElems + (DG ? 1024 : 0); }
+  static constexpr int NBUF = !STATE && bytes(2) <= kLds ? 2 : 1;
+  static constexpr bool kFits = bytes(NBUF) <= kLds;
+  // Waves of a group along the columns v: a half of them each where there are
+  // four tiles.  Group B's then split the rows kappa in two, group A's
+  // take two of the four token blocks each -- 0 and 3, or 1 and 2, which see
+  // the same number of blocks -- and every operand read from LDS serves twice.
+  static constexpr int WV = VB >= 64 ? 2 : 1;
+  static constexpr int WK = 4 / WV;
+  static constexpr int NB = WV;             // token blocks of a group A wave
+  static constexpr int NVW = VB / 16 / WV;  // column tiles of a wave
+  static constexpr int JK = KP / 16 / WK;   // row tiles of the state of a group B wave
+  static constexpr int kThreads = STATE ? 256 : 512;
+  // waves per SIMD that the registers are shared out for: what the LDS lets in
+  static constexpr int kWaves = STATE ? (2 * bytes(1) <= kLds ? 2 : 1)
+                                      : (2 * bytes(NBUF) <= kLds ? 4 : 2);
 };
 
 __device__ __forceinline__ uint64_t low_bits(int n) {
@@ -171,28 +205,24 @@ __device__ __forceinline__ float power(float g2, int e) {
 }
 
 template <int NP, int KP, int VB, bool REV, bool DG, bool STATE>
-__global__ __launch_bounds__(256, NP == 1 ? 2 : 1) void walk_kernel(const WalkArgs p) {
+__global__ __launch_bounds__((Shape<NP, KP, VB, DG, STATE>::kThreads), (Shape<NP, KP, VB, DG, STATE>::kWaves))
+void walk_kernel(const WalkArgs p) {
   typedef typename Io<NP>::T T;
   typedef Shape<NP, KP, VB, DG, STATE> Sh;
   constexpr int ES = sizeof(T);
   constexpr int EPP = 16 / ES;                 // elements of a 16-byte piece
   constexpr int PRB = KP / EPP;                // pieces in a row of b
   constexpr int PRC = VB / EPP;                // pieces in a row of c
-  constexpr int RB = kQ * PRB / 256;           // pieces of b per thread
+  constexpr int RB = kQ * PRB / 256;           // pieces of b per thread of group B
   constexpr int RC = kQ * PRC / 256;
   constexpr int NK = KP / 32;                  // k-steps of a . b
-  constexpr int NV = VB / 16;                  // column tiles of out
-  constexpr int JK = KP / 64;                  // row tiles of the state per wave
-  constexpr int RA = NP == 1 ? NK : 2 * NK;    // 16-byte pieces of a per lane
-  static_assert(RB >= 1 && RC >= 1 && JK >= 1, "tile too small");
+  constexpr int NVW = Sh::NVW;                 // column tiles of a wave
+  constexpr int NBUF = Sh::NBUF;
+  static_assert(RB >= 1 && RC >= 1 && NVW >= 1, "tile too small");
 
-  __shared__ __align__(16) __bf16 lds[Sh::kElems];
-  __bf16* const Bs = lds;
-  __bf16* const Cs = Bs + Sh::kB;
-  __bf16* const Cw = Cs + Sh::kC;
-  __bf16* const Cw2 = Cw + Sh::kW;
-  __bf16* const Ss = Cw2 + Sh::kW2;
-  __bf16* const Ts = Ss + Sh::kS;
+  // a buffer: b, c, c weighted (for S, for T), parts of S and of T
+  __shared__ __align__(16) __bf16 lds[NBUF * Sh::kElems];
+  constexpr int kCs = Sh::kB, kCw = kCs + Sh::kC, kCw2 = kCw + Sh::kW, kSs = kCw2 + Sh::kW2, kTs = kSs + Sh::kS;
 
   // Consecutive block ids go round-robin to the 8 XCDs; each XCD gets a
   // contiguous run of (entry, head, span, slice), so the slices that read the
@@ -208,13 +238,14 @@ __global__ __launch_bounds__(256, NP == 1 ? 2 : 1) void walk_kernel(const WalkAr
   const int h = (int)(rest % (uint32_t)p.H);
   const int b = (int)(rest / (uint32_t)p.H);
 
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x & 255, lane = tid & 63;  // within the group
+  const bool group_a = !STATE && __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 8) == 0;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lk = lane >> 4;
+  const int g4 = lane >> 4, kk = (lane & 15) >> 2, qq = lane & 3;  // of the transposing reads
   const int K = p.K, V = p.V;
   const int v0 = sl * VB;
   const float g2 = p.log_decay[h] * kLog2e;
-  const float lam64 = power(g2, kQ);
 
   const int64_t L = p.L;
   int64_t len = L;
@@ -231,501 +262,401 @@ __global__ __launch_bounds__(256, NP == 1 ? 2 : 1) void walk_kernel(const WalkAr
   };
   const int i0 = span * p.span_chunks;
   const int i1 = i0 + p.span_chunks < nc ? i0 + p.span_chunks : nc;
+  // the chunks of the span that hold real tokens, in the walk's order
+  const int first = REV ? (i0 > nc - nlive ? i0 : nc - nlive) : i0;
+  const int last = REV ? i1 : (i1 < nlive ? i1 : nlive);
 
-  // ---- where this block's rows are.  One sequence and head of a tensor of
-  // (L, heads, width): byte offsets within a chunk fit 32 bits (the launch
-  // bounds heads * width).
+  // One sequence and head of a tensor of (L, heads, width): byte offsets
+  // within a chunk fit 32 bits (the launch bounds heads * width).
   const int64_t bL = (int64_t)b * L;
-  const uint32_t rsa = (uint32_t)p.Ha * K * ES, rsb = (uint32_t)p.Hb * K * ES, rsc = (uint32_t)p.Hc * V * ES;
-  const char* const pa = STATE ? nullptr : (const char*)p.a + (bL * p.Ha + h / (p.H / p.Ha)) * (int64_t)K * ES;
-  const char* const pb = (const char*)p.b + (bL * p.Hb + h / (p.H / p.Hb)) * (int64_t)K * ES;
-  const char* const pc = (const char*)p.c + ((bL * p.Hc + h / (p.H / p.Hc)) * (int64_t)V + v0) * ES;
-  const char* const px = DG && !STATE ? (const char*)p.x + ((bL * p.Hc + h / (p.H / p.Hc)) * (int64_t)V + v0) * ES : nullptr;
-
-  u32x4 rB[RB], rC[RC], rA[STATE ? 1 : RA];
-  uint32_t rR = 0;
-  const int rowB = tid / PRB, pieceB = tid % PRB;
-  const int rowC = tid / PRC, pieceC = tid % PRC;
-  auto load_chunk = [&](int c) {
-    const int n = live_in(c);
-    const int64_t t0 = (int64_t)c * kQ;
-    {
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(pb + t0 * rsb), (short)0, n ? (int)((uint32_t)(n - 1) * rsb + (uint32_t)K * ES) : 0, kBufferFlags);
-      const uint32_t o = pieceB * EPP < K ? (uint32_t)rowB * rsb + pieceB * 16u : kOutside;
-#pragma unroll
-      for (int j = 0; j < RB; ++j)
-        rB[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-            r, (int)(o == kOutside ? o : o + (uint32_t)j * (256u / PRB) * rsb), 0, 0));
-    }
-    {
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(pc + t0 * rsc), (short)0, n ? (int)((uint32_t)(n - 1) * rsc + (uint32_t)(V - v0) * ES) : 0, kBufferFlags);
-      const uint32_t o = v0 + pieceC * EPP < V ? (uint32_t)rowC * rsc + pieceC * 16u : kOutside;
-#pragma unroll
-      for (int j = 0; j < RC; ++j)
-        rC[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-            r, (int)(o == kOutside ? o : o + (uint32_t)j * (256u / PRC) * rsc), 0, 0));
-    }
-    if constexpr (!STATE) {
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(pa + t0 * rsa), (short)0, n ? (int)((uint32_t)(n - 1) * rsa + (uint32_t)K * ES) : 0, kBufferFlags);
-      const uint32_t o = (uint32_t)(16 * w + lr) * rsa + (uint32_t)lk * 8u * ES;
-#pragma unroll
-      for (int j = 0; j < RA; ++j) {
-        const int k = NP == 1 ? j : j / 2, half = NP == 1 ? 0 : j % 2;
-        const bool in = 32 * k + 8 * lk < K;
-        rA[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-            r, (int)(in ? o + (uint32_t)(32 * k * ES + 16 * half) : kOutside), 0, 0));
-      }
-    }
-    if (p.reset) {
-      const __amdgpu_buffer_rsrc_t r =
-          __builtin_amdgcn_make_buffer_rsrc((void*)(p.reset + bL + t0), (short)0, n, kBufferFlags);
-      rR = __builtin_amdgcn_raw_buffer_load_b8(r, lane, 0, 0);
-    }
-  };
-
-  // ---- a chunk from the registers into LDS
-  bf16x8 aF[STATE ? 1 : NK][NP];
-  uint64_t starts = 0;  // document starts of the staged chunk, one bit per token
-  auto stage = [&](int n) {
-    starts = p.reset ? __ballot((rR & 0xffu) != 0) : 0;
-#pragma unroll
-    for (int j = 0; j < RB; ++j) {
-      const int row = rowB + j * (256 / PRB), col = pieceB * EPP;
-      __bf16* d = Bs + row * KP + sw<KP>(row, col);
-      if constexpr (NP == 1) {
-        *(u32x4*)d = rB[j];
-      } else {
-        uint32_t p0[3], p1[3];
-        split2<3>(__uint_as_float(rB[j][0]), __uint_as_float(rB[j][1]), p0);
-        split2<3>(__uint_as_float(rB[j][2]), __uint_as_float(rB[j][3]), p1);
-#pragma unroll
-        for (int q = 0; q < 3; ++q) *(u32x2*)(d + q * kQ * KP) = u32x2{p0[q], p1[q]};
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < RC; ++j) {
-      const int row = rowC + j * (256 / PRC), col = pieceC * EPP;
-      const int at = row * VB + swc<VB>(row, col);
-      // the weight of this token in the state at the walk's end of the chunk
-      const int e = REV ? row + 1 : n - 1 - row;
-      const bool reaches = REV ? (starts & low_bits(row + 1)) == 0 : ((starts >> row) >> 1) == 0;
-      const bool in = row < n && reaches;
-      const float wt = in ? p.s_state * power(g2, e) : 0.0f;
-      float f[EPP];
-#pragma unroll
-      for (int i = 0; i < EPP; ++i)
-        f[i] = NP == 1 ? ((i & 1) ? hi_bf(rC[j][i / 2]) : lo_bf(rC[j][i / 2])) : __uint_as_float(rC[j][i % 4]);
-      if constexpr (!STATE) {
-        if constexpr (NP == 1) {
-          *(u32x4*)(Cs + at) = rC[j];
-        } else {
-          uint32_t p0[3], p1[3];
-          split2<3>(f[0], f[1], p0);
-          split2<3>(f[2], f[3], p1);
-#pragma unroll
-          for (int q = 0; q < 3; ++q) *(u32x2*)(Cs + q * kQ * VB + at) = u32x2{p0[q], p1[q]};
-        }
-      }
-#pragma unroll
-      for (int which = 0; which < (DG ? 2 : 1); ++which) {
-        const float wq = which == 0 ? wt : wt * (float)(in ? e : 0);
-        __bf16* const d = (which == 0 ? Cw : Cw2) + at;
-        uint32_t pt[EPP / 2][3];
-#pragma unroll
-        for (int i = 0; i < EPP / 2; ++i) {
-          const float x0 = in ? f[2 * i] * wq : 0.0f, x1 = in ? f[2 * i + 1] * wq : 0.0f;
-          split2<3>(x0, x1, pt[i]);
-        }
-#pragma unroll
-        for (int q = 0; q < 3; ++q) {
-          if constexpr (NP == 1)
-            *(u32x4*)(d + q * kQ * VB) = u32x4{pt[0][q], pt[1][q], pt[EPP / 2 - 2][q], pt[EPP / 2 - 1][q]};
-          else
-            *(u32x2*)(d + q * kQ * VB) = u32x2{pt[0][q], pt[1][q]};
-        }
-      }
-    }
-    if constexpr (!STATE) {
-#pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        if constexpr (NP == 1) {
-          aF[k][0] = __builtin_bit_cast(bf16x8, rA[k]);
-        } else {
-          uint32_t pt[4][3];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            split2<3>(__uint_as_float(rA[2 * k + i / 2][2 * (i % 2)]),
-                      __uint_as_float(rA[2 * k + i / 2][2 * (i % 2) + 1]), pt[i]);
-#pragma unroll
-          for (int q = 0; q < 3; ++q)
-            aF[k][q] = __builtin_bit_cast(bf16x8, u32x4{pt[0][q], pt[1][q], pt[2][q], pt[3][q]});
-        }
-      }
-    }
-  };
-
-  // ---- the state, fp32, in the matrix cores' result layout: wave w holds
-  // row tiles kt = w + 4 j; lane value i is W[v = 16 vt + lr][kappa = 16 kt + 4 lk + i]
-  f32x4 S[JK][NV], D[DG ? JK : 1][DG ? NV : 1];
   const int64_t bh = (int64_t)b * p.H + h;
   const int64_t state_elems = (int64_t)K * V;
-#pragma unroll
-  for (int j = 0; j < JK; ++j)
-#pragma unroll
-    for (int vt = 0; vt < NV; ++vt) {
-      S[j][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if constexpr (DG) D[j][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-  if constexpr (!STATE) {
-    auto for_state = [&](auto&& f) {
-#pragma unroll
-      for (int j = 0; j < JK; ++j)
-#pragma unroll
-        for (int vt = 0; vt < NV; ++vt) {
-          const int v = v0 + 16 * vt + lr, k = 16 * (w + 4 * j) + 4 * lk;
-          if (v < V && k < K) f(j, vt, v, k);
-        }
-    };
-    if (p.init) {
-      const float* s0 = p.init + bh * state_elems;
-      for_state([&](int j, int vt, int v, int k) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S[j][vt][i] = s0[v * p.state_sv + (k + i) * p.state_sk];
-      });
-    }
-    // the states that the spans before this one add, in the walk's order
-    for (int m = 0; m < span; ++m) {
-      const float* loc = p.ws + ((int64_t)m * p.batch * p.H + bh) * (DG ? 2 : 1) * state_elems;
-      // real tokens of the span
-      const int m0 = m * p.span_chunks, m1 = m0 + p.span_chunks - 1;
-      const int64_t ca = chunk_of(REV ? m1 : m0), cb = chunk_of(REV ? m0 : m1) + 1;
-      int64_t hi = cb * kQ < len ? cb * kQ : len;
-      const int64_t n = hi > ca * kQ ? hi - ca * kQ : 0;
-      const bool cut = p.span_cut[(int64_t)m * p.batch + b] != 0;
-      const float d = n == 0 ? 1.0f : (cut ? 0.0f : exp2_hw(g2 * (float)n));
-      for_state([&](int j, int vt, int v, int k) {
-        const float4 a = *(const float4*)(loc + (int64_t)v * K + k);
-        const float av[4] = {a.x, a.y, a.z, a.w};
-        if constexpr (DG) {
-          const float4 t = *(const float4*)(loc + state_elems + (int64_t)v * K + k);
-          const float tv[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            D[j][vt][i] = cut ? tv[i] : d * (D[j][vt][i] + (float)n * S[j][vt][i]) + tv[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S[j][vt][i] = cut ? av[i] : d * S[j][vt][i] + av[i];
-      });
-    }
-  }
-  // the state's parts into LDS: four consecutive kappa of one row per lane
-  auto put_state = [&]() {
-    if constexpr (!STATE) {
-#pragma unroll
-      for (int j = 0; j < JK; ++j)
-#pragma unroll
-        for (int vt = 0; vt < NV; ++vt) {
-          const int at = (16 * vt + lr) * KP + sw<KP>(lr, 16 * (w + 4 * j) + 4 * lk);
-          {
-            uint32_t p0[Sh::PS], p1[Sh::PS];
-            split2<Sh::PS>(S[j][vt][0], S[j][vt][1], p0);
-            split2<Sh::PS>(S[j][vt][2], S[j][vt][3], p1);
-#pragma unroll
-            for (int q = 0; q < Sh::PS; ++q) *(u32x2*)(Ss + q * VB * KP + at) = u32x2{p0[q], p1[q]};
-          }
-          if constexpr (DG) {
-            uint32_t p0[Sh::PT], p1[Sh::PT];
-            split2<Sh::PT>(D[j][vt][0], D[j][vt][1], p0);
-            split2<Sh::PT>(D[j][vt][2], D[j][vt][3], p1);
-#pragma unroll
-            for (int q = 0; q < Sh::PT; ++q) *(u32x2*)(Ts + q * VB * KP + at) = u32x2{p0[q], p1[q]};
-          }
-        }
-    }
+  const uint32_t rsc = (uint32_t)p.Hc * V * ES;
+  auto rows_of = [&](const char* base, int64_t t0, uint32_t stride, int n, int width) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(base + t0 * stride), (short)0,
+                                             n ? (int)((uint32_t)(n - 1) * stride + (uint32_t)width * ES) : 0,
+                                             kBufferFlags);
+  };
+  auto load16 = [&](__amdgpu_buffer_rsrc_t r, uint32_t o) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)o, 0, 0));
+  };
+  // the document starts of a chunk, one byte per token (without a branch: an
+  // empty range reads zeros)
+  auto load_starts = [&](int c) -> uint32_t {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(p.reset + bL + (int64_t)c * kQ), (short)0, p.reset ? live_in(c) : 0, kBufferFlags);
+    return __builtin_amdgcn_raw_buffer_load_b8(r, lane, 0, 0);
   };
 
-  // ---- lane constants of the intra-chunk weights, of token t = 16 W + lr and
-  // s = 16 sb + 4 lk + i: on the diagonal block lam^|lr - 4 lk - i|, m blocks
-  // away lam^(16 m - 16) times the weight one block away
-  float wd[4], w1[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = REV ? 4 * lk + i - lr : lr - 4 * lk - i;  // tokens from s to t along the walk
-    wd[i] = e >= 0 ? power(g2, e) : 0.0f;
-    w1[i] = power(g2, 16 + e);  // e > -16
-  }
-  const float lam16 = power(g2, 16);
   float dg = 0.0f;
 
-  // ---- the outputs of token block W (uniform in a wave) of the staged chunk
-  auto outputs = [&](auto Wc, int c, int n) {
-    constexpr int W = decltype(Wc)::value;
-    constexpr int PP = NP == 3 ? 3 : 1;  // parts of the scores that lead to out
-    const int t = 16 * W + lr;
-    const int64_t row = bL + (int64_t)c * kQ + t;
-    // x of this lane's outputs, asked for early
-    u32x4 rX[DG ? NV : 1];
-    if constexpr (DG) {
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(px + (int64_t)c * kQ * rsc), (short)0, (int)((uint32_t)(n - 1) * rsc + (uint32_t)(V - v0) * ES), kBufferFlags);
+  if (!STATE && group_a) {
+    // ================================================== group A: the outputs
+    constexpr int PP = NP == 3 ? 3 : 2;  // parts of the scores that lead to out
+    constexpr int RA = NP == 1 ? NK : 2 * NK;
+    constexpr int NB = Sh::NB;
+    const int wv = w % Sh::WV;                       // which columns
+    const int wt = w / Sh::WV;                       // which token blocks
+    const int vw = 16 * NVW * wv;                    // first column of the wave in the slice
+    // the wave's blocks, first to last: {0, 3} or {1, 2}; one of the four
+    const int blk[2] = {NB == 2 ? wt : w, 3 - wt};
+    const uint32_t rsa = (uint32_t)p.Ha * K * ES;
+    const char* const pa = (const char*)p.a + (bL * p.Ha + h / (p.H / p.Ha)) * (int64_t)K * ES;
+    const char* const px = DG ? (const char*)p.x + ((bL * p.Hc + h / (p.H / p.Hc)) * (int64_t)V + v0) * ES : nullptr;
+
+    u32x4 rA[NB][RA];
+    uint32_t rR = 0;
+    // Two loads cover 128 bytes of the block's 16 rows, 8 whole row pieces each
+    // (reading 64 bytes of 16 rows at a time ran at 2.1 TB/s, this way at the
+    // rate of a copy): load u, lane (lk, lr) takes row 8 u + lr % 8, 16 bytes
+    // at 16 (2 lk + lr / 8).  take_a trades halves between the two.
+    constexpr int kPairElems = 128 / ES;
+    auto load_a = [&](int c) {
+      const __amdgpu_buffer_rsrc_t r = rows_of(pa, (int64_t)c * kQ, rsa, live_in(c), K);
+      const int piece = 2 * lk + (lr >> 3);
 #pragma unroll
-      for (int vt = 0; vt < NV; ++vt) {
-        const int col = 16 * vt + 4 * lk;
-        const int o = (int)(v0 + col < V ? (uint32_t)t * rsc + (uint32_t)col * ES : kOutside);
-        if constexpr (NP == 1) {
-          const u32x2 q = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, o, 0, 0));
-          rX[vt] = u32x4{q[0] << 16, q[0] & 0xffff0000u, q[1] << 16, q[1] & 0xffff0000u};
-        } else {
-          rX[vt] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
+      for (int q = 0; q < NB; ++q)
+#pragma unroll
+        for (int j = 0; j < RA; ++j) {
+          const uint32_t row = (uint32_t)(16 * blk[q] + 8 * (j % 2) + (lr & 7));
+          const int col = kPairElems * (j / 2) + EPP * piece;
+          rA[q][j] = load16(r, col < K ? row * rsa + (uint32_t)(col * ES) : kOutside);
+        }
+      rR = load_starts(c);
+    };
+    bf16x8 aF[NB][NK][NP];
+    uint64_t starts = 0;
+    int edge[NB];  // where token t's document begins; backwards, where the next one does
+    auto take_a = [&]() {
+      starts = __ballot((rR & 0xffu) != 0);
+      if (starts) {
+#pragma unroll
+        for (int q = 0; q < NB; ++q) {
+          const int t = 16 * blk[q] + lr;
+          const uint64_t m = REV ? (starts >> t) >> 1 : starts & low_bits(t + 1);
+          edge[q] = REV ? (m ? t + 1 + __builtin_ctzll(m) : kQ) : (m ? 63 - __builtin_clzll(m) : -1);
         }
       }
-    }
-    // the state's part: acc = W a_t (rows v, columns t)
-    f32x4 acc[NV], acc2[DG ? NV : 1];
-    const int je = REV ? n - 1 - t : t + 1;
-    const bool sees = REV ? ((starts >> t) >> 1) == 0 : (starts & low_bits(t + 1)) == 0;
-    const bool from = sees && t < n;
-    const float wi = from ? p.s_inter * power(g2, je > 0 ? je : 0) : 0.0f;
 #pragma unroll
-    for (int vt = 0; vt < NV; ++vt) {
-      f32x4 q = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int q = 0; q < NB; ++q)
 #pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        bf16x8 sF[Sh::PS > 0 ? Sh::PS : 1];
-#pragma unroll
-        for (int e = 0; e < Sh::PS; ++e)
-          sF[e] = *(const bf16x8*)(Ss + e * VB * KP + (16 * vt + lr) * KP + sw<KP>(lr, 32 * k + 8 * lk));
-        q = mfma_parts(sF, aF[k], q);
-      }
-      if constexpr (DG) {
-        f32x4 u = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          bf16x8 sF[Sh::PT > 0 ? Sh::PT : 1];
-#pragma unroll
-          for (int e = 0; e < Sh::PT; ++e)
-            sF[e] = *(const bf16x8*)(Ts + e * VB * KP + (16 * vt + lr) * KP + sw<KP>(lr, 32 * k + 8 * lk));
-          u = mfma_parts(sF, aF[k], u);
-        }
-        acc2[vt] = u;
-      }
-      acc[vt] = q;
-    }
-    settle(acc);
-    if constexpr (DG) settle(acc2);
-#pragma unroll
-    for (int vt = 0; vt < NV; ++vt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (DG) acc2[vt][i] = from ? wi * (acc2[vt][i] + (float)je * acc[vt][i]) : 0.0f;
-        acc[vt][i] = from ? wi * acc[vt][i] : 0.0f;
-      }
-    // the chunk's own part, two 16-token blocks of s at a time: scores
-    // transposed (s by t), weighted, and as they stand the operand of the
-    // product with c
-#pragma unroll
-    for (int pair = REV ? W / 2 : 0; pair <= (REV ? 1 : W / 2); ++pair) {
-      uint32_t pw[2][2][PP], pw2[2][2][DG ? 3 : 1];  // [block][half][part]
-      f32x4 g[2];
-      uint32_t sees_s[2];  // bit i: token t sees token s = 16 sb + 4 lk + i
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int sb = 2 * pair + u;
-        const int m = REV ? sb - W : W - sb;  // blocks from s to t
-        g[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        sees_s[u] = 0;
-        if (m < 0) continue;
-        sees_s[u] = m > 0 ? 15u : 0u;
-        if (m == 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sees_s[u] |= (REV ? 4 * lk + i >= lr : 4 * lk + i <= lr) ? 1u << i : 0u;
-        }
-        if (starts) {
+        for (int j = 0; j < RA / 2; ++j) {
+          // pieces 2 lk and 2 lk + 1 of row lr: within each 16 lanes, the upper
+          // half of one comes from the other load 8 lanes down, the lower half
+          // of the other 8 lanes up
+          u32x4 lo, hi;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int s = 16 * sb + 4 * lk + i;
-            const int lo = REV ? t : s, hi = REV ? s : t;
-            if ((starts & low_bits(hi + 1) & ~low_bits(lo + 1)) != 0) sees_s[u] &= ~(1u << i);
+            const int r0 = (int)rA[q][2 * j][i], r1 = (int)rA[q][2 * j + 1][i];
+            lo[i] = (uint32_t)__builtin_amdgcn_update_dpp(r0, r1, 0x118, 0xf, 0xc, false);  // row_shr:8
+            hi[i] = (uint32_t)__builtin_amdgcn_update_dpp(r1, r0, 0x108, 0xf, 0x3, false);  // row_shl:8
+          }
+          if constexpr (NP == 1) {
+            aF[q][2 * j][0] = __builtin_bit_cast(bf16x8, lo);
+            aF[q][2 * j + 1][0] = __builtin_bit_cast(bf16x8, hi);
+          } else {
+            uint32_t pt[4][3];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              split2<3>(__uint_as_float(lo[2 * i]), __uint_as_float(lo[2 * i + 1]), pt[i]);
+              split2<3>(__uint_as_float(hi[2 * i]), __uint_as_float(hi[2 * i + 1]), pt[2 + i]);
+            }
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+              aF[q][j][e] = __builtin_bit_cast(bf16x8, u32x4{pt[0][e], pt[1][e], pt[2][e], pt[3][e]});
+          }
+        }
+    };
+
+    // lane constants of the intra-chunk weights, of token t = 16 W + lr and
+    // s = 16 sb + 4 lk + i: on the diagonal block lam^|lr - 4 lk - i|, m blocks
+    // away lam^(16 m - 16) times the weight one block away
+    float wd[4], w1[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = REV ? 4 * lk + i - lr : lr - 4 * lk - i;  // tokens from s to t along the walk
+      wd[i] = e >= 0 ? p.s_intra * power(g2, e) : 0.0f;
+      w1[i] = p.s_intra * power(g2, 16 + e);  // e > -16
+    }
+    const float lam16 = power(g2, 16), lam32 = power(g2, 32);
+    // the weight of the state at this lane's tokens of a full chunk
+    float wi_full[NB];
+#pragma unroll
+    for (int q = 0; q < NB; ++q)
+      wi_full[q] = p.s_inter * power(g2, REV ? kQ - 1 - 16 * blk[q] - lr : 16 * blk[q] + lr + 1);
+
+    f32x4 acc[NB][NVW], acc2[DG ? NB : 1][DG ? NVW : 1];
+    u32x4 rX[DG ? NB : 1][DG ? NVW : 1];
+
+    // acc = W a_t (rows v, columns t), weighted
+    auto state_part = [&](int n, const __bf16* Ss, const __bf16* Ts) {
+#pragma unroll
+      for (int q = 0; q < NB; ++q)
+#pragma unroll
+        for (int vt = 0; vt < NVW; ++vt) {
+          acc[q][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          if constexpr (DG) acc2[q][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        bf16x8 sF[NVW][Sh::PS > 0 ? Sh::PS : 1], tF[DG ? NVW : 1][Sh::PT > 0 ? Sh::PT : 1];
+#pragma unroll
+        for (int vt = 0; vt < NVW; ++vt) {
+          const int at = (vw + 16 * vt + lr) * KP + sw<KP>(lr, kcol<NP>(k, lk));
+#pragma unroll
+          for (int e = 0; e < Sh::PS; ++e) sF[vt][e] = *(const bf16x8*)(Ss + e * VB * KP + at);
+          if constexpr (DG) {
+#pragma unroll
+            for (int e = 0; e < Sh::PT; ++e) tF[vt][e] = *(const bf16x8*)(Ts + e * VB * KP + at);
           }
         }
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
+        for (int vt = 0; vt < NVW; ++vt)
+#pragma unroll
+          for (int q = 0; q < NB; ++q) {
+            acc[q][vt] = mfma_parts(sF[vt], aF[q][k], acc[q][vt]);
+            if constexpr (DG) acc2[q][vt] = mfma_parts(tF[vt], aF[q][k], acc2[q][vt]);
+          }
+      }
+#pragma unroll
+      for (int q = 0; q < NB; ++q) {
+        settle(acc[q]);
+        if constexpr (DG) settle(acc2[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < NB; ++q) {
+        const int t = 16 * blk[q] + lr;
+        const int je = REV ? n - 1 - t : t + 1;
+        float wi = REV && n < kQ ? p.s_inter * power(g2, je > 0 ? je : 0) : wi_full[q];
+        bool from = true;
+        if (n < kQ || starts) {
+          from = t < n && (!starts || edge[q] == (REV ? kQ : -1));
+        }
+#pragma unroll
+        for (int vt = 0; vt < NVW; ++vt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (DG) acc2[q][vt][i] = from ? wi * (acc2[q][vt][i] + (float)je * acc[q][vt][i]) : 0.0f;
+            acc[q][vt][i] = from ? wi * acc[q][vt][i] : 0.0f;
+          }
+      }
+    };
+
+    // The chunk's own part, two 16-token blocks of s at a time: scores
+    // transposed (s by t), weighted, and as they stand the operand of the
+    // product with c.  W0, W1: the wave's token blocks (uniform in a wave).
+    auto chunk_part = [&](auto W0c, auto W1c, const __bf16* Bs, const __bf16* Cs) {
+      constexpr int Ws[2] = {decltype(W0c)::value, decltype(W1c)::value};
+      constexpr int Wmin = Ws[0], Wmax = NB == 2 ? Ws[1] : Ws[0];
+      f32x4 g[2][NB][2];
+#pragma unroll
+      for (int pair = 0; pair < 2; ++pair)
+#pragma unroll
+        for (int q = 0; q < NB; ++q) g[pair][q][0] = g[pair][q][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < NK; ++k)
+#pragma unroll
+        for (int sb = REV ? Wmin : 0; sb <= (REV ? 3 : Wmax); ++sb) {
           bf16x8 bF[NP];
 #pragma unroll
           for (int e = 0; e < NP; ++e)
-            bF[e] = *(const bf16x8*)(Bs + e * kQ * KP + (16 * sb + lr) * KP + sw<KP>(lr, 32 * k + 8 * lk));
-          g[u] = mfma_parts(bF, aF[k], g[u]);
+            bF[e] = *(const bf16x8*)(Bs + e * kQ * KP + (16 * sb + lr) * KP + sw<KP>(lr, kcol<NP>(k, lk)));
+#pragma unroll
+          for (int q = 0; q < NB; ++q)
+            if (REV ? sb >= Ws[q] : sb <= Ws[q]) g[sb / 2][q][sb % 2] = mfma_parts(bF, aF[q][k], g[sb / 2][q][sb % 2]);
+        }
+#pragma unroll
+      for (int pair = REV ? Wmin / 2 : 0; pair <= (REV ? 1 : Wmax / 2); ++pair)
+#pragma unroll
+        for (int q = 0; q < NB; ++q) settle(g[pair][q]);
+#pragma unroll
+      for (int pair = REV ? Wmin / 2 : 0; pair <= (REV ? 1 : Wmax / 2); ++pair) {
+        const int ra = 32 * pair + 4 * g4 + kk, rb = ra + 16;
+        bf16x8 cF[NVW][NP];
+#pragma unroll
+        for (int vt = 0; vt < NVW; ++vt)
+#pragma unroll
+          for (int e = 0; e < NP; ++e)
+            cF[vt][e] = join(tr_read(Cs + e * kQ * VB + ra * VB + swc<VB>(ra, vw + 16 * vt + 4 * qq)),
+                             tr_read(Cs + e * kQ * VB + rb * VB + swc<VB>(rb, vw + 16 * vt + 4 * qq)));
+#pragma unroll
+        for (int q = 0; q < NB; ++q) {
+          if (REV ? 2 * pair + 1 < Ws[q] : 2 * pair > Ws[q]) continue;  // it sees neither block
+          uint32_t pw[2][2][PP], pw2[2][2][DG ? 3 : 1];  // [block][half][part]
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int sb = 2 * pair + u;
+            const int m = REV ? sb - Ws[q] : Ws[q] - sb;  // blocks from s to t
+            if (m < 0) {
+#pragma unroll
+              for (int e = 0; e < PP; ++e) pw[u][0][e] = pw[u][1][e] = 0;
+              if constexpr (DG) {
+#pragma unroll
+                for (int e = 0; e < 3; ++e) pw2[u][0][e] = pw2[u][1][e] = 0;
+              }
+              continue;
+            }
+            float x[4], x2[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float y = g[pair][q][u][i] * (m == 0 ? wd[i] : w1[i]);
+              if (m == 2) y *= lam16;
+              if (m == 3) y *= lam32;
+              // a token that t does not see leaves nothing, whatever it holds
+              if (m == 0) y = (REV ? 4 * lk + i >= lr : 4 * lk + i <= lr) ? y : 0.0f;
+              x[i] = y;
+            }
+            if (starts) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int s = 16 * sb + 4 * lk + i;
+                x[i] = (REV ? s < edge[q] : s >= edge[q]) ? x[i] : 0.0f;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              x2[i] = DG ? x[i] * (float)(16 * m + (REV ? 4 * lk + i - lr : lr - 4 * lk - i)) : 0.0f;
+            split2<PP>(x[0], x[1], pw[u][0]);
+            split2<PP>(x[2], x[3], pw[u][1]);
+            if constexpr (DG) {
+              split2<3>(x2[0], x2[1], pw2[u][0]);
+              split2<3>(x2[2], x2[3], pw2[u][1]);
+            }
+          }
+          bf16x8 pF[PP], pF2[DG ? 3 : 1];
+#pragma unroll
+          for (int e = 0; e < PP; ++e)
+            pF[e] = __builtin_bit_cast(bf16x8, u32x4{pw[0][0][e], pw[0][1][e], pw[1][0][e], pw[1][1][e]});
+          if constexpr (DG) {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+              pF2[e] = __builtin_bit_cast(bf16x8, u32x4{pw2[0][0][e], pw2[0][1][e], pw2[1][0][e], pw2[1][1][e]});
+          }
+#pragma unroll
+          for (int vt = 0; vt < NVW; ++vt) {
+            acc[q][vt] = mfma_parts(cF[vt], pF, acc[q][vt]);
+            if constexpr (DG) acc2[q][vt] = mfma_parts(cF[vt], pF2, acc2[q][vt]);
+          }
         }
       }
-      settle(g);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int sb = 2 * pair + u;
-        const int m = REV ? sb - W : W - sb;
-        const float f = m >= 3 ? p.s_intra * lam16 * lam16 : (m == 2 ? p.s_intra * lam16 : p.s_intra);
-        float x[4], x2[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float y = g[u][i] * (f * (m <= 0 ? wd[i] : w1[i]));
-          x[i] = (sees_s[u] >> i) & 1u ? y : 0.0f;
-          if constexpr (DG) x2[i] = x[i] * (float)(16 * m + (REV ? 4 * lk + i - lr : lr - 4 * lk - i));
-        }
-        split2<PP>(x[0], x[1], pw[u][0]);
-        split2<PP>(x[2], x[3], pw[u][1]);
-        if constexpr (DG) {
-          split2<3>(x2[0], x2[1], pw2[u][0]);
-          split2<3>(x2[2], x2[3], pw2[u][1]);
-        }
+      for (int q = 0; q < NB; ++q) {
+        settle(acc[q]);
+        if constexpr (DG) settle(acc2[q]);
       }
-      bf16x8 pF[PP], pF2[DG ? 3 : 1];
-#pragma unroll
-      for (int e = 0; e < PP; ++e)
-        pF[e] = __builtin_bit_cast(bf16x8, u32x4{pw[0][0][e], pw[0][1][e], pw[1][0][e], pw[1][1][e]});
-      if constexpr (DG) {
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-          pF2[e] = __builtin_bit_cast(bf16x8, u32x4{pw2[0][0][e], pw2[0][1][e], pw2[1][0][e], pw2[1][1][e]});
-      }
-      const int g4 = lane >> 4, kk = (lane & 15) >> 2, qq = lane & 3;
-      const int ra = 32 * pair + 4 * g4 + kk, rb = ra + 16;
-#pragma unroll
-      for (int vt = 0; vt < NV; ++vt) {
-        bf16x8 cF[NP];
-#pragma unroll
-        for (int e = 0; e < NP; ++e)
-          cF[e] = join(tr_read(Cs + e * kQ * VB + ra * VB + swc<VB>(ra, 16 * vt + 4 * qq)),
-                       tr_read(Cs + e * kQ * VB + rb * VB + swc<VB>(rb, 16 * vt + 4 * qq)));
-        acc[vt] = mfma_parts(cF, pF, acc[vt]);
-        if constexpr (DG) acc2[vt] = mfma_parts(cF, pF2, acc2[vt]);
-      }
-    }
-    settle(acc);
-    if constexpr (DG) settle(acc2);
-    // out rows of real tokens, and zeros at padding inside the chunk
-    if (row < bL + L) {
-#pragma unroll
-      for (int vt = 0; vt < NV; ++vt) {
-        const int v = v0 + 16 * vt + 4 * lk;
-        if (v < V) {
-          const f32x4 o = t < n ? acc[vt] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-          const int64_t at = (row * p.H + h) * V + v;
-          if (NP == 3 || p.out_f32)
-            *(float4*)((float*)p.out + at) = float4{o[0], o[1], o[2], o[3]};
-          else
-            *(u32x2*)((bf16_bits*)p.out + at) = u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
-        }
-      }
-    }
-    if constexpr (DG) {
-#pragma unroll
-      for (int vt = 0; vt < NV; ++vt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (t < n) dg = fmaf(acc2[vt][i], __uint_as_float(rX[vt][i]), dg);
-    }
-  };
+    };
 
-  // ---- the state at the walk's end of the staged chunk
-  auto update = [&](int n) {
-    const bool cut = starts != 0;
-    const float d = cut ? 0.0f : (n == kQ ? lam64 : power(g2, n));
-    const float nf = (float)n;
-#pragma unroll
-    for (int j = 0; j < JK; ++j)
-#pragma unroll
-      for (int vt = 0; vt < NV; ++vt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (DG) D[j][vt][i] = cut ? 0.0f : d * (D[j][vt][i] + nf * S[j][vt][i]);
-          S[j][vt][i] = cut ? 0.0f : d * S[j][vt][i];
-        }
-    const int g4 = lane >> 4, kk = (lane & 15) >> 2, qq = lane & 3;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const int ra = 32 * ks + 8 * g4 + kk, rb = ra + 4;
-      bf16x8 bF[JK][NP];
-#pragma unroll
-      for (int j = 0; j < JK; ++j)
-#pragma unroll
-        for (int e = 0; e < NP; ++e) {
-          const int col = 16 * (w + 4 * j) + 4 * qq;
-          bF[j][e] = join(tr_read(Bs + e * kQ * KP + ra * KP + sw<KP>(ra, col)),
-                          tr_read(Bs + e * kQ * KP + rb * KP + sw<KP>(rb, col)));
-        }
-#pragma unroll
-      for (int vt = 0; vt < NV; ++vt) {
-        const int col = 16 * vt + 4 * qq;
-        bf16x8 cF[3];
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-          cF[e] = join(tr_read(Cw + e * kQ * VB + ra * VB + swc<VB>(ra, col)),
-                       tr_read(Cw + e * kQ * VB + rb * VB + swc<VB>(rb, col)));
-#pragma unroll
-        for (int j = 0; j < JK; ++j) S[j][vt] = mfma_parts(bF[j], cF, S[j][vt]);
-        if constexpr (DG) {
-#pragma unroll
-          for (int e = 0; e < 3; ++e)
-            cF[e] = join(tr_read(Cw2 + e * kQ * VB + ra * VB + swc<VB>(ra, col)),
-                         tr_read(Cw2 + e * kQ * VB + rb * VB + swc<VB>(rb, col)));
-#pragma unroll
-          for (int j = 0; j < JK; ++j) D[j][vt] = mfma_parts(bF[j], cF, D[j][vt]);
-        }
-      }
+    if (first < last) {
+      load_a(chunk_of(first));
+      take_a();
+      if (first + 1 < last) load_a(chunk_of(first + 1));
     }
-#pragma unroll
-    for (int j = 0; j < JK; ++j) {
-      settle(S[j]);
-      if constexpr (DG) settle(D[j]);
-    }
-  };
-
-  // ---- the walk
-  const int first = REV ? (i0 > nc - nlive ? i0 : nc - nlive) : i0;
-  const int last = REV ? i1 : (i1 < nlive ? i1 : nlive);
-  int any_start = 0;
-  if (first < last) {
-    load_chunk(chunk_of(first));
-    stage(live_in(chunk_of(first)));
-    put_state();
     lds_barrier();
     for (int i = first; i < last; ++i) {
       const int c = chunk_of(i), n = live_in(c);
-      if (i + 1 < last) load_chunk(chunk_of(i + 1));
-      if constexpr (!STATE) {
-        if (w == 0) outputs(std::integral_constant<int, 0>{}, c, n);
-        else if (w == 1) outputs(std::integral_constant<int, 1>{}, c, n);
-        else if (w == 2) outputs(std::integral_constant<int, 2>{}, c, n);
-        else outputs(std::integral_constant<int, 3>{}, c, n);
+      const __bf16* const buf = lds + (NBUF == 2 ? ((i - first) & 1) * Sh::kElems : 0);
+      if constexpr (DG) {  // x of this lane's outputs
+        const __amdgpu_buffer_rsrc_t r = rows_of(px, (int64_t)c * kQ, rsc, n, V - v0);
+#pragma unroll
+        for (int q = 0; q < NB; ++q)
+#pragma unroll
+          for (int vt = 0; vt < NVW; ++vt) {
+            const int col = vw + 16 * vt + 4 * lk, t = 16 * blk[q] + lr;
+            const uint32_t o = v0 + col < V ? (uint32_t)t * rsc + (uint32_t)col * ES : kOutside;
+            if constexpr (NP == 1) {
+              const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)o, 0, 0));
+              rX[q][vt] = u32x4{x[0], x[1], 0u, 0u};
+            } else {
+              rX[q][vt] = load16(r, o);
+            }
+          }
       }
-      any_start |= starts != 0;
-      update(n);
+      state_part(n, buf + kSs, buf + kTs);
+      constexpr std::integral_constant<int, 0> k0{};
+      constexpr std::integral_constant<int, 1> k1{};
+      constexpr std::integral_constant<int, 2> k2{};
+      constexpr std::integral_constant<int, 3> k3{};
+      if constexpr (NB == 2) {
+        if (wt == 0) chunk_part(k0, k3, buf, buf + kCs);
+        else chunk_part(k1, k2, buf, buf + kCs);
+      } else {
+        if (w == 0) chunk_part(k0, k0, buf, buf + kCs);
+        else if (w == 1) chunk_part(k1, k1, buf, buf + kCs);
+        else if (w == 2) chunk_part(k2, k2, buf, buf + kCs);
+        else chunk_part(k3, k3, buf, buf + kCs);
+      }
+      if constexpr (DG) {
+#pragma unroll
+        for (int q = 0; q < NB; ++q)
+#pragma unroll
+          for (int vt = 0; vt < NVW; ++vt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = NP == 1 ? ((e & 1) ? hi_bf(rX[q][vt][e / 2]) : lo_bf(rX[q][vt][e / 2]))
+                                      : __uint_as_float(rX[q][vt][e]);
+              dg = 16 * blk[q] + lr < n ? fmaf(acc2[q][vt][e], x, dg) : dg;
+            }
+      }
+      if (NBUF == 1) lds_barrier();  // group B may write
+      // the next chunk's a, from loads a chunk old, and the loads after it
+      // (before the stores, so that no wait for loads is one for stores)
       if (i + 1 < last) {
-        lds_barrier();
-        stage(live_in(chunk_of(i + 1)));
-        put_state();
-        lds_barrier();
+        take_a();
+        if (i + 2 < last) load_a(chunk_of(i + 2));
       }
-    }
-  }
-
-  if constexpr (STATE) {
-    float* loc = p.ws + ((int64_t)span * p.batch * p.H + bh) * (DG ? 2 : 1) * state_elems;
+      // out rows of real tokens, and zeros at padding inside the chunk
+      {
+        const bool wide = NP == 3 || p.out_f32;
+        const uint32_t oes = wide ? 4u : 2u;
+        const uint32_t rso = (uint32_t)p.H * V * oes;
+        const int64_t rows = L - (int64_t)c * kQ < kQ ? L - (int64_t)c * kQ : kQ;
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)((char*)p.out + (((bL + (int64_t)c * kQ) * p.H + h) * V + v0) * (int64_t)oes), (short)0,
+            (int)((uint32_t)(rows - 1) * rso + (uint32_t)(V - v0) * oes), kBufferFlags);
+        if (n < kQ) {
 #pragma unroll
-    for (int j = 0; j < JK; ++j)
+          for (int q = 0; q < NB; ++q)
 #pragma unroll
-      for (int vt = 0; vt < NV; ++vt) {
-        const int v = v0 + 16 * vt + lr, k = 16 * (w + 4 * j) + 4 * lk;
-        if (v < V && k < K) {
-          *(f32x4*)(loc + (int64_t)v * K + k) = S[j][vt];
-          if constexpr (DG) *(f32x4*)(loc + state_elems + (int64_t)v * K + k) = D[j][vt];
+            for (int vt = 0; vt < NVW; ++vt)
+              if (16 * blk[q] + lr >= n) acc[q][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        if (wide) {
+#pragma unroll
+          for (int q = 0; q < NB; ++q)
+#pragma unroll
+            for (int vt = 0; vt < NVW; ++vt) {
+              const int t = 16 * blk[q] + lr, v = vw + 16 * vt + 4 * lk;
+              const int at = v0 + v < V ? (int)((uint32_t)t * rso + (uint32_t)v * 4u) : (int)kOutside;
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[q][vt]), r, at, 0, 0);
+            }
+        } else if constexpr (NVW == 2) {
+          // lanes hold 4 columns of each of two tiles; the swaps (odd rows of
+          // 16 lanes of one operand with the even rows of the other) leave 8
+          // columns of one, so that a store writes 64 bytes of each row
+          const int v = vw + 16 * (lk & 1) + 8 * (lk >> 1);
+#pragma unroll
+          for (int q = 0; q < NB; ++q) {
+            const int t = 16 * blk[q] + lr;
+            const int at = v0 + v < V ? (int)((uint32_t)t * rso + (uint32_t)v * 2u) : (int)kOutside;
+            const f32x4 o0 = acc[q][0], o1 = acc[q][1];
+            const auto s0 = __builtin_amdgcn_permlane16_swap(pack_bf16x2(o0[0], o0[1]), pack_bf16x2(o1[0], o1[1]), false, false);
+            const auto s1 = __builtin_amdgcn_permlane16_swap(pack_bf16x2(o0[2], o0[3]), pack_bf16x2(o1[2], o1[3]), false, false);
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{s0[0], s1[0], s0[1], s1[1]}, r, at, 0, 0);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < NB; ++q)
+#pragma unroll
+            for (int vt = 0; vt < NVW; ++vt) {
+              const int t = 16 * blk[q] + lr, v = vw + 16 * vt + 4 * lk;
+              const int at = v0 + v < V ? (int)((uint32_t)t * rso + (uint32_t)v * 2u) : (int)kOutside;
+              const f32x4 o = acc[q][vt];
+              __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])}, r, at, 0, 0);
+            }
         }
       }
-    if (h == 0 && sl == 0 && tid == 0) p.span_cut[(int64_t)span * p.batch + b] = any_start;
-  } else {
+      lds_barrier();
+    }
     // padding rows of the span that no chunk above held: zeros
     const int ca = chunk_of(REV ? i1 - 1 : i0), cb = chunk_of(REV ? i0 : i1 - 1) + 1;
     const int64_t z0 = ((int64_t)(ca > nlive ? ca : nlive)) * kQ;
@@ -742,42 +673,316 @@ __global__ __launch_bounds__(256, NP == 1 ? 2 : 1) void walk_kernel(const WalkAr
           *(u32x2*)((bf16_bits*)p.out + at) = u32x2{0u, 0u};
       }
     }
-    const bool ends = span == p.nspan - 1;  // this block ends the walk
-    if (ends && p.final_state) {
-      float* fs = p.final_state + bh * state_elems;
+  } else {
+    // ======================================= group B: b, c and the state
+    const uint32_t rsb = (uint32_t)p.Hb * K * ES;
+    const char* const pb = (const char*)p.b + (bL * p.Hb + h / (p.H / p.Hb)) * (int64_t)K * ES;
+    const char* const pc = (const char*)p.c + ((bL * p.Hc + h / (p.H / p.Hc)) * (int64_t)V + v0) * ES;
+    const float lam64 = power(g2, kQ);
+
+    u32x4 rB[RB], rC[RC];
+    uint32_t rR = 0;
+    const int rowB = tid / PRB, pieceB = tid % PRB;
+    const int rowC = tid / PRC, pieceC = tid % PRC;
+    auto load_bc = [&](int c) {
+      const int n = live_in(c);
+      const __amdgpu_buffer_rsrc_t qb = rows_of(pb, (int64_t)c * kQ, rsb, n, K);
+      const __amdgpu_buffer_rsrc_t qc = rows_of(pc, (int64_t)c * kQ, rsc, n, V - v0);
+      const bool inb = pieceB * EPP < K, inc = v0 + pieceC * EPP < V;
+#pragma unroll
+      for (int j = 0; j < RB; ++j)
+        rB[j] = load16(qb, inb ? (uint32_t)(rowB + j * (256 / PRB)) * rsb + pieceB * 16u : kOutside);
+#pragma unroll
+      for (int j = 0; j < RC; ++j)
+        rC[j] = load16(qc, inc ? (uint32_t)(rowC + j * (256 / PRC)) * rsc + pieceC * 16u : kOutside);
+      rR = load_starts(c);
+    };
+
+    uint64_t starts = 0;  // of the staged chunk
+    // the weight of this thread's rows of a full chunk in the state at its end
+    float w_full[RC];
+#pragma unroll
+    for (int j = 0; j < RC; ++j) {
+      const int row = rowC + j * (256 / PRC);
+      w_full[j] = p.s_state * power(g2, REV ? row + 1 : kQ - 1 - row);
+    }
+    u32x4 cC[RC];          // c of the chunk being staged
+    uint32_t cR = 0;
+    auto c_value = [&](int j, int i) {
+      return NP == 1 ? ((i & 1) ? hi_bf(cC[j][i / 2]) : lo_bf(cC[j][i / 2])) : __uint_as_float(cC[j][i % 4]);
+    };
+    // the weighted c of the loaded chunk
+    auto stage_weighted = [&](int n, __bf16* Cw, __bf16* Cw2) {
+      starts = __ballot((cR & 0xffu) != 0);
+#pragma unroll
+      for (int j = 0; j < RC; ++j) {
+        const int row = rowC + j * (256 / PRC), col = pieceC * EPP;
+        const int at = row * VB + swc<VB>(row, col);
+        const int e = REV ? row + 1 : n - 1 - row;
+        float wt = w_full[j];
+        bool in = true;
+        if (n < kQ) {
+          in = row < n;
+          if (!REV) wt = in ? p.s_state * power(g2, e) : 0.0f;
+        }
+        if (starts) in = in && (REV ? (starts & low_bits(row + 1)) == 0 : ((starts >> row) >> 1) == 0);
+        wt = in ? wt : 0.0f;
+#pragma unroll
+        for (int which = 0; which < (DG ? 2 : 1); ++which) {
+          const float wq = which == 0 ? wt : wt * (float)(in ? e : 0);
+          __bf16* const d = (which == 0 ? Cw : Cw2) + at;
+          uint32_t pt[EPP / 2][3];
+#pragma unroll
+          for (int i = 0; i < EPP / 2; ++i) split2<3>(c_value(j, 2 * i) * wq, c_value(j, 2 * i + 1) * wq, pt[i]);
+          if (starts) {  // a token that does not reach the end leaves nothing, whatever it holds
+#pragma unroll
+            for (int i = 0; i < EPP / 2; ++i)
+#pragma unroll
+              for (int q = 0; q < 3; ++q) pt[i][q] = in ? pt[i][q] : 0u;
+          }
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            if constexpr (NP == 1)
+              *(u32x4*)(d + q * kQ * VB) = u32x4{pt[0][q], pt[1][q], pt[EPP / 2 - 2][q], pt[EPP / 2 - 1][q]};
+            else
+              *(u32x2*)(d + q * kQ * VB) = u32x2{pt[0][q], pt[1][q]};
+          }
+        }
+      }
+    };
+    auto stage_rows = [&](__bf16* Bs, __bf16* Cs) {
+#pragma unroll
+      for (int j = 0; j < RC; ++j) cC[j] = rC[j];
+      cR = rR;
+#pragma unroll
+      for (int j = 0; j < RB; ++j) {
+        const int row = rowB + j * (256 / PRB), col = pieceB * EPP;
+        __bf16* const d = Bs + row * KP + sw<KP>(row, col);
+        if constexpr (NP == 1) {
+          *(u32x4*)d = rB[j];
+        } else {
+          uint32_t p0[3], p1[3];
+          split2<3>(__uint_as_float(rB[j][0]), __uint_as_float(rB[j][1]), p0);
+          split2<3>(__uint_as_float(rB[j][2]), __uint_as_float(rB[j][3]), p1);
+#pragma unroll
+          for (int q = 0; q < 3; ++q) *(u32x2*)(d + q * kQ * KP) = u32x2{p0[q], p1[q]};
+        }
+      }
+      if constexpr (!STATE) {
+#pragma unroll
+        for (int j = 0; j < RC; ++j) {
+          const int row = rowC + j * (256 / PRC), col = pieceC * EPP;
+          __bf16* const d = Cs + row * VB + swc<VB>(row, col);
+          if constexpr (NP == 1) {
+            *(u32x4*)d = cC[j];
+          } else {
+            uint32_t p0[3], p1[3];
+            split2<3>(c_value(j, 0), c_value(j, 1), p0);
+            split2<3>(c_value(j, 2), c_value(j, 3), p1);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) *(u32x2*)(d + q * kQ * VB) = u32x2{p0[q], p1[q]};
+          }
+        }
+      }
+    };
+
+    // the state, fp32, in the matrix cores' result layout: lane value i of tile
+    // (j, vt) is W[v = vw + 16 vt + lr][kappa = kw + 16 j + 4 lk + i]
+    constexpr int JK = Sh::JK;
+    const int vw = 16 * NVW * (w % Sh::WV), kw = 16 * JK * (w / Sh::WV);
+    f32x4 S[JK][NVW], D[DG ? JK : 1][DG ? NVW : 1];
+#pragma unroll
+    for (int j = 0; j < JK; ++j)
+#pragma unroll
+      for (int vt = 0; vt < NVW; ++vt) {
+        S[j][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (DG) D[j][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+    auto for_state = [&](auto&& f) {
 #pragma unroll
       for (int j = 0; j < JK; ++j)
 #pragma unroll
-        for (int vt = 0; vt < NV; ++vt) {
-          const int v = v0 + 16 * vt + lr, k = 16 * (w + 4 * j) + 4 * lk;
-          if (v < V && k < K) *(f32x4*)(fs + (int64_t)v * K + k) = S[j][vt];
+        for (int vt = 0; vt < NVW; ++vt) {
+          const int v = v0 + vw + 16 * vt + lr, k = kw + 16 * j + 4 * lk;
+          if (v < V && k < K) f(j, vt, v, k);
         }
-    }
-    if constexpr (DG) {
-      if (ends && p.dlast) {  // <dlast, T after the last token>; dlast is K-major here
-        const float* dl = p.dlast + bh * state_elems;
+    };
+    auto put_state = [&](__bf16* Ss, __bf16* Ts) {
+      if constexpr (!STATE) {
 #pragma unroll
         for (int j = 0; j < JK; ++j)
 #pragma unroll
-          for (int vt = 0; vt < NV; ++vt) {
-            const int v = v0 + 16 * vt + lr, k = 16 * (w + 4 * j) + 4 * lk;
-            if (v < V && k < K) {
+          for (int vt = 0; vt < NVW; ++vt) {
+            const int at = (vw + 16 * vt + lr) * KP + sw<KP>(lr, kw + 16 * j + 4 * lk);
+            {
+              uint32_t p0[Sh::PS], p1[Sh::PS];
+              split2<Sh::PS>(S[j][vt][0], S[j][vt][1], p0);
+              split2<Sh::PS>(S[j][vt][2], S[j][vt][3], p1);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) dg = fmaf(dl[(int64_t)(k + i) * V + v], D[j][vt][i], dg);
+              for (int q = 0; q < Sh::PS; ++q) *(u32x2*)(Ss + q * VB * KP + at) = u32x2{p0[q], p1[q]};
+            }
+            if constexpr (DG) {
+              uint32_t p0[Sh::PT], p1[Sh::PT];
+              split2<Sh::PT>(D[j][vt][0], D[j][vt][1], p0);
+              split2<Sh::PT>(D[j][vt][2], D[j][vt][3], p1);
+#pragma unroll
+              for (int q = 0; q < Sh::PT; ++q) *(u32x2*)(Ts + q * VB * KP + at) = u32x2{p0[q], p1[q]};
             }
           }
       }
-      // the block's sum, in a fixed order
-      __shared__ float sums[256];
-      sums[tid] = dg;
-      __syncthreads();
+    };
+    // the state at the walk's end of the staged chunk
+    auto update = [&](int n, const __bf16* Bs, const __bf16* Cw, const __bf16* Cw2) {
+      const bool cut = starts != 0;
+      const float d = cut ? 0.0f : (n == kQ ? lam64 : power(g2, n));
+      const float nf = (float)n;
 #pragma unroll
-      for (int s = 128; s > 0; s >>= 1) {
-        if (tid < s) sums[tid] += sums[tid + s];
-        __syncthreads();
+      for (int j = 0; j < JK; ++j)
+#pragma unroll
+        for (int vt = 0; vt < NVW; ++vt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (DG) D[j][vt][i] = cut ? 0.0f : d * (D[j][vt][i] + nf * S[j][vt][i]);
+            S[j][vt][i] = cut ? 0.0f : d * S[j][vt][i];
+          }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int ra = 32 * ks + 8 * g4 + kk, rb = ra + 4;
+        bf16x8 bF[JK][NP];
+#pragma unroll
+        for (int j = 0; j < JK; ++j)
+#pragma unroll
+          for (int e = 0; e < NP; ++e) {
+            const int col = kw + 16 * j + 4 * qq;
+            bF[j][e] = join(tr_read(Bs + e * kQ * KP + ra * KP + sw<KP>(ra, col)),
+                            tr_read(Bs + e * kQ * KP + rb * KP + sw<KP>(rb, col)));
+          }
+#pragma unroll
+        for (int vt = 0; vt < NVW; ++vt) {
+          const int col = vw + 16 * vt + 4 * qq;
+          bf16x8 cF[3], cF2[DG ? 3 : 1];
+#pragma unroll
+          for (int e = 0; e < 3; ++e) {
+            const int at = e * kQ * VB;
+            cF[e] = join(tr_read(Cw + at + ra * VB + swc<VB>(ra, col)),
+                         tr_read(Cw + at + rb * VB + swc<VB>(rb, col)));
+            if constexpr (DG)
+              cF2[e] = join(tr_read(Cw2 + at + ra * VB + swc<VB>(ra, col)),
+                            tr_read(Cw2 + at + rb * VB + swc<VB>(rb, col)));
+          }
+#pragma unroll
+          for (int j = 0; j < JK; ++j) {
+            S[j][vt] = mfma_parts(bF[j], cF, S[j][vt]);
+            if constexpr (DG) D[j][vt] = mfma_parts(bF[j], cF2, D[j][vt]);
+          }
+        }
       }
-      if (tid == 0)
-        p.dg_part[(int64_t)h * p.batch * p.nsl * p.nspan + ((int64_t)b * p.nsl + sl) * p.nspan + span] = sums[0];
+#pragma unroll
+      for (int j = 0; j < JK; ++j) {
+        settle(S[j]);
+        if constexpr (DG) settle(D[j]);
+      }
+    };
+
+    if (first < last) load_bc(chunk_of(first));
+    if constexpr (!STATE) {
+      if (p.init) {
+        const float* s0 = p.init + bh * state_elems;
+        for_state([&](int j, int vt, int v, int k) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) S[j][vt][i] = s0[v * p.state_sv + (k + i) * p.state_sk];
+        });
+      }
+      // the states that the spans before this one add, in the walk's order
+      for (int m = 0; m < span; ++m) {
+        const float* loc = p.ws + ((int64_t)m * p.batch * p.H + bh) * (DG ? 2 : 1) * state_elems;
+        // real tokens of the span
+        const int m0 = m * p.span_chunks, m1 = m0 + p.span_chunks - 1;
+        const int64_t ca = chunk_of(REV ? m1 : m0), cb = chunk_of(REV ? m0 : m1) + 1;
+        const int64_t hi = cb * kQ < len ? cb * kQ : len;
+        const int64_t n = hi > ca * kQ ? hi - ca * kQ : 0;
+        const bool cut = p.span_cut[(int64_t)m * p.batch + b] != 0;
+        const float d = n == 0 ? 1.0f : exp2_hw(g2 * (float)n);
+        for_state([&](int j, int vt, int v, int k) {
+          const f32x4 av = *(const f32x4*)(loc + (int64_t)v * K + k);
+          if constexpr (DG) {
+            const f32x4 tv = *(const f32x4*)(loc + state_elems + (int64_t)v * K + k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              D[j][vt][i] = cut ? tv[i] : d * (D[j][vt][i] + (float)n * S[j][vt][i]) + tv[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) S[j][vt][i] = cut ? av[i] : d * S[j][vt][i] + av[i];
+        });
+      }
+    }
+    int any_start = 0;
+    if (first < last) {
+      stage_rows(lds, lds + kCs);
+      if (first + 1 < last) load_bc(chunk_of(first + 1));
+      stage_weighted(live_in(chunk_of(first)), lds + kCw, lds + kCw2);
+      put_state(lds + kSs, lds + kTs);
+    }
+    lds_barrier();
+    for (int i = first; i < last; ++i) {
+      const __bf16* const buf = lds + (NBUF == 2 ? ((i - first) & 1) * Sh::kElems : 0);
+      __bf16* const next = lds + (NBUF == 2 ? ((i + 1 - first) & 1) * Sh::kElems : 0);
+      const bool more = i + 1 < last;
+      auto stage_next = [&]() {
+        stage_rows(next, next + kCs);
+        if (i + 2 < last) load_bc(chunk_of(i + 2));  // a chunk ahead of its use
+      };
+      any_start |= starts != 0;
+      if (NBUF == 2 && more) stage_next();
+      update(live_in(chunk_of(i)), buf, buf + kCw, buf + kCw2);
+      if (NBUF == 1) {
+        lds_barrier();  // the buffer is read
+        if (more) stage_next();
+      }
+      if (more) {
+        put_state(next + kSs, next + kTs);
+        stage_weighted(live_in(chunk_of(i + 1)), next + kCw, next + kCw2);
+      }
+      lds_barrier();
+    }
+
+    if constexpr (STATE) {
+      float* loc = p.ws + ((int64_t)span * p.batch * p.H + bh) * (DG ? 2 : 1) * state_elems;
+      for_state([&](int j, int vt, int v, int k) {
+        *(f32x4*)(loc + (int64_t)v * K + k) = S[j][vt];
+        if constexpr (DG) *(f32x4*)(loc + state_elems + (int64_t)v * K + k) = D[j][vt];
+      });
+      if (h == 0 && sl == 0 && tid == 0) p.span_cut[(int64_t)span * p.batch + b] = any_start;
+    } else {
+      const bool ends = span == p.nspan - 1;  // this block ends the walk
+      if (ends && p.final_state) {
+        float* fs = p.final_state + bh * state_elems;
+        for_state([&](int j, int vt, int v, int k) { *(f32x4*)(fs + (int64_t)v * K + k) = S[j][vt]; });
+      }
+      if constexpr (DG) {
+        if (ends && p.dlast) {  // <dlast, T after the last token>; dlast is K-major here
+          const float* dl = p.dlast + bh * state_elems;
+          for_state([&](int j, int vt, int v, int k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dg = fmaf(dl[(int64_t)(k + i) * V + v], D[j][vt][i], dg);
+          });
+        }
+      }
+    }
+  }
+
+  if constexpr (DG && !STATE) {
+    // the block's sum, in a fixed order
+    __shared__ float sums[8];
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) dg += __shfl_xor(dg, m);
+    if (lane == 0) sums[threadIdx.x >> 6] = dg;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += sums[i];
+      p.dg_part[(int64_t)h * p.batch * p.nsl * p.nspan + ((int64_t)b * p.nsl + sl) * p.nspan + span] = s;
     }
   }
 }
@@ -796,14 +1001,14 @@ hipError_t launch_walk(const WalkArgs& args, bool rev, bool dg, bool state, hipS
     else if (dg) walk_kernel<NP, KP, VB, false, true, true><<<grid, 256, 0, stream>>>(a);
     else walk_kernel<NP, KP, VB, false, false, true><<<grid, 256, 0, stream>>>(a);
   } else {
-    if (rev) walk_kernel<NP, KP, VB, true, false, false><<<grid, 256, 0, stream>>>(a);
+    if (rev) walk_kernel<NP, KP, VB, true, false, false><<<grid, 512, 0, stream>>>(a);
     else if (dg) {
       if constexpr (Shape<NP, KP, VB, true, false>::kFits)
-        walk_kernel<NP, KP, VB, false, true, false><<<grid, 256, 0, stream>>>(a);
+        walk_kernel<NP, KP, VB, false, true, false><<<grid, 512, 0, stream>>>(a);
       else
         return hipErrorInvalidValue;  // walk_tile takes a narrower tile
     }
-    else walk_kernel<NP, KP, VB, false, false, false><<<grid, 256, 0, stream>>>(a);
+    else walk_kernel<NP, KP, VB, false, false, false><<<grid, 512, 0, stream>>>(a);
   }
   return hipGetLastError();
 }
