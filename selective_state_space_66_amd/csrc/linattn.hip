@@ -7,51 +7,69 @@
 namespace ssm66 {
 namespace linattn {
 
-Tile walk_tile(bool f32, int K, int V, bool dg) {
-  Tile t;
-  t.KP = K <= 64 ? 64 : (K <= 128 ? 128 : 256);
-  if (f32) t.VB = t.KP == 256 ? 16 : 32;
-  else t.VB = (t.KP == 256 || V <= 32 || (dg && t.KP == 128)) ? 32 : 64;
-  return t;
-}
-
 namespace {
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// A walk's spans: blocks of one (entry, head, column slice) each, cut along
-// the tokens when there are too few of them to fill the 256 CUs.
-struct Spans { int n, chunks; };
-Spans spans_for(int64_t blocks, int64_t L) {
-  const int64_t nc = (L + kChunk - 1) / kChunk;
-  int64_t n = 1;
-  if (blocks > 0 && blocks < 256) {
-    n = (512 + blocks - 1) / blocks;
-    if (n > nc / 4) n = nc / 4;
-    if (n > 64) n = 64;
-    if (n < 1) n = 1;
-  }
-  Spans s;
-  s.chunks = nc == 0 ? 1 : (int)((nc + n - 1) / n);
-  s.n = nc == 0 ? 1 : (int)((nc + s.chunks - 1) / s.chunks);
-  return s;
-}
+int64_t chunks_of(int64_t L) { return (L + kChunk - 1) / kChunk; }
 
+int padded(int K) { return K <= 64 ? 64 : (K <= 128 ? 128 : 256); }
+
+// How a walk is laid out.
+//
+// Tile.  A block takes 64 columns where its CU is its own (bf16 rows of up to
+// 128; 75.8 us against 78.4 with 32 for 192 (entry, head) pairs of 64 columns,
+// 128 keys, 2048 tokens), but 32, two blocks to a CU, where 64 would leave a
+// second round of blocks partly filled (112 against 121 us for 192 pairs of
+// 128 columns, 64 keys).  fp32 rows and the walk with the log-decay's gradient
+// have three parts of most operands and take 32, fp32 rows of 256 take 16.
+//
+// Spans.  Too few blocks for one round are cut along the tokens as often as
+// fills it; each span then needs the state before it, from a walk that reads b
+// and c once more (1 x 65536 x 16 heads of 128: 8 spans, 360 us and 150 us for
+// the states).  Cutting two thirds of a round costs more than it gives (119 +
+// 33 against 76 us for the 192 pairs above), and so do sequences under 16 chunks.
 struct Walk {
-  Tile tile;
-  Spans spans;
-  int nsl;
+  Tile tile, state_tile;
+  int nsl, nspan, span_chunks, pieces, piece_chunks;
   size_t state_bytes, cut_bytes, part_bytes;
 };
 Walk plan(const Problem& p, int K, int V, bool dg) {
   Walk w;
-  w.tile = walk_tile(p.f32, K, V, dg);
+  const int KP = padded(K);
+  const int64_t pairs = p.batch * p.H;
+  const int64_t n64 = pairs * ((V + 63) / 64);
+  w.tile.KP = w.state_tile.KP = KP;
+  if (p.f32) w.tile.VB = KP == 256 ? 16 : 32;
+  else w.tile.VB = !dg && KP <= 128 && V > 32 && n64 <= 256 ? 64 : 32;
   w.nsl = (V + w.tile.VB - 1) / w.tile.VB;
-  w.spans = spans_for(p.batch * p.H * w.nsl, p.L);
-  const size_t m = (size_t)(w.spans.n - 1);
-  w.state_bytes = up256(m * p.batch * p.H * (dg ? 2 : 1) * (size_t)K * V * 4);
-  w.cut_bytes = up256(m * p.batch * 4);
-  w.part_bytes = dg ? up256((size_t)p.H * p.batch * w.nsl * w.spans.n * 4) : 0;
+  const int64_t blocks = pairs * w.nsl;
+  const int64_t round = !p.f32 && !dg && KP <= 128 && w.tile.VB == 32 ? 512 : 256;
+  const int64_t nc = chunks_of(p.L);
+  int64_t spans = blocks > 0 && nc >= 16 ? round / blocks : 1;
+  if (spans > nc / 4) spans = nc / 4;
+  if (spans < 1) spans = 1;
+  // pieces for the state walk: about 512 blocks of it, four chunks at least,
+  // and no more than 64 states to add up
+  w.state_tile.VB = p.f32 || KP == 256 ? w.tile.VB : (V > 64 && !dg ? 128 : (V > 32 && !(dg && KP == 128) ? 64 : 32));
+  const int64_t state_blocks = pairs * ((V + w.state_tile.VB - 1) / w.state_tile.VB);
+  int64_t per = (nc + spans - 1) / spans;  // chunks of a span
+  int64_t split = 1;                       // pieces of a span
+  if (spans > 1) {
+    split = 512 / (state_blocks * (spans - 1));
+    if (split > per / 4) split = per / 4;
+    if (split > 64 / (spans - 1)) split = 64 / (spans - 1);
+    if (split < 1) split = 1;
+    per = (per + split - 1) / split * split;
+  }
+  if (per < 1) per = 1;
+  w.span_chunks = (int)per;
+  w.piece_chunks = (int)(per / split);
+  w.nspan = nc == 0 ? 1 : (int)((nc + per - 1) / per);
+  w.pieces = (int)((w.nspan - 1) * split);
+  w.state_bytes = up256((size_t)w.pieces * pairs * (dg ? 2 : 1) * (size_t)K * V * 4);
+  w.cut_bytes = up256((size_t)w.pieces * p.batch * 4);
+  w.part_bytes = dg ? up256((size_t)pairs * w.nsl * w.nspan * 4) : 0;
   return w;
 }
 
@@ -77,11 +95,14 @@ BwdLayout bwd_layout(const Problem& p, bool dg) {
 
 hipError_t run_walk(WalkArgs a, const Problem& p, const Walk& w, bool rev, bool dg,
                     hipStream_t stream) {
-  a.nspan = w.spans.n;
-  a.span_chunks = w.spans.chunks;
-  for (int state = w.spans.n > 1 ? 1 : 0; state >= 0; --state) {
-    const hipError_t e = p.f32 ? walk_f32(a, w.tile, rev, dg, state != 0, stream)
-                               : walk_bf16(a, w.tile, rev, dg, state != 0, stream);
+  a.nspan = w.nspan;
+  a.span_chunks = w.span_chunks;
+  a.pieces = w.pieces;
+  a.piece_chunks = w.piece_chunks;
+  for (int state = w.pieces > 0 ? 1 : 0; state >= 0; --state) {
+    const Tile t = state ? w.state_tile : w.tile;
+    const hipError_t e = p.f32 ? walk_f32(a, t, rev, dg, state != 0, stream)
+                               : walk_bf16(a, t, rev, dg, state != 0, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -90,7 +111,7 @@ hipError_t run_walk(WalkArgs a, const Problem& p, const Walk& w, bool rev, bool 
 WalkArgs walk_args(const Problem& p, char* ws, size_t cuts_at) {
   WalkArgs a = {};
   a.ws = (float*)ws;
-  a.span_cut = (int32_t*)(ws + cuts_at);
+  a.piece_cut = (int32_t*)(ws + cuts_at);
   a.log_decay = p.log_decay;
   a.seq_lens = p.seq_lens;
   a.reset = p.reset;
@@ -195,7 +216,7 @@ hipError_t backward(const Problem& p, const BwdArgs& g, void* workspace, hipStre
     if (l.shared && (e = sum_heads(p, shared, g.dq, stream)) != hipSuccess) return e;
     if (dg) {
       sum_parts_kernel<<<dim3((uint32_t)p.H), 64, 0, stream>>>(parts, g.dlog_decay,
-                                                               p.batch * l.q.nsl * l.q.spans.n);
+                                                               p.batch * l.q.nsl * l.q.nspan);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   }

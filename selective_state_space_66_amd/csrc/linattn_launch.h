@@ -20,8 +20,8 @@ struct WalkArgs {
   const float* init;         // nullable: the state before the walk, element (v, k) of a head
                              // at v * state_sv + k * state_sk
   float* final_state;        // nullable: the state after it, (batch, H, V, K)
-  float* ws;                 // span states, (nspan - 1, batch, H, 1 or 2, V, K)
-  int32_t* span_cut;         // (nspan - 1, batch): whether a document starts in the span
+  float* ws;                 // the pieces' states, (pieces, batch, H, 1 or 2, V, K)
+  int32_t* piece_cut;        // (pieces, batch): whether a document starts in the piece
   const float* log_decay;    // (H)
   const int32_t* seq_lens;   // nullable (batch)
   const uint8_t* reset;      // nullable (batch, L)
@@ -30,7 +30,10 @@ struct WalkArgs {
   int64_t batch, L;
   int H, Ha, Hb, Hc, K, V;
   int64_t state_sv, state_sk;
-  int nspan, span_chunks;    // the walk's spans, of span_chunks chunks each
+  // The walk runs in nspan spans of span_chunks chunks at once; each starts
+  // from the states of the pieces before it (piece_chunks chunks each, a
+  // divisor of span_chunks), which a state walk leaves in ws.
+  int nspan, span_chunks, pieces, piece_chunks;
   int out_f32;
   float s_intra, s_state, s_inter;
   // set by the launch
@@ -38,9 +41,8 @@ struct WalkArgs {
   uint32_t nblk;
 };
 
+// the padded row width and the columns per block of a kernel
 struct Tile { int KP, VB; };
-// the padded row width and the columns per block that a walk of these widths runs with
-Tile walk_tile(bool f32, int K, int V, bool dg);
 hipError_t walk_bf16(const WalkArgs& a, Tile t, bool rev, bool dg, bool state, hipStream_t stream);
 hipError_t walk_f32(const WalkArgs& a, Tile t, bool rev, bool dg, bool state, hipStream_t stream);
 

@@ -49,8 +49,9 @@
 // outputs, with the rows of a straight from memory in operand registers.  Group B keeps the state in registers,
 // updates it, and brings b and c in: it stages chunk i + 1 while chunk i is
 // worked on, from loads issued a chunk earlier, into the other of two buffers:
-// one barrier per chunk.  (Where the LDS holds one buffer only, group B waits
-// for both groups to be done with it: two barriers.)
+// one barrier per chunk.  Where the LDS does not hold two of everything, the
+// rows of b and c have two and the weighted c and the state one, written after
+// a second barrier behind their readers; or everything has one.
 // Chunks of 64 tokens: the starts of documents fit one ballot.
 #pragma once
 
@@ -73,6 +74,10 @@ constexpr int kQ = kChunk;  // tokens per chunk: the width of a ballot, which ho
 // past the range in word 2 give 0, so rows past a sequence's end and columns
 // past a head's width arrive as zeros, whatever memory holds there.
 constexpr int kBufferFlags = 0x00020000;
+// Cache policy of the output's stores: non-temporal.  The loads and stores of a
+// walk without its arithmetic took 52 us this way and 72 us with plain stores
+// (8 x 2048 x 24 heads, 128 keys, 64 values); nt loads gained nothing.
+constexpr int kNt = 2;
 constexpr uint32_t kOutside = 0x7ffffff0u;  // an offset past every range
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
@@ -131,12 +136,11 @@ __device__ __forceinline__ constexpr int sw(int r, int col) {
   return (((col >> 3) ^ swz<KP>(r)) << 3) | (col & 7);
 }
 // c's rows of VB bf16 are only read by the transposing reads (32 bytes from
-// each of four rows at a time): pairs of pieces change places by row
+// each of four rows at a time, over 64 banks of 4 bytes): where one row or two
+// fill the banks, the others change places by pairs of pieces
 template <int VB>
 __device__ __forceinline__ constexpr int swc(int r, int col) {
-  constexpr int kShift = VB == 64 ? 0 : 1;
-  constexpr int kMask = VB == 64 ? 3 : (VB == 32 ? 1 : 0);
-  return (((col >> 3) ^ (((r >> kShift) & kMask) << 1)) << 3) | (col & 7);
+  return VB >= 64 ? (((col >> 3) ^ ((VB == 128 ? r & 3 : (r >> 1) & 1) << 1)) << 3) | (col & 7) : col;
 }
 
 // The contractions over kappa take it in steps of 32; lane group lk of step k
@@ -176,23 +180,28 @@ struct Shape {
   static constexpr int kS = PS * VB * KP;
   static constexpr int kT = PT * VB * KP;
   static constexpr int kLds = 160 * 1024;                         // of a CU
-  static constexpr int kElems = kB + kC + kW + kW2 + kS + kT;
-  static constexpr int bytes(int nbuf) { return 2 * nbuf * kElems + (DG ? 1024 : 0); }
-  static constexpr int NBUF = !STATE && bytes(2) <= kLds ? 2 : 1;
-  static constexpr bool kFits = bytes(NBUF) <= kLds;
-  // Waves of a group along the columns v: a half of them each where there are
-  // four tiles.  Group B's then split the rows kappa in two, group A's
-  // take two of the four token blocks each -- 0 and 3, or 1 and 2, which see
-  // the same number of blocks -- and every operand read from LDS serves twice.
-  static constexpr int WV = VB >= 64 ? 2 : 1;
-  static constexpr int WK = 4 / WV;
-  static constexpr int NB = WV;             // token blocks of a group A wave
+  static constexpr int kRows = kB + kC;                           // one buffer of rows
+  static constexpr int kRest = kW + kW2 + kS + kT;                // one of weighted c and state
+  static constexpr int bytes(int rows, int rest) { return 2 * (rows * kRows + rest * kRest) + (DG ? 1024 : 0); }
+  // buffers of each, as the LDS allows
+  static constexpr int NREST = !STATE && bytes(2, 2) <= kLds ? 2 : 1;
+  static constexpr int NROWS = !STATE && bytes(2, NREST) <= kLds ? 2 : 1;
+  static constexpr int kBytes = bytes(NROWS, NREST);
+  static constexpr bool kFits = kBytes <= kLds;
+  // Waves of a group: eight for 64 columns, where a block has its CU to itself
+  // and only more waves of its own hide its latencies.  WV of them lie along
+  // the columns v; group B's others along the rows kappa, group A's along the
+  // four token blocks.
+  static constexpr int NW = VB >= 64 && !STATE && !DG ? 8 : 4;
+  static constexpr int WV = NW / 4;         // group A has a wave for every token block
+  static constexpr int WK = NW / WV;
   static constexpr int NVW = VB / 16 / WV;  // column tiles of a wave
   static constexpr int JK = KP / 16 / WK;   // row tiles of the state of a group B wave
-  static constexpr int kThreads = STATE ? 256 : 512;
+  static constexpr int kGroup = 64 * NW;
+  static constexpr int kThreads = STATE ? kGroup : 2 * kGroup;
   // waves per SIMD that the registers are shared out for: what the LDS lets in
-  static constexpr int kWaves = STATE ? (2 * bytes(1) <= kLds ? 2 : 1)
-                                      : (2 * bytes(NBUF) <= kLds ? 4 : 2);
+  static constexpr int kWaves = STATE ? (4 * kBytes <= kLds ? 4 : (2 * kBytes <= kLds ? 2 : 1))
+                                      : (NW == 8 || 2 * kBytes <= kLds ? 4 : 2);
 };
 
 __device__ __forceinline__ uint64_t low_bits(int n) {
@@ -213,16 +222,19 @@ void walk_kernel(const WalkArgs p) {
   constexpr int EPP = 16 / ES;                 // elements of a 16-byte piece
   constexpr int PRB = KP / EPP;                // pieces in a row of b
   constexpr int PRC = VB / EPP;                // pieces in a row of c
-  constexpr int RB = kQ * PRB / 256;           // pieces of b per thread of group B
-  constexpr int RC = kQ * PRC / 256;
+  constexpr int RB = kQ * PRB / Sh::kGroup;    // pieces of b per thread of group B
+  constexpr int RC = kQ * PRC / Sh::kGroup;
   constexpr int NK = KP / 32;                  // k-steps of a . b
   constexpr int NVW = Sh::NVW;                 // column tiles of a wave
-  constexpr int NBUF = Sh::NBUF;
-  static_assert(RB >= 1 && RC >= 1 && NVW >= 1, "tile too small");
+  constexpr int NROWS = Sh::NROWS, NREST = Sh::NREST;
+  static_assert(RB >= 1 && RC >= 1 && NVW >= 1 && Sh::JK >= 1, "tile too small");
+  static_assert(NP == 3 || NVW % 2 == 0, "bf16 outputs leave two tiles at a time");
 
-  // a buffer: b, c, c weighted (for S, for T), parts of S and of T
-  __shared__ __align__(16) __bf16 lds[NBUF * Sh::kElems];
-  constexpr int kCs = Sh::kB, kCw = kCs + Sh::kC, kCw2 = kCw + Sh::kW, kSs = kCw2 + Sh::kW2, kTs = kSs + Sh::kS;
+  __shared__ __align__(16) __bf16 lds[NROWS * Sh::kRows + NREST * Sh::kRest];
+  // chunk i's rows (b, c) and the rest (c weighted for S, for T; parts of S, of T)
+  constexpr int kCs = Sh::kB, kCw2 = Sh::kW, kSs = kCw2 + Sh::kW2, kTs = kSs + Sh::kS;
+  auto rows_at = [&](int i) { return lds + (NROWS == 2 ? (i & 1) * Sh::kRows : 0); };
+  auto rest_at = [&](int i) { return lds + NROWS * Sh::kRows + (NREST == 2 ? (i & 1) * Sh::kRest : 0); };
 
   // Consecutive block ids go round-robin to the 8 XCDs; each XCD gets a
   // contiguous run of (entry, head, span, slice), so the slices that read the
@@ -238,8 +250,9 @@ void walk_kernel(const WalkArgs p) {
   const int h = (int)(rest % (uint32_t)p.H);
   const int b = (int)(rest / (uint32_t)p.H);
 
-  const int tid = threadIdx.x & 255, lane = tid & 63;  // within the group
-  const bool group_a = !STATE && __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 8) == 0;
+  constexpr int GT = Sh::kGroup;
+  const int tid = threadIdx.x % GT, lane = tid & 63;  // within the group
+  const bool group_a = !STATE && __builtin_amdgcn_readfirstlane((int)threadIdx.x / GT) == 0;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lk = lane >> 4;
   const int g4 = lane >> 4, kk = (lane & 15) >> 2, qq = lane & 3;  // of the transposing reads
@@ -294,78 +307,66 @@ void walk_kernel(const WalkArgs p) {
     // ================================================== group A: the outputs
     constexpr int PP = NP == 3 ? 3 : 2;  // parts of the scores that lead to out
     constexpr int RA = NP == 1 ? NK : 2 * NK;
-    constexpr int NB = Sh::NB;
-    const int wv = w % Sh::WV;                       // which columns
-    const int wt = w / Sh::WV;                       // which token blocks
-    const int vw = 16 * NVW * wv;                    // first column of the wave in the slice
-    // the wave's blocks, first to last: {0, 3} or {1, 2}; one of the four
-    const int blk[2] = {NB == 2 ? wt : w, 3 - wt};
+    const int vw = 16 * NVW * (w % Sh::WV);                             // first column of the wave in the slice
+    const int blk = __builtin_amdgcn_readfirstlane(w / Sh::WV);         // its token block
+    const int t = 16 * blk + lr;                                        // this lane's token in a chunk
     const uint32_t rsa = (uint32_t)p.Ha * K * ES;
     const char* const pa = (const char*)p.a + (bL * p.Ha + h / (p.H / p.Ha)) * (int64_t)K * ES;
     const char* const px = DG ? (const char*)p.x + ((bL * p.Hc + h / (p.H / p.Hc)) * (int64_t)V + v0) * ES : nullptr;
 
-    u32x4 rA[NB][RA];
+    u32x4 rA[RA];
     uint32_t rR = 0;
-    // Two loads cover 128 bytes of the block's 16 rows, 8 whole row pieces each
-    // (reading 64 bytes of 16 rows at a time ran at 2.1 TB/s, this way at the
-    // rate of a copy): load u, lane (lk, lr) takes row 8 u + lr % 8, 16 bytes
-    // at 16 (2 lk + lr / 8).  take_a trades halves between the two.
+    // Two loads cover 128 bytes of the block's 16 rows, 8 whole row pieces each:
+    // load u, lane (lk, lr) takes row 8 u + lr % 8, 16 bytes at 16 (2 lk +
+    // lr / 8).  take_a trades halves between the two.
     constexpr int kPairElems = 128 / ES;
     auto load_a = [&](int c) {
       const __amdgpu_buffer_rsrc_t r = rows_of(pa, (int64_t)c * kQ, rsa, live_in(c), K);
       const int piece = 2 * lk + (lr >> 3);
 #pragma unroll
-      for (int q = 0; q < NB; ++q)
-#pragma unroll
-        for (int j = 0; j < RA; ++j) {
-          const uint32_t row = (uint32_t)(16 * blk[q] + 8 * (j % 2) + (lr & 7));
-          const int col = kPairElems * (j / 2) + EPP * piece;
-          rA[q][j] = load16(r, col < K ? row * rsa + (uint32_t)(col * ES) : kOutside);
-        }
+      for (int j = 0; j < RA; ++j) {
+        const uint32_t row = (uint32_t)(16 * blk + 8 * (j % 2) + (lr & 7));
+        const int col = kPairElems * (j / 2) + EPP * piece;
+        rA[j] = load16(r, col < K ? row * rsa + (uint32_t)(col * ES) : kOutside);
+      }
       rR = load_starts(c);
     };
-    bf16x8 aF[NB][NK][NP];
+    bf16x8 aF[NK][NP];
     uint64_t starts = 0;
-    int edge[NB];  // where token t's document begins; backwards, where the next one does
+    int edge = 0;  // where token t's document begins; backwards, where the next one does
     auto take_a = [&]() {
       starts = __ballot((rR & 0xffu) != 0);
       if (starts) {
-#pragma unroll
-        for (int q = 0; q < NB; ++q) {
-          const int t = 16 * blk[q] + lr;
-          const uint64_t m = REV ? (starts >> t) >> 1 : starts & low_bits(t + 1);
-          edge[q] = REV ? (m ? t + 1 + __builtin_ctzll(m) : kQ) : (m ? 63 - __builtin_clzll(m) : -1);
-        }
+        const uint64_t m = REV ? (starts >> t) >> 1 : starts & low_bits(t + 1);
+        edge = REV ? (m ? t + 1 + __builtin_ctzll(m) : kQ) : (m ? 63 - __builtin_clzll(m) : -1);
       }
 #pragma unroll
-      for (int q = 0; q < NB; ++q)
+      for (int j = 0; j < RA / 2; ++j) {
+        // pieces 2 lk and 2 lk + 1 of row lr: within each 16 lanes, the upper
+        // half of one comes from the other load 8 lanes down, the lower half
+        // of the other 8 lanes up
+        u32x4 lo, hi;
 #pragma unroll
-        for (int j = 0; j < RA / 2; ++j) {
-          // pieces 2 lk and 2 lk + 1 of row lr: within each 16 lanes, the upper
-          // half of one comes from the other load 8 lanes down, the lower half
-          // of the other 8 lanes up
-          u32x4 lo, hi;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r0 = (int)rA[q][2 * j][i], r1 = (int)rA[q][2 * j + 1][i];
-            lo[i] = (uint32_t)__builtin_amdgcn_update_dpp(r0, r1, 0x118, 0xf, 0xc, false);  // row_shr:8
-            hi[i] = (uint32_t)__builtin_amdgcn_update_dpp(r1, r0, 0x108, 0xf, 0x3, false);  // row_shl:8
-          }
-          if constexpr (NP == 1) {
-            aF[q][2 * j][0] = __builtin_bit_cast(bf16x8, lo);
-            aF[q][2 * j + 1][0] = __builtin_bit_cast(bf16x8, hi);
-          } else {
-            uint32_t pt[4][3];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              split2<3>(__uint_as_float(lo[2 * i]), __uint_as_float(lo[2 * i + 1]), pt[i]);
-              split2<3>(__uint_as_float(hi[2 * i]), __uint_as_float(hi[2 * i + 1]), pt[2 + i]);
-            }
-#pragma unroll
-            for (int e = 0; e < 3; ++e)
-              aF[q][j][e] = __builtin_bit_cast(bf16x8, u32x4{pt[0][e], pt[1][e], pt[2][e], pt[3][e]});
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int r0 = (int)rA[2 * j][i], r1 = (int)rA[2 * j + 1][i];
+          lo[i] = (uint32_t)__builtin_amdgcn_update_dpp(r0, r1, 0x118, 0xf, 0xc, false);  // row_shr:8
+          hi[i] = (uint32_t)__builtin_amdgcn_update_dpp(r1, r0, 0x108, 0xf, 0x3, false);  // row_shl:8
         }
+        if constexpr (NP == 1) {
+          aF[2 * j][0] = __builtin_bit_cast(bf16x8, lo);
+          aF[2 * j + 1][0] = __builtin_bit_cast(bf16x8, hi);
+        } else {
+          uint32_t pt[4][3];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            split2<3>(__uint_as_float(lo[2 * i]), __uint_as_float(lo[2 * i + 1]), pt[i]);
+            split2<3>(__uint_as_float(hi[2 * i]), __uint_as_float(hi[2 * i + 1]), pt[2 + i]);
+          }
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            aF[j][e] = __builtin_bit_cast(bf16x8, u32x4{pt[0][e], pt[1][e], pt[2][e], pt[3][e]});
+        }
+      }
     };
 
     // lane constants of the intra-chunk weights, of token t = 16 W + lr and
@@ -379,24 +380,19 @@ void walk_kernel(const WalkArgs p) {
       w1[i] = p.s_intra * power(g2, 16 + e);  // e > -16
     }
     const float lam16 = power(g2, 16), lam32 = power(g2, 32);
-    // the weight of the state at this lane's tokens of a full chunk
-    float wi_full[NB];
-#pragma unroll
-    for (int q = 0; q < NB; ++q)
-      wi_full[q] = p.s_inter * power(g2, REV ? kQ - 1 - 16 * blk[q] - lr : 16 * blk[q] + lr + 1);
+    // the weight of the state at this lane's token of a full chunk
+    const float wi_full = p.s_inter * power(g2, REV ? kQ - 1 - t : t + 1);
 
-    f32x4 acc[NB][NVW], acc2[DG ? NB : 1][DG ? NVW : 1];
-    u32x4 rX[DG ? NB : 1][DG ? NVW : 1];
+    f32x4 acc[NVW], acc2[DG ? NVW : 1];
+    u32x4 rX[DG ? NVW : 1];
 
     // acc = W a_t (rows v, columns t), weighted
     auto state_part = [&](int n, const __bf16* Ss, const __bf16* Ts) {
 #pragma unroll
-      for (int q = 0; q < NB; ++q)
-#pragma unroll
-        for (int vt = 0; vt < NVW; ++vt) {
-          acc[q][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-          if constexpr (DG) acc2[q][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        }
+      for (int vt = 0; vt < NVW; ++vt) {
+        acc[vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (DG) acc2[vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
         bf16x8 sF[NVW][Sh::PS > 0 ? Sh::PS : 1], tF[DG ? NVW : 1][Sh::PT > 0 ? Sh::PT : 1];
@@ -411,66 +407,55 @@ void walk_kernel(const WalkArgs p) {
           }
         }
 #pragma unroll
-        for (int vt = 0; vt < NVW; ++vt)
-#pragma unroll
-          for (int q = 0; q < NB; ++q) {
-            acc[q][vt] = mfma_parts(sF[vt], aF[q][k], acc[q][vt]);
-            if constexpr (DG) acc2[q][vt] = mfma_parts(tF[vt], aF[q][k], acc2[q][vt]);
-          }
-      }
-#pragma unroll
-      for (int q = 0; q < NB; ++q) {
-        settle(acc[q]);
-        if constexpr (DG) settle(acc2[q]);
-      }
-#pragma unroll
-      for (int q = 0; q < NB; ++q) {
-        const int t = 16 * blk[q] + lr;
-        const int je = REV ? n - 1 - t : t + 1;
-        float wi = REV && n < kQ ? p.s_inter * power(g2, je > 0 ? je : 0) : wi_full[q];
-        bool from = true;
-        if (n < kQ || starts) {
-          from = t < n && (!starts || edge[q] == (REV ? kQ : -1));
+        for (int vt = 0; vt < NVW; ++vt) {
+          acc[vt] = mfma_parts(sF[vt], aF[k], acc[vt]);
+          if constexpr (DG) acc2[vt] = mfma_parts(tF[vt], aF[k], acc2[vt]);
         }
+      }
+      settle(acc);
+      if constexpr (DG) settle(acc2);
+      const int je = REV ? n - 1 - t : t + 1;
+      const float wi = REV && n < kQ ? p.s_inter * power(g2, je > 0 ? je : 0) : wi_full;
+#pragma unroll
+      for (int vt = 0; vt < NVW; ++vt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (DG) acc2[vt][i] = wi * (acc2[vt][i] + (float)je * acc[vt][i]);
+          acc[vt][i] *= wi;
+        }
+      if (n < kQ || starts) {
+        const bool from = t < n && (!starts || edge == (REV ? kQ : -1));
 #pragma unroll
         for (int vt = 0; vt < NVW; ++vt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if constexpr (DG) acc2[q][vt][i] = from ? wi * (acc2[q][vt][i] + (float)je * acc[q][vt][i]) : 0.0f;
-            acc[q][vt][i] = from ? wi * acc[q][vt][i] : 0.0f;
+            if constexpr (DG) acc2[vt][i] = from ? acc2[vt][i] : 0.0f;
+            acc[vt][i] = from ? acc[vt][i] : 0.0f;
           }
       }
     };
 
-    // The chunk's own part, two 16-token blocks of s at a time: scores
-    // transposed (s by t), weighted, and as they stand the operand of the
-    // product with c.  W0, W1: the wave's token blocks (uniform in a wave).
-    auto chunk_part = [&](auto W0c, auto W1c, const __bf16* Bs, const __bf16* Cs) {
-      constexpr int Ws[2] = {decltype(W0c)::value, decltype(W1c)::value};
-      constexpr int Wmin = Ws[0], Wmax = NB == 2 ? Ws[1] : Ws[0];
-      f32x4 g[2][NB][2];
+    // The chunk's own part for token block W (uniform in a wave): scores
+    // transposed (s by t), weighted, and as they stand, two 16-token blocks of
+    // s at a time, the operand of the product with c.
+    auto chunk_part = [&](auto Wc, const __bf16* Bs, const __bf16* Cs) {
+      constexpr int W = decltype(Wc)::value;
+      f32x4 g[4];
 #pragma unroll
-      for (int pair = 0; pair < 2; ++pair)
-#pragma unroll
-        for (int q = 0; q < NB; ++q) g[pair][q][0] = g[pair][q][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int sb = 0; sb < 4; ++sb) g[sb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < NK; ++k)
 #pragma unroll
-        for (int sb = REV ? Wmin : 0; sb <= (REV ? 3 : Wmax); ++sb) {
+        for (int sb = REV ? W : 0; sb <= (REV ? 3 : W); ++sb) {
           bf16x8 bF[NP];
 #pragma unroll
           for (int e = 0; e < NP; ++e)
             bF[e] = *(const bf16x8*)(Bs + e * kQ * KP + (16 * sb + lr) * KP + sw<KP>(lr, kcol<NP>(k, lk)));
-#pragma unroll
-          for (int q = 0; q < NB; ++q)
-            if (REV ? sb >= Ws[q] : sb <= Ws[q]) g[sb / 2][q][sb % 2] = mfma_parts(bF, aF[q][k], g[sb / 2][q][sb % 2]);
+          g[sb] = mfma_parts(bF, aF[k], g[sb]);
         }
+      settle(g);
 #pragma unroll
-      for (int pair = REV ? Wmin / 2 : 0; pair <= (REV ? 1 : Wmax / 2); ++pair)
-#pragma unroll
-        for (int q = 0; q < NB; ++q) settle(g[pair][q]);
-#pragma unroll
-      for (int pair = REV ? Wmin / 2 : 0; pair <= (REV ? 1 : Wmax / 2); ++pair) {
+      for (int pair = REV ? W / 2 : 0; pair <= (REV ? 1 : W / 2); ++pair) {
         const int ra = 32 * pair + 4 * g4 + kk, rb = ra + 16;
         bf16x8 cF[NVW][NP];
 #pragma unroll
@@ -479,71 +464,64 @@ void walk_kernel(const WalkArgs p) {
           for (int e = 0; e < NP; ++e)
             cF[vt][e] = join(tr_read(Cs + e * kQ * VB + ra * VB + swc<VB>(ra, vw + 16 * vt + 4 * qq)),
                              tr_read(Cs + e * kQ * VB + rb * VB + swc<VB>(rb, vw + 16 * vt + 4 * qq)));
+        uint32_t pw[2][2][PP], pw2[2][2][DG ? 3 : 1];  // [block][half][part]
 #pragma unroll
-        for (int q = 0; q < NB; ++q) {
-          if (REV ? 2 * pair + 1 < Ws[q] : 2 * pair > Ws[q]) continue;  // it sees neither block
-          uint32_t pw[2][2][PP], pw2[2][2][DG ? 3 : 1];  // [block][half][part]
+        for (int u = 0; u < 2; ++u) {
+          const int sb = 2 * pair + u;
+          const int m = REV ? sb - W : W - sb;  // blocks from s to t
+          if (m < 0) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int sb = 2 * pair + u;
-            const int m = REV ? sb - Ws[q] : Ws[q] - sb;  // blocks from s to t
-            if (m < 0) {
+            for (int e = 0; e < PP; ++e) pw[u][0][e] = pw[u][1][e] = 0;
+            if constexpr (DG) {
 #pragma unroll
-              for (int e = 0; e < PP; ++e) pw[u][0][e] = pw[u][1][e] = 0;
-              if constexpr (DG) {
-#pragma unroll
-                for (int e = 0; e < 3; ++e) pw2[u][0][e] = pw2[u][1][e] = 0;
-              }
-              continue;
+              for (int e = 0; e < 3; ++e) pw2[u][0][e] = pw2[u][1][e] = 0;
             }
-            float x[4], x2[4];
+            continue;
+          }
+          float x[4], x2[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float y = g[sb][i] * (m == 0 ? wd[i] : w1[i]);
+            if (m == 2) y *= lam16;
+            if (m == 3) y *= lam32;
+            // a token that t does not see leaves nothing, whatever it holds
+            if (m == 0) y = (REV ? 4 * lk + i >= lr : 4 * lk + i <= lr) ? y : 0.0f;
+            x[i] = y;
+          }
+          if (starts) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float y = g[pair][q][u][i] * (m == 0 ? wd[i] : w1[i]);
-              if (m == 2) y *= lam16;
-              if (m == 3) y *= lam32;
-              // a token that t does not see leaves nothing, whatever it holds
-              if (m == 0) y = (REV ? 4 * lk + i >= lr : 4 * lk + i <= lr) ? y : 0.0f;
-              x[i] = y;
-            }
-            if (starts) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int s = 16 * sb + 4 * lk + i;
-                x[i] = (REV ? s < edge[q] : s >= edge[q]) ? x[i] : 0.0f;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              x2[i] = DG ? x[i] * (float)(16 * m + (REV ? 4 * lk + i - lr : lr - 4 * lk - i)) : 0.0f;
-            split2<PP>(x[0], x[1], pw[u][0]);
-            split2<PP>(x[2], x[3], pw[u][1]);
-            if constexpr (DG) {
-              split2<3>(x2[0], x2[1], pw2[u][0]);
-              split2<3>(x2[2], x2[3], pw2[u][1]);
+              const int s = 16 * sb + 4 * lk + i;
+              x[i] = (REV ? s < edge : s >= edge) ? x[i] : 0.0f;
             }
           }
-          bf16x8 pF[PP], pF2[DG ? 3 : 1];
 #pragma unroll
-          for (int e = 0; e < PP; ++e)
-            pF[e] = __builtin_bit_cast(bf16x8, u32x4{pw[0][0][e], pw[0][1][e], pw[1][0][e], pw[1][1][e]});
+          for (int i = 0; i < 4; ++i)
+            x2[i] = DG ? x[i] * (float)(16 * m + (REV ? 4 * lk + i - lr : lr - 4 * lk - i)) : 0.0f;
+          split2<PP>(x[0], x[1], pw[u][0]);
+          split2<PP>(x[2], x[3], pw[u][1]);
           if constexpr (DG) {
-#pragma unroll
-            for (int e = 0; e < 3; ++e)
-              pF2[e] = __builtin_bit_cast(bf16x8, u32x4{pw2[0][0][e], pw2[0][1][e], pw2[1][0][e], pw2[1][1][e]});
-          }
-#pragma unroll
-          for (int vt = 0; vt < NVW; ++vt) {
-            acc[q][vt] = mfma_parts(cF[vt], pF, acc[q][vt]);
-            if constexpr (DG) acc2[q][vt] = mfma_parts(cF[vt], pF2, acc2[q][vt]);
+            split2<3>(x2[0], x2[1], pw2[u][0]);
+            split2<3>(x2[2], x2[3], pw2[u][1]);
           }
         }
-      }
+        bf16x8 pF[PP], pF2[DG ? 3 : 1];
 #pragma unroll
-      for (int q = 0; q < NB; ++q) {
-        settle(acc[q]);
-        if constexpr (DG) settle(acc2[q]);
+        for (int e = 0; e < PP; ++e)
+          pF[e] = __builtin_bit_cast(bf16x8, u32x4{pw[0][0][e], pw[0][1][e], pw[1][0][e], pw[1][1][e]});
+        if constexpr (DG) {
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            pF2[e] = __builtin_bit_cast(bf16x8, u32x4{pw2[0][0][e], pw2[0][1][e], pw2[1][0][e], pw2[1][1][e]});
+        }
+#pragma unroll
+        for (int vt = 0; vt < NVW; ++vt) {
+          acc[vt] = mfma_parts(cF[vt], pF, acc[vt]);
+          if constexpr (DG) acc2[vt] = mfma_parts(cF[vt], pF2, acc2[vt]);
+        }
       }
+      settle(acc);
+      if constexpr (DG) settle(acc2);
     };
 
     if (first < last) {
@@ -554,50 +532,39 @@ void walk_kernel(const WalkArgs p) {
     lds_barrier();
     for (int i = first; i < last; ++i) {
       const int c = chunk_of(i), n = live_in(c);
-      const __bf16* const buf = lds + (NBUF == 2 ? ((i - first) & 1) * Sh::kElems : 0);
+      const __bf16* const rows = rows_at(i);
+      const __bf16* const rest = rest_at(i);
       if constexpr (DG) {  // x of this lane's outputs
         const __amdgpu_buffer_rsrc_t r = rows_of(px, (int64_t)c * kQ, rsc, n, V - v0);
 #pragma unroll
-        for (int q = 0; q < NB; ++q)
-#pragma unroll
-          for (int vt = 0; vt < NVW; ++vt) {
-            const int col = vw + 16 * vt + 4 * lk, t = 16 * blk[q] + lr;
-            const uint32_t o = v0 + col < V ? (uint32_t)t * rsc + (uint32_t)col * ES : kOutside;
-            if constexpr (NP == 1) {
-              const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)o, 0, 0));
-              rX[q][vt] = u32x4{x[0], x[1], 0u, 0u};
-            } else {
-              rX[q][vt] = load16(r, o);
-            }
+        for (int vt = 0; vt < NVW; ++vt) {
+          const int col = vw + 16 * vt + 4 * lk;
+          const uint32_t o = v0 + col < V ? (uint32_t)t * rsc + (uint32_t)col * ES : kOutside;
+          if constexpr (NP == 1) {
+            const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)o, 0, 0));
+            rX[vt] = u32x4{x[0], x[1], 0u, 0u};
+          } else {
+            rX[vt] = load16(r, o);
           }
+        }
       }
-      state_part(n, buf + kSs, buf + kTs);
-      constexpr std::integral_constant<int, 0> k0{};
-      constexpr std::integral_constant<int, 1> k1{};
-      constexpr std::integral_constant<int, 2> k2{};
-      constexpr std::integral_constant<int, 3> k3{};
-      if constexpr (NB == 2) {
-        if (wt == 0) chunk_part(k0, k3, buf, buf + kCs);
-        else chunk_part(k1, k2, buf, buf + kCs);
-      } else {
-        if (w == 0) chunk_part(k0, k0, buf, buf + kCs);
-        else if (w == 1) chunk_part(k1, k1, buf, buf + kCs);
-        else if (w == 2) chunk_part(k2, k2, buf, buf + kCs);
-        else chunk_part(k3, k3, buf, buf + kCs);
-      }
+      state_part(n, rest + kSs, rest + kTs);
+      if (NREST == 1 && NROWS == 2) lds_barrier();  // group B may write the rest
+      if (blk == 0) chunk_part(std::integral_constant<int, 0>{}, rows, rows + kCs);
+      else if (blk == 1) chunk_part(std::integral_constant<int, 1>{}, rows, rows + kCs);
+      else if (blk == 2) chunk_part(std::integral_constant<int, 2>{}, rows, rows + kCs);
+      else chunk_part(std::integral_constant<int, 3>{}, rows, rows + kCs);
       if constexpr (DG) {
 #pragma unroll
-        for (int q = 0; q < NB; ++q)
+        for (int vt = 0; vt < NVW; ++vt)
 #pragma unroll
-          for (int vt = 0; vt < NVW; ++vt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = NP == 1 ? ((e & 1) ? hi_bf(rX[q][vt][e / 2]) : lo_bf(rX[q][vt][e / 2]))
-                                      : __uint_as_float(rX[q][vt][e]);
-              dg = 16 * blk[q] + lr < n ? fmaf(acc2[q][vt][e], x, dg) : dg;
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float x = NP == 1 ? ((e & 1) ? hi_bf(rX[vt][e / 2]) : lo_bf(rX[vt][e / 2]))
+                                    : __uint_as_float(rX[vt][e]);
+            dg = t < n ? fmaf(acc2[vt][e], x, dg) : dg;
+          }
       }
-      if (NBUF == 1) lds_barrier();  // group B may write
+      if (NROWS == 1) lds_barrier();  // group B may write both
       // the next chunk's a, from loads a chunk old, and the loads after it
       // (before the stores, so that no wait for loads is one for stores)
       if (i + 1 < last) {
@@ -609,50 +576,34 @@ void walk_kernel(const WalkArgs p) {
         const bool wide = NP == 3 || p.out_f32;
         const uint32_t oes = wide ? 4u : 2u;
         const uint32_t rso = (uint32_t)p.H * V * oes;
-        const int64_t rows = L - (int64_t)c * kQ < kQ ? L - (int64_t)c * kQ : kQ;
+        const int64_t left = L - (int64_t)c * kQ < kQ ? L - (int64_t)c * kQ : kQ;
         const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
             (void*)((char*)p.out + (((bL + (int64_t)c * kQ) * p.H + h) * V + v0) * (int64_t)oes), (short)0,
-            (int)((uint32_t)(rows - 1) * rso + (uint32_t)(V - v0) * oes), kBufferFlags);
-        if (n < kQ) {
+            (int)((uint32_t)(left - 1) * rso + (uint32_t)(V - v0) * oes), kBufferFlags);
+        if (t >= n) {
 #pragma unroll
-          for (int q = 0; q < NB; ++q)
-#pragma unroll
-            for (int vt = 0; vt < NVW; ++vt)
-              if (16 * blk[q] + lr >= n) acc[q][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int vt = 0; vt < NVW; ++vt) acc[vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
         if (wide) {
 #pragma unroll
-          for (int q = 0; q < NB; ++q)
-#pragma unroll
-            for (int vt = 0; vt < NVW; ++vt) {
-              const int t = 16 * blk[q] + lr, v = vw + 16 * vt + 4 * lk;
-              const int at = v0 + v < V ? (int)((uint32_t)t * rso + (uint32_t)v * 4u) : (int)kOutside;
-              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[q][vt]), r, at, 0, 0);
-            }
-        } else if constexpr (NVW == 2) {
+          for (int vt = 0; vt < NVW; ++vt) {
+            const int v = vw + 16 * vt + 4 * lk;
+            const int at = v0 + v < V ? (int)((uint32_t)t * rso + (uint32_t)v * 4u) : (int)kOutside;
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[vt]), r, at, 0, kNt);
+          }
+        } else if constexpr (NP == 1) {
           // lanes hold 4 columns of each of two tiles; the swaps (odd rows of
           // 16 lanes of one operand with the even rows of the other) leave 8
           // columns of one, so that a store writes 64 bytes of each row
-          const int v = vw + 16 * (lk & 1) + 8 * (lk >> 1);
 #pragma unroll
-          for (int q = 0; q < NB; ++q) {
-            const int t = 16 * blk[q] + lr;
+          for (int vt = 0; vt < NVW; vt += 2) {
+            const int v = vw + 16 * (vt + (lk & 1)) + 8 * (lk >> 1);
             const int at = v0 + v < V ? (int)((uint32_t)t * rso + (uint32_t)v * 2u) : (int)kOutside;
-            const f32x4 o0 = acc[q][0], o1 = acc[q][1];
+            const f32x4 o0 = acc[vt], o1 = acc[vt + 1];
             const auto s0 = __builtin_amdgcn_permlane16_swap(pack_bf16x2(o0[0], o0[1]), pack_bf16x2(o1[0], o1[1]), false, false);
             const auto s1 = __builtin_amdgcn_permlane16_swap(pack_bf16x2(o0[2], o0[3]), pack_bf16x2(o1[2], o1[3]), false, false);
-            __builtin_amdgcn_raw_buffer_store_b128(u32x4{s0[0], s1[0], s0[1], s1[1]}, r, at, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{s0[0], s1[0], s0[1], s1[1]}, r, at, 0, kNt);
           }
-        } else {
-#pragma unroll
-          for (int q = 0; q < NB; ++q)
-#pragma unroll
-            for (int vt = 0; vt < NVW; ++vt) {
-              const int t = 16 * blk[q] + lr, v = vw + 16 * vt + 4 * lk;
-              const int at = v0 + v < V ? (int)((uint32_t)t * rso + (uint32_t)v * 2u) : (int)kOutside;
-              const f32x4 o = acc[q][vt];
-              __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])}, r, at, 0, 0);
-            }
         }
       }
       lds_barrier();
@@ -662,7 +613,7 @@ void walk_kernel(const WalkArgs p) {
     const int64_t z0 = ((int64_t)(ca > nlive ? ca : nlive)) * kQ;
     const int64_t z1 = (int64_t)cb * kQ < L ? (int64_t)cb * kQ : L;
     const int cols = V - v0 < VB ? V - v0 : VB;
-    for (int64_t q = tid; q < (z1 - z0) * (VB / 4); q += 256) {
+    for (int64_t q = tid; q < (z1 - z0) * (VB / 4); q += GT) {
       const int64_t row = bL + z0 + q / (VB / 4);
       const int v = 4 * (int)(q % (VB / 4));
       if (v < cols) {
@@ -691,10 +642,10 @@ void walk_kernel(const WalkArgs p) {
       const bool inb = pieceB * EPP < K, inc = v0 + pieceC * EPP < V;
 #pragma unroll
       for (int j = 0; j < RB; ++j)
-        rB[j] = load16(qb, inb ? (uint32_t)(rowB + j * (256 / PRB)) * rsb + pieceB * 16u : kOutside);
+        rB[j] = load16(qb, inb ? (uint32_t)(rowB + j * (GT / PRB)) * rsb + pieceB * 16u : kOutside);
 #pragma unroll
       for (int j = 0; j < RC; ++j)
-        rC[j] = load16(qc, inc ? (uint32_t)(rowC + j * (256 / PRC)) * rsc + pieceC * 16u : kOutside);
+        rC[j] = load16(qc, inc ? (uint32_t)(rowC + j * (GT / PRC)) * rsc + pieceC * 16u : kOutside);
       rR = load_starts(c);
     };
 
@@ -703,7 +654,7 @@ void walk_kernel(const WalkArgs p) {
     float w_full[RC];
 #pragma unroll
     for (int j = 0; j < RC; ++j) {
-      const int row = rowC + j * (256 / PRC);
+      const int row = rowC + j * (GT / PRC);
       w_full[j] = p.s_state * power(g2, REV ? row + 1 : kQ - 1 - row);
     }
     u32x4 cC[RC];          // c of the chunk being staged
@@ -716,7 +667,7 @@ void walk_kernel(const WalkArgs p) {
       starts = __ballot((cR & 0xffu) != 0);
 #pragma unroll
       for (int j = 0; j < RC; ++j) {
-        const int row = rowC + j * (256 / PRC), col = pieceC * EPP;
+        const int row = rowC + j * (GT / PRC), col = pieceC * EPP;
         const int at = row * VB + swc<VB>(row, col);
         const int e = REV ? row + 1 : n - 1 - row;
         float wt = w_full[j];
@@ -756,7 +707,7 @@ void walk_kernel(const WalkArgs p) {
       cR = rR;
 #pragma unroll
       for (int j = 0; j < RB; ++j) {
-        const int row = rowB + j * (256 / PRB), col = pieceB * EPP;
+        const int row = rowB + j * (GT / PRB), col = pieceB * EPP;
         __bf16* const d = Bs + row * KP + sw<KP>(row, col);
         if constexpr (NP == 1) {
           *(u32x4*)d = rB[j];
@@ -771,7 +722,7 @@ void walk_kernel(const WalkArgs p) {
       if constexpr (!STATE) {
 #pragma unroll
         for (int j = 0; j < RC; ++j) {
-          const int row = rowC + j * (256 / PRC), col = pieceC * EPP;
+          const int row = rowC + j * (GT / PRC), col = pieceC * EPP;
           __bf16* const d = Cs + row * VB + swc<VB>(row, col);
           if constexpr (NP == 1) {
             *(u32x4*)d = cC[j];
@@ -834,7 +785,7 @@ void walk_kernel(const WalkArgs p) {
     // the state at the walk's end of the staged chunk
     auto update = [&](int n, const __bf16* Bs, const __bf16* Cw, const __bf16* Cw2) {
       const bool cut = starts != 0;
-      const float d = cut ? 0.0f : (n == kQ ? lam64 : power(g2, n));
+      const float d = n == kQ ? lam64 : power(g2, n);
       const float nf = (float)n;
 #pragma unroll
       for (int j = 0; j < JK; ++j)
@@ -842,9 +793,18 @@ void walk_kernel(const WalkArgs p) {
         for (int vt = 0; vt < NVW; ++vt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if constexpr (DG) D[j][vt][i] = cut ? 0.0f : d * (D[j][vt][i] + nf * S[j][vt][i]);
-            S[j][vt][i] = cut ? 0.0f : d * S[j][vt][i];
+            if constexpr (DG) D[j][vt][i] = d * (D[j][vt][i] + nf * S[j][vt][i]);
+            S[j][vt][i] *= d;
           }
+      if (cut) {
+#pragma unroll
+        for (int j = 0; j < JK; ++j)
+#pragma unroll
+          for (int vt = 0; vt < NVW; ++vt) {
+            S[j][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (DG) D[j][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          }
+      }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const int ra = 32 * ks + 8 * g4 + kk, rb = ra + 4;
@@ -893,15 +853,15 @@ void walk_kernel(const WalkArgs p) {
           for (int i = 0; i < 4; ++i) S[j][vt][i] = s0[v * p.state_sv + (k + i) * p.state_sk];
         });
       }
-      // the states that the spans before this one add, in the walk's order
-      for (int m = 0; m < span; ++m) {
+      // the states that the pieces of the walk before this span add, in order
+      for (int m = 0; m < i0 / p.piece_chunks; ++m) {
         const float* loc = p.ws + ((int64_t)m * p.batch * p.H + bh) * (DG ? 2 : 1) * state_elems;
-        // real tokens of the span
-        const int m0 = m * p.span_chunks, m1 = m0 + p.span_chunks - 1;
+        // real tokens of the piece
+        const int m0 = m * p.piece_chunks, m1 = m0 + p.piece_chunks - 1;
         const int64_t ca = chunk_of(REV ? m1 : m0), cb = chunk_of(REV ? m0 : m1) + 1;
         const int64_t hi = cb * kQ < len ? cb * kQ : len;
         const int64_t n = hi > ca * kQ ? hi - ca * kQ : 0;
-        const bool cut = p.span_cut[(int64_t)m * p.batch + b] != 0;
+        const bool cut = p.piece_cut[(int64_t)m * p.batch + b] != 0;
         const float d = n == 0 ? 1.0f : exp2_hw(g2 * (float)n);
         for_state([&](int j, int vt, int v, int k) {
           const f32x4 av = *(const f32x4*)(loc + (int64_t)v * K + k);
@@ -918,30 +878,29 @@ void walk_kernel(const WalkArgs p) {
     }
     int any_start = 0;
     if (first < last) {
-      stage_rows(lds, lds + kCs);
+      stage_rows(rows_at(first), rows_at(first) + kCs);
       if (first + 1 < last) load_bc(chunk_of(first + 1));
-      stage_weighted(live_in(chunk_of(first)), lds + kCw, lds + kCw2);
-      put_state(lds + kSs, lds + kTs);
+      __bf16* const rest = rest_at(first);
+      stage_weighted(live_in(chunk_of(first)), rest, rest + kCw2);
+      put_state(rest + kSs, rest + kTs);
     }
     lds_barrier();
     for (int i = first; i < last; ++i) {
-      const __bf16* const buf = lds + (NBUF == 2 ? ((i - first) & 1) * Sh::kElems : 0);
-      __bf16* const next = lds + (NBUF == 2 ? ((i + 1 - first) & 1) * Sh::kElems : 0);
+      const __bf16* const rest = rest_at(i);
+      __bf16* const next = rest_at(i + 1);
       const bool more = i + 1 < last;
       auto stage_next = [&]() {
-        stage_rows(next, next + kCs);
+        stage_rows(rows_at(i + 1), rows_at(i + 1) + kCs);
         if (i + 2 < last) load_bc(chunk_of(i + 2));  // a chunk ahead of its use
       };
       any_start |= starts != 0;
-      if (NBUF == 2 && more) stage_next();
-      update(live_in(chunk_of(i)), buf, buf + kCw, buf + kCw2);
-      if (NBUF == 1) {
-        lds_barrier();  // the buffer is read
-        if (more) stage_next();
-      }
+      if (NROWS == 2 && more) stage_next();
+      update(live_in(chunk_of(i)), rows_at(i), rest, rest + kCw2);
+      if (NREST == 1) lds_barrier();  // what update read may be written
+      if (NROWS == 1 && more) stage_next();
       if (more) {
         put_state(next + kSs, next + kTs);
-        stage_weighted(live_in(chunk_of(i + 1)), next + kCw, next + kCw2);
+        stage_weighted(live_in(chunk_of(i + 1)), next, next + kCw2);
       }
       lds_barrier();
     }
@@ -952,7 +911,7 @@ void walk_kernel(const WalkArgs p) {
         *(f32x4*)(loc + (int64_t)v * K + k) = S[j][vt];
         if constexpr (DG) *(f32x4*)(loc + state_elems + (int64_t)v * K + k) = D[j][vt];
       });
-      if (h == 0 && sl == 0 && tid == 0) p.span_cut[(int64_t)span * p.batch + b] = any_start;
+      if (h == 0 && sl == 0 && tid == 0) p.piece_cut[(int64_t)span * p.batch + b] = any_start;
     } else {
       const bool ends = span == p.nspan - 1;  // this block ends the walk
       if (ends && p.final_state) {
@@ -973,7 +932,7 @@ void walk_kernel(const WalkArgs p) {
 
   if constexpr (DG && !STATE) {
     // the block's sum, in a fixed order
-    __shared__ float sums[8];
+    __shared__ float sums[16];
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1) dg += __shfl_xor(dg, m);
     if (lane == 0) sums[threadIdx.x >> 6] = dg;
@@ -981,7 +940,7 @@ void walk_kernel(const WalkArgs p) {
     if (threadIdx.x == 0) {
       float s = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += sums[i];
+      for (int i = 0; i < 2 * Sh::NW; ++i) s += sums[i];
       p.dg_part[(int64_t)h * p.batch * p.nsl * p.nspan + ((int64_t)b * p.nsl + sl) * p.nspan + span] = s;
     }
   }
@@ -990,26 +949,32 @@ void walk_kernel(const WalkArgs p) {
 template <int NP, int KP, int VB>
 hipError_t launch_walk(const WalkArgs& args, bool rev, bool dg, bool state, hipStream_t stream) {
   WalkArgs a = args;
-  a.nspan_run = state ? a.nspan - 1 : a.nspan;
+  a.nspan_run = state ? a.pieces : a.nspan;
+  if (state) a.span_chunks = a.piece_chunks;
   a.nsl = (a.V + VB - 1) / VB;
   const int64_t n = (int64_t)a.batch * a.H * a.nsl * a.nspan_run;
   if (n == 0) return hipSuccess;
   a.nblk = (uint32_t)n;
   const dim3 grid((uint32_t)((n + 7) / 8 * 8));
-  if (state) {
-    if (rev) walk_kernel<NP, KP, VB, true, false, true><<<grid, 256, 0, stream>>>(a);
-    else if (dg) walk_kernel<NP, KP, VB, false, true, true><<<grid, 256, 0, stream>>>(a);
-    else walk_kernel<NP, KP, VB, false, false, true><<<grid, 256, 0, stream>>>(a);
-  } else {
-    if (rev) walk_kernel<NP, KP, VB, true, false, false><<<grid, 512, 0, stream>>>(a);
-    else if (dg) {
-      if constexpr (Shape<NP, KP, VB, true, false>::kFits)
-        walk_kernel<NP, KP, VB, false, true, false><<<grid, 512, 0, stream>>>(a);
-      else
-        return hipErrorInvalidValue;  // walk_tile takes a narrower tile
-    }
-    else walk_kernel<NP, KP, VB, false, false, false><<<grid, 512, 0, stream>>>(a);
-  }
+  // the kernels that a plan can choose: the outputs' walk takes 64 columns at
+  // most, and 32 with the log-decay's gradient, whose state walk takes 64
+#define SSM_WALK(REV, DG, STATE)                                                                       \
+  do {                                                                                                 \
+    if constexpr (VB <= (STATE ? (DG ? 64 : 128) : (DG ? 32 : 64)))                                    \
+      static_assert(Shape<NP, KP, VB, DG, STATE>::kFits, "more than the LDS of a CU");                  \
+    if constexpr (VB <= (STATE ? (DG ? 64 : 128) : (DG ? 32 : 64)))                                              \
+      walk_kernel<NP, KP, VB, REV, DG, STATE>                                                          \
+          <<<grid, dim3(Shape<NP, KP, VB, DG, STATE>::kThreads), 0, stream>>>(a);                      \
+    else                                                                                               \
+      return hipErrorInvalidValue;                                                                     \
+  } while (0)
+  if (state && rev) SSM_WALK(true, false, true);
+  else if (state && dg) SSM_WALK(false, true, true);
+  else if (state) SSM_WALK(false, false, true);
+  else if (rev) SSM_WALK(true, false, false);
+  else if (dg) SSM_WALK(false, true, false);
+  else SSM_WALK(false, false, false);
+#undef SSM_WALK
   return hipGetLastError();
 }
 

@@ -14,6 +14,7 @@ arguments; every step of the computation runs in the library's HIP kernels.
     norm = clip_grad_norm(grads, max_norm, outs=None)            # grads clipped in place
 """
 import ctypes
+import functools
 
 SSM_F32, SSM_BF16 = 0, 1
 _ACTS = {"none": 0, "silu": 1}
@@ -45,68 +46,114 @@ def declare(lib):
     lib.ssm_clip_grad_norm.argtypes = [vp] * 4 + [i64, cf, vp, vp, sz, vp]
 
 
+_SSM = None
+_TORCH = None
+
+
 def _core():
-    import selective_state_space_66_amd as ssm
-    return ssm
+    """The package and torch (imported at the first call: the package imports without it)."""
+    global _SSM, _TORCH
+    if _SSM is None:
+        import torch
+
+        import selective_state_space_66_amd
+        _TORCH, _SSM = torch, selective_state_space_66_amd
+    return _SSM, _TORCH
 
 
-def _workspace(workspace, need, device):
-    """The caller's workspace, checked, or a new one; None where none is needed."""
-    import torch
+# The small calls take a few microseconds on the GPU, so the checks before them are kept as
+# short: one expression per tensor, and the checks that name what is wrong only where it fails.
+
+
+def _want(t, name, shape, dtype, device, index):
+    if t is None or (t.shape == shape and t.dtype is dtype and t.get_device() == index
+                     and t.is_contiguous()):
+        return
+    _core()[0]._check(t, name, shape, dtype, device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(torch, index):
+    """The current stream of GPU `index`, as an integer."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _workspace(torch, workspace, need, device):
+    """The caller's workspace, checked, or a new one, and its size."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        if not need:
+            return None, 0
+        return torch.empty(need, dtype=torch.uint8, device=device), need
     if workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous uint8 tensor on {device}")
     if workspace.numel() < need:
         raise ValueError(f"workspace: need {need} bytes, got {workspace.numel()}")
-    return workspace
+    return workspace, workspace.numel()
 
 
-def _flags(reset):
-    import torch
+def _flags(torch, reset):
     return reset.view(torch.uint8) if reset is not None and reset.dtype == torch.bool else reset
 
 
 def _on_gpu(t, name, dims, layout):
+    """The GPU's index."""
     if t.dim() != dims:
         raise ValueError(f"{name} must be {layout}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("tensors must be on the GPU")
+    return t.get_device()
 
 
-def _linattn_check(q, k, v, log_decay, h0, seq_lens, reset):
-    import torch
-    c = _core()
-    _on_gpu(q, "q", 4, "(batch, L, kheads, dk)")
+def _code(c, torch, t):
+    return SSM_BF16 if t.dtype is torch.bfloat16 else c._io_code(t)
+
+
+# sizes alone decide a workspace
+@functools.lru_cache(maxsize=512)
+def _linattn_ws(backward, batch, L, H, Hk, Dk, Dv, need_dg, io):
+    lib = _core()[0].load_library()
+    if backward:
+        return int(lib.ssm_linattn_bwd_workspace_size(batch, L, H, Hk, Dk, Dv, need_dg, io))
+    return int(lib.ssm_linattn_fwd_workspace_size(batch, L, H, Hk, Dk, Dv, io))
+
+
+@functools.lru_cache(maxsize=512)
+def _norm_ws(batch, rows, C, groups, backward, io):
+    return int(_core()[0].load_library().ssm_group_norm_workspace_size(batch, rows, C, groups,
+                                                                       backward, io))
+
+
+def _linattn_check(c, torch, q, k, v, log_decay, h0, seq_lens, reset):
+    index = _on_gpu(q, "q", 4, "(batch, L, kheads, dk)")
     _on_gpu(v, "v", 4, "(batch, L, nheads, dv)")
     batch, L, Hk, Dk = q.shape
     H, Dv = v.shape[2:]
-    io, dev = q.dtype, q.device
-    c._io_code(q)
-    c._check(q, "q", (batch, L, Hk, Dk), io, dev)
-    c._check(k, "k", (batch, L, Hk, Dk), io, dev)
-    c._check(v, "v", (batch, L, H, Dv), io, dev)
-    c._check(log_decay, "log_decay", (H,), torch.float32, dev)
-    c._check(h0, "h0", (batch, H, Dv, Dk), torch.float32, dev)
-    c._check(seq_lens, "seq_lens", (batch,), torch.int32, dev)
-    c._check(reset, "reset", (batch, L), torch.uint8, dev)
-    return batch, L, H, Hk, Dk, Dv
+    io, dev, f32 = q.dtype, q.device, torch.float32
+    code = _code(c, torch, q)
+    _want(q, "q", (batch, L, Hk, Dk), io, dev, index)
+    _want(k, "k", (batch, L, Hk, Dk), io, dev, index)
+    _want(v, "v", (batch, L, H, Dv), io, dev, index)
+    _want(log_decay, "log_decay", (H,), f32, dev, index)
+    _want(h0, "h0", (batch, H, Dv, Dk), f32, dev, index)
+    _want(seq_lens, "seq_lens", (batch,), torch.int32, dev, index)
+    _want(reset, "reset", (batch, L), torch.uint8, dev, index)
+    return batch, L, H, Hk, Dk, Dv, dev, index, code
 
 
 def linattn_fwd_workspace_size(batch, L, nheads, kheads, dk, dv, io_dtype):
     """Bytes of workspace ssm_linattn_fwd needs (io_dtype: a torch dtype)."""
-    import torch
-    code = SSM_F32 if io_dtype == torch.float32 else SSM_BF16
-    return int(_core().load_library().ssm_linattn_fwd_workspace_size(batch, L, nheads, kheads, dk,
-                                                                     dv, code))
+    code = SSM_F32 if io_dtype == _core()[1].float32 else SSM_BF16
+    return _linattn_ws(False, batch, L, nheads, kheads, dk, dv, 0, code)
 
 
 def linattn_bwd_workspace_size(batch, L, nheads, kheads, dk, dv, io_dtype, need_dlog_decay=True):
     """Bytes of workspace ssm_linattn_bwd needs (io_dtype: a torch dtype)."""
-    import torch
-    code = SSM_F32 if io_dtype == torch.float32 else SSM_BF16
-    return int(_core().load_library().ssm_linattn_bwd_workspace_size(
-        batch, L, nheads, kheads, dk, dv, int(bool(need_dlog_decay)), code))
+    code = SSM_F32 if io_dtype == _core()[1].float32 else SSM_BF16
+    return _linattn_ws(True, batch, L, nheads, kheads, dk, dv, int(bool(need_dlog_decay)), code)
 
 
 def linattn_fwd(q, k, v, log_decay, scale=None, h0=None, seq_lens=None, reset=None, o=None,
@@ -122,26 +169,24 @@ def linattn_fwd(q, k, v, log_decay, scale=None, h0=None, seq_lens=None, reset=No
     reset: optional (batch, L) bool or uint8, state zeroed before each flagged token.
     Returns (o like v, last_state (batch, nheads, dv, dk) float32, or None if not requested).
     """
-    import torch
-    c = _core()
+    c, torch = _core()
     lib = c.load_library()
-    reset = _flags(reset)
-    batch, L, H, Hk, Dk, Dv = _linattn_check(q, k, v, log_decay, h0, seq_lens, reset)
-    dev = q.device
+    reset = _flags(torch, reset)
+    batch, L, H, Hk, Dk, Dv, dev, index, io = _linattn_check(c, torch, q, k, v, log_decay, h0,
+                                                             seq_lens, reset)
     if o is None:
         o = torch.empty_like(v)
-    c._check(o, "o", (batch, L, H, Dv), q.dtype, dev)
-    if last_state is None and return_last_state:
+    else:
+        _want(o, "o", (batch, L, H, Dv), q.dtype, dev, index)
+    if last_state is not None:
+        _want(last_state, "last_state", (batch, H, Dv, Dk), torch.float32, dev, index)
+    elif return_last_state:
         last_state = torch.empty((batch, H, Dv, Dk), dtype=torch.float32, device=dev)
-    c._check(last_state, "last_state", (batch, H, Dv, Dk), torch.float32, dev)
-    io = c._io_code(q)
-    ws = _workspace(workspace, int(lib.ssm_linattn_fwd_workspace_size(batch, L, H, Hk, Dk, Dv, io)),
-                    dev)
-    st = lib.ssm_linattn_fwd(c._ptr(q), c._ptr(k), c._ptr(v), c._ptr(log_decay),
-                             Dk ** -0.5 if scale is None else float(scale), c._ptr(h0),
-                             c._ptr(seq_lens), c._ptr(reset), c._ptr(o), c._ptr(last_state),
-                             c._ptr(ws), 0 if ws is None else ws.numel(), batch, L, H, Hk, Dk, Dv,
-                             io, c._stream(dev))
+    ws, size = _workspace(torch, workspace, _linattn_ws(False, batch, L, H, Hk, Dk, Dv, 0, io), dev)
+    st = lib.ssm_linattn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                             Dk ** -0.5 if scale is None else scale, _ptr(h0), _ptr(seq_lens),
+                             _ptr(reset), _ptr(o), _ptr(last_state), _ptr(ws), size, batch, L, H,
+                             Hk, Dk, Dv, io, _stream(torch, index))
     if st != 0:
         raise c.SsmError(st, "ssm_linattn_fwd")
     return o, last_state
@@ -155,29 +200,23 @@ def linattn_bwd(q, k, v, log_decay, do, scale=None, h0=None, dlast=None, seq_len
     Returns a dict: dq, dk, dv (io dtype), dlog_decay (float32, None if not needed) and,
     where h0 was given, dh0 (float32).
     """
-    import torch
-    c = _core()
+    c, torch = _core()
     lib = c.load_library()
-    reset = _flags(reset)
-    batch, L, H, Hk, Dk, Dv = _linattn_check(q, k, v, log_decay, h0, seq_lens, reset)
-    dev = q.device
-    c._check(do, "do", (batch, L, H, Dv), q.dtype, dev)
-    c._check(dlast, "dlast", (batch, H, Dv, Dk), torch.float32, dev)
-    f32 = dict(dtype=torch.float32, device=dev)
+    reset = _flags(torch, reset)
+    batch, L, H, Hk, Dk, Dv, dev, index, io = _linattn_check(c, torch, q, k, v, log_decay, h0,
+                                                             seq_lens, reset)
+    _want(do, "do", (batch, L, H, Dv), q.dtype, dev, index)
+    _want(dlast, "dlast", (batch, H, Dv, Dk), torch.float32, dev, index)
     g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
-             dlog_decay=torch.empty((H,), **f32) if need_dlog_decay else None,
-             dh0=torch.empty((batch, H, Dv, Dk), **f32) if h0 is not None else None)
-    io = c._io_code(q)
-    need = int(lib.ssm_linattn_bwd_workspace_size(batch, L, H, Hk, Dk, Dv,
-                                                  int(bool(need_dlog_decay)), io))
-    ws = _workspace(workspace, need, dev)
-    st = lib.ssm_linattn_bwd(c._ptr(q), c._ptr(k), c._ptr(v), c._ptr(log_decay),
-                             Dk ** -0.5 if scale is None else float(scale), c._ptr(h0),
-                             c._ptr(seq_lens), c._ptr(reset), c._ptr(do), c._ptr(dlast),
-                             c._ptr(g["dq"]), c._ptr(g["dk"]), c._ptr(g["dv"]),
-                             c._ptr(g["dlog_decay"]), c._ptr(g["dh0"]), c._ptr(ws),
-                             0 if ws is None else ws.numel(), batch, L, H, Hk, Dk, Dv, io,
-                             c._stream(dev))
+             dlog_decay=torch.empty_like(log_decay) if need_dlog_decay else None,
+             dh0=torch.empty_like(h0) if h0 is not None else None)
+    ws, size = _workspace(torch, workspace, _linattn_ws(True, batch, L, H, Hk, Dk, Dv,
+                                                        int(bool(need_dlog_decay)), io), dev)
+    st = lib.ssm_linattn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                             Dk ** -0.5 if scale is None else scale, _ptr(h0), _ptr(seq_lens),
+                             _ptr(reset), _ptr(do), _ptr(dlast), _ptr(g["dq"]), _ptr(g["dk"]),
+                             _ptr(g["dv"]), _ptr(g["dlog_decay"]), _ptr(g["dh0"]), _ptr(ws), size,
+                             batch, L, H, Hk, Dk, Dv, io, _stream(torch, index))
     if st != 0:
         raise c.SsmError(st, "ssm_linattn_bwd")
     return g
@@ -186,26 +225,26 @@ def linattn_bwd(q, k, v, log_decay, do, scale=None, h0=None, dlast=None, seq_len
 def linattn_step(state, q, k, v, log_decay, scale=None, o=None):
     """One token of linear attention on the GPU; `state` (batch, nheads, dv, dk) float32 is
     updated in place.  q, k: (batch, kheads, dk); v: (batch, nheads, dv). Returns o like v."""
-    import torch
-    c = _core()
+    c, torch = _core()
     lib = c.load_library()
-    _on_gpu(q, "q", 3, "(batch, kheads, dk)")
+    index = _on_gpu(q, "q", 3, "(batch, kheads, dk)")
     _on_gpu(v, "v", 3, "(batch, nheads, dv)")
     batch, Hk, Dk = q.shape
     H, Dv = v.shape[1:]
     io, dev = q.dtype, q.device
-    c._io_code(q)
-    c._check(state, "state", (batch, H, Dv, Dk), torch.float32, dev)
-    c._check(q, "q", (batch, Hk, Dk), io, dev)
-    c._check(k, "k", (batch, Hk, Dk), io, dev)
-    c._check(v, "v", (batch, H, Dv), io, dev)
-    c._check(log_decay, "log_decay", (H,), torch.float32, dev)
+    code = _code(c, torch, q)
+    _want(state, "state", (batch, H, Dv, Dk), torch.float32, dev, index)
+    _want(q, "q", (batch, Hk, Dk), io, dev, index)
+    _want(k, "k", (batch, Hk, Dk), io, dev, index)
+    _want(v, "v", (batch, H, Dv), io, dev, index)
+    _want(log_decay, "log_decay", (H,), torch.float32, dev, index)
     if o is None:
         o = torch.empty_like(v)
-    c._check(o, "o", (batch, H, Dv), io, dev)
-    st = lib.ssm_linattn_step(c._ptr(state), c._ptr(q), c._ptr(k), c._ptr(v), c._ptr(log_decay),
-                              Dk ** -0.5 if scale is None else float(scale), c._ptr(o), batch, H,
-                              Hk, Dk, Dv, c._io_code(q), c._stream(dev))
+    else:
+        _want(o, "o", (batch, H, Dv), io, dev, index)
+    st = lib.ssm_linattn_step(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                              Dk ** -0.5 if scale is None else scale, _ptr(o), batch, H, Hk, Dk,
+                              Dv, code, _stream(torch, index))
     if st != 0:
         raise c.SsmError(st, "ssm_linattn_step")
     return o
@@ -213,28 +252,24 @@ def linattn_step(state, q, k, v, log_decay, scale=None, o=None):
 
 def group_norm_workspace_size(batch, rows, channels, groups, io_dtype, backward=False):
     """Bytes of workspace group_norm_fwd (or, with backward, group_norm_bwd) needs."""
-    import torch
-    code = SSM_F32 if io_dtype == torch.float32 else SSM_BF16
-    return int(_core().load_library().ssm_group_norm_workspace_size(
-        batch, rows, channels, groups, int(bool(backward)), code))
+    code = SSM_F32 if io_dtype == _core()[1].float32 else SSM_BF16
+    return _norm_ws(batch, rows, channels, groups, int(bool(backward)), code)
 
 
-def _group_norm_check(x, groups, weight, bias, z, act):
-    import torch
-    c = _core()
-    _on_gpu(x, "x", 3, "(batch, rows, channels)")
+def _group_norm_check(c, torch, x, groups, weight, bias, z, act):
+    index = _on_gpu(x, "x", 3, "(batch, rows, channels)")
     batch, rows, C = x.shape
     io, dev = x.dtype, x.device
-    c._io_code(x)
+    code = _code(c, torch, x)
     if act not in _ACTS:
         raise ValueError(f"act: expected one of {sorted(_ACTS)}, got {act!r}")
     if groups < 1 or C < 1 or C % groups != 0:
         raise ValueError(f"groups: {groups} does not divide {C} channels")
-    c._check(x, "x", (batch, rows, C), io, dev)
-    c._check(weight, "weight", (C,), torch.float32, dev)
-    c._check(bias, "bias", (C,), torch.float32, dev)
-    c._check(z, "z", (batch, rows, C), io, dev)
-    return batch, rows, C
+    _want(x, "x", (batch, rows, C), io, dev, index)
+    _want(weight, "weight", (C,), torch.float32, dev, index)
+    _want(bias, "bias", (C,), torch.float32, dev, index)
+    _want(z, "z", (batch, rows, C), io, dev, index)
+    return batch, rows, C, dev, index, code
 
 
 def group_norm_fwd(x, groups, weight=None, bias=None, z=None, act="none", eps=1e-5, y=None,
@@ -248,25 +283,21 @@ def group_norm_fwd(x, groups, weight=None, bias=None, z=None, act="none", eps=1e
     Returns (y like x, mean, rstd): mean and rstd (batch, groups) float32, what
     group_norm_bwd takes (None if not requested).
     """
-    import torch
-    c = _core()
+    c, torch = _core()
     lib = c.load_library()
-    batch, rows, C = _group_norm_check(x, groups, weight, bias, z, act)
-    dev = x.device
+    batch, rows, C, dev, index, io = _group_norm_check(c, torch, x, groups, weight, bias, z, act)
     if y is None:
         y = torch.empty_like(x)
-    c._check(y, "y", (batch, rows, C), x.dtype, dev)
+    else:
+        _want(y, "y", (batch, rows, C), x.dtype, dev, index)
     mean = rstd = None
     if return_stats:
         mean = torch.empty((batch, groups), dtype=torch.float32, device=dev)
-        rstd = torch.empty((batch, groups), dtype=torch.float32, device=dev)
-    io = c._io_code(x)
-    ws = _workspace(workspace, int(lib.ssm_group_norm_workspace_size(batch, rows, C, groups, 0, io)),
-                    dev)
-    st = lib.ssm_group_norm_fwd(c._ptr(x), c._ptr(weight), c._ptr(bias), c._ptr(z), _ACTS[act],
-                                float(eps), c._ptr(y), c._ptr(mean), c._ptr(rstd), c._ptr(ws),
-                                0 if ws is None else ws.numel(), batch, rows, C, groups, io,
-                                c._stream(dev))
+        rstd = torch.empty_like(mean)
+    ws, size = _workspace(torch, workspace, _norm_ws(batch, rows, C, groups, 0, io), dev)
+    st = lib.ssm_group_norm_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(z), _ACTS[act], eps,
+                                _ptr(y), _ptr(mean), _ptr(rstd), _ptr(ws), size, batch, rows, C,
+                                groups, io, _stream(torch, index))
     if st != 0:
         raise c.SsmError(st, "ssm_group_norm_fwd")
     return y, mean, rstd
@@ -279,26 +310,21 @@ def group_norm_bwd(x, groups, dy, mean, rstd, weight=None, bias=None, z=None, ac
     dy: like x.  Returns a dict: dx (io dtype) and, where their inputs were given, dweight,
     dbias (float32) and dz (io dtype).
     """
-    import torch
-    c = _core()
+    c, torch = _core()
     lib = c.load_library()
-    batch, rows, C = _group_norm_check(x, groups, weight, bias, z, act)
-    dev = x.device
-    c._check(dy, "dy", (batch, rows, C), x.dtype, dev)
-    c._check(mean, "mean", (batch, groups), torch.float32, dev)
-    c._check(rstd, "rstd", (batch, groups), torch.float32, dev)
+    batch, rows, C, dev, index, io = _group_norm_check(c, torch, x, groups, weight, bias, z, act)
+    _want(dy, "dy", (batch, rows, C), x.dtype, dev, index)
+    _want(mean, "mean", (batch, groups), torch.float32, dev, index)
+    _want(rstd, "rstd", (batch, groups), torch.float32, dev, index)
     g = dict(dx=torch.empty_like(x),
              dweight=torch.empty_like(weight) if weight is not None else None,
              dbias=torch.empty_like(bias) if bias is not None else None,
              dz=torch.empty_like(z) if z is not None else None)
-    io = c._io_code(x)
-    ws = _workspace(workspace, int(lib.ssm_group_norm_workspace_size(batch, rows, C, groups, 1, io)),
-                    dev)
-    st = lib.ssm_group_norm_bwd(c._ptr(x), c._ptr(weight), c._ptr(bias), c._ptr(z), _ACTS[act],
-                                c._ptr(mean), c._ptr(rstd), c._ptr(dy), c._ptr(g["dx"]),
-                                c._ptr(g["dweight"]), c._ptr(g["dbias"]), c._ptr(g["dz"]),
-                                c._ptr(ws), 0 if ws is None else ws.numel(), batch, rows, C,
-                                groups, io, c._stream(dev))
+    ws, size = _workspace(torch, workspace, _norm_ws(batch, rows, C, groups, 1, io), dev)
+    st = lib.ssm_group_norm_bwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(z), _ACTS[act], _ptr(mean),
+                                _ptr(rstd), _ptr(dy), _ptr(g["dx"]), _ptr(g["dweight"]),
+                                _ptr(g["dbias"]), _ptr(g["dz"]), _ptr(ws), size, batch, rows, C,
+                                groups, io, _stream(torch, index))
     if st != 0:
         raise c.SsmError(st, "ssm_group_norm_bwd")
     return g
@@ -312,8 +338,7 @@ def clip_grad_norm(grads, max_norm, outs=None, workspace=None):
     out = grad * min(1, max_norm / (norm + 1e-6)).  Returns the norm before clipping, a
     float32 tensor with no dimensions, on the GPU (nothing waits for it).
     """
-    import torch
-    c = _core()
+    c, torch = _core()
     lib = c.load_library()
     grads = list(grads)
     outs = grads if outs is None else list(outs)
@@ -322,31 +347,34 @@ def clip_grad_norm(grads, max_norm, outs=None, workspace=None):
         raise ValueError("grads: at least one tensor is needed (they say which GPU)")
     if len(outs) != n:
         raise ValueError(f"outs: expected {n} tensors, got {len(outs)}")
-    dev = grads[0].device
-    if dev.type != "cuda":
+    if not grads[0].is_cuda:
         raise ValueError("tensors must be on the GPU")
+    dev, index = grads[0].device, grads[0].get_device()
     codes = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
+    types = [codes.get(t.dtype) for t in grads]
+    # one pass over the list each; the loops that name a culprit run only if there is one
+    if None in types:
+        i = types.index(None)
+        raise TypeError(f"grads[{i}]: expected float32 or bfloat16, got {grads[i].dtype}")
     for i, t in enumerate(grads):
-        if t.dtype not in codes:
-            raise TypeError(f"grads[{i}]: expected float32 or bfloat16, got {t.dtype}")
-        if t.device != dev:
-            raise ValueError(f"grads[{i}]: expected device {dev}, got {t.device}")
-        if not t.is_contiguous():
+        if t.get_device() != index or not t.is_contiguous():
+            if t.device != dev:
+                raise ValueError(f"grads[{i}]: expected device {dev}, got {t.device}")
             raise ValueError(f"grads[{i}]: must be contiguous")
     if outs is not grads:
         for i, (t, o) in enumerate(zip(grads, outs)):
-            if o.shape != t.shape or o.dtype != t.dtype or o.device != dev or not o.is_contiguous():
+            if (o.shape != t.shape or o.dtype is not t.dtype or o.get_device() != index
+                    or not o.is_contiguous()):
                 raise ValueError(f"outs[{i}]: expected a contiguous {t.dtype} tensor of shape "
                                  f"{tuple(t.shape)} on {dev}")
-    pointers = ctypes.c_void_p * n
+    pointers, counts = ctypes.c_void_p * n, ctypes.c_int64 * n
     src = pointers(*[t.data_ptr() for t in grads])
     dst = src if outs is grads else pointers(*[o.data_ptr() for o in outs])
-    counts = (ctypes.c_int64 * n)(*[t.numel() for t in grads])
-    types = (ctypes.c_int32 * n)(*[codes[t.dtype] for t in grads])
     norm = torch.empty((), dtype=torch.float32, device=dev)
-    ws = _workspace(workspace, int(lib.ssm_clip_grad_norm_workspace_size(n)), dev)
-    st = lib.ssm_clip_grad_norm(src, dst, counts, types, n, float(max_norm), c._ptr(norm),
-                                c._ptr(ws), 0 if ws is None else ws.numel(), c._stream(dev))
+    ws, size = _workspace(torch, workspace, int(lib.ssm_clip_grad_norm_workspace_size(n)), dev)
+    st = lib.ssm_clip_grad_norm(src, dst, counts(*[t.numel() for t in grads]),
+                                (ctypes.c_int32 * n)(*types), n, max_norm, _ptr(norm), _ptr(ws),
+                                size, _stream(torch, index))
     if st != 0:
         raise c.SsmError(st, "ssm_clip_grad_norm")
     return norm
