@@ -14,6 +14,8 @@
 // than the loads.  Every block leaves one partial sum, and each block of the
 // second pass adds all of them itself, in the same order: one launch less than
 // a kernel of its own, and identical bits on every call.
+#include <vector>
+
 #include "grad_clip_launch.h"
 #include "ssm_device.h"
 
@@ -130,9 +132,11 @@ __device__ __forceinline__ void scale(const T* p, T* q, int64_t n, float c) {
 #pragma unroll
       for (int u = 0; u < U; ++u) v[u] = ((const u32x4*)p)[k + u * 256];
 #pragma unroll
-      for (int u = 0; u < U; ++u) ((u32x4*)q)[k + u * 256] = piece_scaled<T>(v[u], c);
+      for (int u = 0; u < U; ++u)
+        __builtin_nontemporal_store(piece_scaled<T>(v[u], c), (u32x4*)q + k + u * 256);
     }
-    for (; k < nv; k += 256) ((u32x4*)q)[k] = piece_scaled<T>(((const u32x4*)p)[k], c);
+    for (; k < nv; k += 256)
+      __builtin_nontemporal_store(piece_scaled<T>(((const u32x4*)p)[k], c), (u32x4*)q + k);
     i = nv * V;
   }
   for (i += threadIdx.x; i < n; i += 256) store_io(q + i, to_f32(p[i]) * c);
@@ -159,7 +163,9 @@ __global__ __launch_bounds__(256) void clip_kernel(const List l, const double* p
   if (first && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
   float coef = max_norm / (total + 1e-6f);
   coef = coef > 1.0f ? 1.0f : coef;  // a NaN stays one
-  for (uint32_t c = blockIdx.x; c < l.chunks; c += gridDim.x) {
+  // from the end: what the first pass read last is still in the caches
+  for (uint32_t k = blockIdx.x; k < l.chunks; k += gridDim.x) {
+    const uint32_t c = l.chunks - 1 - k;
     const Entry& e = l.e[entry_of(l, c)];
     if (coef == 1.0f && e.src == e.dst) continue;  // in place, and every value times one
     const int64_t per = kChunkBytes / (e.f32 ? 4 : 2);
@@ -170,12 +176,18 @@ __global__ __launch_bounds__(256) void clip_kernel(const List l, const double* p
   }
 }
 
-// the next list of a call: entries from *at on, empty tensors left out
-void next_list(const Call& c, int64_t* at, List* l) {
+// The lists of a call: entry i of the non-empty tensors is in list i / kTensors.
+int64_t lists_of(const Call& c) {
+  int64_t n = 0;
+  for (int64_t i = 0; i < c.n; ++i) n += c.counts[i] != 0;
+  return (n + kTensors - 1) / kTensors;
+}
+// the next list, from tensor *at on
+void fill_list(const Call& c, int64_t* at, List* l) {
   l->n = 0;
   l->chunks = 0;
-  while (*at < c.n && l->n < kTensors) {
-    const int64_t i = (*at)++;
+  for (; *at < c.n && l->n < kTensors; ++*at) {
+    const int64_t i = *at;
     if (c.counts[i] == 0) continue;
     const int64_t per = kChunkBytes / (c.io_dtypes[i] == 0 ? 4 : 2);
     Entry& e = l->e[l->n++];
@@ -198,29 +210,26 @@ size_t workspace_bytes(int64_t n) {
 
 hipError_t run(const Call& c, hipStream_t s) {
   double* const parts = (double*)c.ws;
-  List l;
+  const int64_t lists = lists_of(c);
+  // the first pass over the lists in order, the second from the last one back
+  std::vector<List> all((size_t)(lists > 0 ? lists : 1));
   int nparts = 0;
-  for (int64_t at = 0; at < c.n;) {
-    next_list(c, &at, &l);
-    const uint32_t nb = blocks_of(l);
-    if (nb == 0) continue;
-    norm_kernel<<<dim3(nb), 256, 0, s>>>(l, parts + nparts);
+  int64_t at = 0;
+  all[0].n = 0;
+  all[0].chunks = 0;
+  for (int64_t k = 0; k < lists; ++k) {
+    fill_list(c, &at, &all[k]);
+    const uint32_t nb = blocks_of(all[k]);
+    norm_kernel<<<dim3(nb), 256, 0, s>>>(all[k], parts + nparts);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     nparts += (int)nb;
   }
-  bool first = true;
-  for (int64_t at = 0; at < c.n || first;) {
-    next_list(c, &at, &l);
-    uint32_t nb = blocks_of(l);
-    if (nb == 0) {
-      if (!first || at < c.n) continue;
-      nb = 1;  // nothing but empty tensors: the norm is still written
-    }
-    clip_kernel<<<dim3(nb), 256, 0, s>>>(l, parts, nparts, c.max_norm, c.norm, first ? 1 : 0);
+  for (int64_t k = (int64_t)all.size() - 1; k >= 0; --k) {
+    const uint32_t nb = blocks_of(all[k]);  // 0 where every tensor is empty: the norm is still written
+    clip_kernel<<<dim3(nb ? nb : 1), 256, 0, s>>>(all[k], parts, nparts, c.max_norm, c.norm, k == 0);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    first = false;
   }
   return hipSuccess;
 }

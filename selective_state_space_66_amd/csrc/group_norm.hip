@@ -272,6 +272,27 @@ __device__ __forceinline__ Where where(const Args& p, int tile, int rpb) {
   return w;
 }
 
+// What a thread reads of a row.
+template <int VEC>
+struct Row { float x[VEC], z[VEC], dy[VEC]; };
+
+// One thread's rows, U of them loaded before the first is used: the pieces are
+// short and few blocks share a CU, so a row at a time waits for memory each time.
+template <int U, typename Load, typename Use, typename V>
+__device__ __forceinline__ void rows_ahead(const Where& w, int rpb, Load load, Use use, V (&v)[U]) {
+  int64_t r = w.row0 + w.r0;
+  for (; r + (int64_t)(U - 1) * rpb < w.row1; r += (int64_t)U * rpb) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(r + (int64_t)u * rpb, v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) use(r + (int64_t)u * rpb, v[u]);
+  }
+  for (; r < w.row1; r += rpb) {
+    load(r, v[0]);
+    use(r, v[0]);
+  }
+}
+
 // (count, mean, sum of squares about it) of two disjoint sets of values
 struct Moments { float n, mean, m2; };
 __device__ __forceinline__ Moments merge(Moments a, Moments b) {
@@ -290,19 +311,19 @@ __global__ __launch_bounds__(256) void piece_stats_kernel(const Args p, int tile
 #pragma unroll
   for (int i = 0; i < VEC; ++i) first[i] = s[i] = q[i] = 0.0f;
   if (w.here) {
-    int64_t r = w.row0 + w.r0;
-    if (r < w.row1) load_vec<T, VEC>(x + r * p.C, first);
-    for (; r < w.row1; r += rpb) {
-      float v[VEC];
-      load_vec<T, VEC>(x + r * p.C, v);
-      cnt += 1.0f;
+    const int64_t r0 = w.row0 + w.r0;
+    if (r0 < w.row1) load_vec<T, VEC>(x + r0 * p.C, first);
+    Row<VEC> buf[4];
+    rows_ahead(w, rpb, [&](int64_t r, Row<VEC>& v) { load_vec<T, VEC>(x + r * p.C, v.x); },
+               [&](int64_t, const Row<VEC>& v) {
+                 cnt += 1.0f;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float d = v[i] - first[i];
-        s[i] += d;
-        q[i] = fmaf(d, d, q[i]);
-      }
-    }
+                 for (int i = 0; i < VEC; ++i) {
+                   const float d = v.x[i] - first[i];
+                   s[i] += d;
+                   q[i] = fmaf(d, d, q[i]);
+                 }
+               }, buf);
   }
   __shared__ float3 all[256];
   float2* const part = (float2*)p.ws + (int64_t)blockIdx.x * p.C;
@@ -390,15 +411,17 @@ __global__ __launch_bounds__(256) void apply_fwd_kernel(const Args p, const floa
     sh[i] = p.bias ? p.bias[c] : 0.0f;
   }
   const int64_t base = w.n * p.rows * p.C + w.col;
-  for (int64_t r = w.row0 + w.r0; r < w.row1; r += rpb) {
-    float v[VEC], z[VEC], y[VEC];
-    load_vec<T, VEC>((const T*)p.x + base + r * p.C, v);
-    if (GATE) load_vec<T, VEC>((const T*)p.z + base + r * p.C, z);
+  Row<VEC> buf[4];
+  rows_ahead(w, rpb, [&](int64_t r, Row<VEC>& v) {
+    load_vec<T, VEC>((const T*)p.x + base + r * p.C, v.x);
+    if (GATE) load_vec<T, VEC>((const T*)p.z + base + r * p.C, v.z);
+  }, [&](int64_t r, const Row<VEC>& v) {
+    float y[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
-      y[i] = Point<SILU, GATE>::forward(fmaf(v[i] - mu[i], sc[i], sh[i]), GATE ? z[i] : 0.0f);
+      y[i] = Point<SILU, GATE>::forward(fmaf(v.x[i] - mu[i], sc[i], sh[i]), GATE ? v.z[i] : 0.0f);
     store_vec<T, VEC>((T*)p.y + base + r * p.C, y);
-  }
+  }, buf);
 }
 
 // pass 1 of the backward: per channel and piece, the sums of du and du xh
@@ -418,21 +441,23 @@ __global__ __launch_bounds__(256) void piece_grads_kernel(const Args p, int tile
     s1[i] = s2[i] = 0.0f;
   }
   const int64_t base = w.n * p.rows * p.C + w.col;
+  Row<VEC> buf[4];
   if (w.here)
-    for (int64_t r = w.row0 + w.r0; r < w.row1; r += rpb) {
-      float v[VEC], z[VEC], dy[VEC], dz[VEC];
-      load_vec<T, VEC>((const T*)p.x + base + r * p.C, v);
-      load_vec<T, VEC>((const T*)p.dy + base + r * p.C, dy);
-      if (GATE) load_vec<T, VEC>((const T*)p.z + base + r * p.C, z);
+    rows_ahead(w, rpb, [&](int64_t r, Row<VEC>& v) {
+      load_vec<T, VEC>((const T*)p.x + base + r * p.C, v.x);
+      load_vec<T, VEC>((const T*)p.dy + base + r * p.C, v.dy);
+      if (GATE) load_vec<T, VEC>((const T*)p.z + base + r * p.C, v.z);
+    }, [&](int64_t, const Row<VEC>& v) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float xh = (v[i] - mu[i]) * rs[i];
+        float dz;
+        const float xh = (v.x[i] - mu[i]) * rs[i];
         const float du =
-            Point<SILU, GATE>::backward(fmaf(xh, wt[i], sh[i]), GATE ? z[i] : 0.0f, dy[i], &dz[i]);
+            Point<SILU, GATE>::backward(fmaf(xh, wt[i], sh[i]), GATE ? v.z[i] : 0.0f, v.dy[i], &dz);
         s1[i] += du;
         s2[i] = fmaf(du, xh, s2[i]);
       }
-    }
+    }, buf);
   __shared__ float2 all[256];
   float2* const part = (float2*)p.ws + (int64_t)blockIdx.x * p.C;
 #pragma unroll
@@ -495,47 +520,51 @@ __global__ __launch_bounds__(256) void apply_bwd_kernel(const Args p, const floa
     a2[i] = s.y;
   }
   const int64_t base = w.n * p.rows * p.C + w.col;
-  for (int64_t r = w.row0 + w.r0; r < w.row1; r += rpb) {
-    float v[VEC], z[VEC], dy[VEC], dz[VEC], dx[VEC];
-    load_vec<T, VEC>((const T*)p.x + base + r * p.C, v);
-    load_vec<T, VEC>((const T*)p.dy + base + r * p.C, dy);
-    if (GATE) load_vec<T, VEC>((const T*)p.z + base + r * p.C, z);
+  Row<VEC> buf[4];
+  rows_ahead(w, rpb, [&](int64_t r, Row<VEC>& v) {
+    load_vec<T, VEC>((const T*)p.x + base + r * p.C, v.x);
+    load_vec<T, VEC>((const T*)p.dy + base + r * p.C, v.dy);
+    if (GATE) load_vec<T, VEC>((const T*)p.z + base + r * p.C, v.z);
+  }, [&](int64_t r, const Row<VEC>& v) {
+    float dz[VEC], dx[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      const float xh = (v[i] - mu[i]) * rs[i];
+      const float xh = (v.x[i] - mu[i]) * rs[i];
       const float du =
-          Point<SILU, GATE>::backward(fmaf(xh, wt[i], sh[i]), GATE ? z[i] : 0.0f, dy[i], &dz[i]);
+          Point<SILU, GATE>::backward(fmaf(xh, wt[i], sh[i]), GATE ? v.z[i] : 0.0f, v.dy[i], &dz[i]);
       dx[i] = rs[i] * (du * wt[i] - a1[i] - xh * a2[i]);
     }
     store_vec<T, VEC>((T*)p.dx + base + r * p.C, dx);
     if (GATE) store_vec<T, VEC>((T*)p.dz + base + r * p.C, dz);
-  }
+  }, buf);
 }
 
-// db and dw: `rows` rows of partial sums (db, dw per channel) added in order,
-// 32 channels and 8 row groups per block.
-__global__ __launch_bounds__(256) void sum_channels_kernel(const float2* part, int64_t rows, int C,
-                                                           float* dweight, float* dbias) {
-  __shared__ float2 all[8][32];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), rg = threadIdx.x >> 5;
+// db and dw: `rows` rows of partial sums (db, dw per channel) added in a fixed
+// order, 16 channels and 64 row groups per block.
+__global__ __launch_bounds__(1024) void sum_channels_kernel(const float2* part, int64_t rows, int C,
+                                                            float* dweight, float* dbias) {
+  __shared__ float2 all[64][17];
+  const int ch = threadIdx.x & 15, c = blockIdx.x * 16 + ch, rg = threadIdx.x >> 4;
   float s1 = 0.0f, s2 = 0.0f;
   if (c < C) {
-#pragma unroll 4
-    for (int64_t r = rg; r < rows; r += 8) {
+#pragma unroll 8
+    for (int64_t r = rg; r < rows; r += 64) {
       const float2 e = part[r * C + c];
       s1 += e.x;
       s2 += e.y;
     }
   }
-  all[rg][threadIdx.x & 31] = make_float2(s1, s2);
-  __syncthreads();
-  if (rg == 0 && c < C) {
-    for (int i = 1; i < 8; ++i) {
-      s1 += all[i][threadIdx.x].x;
-      s2 += all[i][threadIdx.x].y;
+  all[rg][ch] = make_float2(s1, s2);
+  for (int half = 32; half > 0; half >>= 1) {
+    __syncthreads();
+    if (rg < half) {
+      all[rg][ch].x += all[rg + half][ch].x;
+      all[rg][ch].y += all[rg + half][ch].y;
     }
-    if (dbias) dbias[c] = s1;
-    if (dweight) dweight[c] = s2;
+  }
+  if (rg == 0 && c < C) {
+    if (dbias) dbias[c] = all[0][ch].x;
+    if (dweight) dweight[c] = all[0][ch].y;
   }
 }
 
@@ -591,9 +620,9 @@ Plan plan(const Args& p, bool f32, bool bwd, int cap = 8) {
   l.tile = cols < 256 ? cols : 256;
   l.tiles = (cols + l.tile - 1) / l.tile;
   l.rpb = 256 / l.tile;
-  // pieces: about 1024 blocks, and at least 16 rows for each thread of one
+  // pieces: about 1024 blocks, and at least 8 rows for each thread of one
   int64_t pieces = (1024 + p.batch * l.tiles - 1) / (p.batch * l.tiles);
-  const int64_t most = (p.rows + 16 * l.rpb - 1) / (16 * l.rpb);
+  const int64_t most = (p.rows + 8 * l.rpb - 1) / (8 * l.rpb);
   if (pieces > most) pieces = most;
   if (pieces < 1) pieces = 1;
   l.piece_rows = (p.rows + pieces - 1) / pieces;
@@ -737,7 +766,7 @@ hipError_t backward(const Args& p, bool f32, hipStream_t s) {
     rows = l.rows ? l.blocks : p.batch * l.pieces;
   }
   if (p.dweight || p.dbias) {
-    sum_channels_kernel<<<dim3((uint32_t)((p.C + 31) / 32)), 256, 0, s>>>((const float2*)p.ws, rows, p.C,
+    sum_channels_kernel<<<dim3((uint32_t)((p.C + 15) / 16)), 1024, 0, s>>>((const float2*)p.ws, rows, p.C,
                                                                           p.dweight, p.dbias);
     return hipGetLastError();
   }

@@ -185,14 +185,14 @@ struct Shape {
   static constexpr int bytes(int rows, int rest) { return 2 * (rows * kRows + rest * kRest) + (DG ? 1024 : 0); }
   // buffers of each, as the LDS allows
   static constexpr int NREST = !STATE && bytes(2, 2) <= kLds ? 2 : 1;
-  static constexpr int NROWS = !STATE && bytes(2, NREST) <= kLds ? 2 : 1;
+  static constexpr int NROWS = (STATE ? 2 : 1) * bytes(2, NREST) <= kLds ? 2 : 1;
   static constexpr int kBytes = bytes(NROWS, NREST);
   static constexpr bool kFits = kBytes <= kLds;
   // Waves of a group: eight for 64 columns, where a block has its CU to itself
   // and only more waves of its own hide its latencies.  WV of them lie along
   // the columns v; group B's others along the rows kappa, group A's along the
   // four token blocks.
-  static constexpr int NW = VB >= 64 && !STATE && !DG ? 8 : 4;
+  static constexpr int NW = (VB >= 64 && !STATE && !DG) || VB == 128 ? 8 : 4;
   static constexpr int WV = NW / 4;         // group A has a wave for every token block
   static constexpr int WK = NW / WV;
   static constexpr int NVW = VB / 16 / WV;  // column tiles of a wave
@@ -200,7 +200,7 @@ struct Shape {
   static constexpr int kGroup = 64 * NW;
   static constexpr int kThreads = STATE ? kGroup : 2 * kGroup;
   // waves per SIMD that the registers are shared out for: what the LDS lets in
-  static constexpr int kWaves = STATE ? (4 * kBytes <= kLds ? 4 : (2 * kBytes <= kLds ? 2 : 1))
+  static constexpr int kWaves = STATE ? ((NW == 8 ? 2 : 4) * kBytes <= kLds ? 4 : (2 * kBytes <= kLds ? 2 : 1))
                                       : (NW == 8 || 2 * kBytes <= kLds ? 4 : 2);
 };
 
