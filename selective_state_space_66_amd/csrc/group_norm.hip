@@ -370,16 +370,34 @@ __global__ __launch_bounds__(256) void merge_stats_kernel(const Args p, float* m
     const int64_t left = p.rows - piece * p.piece_rows;
     return (float)(left < p.piece_rows ? left : p.piece_rows);
   };
-  // about the first channel's mean, so that a common offset cancels exactly
+  // about the first channel's mean, so that a common offset cancels exactly;
+  // a thread's first kHeld entries stay in registers for the squares
+  constexpr int kHeld = 8;
   const float base = part[0].x;
+  float2 held[kHeld];
+  float cnt[kHeld];
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    const int64_t i = threadIdx.x + 256 * j;
+    const int64_t piece = i < m ? i / cg : 0;
+    held[j] = i < m ? part[piece * p.C + (i - piece * cg)] : make_float2(0.0f, 0.0f);
+    cnt[j] = i < m ? count(piece) : 0.0f;
+  }
   float s = 0.0f;
-  for (int64_t i = threadIdx.x; i < m; i += 256) {
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) s = cnt[j] != 0.0f ? fmaf(cnt[j], held[j].x - base, s) : s;
+  for (int64_t i = threadIdx.x + 256 * kHeld; i < m; i += 256) {
     const int64_t piece = i / cg;
     s = fmaf(count(piece), part[piece * p.C + (i - piece * cg)].x - base, s);
   }
   const float mean = base + block_sum(s, scratch) / total;
   float q = 0.0f;
-  for (int64_t i = threadIdx.x; i < m; i += 256) {
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    const float d = held[j].x - mean;
+    q = cnt[j] != 0.0f ? q + fmaf(cnt[j] * d, d, held[j].y) : q;
+  }
+  for (int64_t i = threadIdx.x + 256 * kHeld; i < m; i += 256) {
     const int64_t piece = i / cg;
     const float2 e = part[piece * p.C + (i - piece * cg)];
     const float d = e.x - mean;
@@ -487,6 +505,7 @@ __global__ __launch_bounds__(256) void merge_grads_kernel(const Args p, float2* 
   const float2* const part = (const float2*)p.ws + n * p.pieces * p.C + g * cg;
   const int64_t m = (int64_t)p.pieces * cg;
   float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll 8
   for (int64_t i = threadIdx.x; i < m; i += 256) {
     const int64_t piece = i / cg;
     const int c = (int)(i - piece * cg);

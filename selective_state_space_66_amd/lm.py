@@ -15,6 +15,7 @@ arguments; every step of the computation runs in the library's HIP kernels.
 """
 import ctypes
 import functools
+from array import array
 
 SSM_F32, SSM_BF16 = 0, 1
 _ACTS = {"none": 0, "silu": 1}
@@ -127,20 +128,33 @@ def _norm_ws(batch, rows, C, groups, backward, io):
                                                                        backward, io))
 
 
+@functools.lru_cache(maxsize=512)
+def _clip_ws(n):
+    return int(_core()[0].load_library().ssm_clip_grad_norm_workspace_size(n))
+
+
 def _linattn_check(c, torch, q, k, v, log_decay, h0, seq_lens, reset):
     index = _on_gpu(q, "q", 4, "(batch, L, kheads, dk)")
     _on_gpu(v, "v", 4, "(batch, L, nheads, dv)")
-    batch, L, Hk, Dk = q.shape
+    batch, L, Hk, Dk = qs = q.shape
     H, Dv = v.shape[2:]
     io, dev, f32 = q.dtype, q.device, torch.float32
     code = _code(c, torch, q)
-    _want(q, "q", (batch, L, Hk, Dk), io, dev, index)
-    _want(k, "k", (batch, L, Hk, Dk), io, dev, index)
-    _want(v, "v", (batch, L, H, Dv), io, dev, index)
-    _want(log_decay, "log_decay", (H,), f32, dev, index)
-    _want(h0, "h0", (batch, H, Dv, Dk), f32, dev, index)
-    _want(seq_lens, "seq_lens", (batch,), torch.int32, dev, index)
-    _want(reset, "reset", (batch, L), torch.uint8, dev, index)
+    if not (k.shape == qs and v.shape == (batch, L, H, Dv) and log_decay.shape == (H,)
+            and k.dtype is io and v.dtype is io and log_decay.dtype is f32
+            and k.get_device() == index and v.get_device() == index
+            and log_decay.get_device() == index and q.is_contiguous() and k.is_contiguous()
+            and v.is_contiguous() and log_decay.is_contiguous()):
+        c._check(q, "q", (batch, L, Hk, Dk), io, dev)
+        c._check(k, "k", (batch, L, Hk, Dk), io, dev)
+        c._check(v, "v", (batch, L, H, Dv), io, dev)
+        c._check(log_decay, "log_decay", (H,), f32, dev)
+    if h0 is not None:
+        _want(h0, "h0", (batch, H, Dv, Dk), f32, dev, index)
+    if seq_lens is not None:
+        _want(seq_lens, "seq_lens", (batch,), torch.int32, dev, index)
+    if reset is not None:
+        _want(reset, "reset", (batch, L), torch.uint8, dev, index)
     return batch, L, H, Hk, Dk, Dv, dev, index, code
 
 
@@ -229,19 +243,26 @@ def linattn_step(state, q, k, v, log_decay, scale=None, o=None):
     lib = c.load_library()
     index = _on_gpu(q, "q", 3, "(batch, kheads, dk)")
     _on_gpu(v, "v", 3, "(batch, nheads, dv)")
-    batch, Hk, Dk = q.shape
+    batch, Hk, Dk = qs = q.shape
     H, Dv = v.shape[1:]
-    io, dev = q.dtype, q.device
+    io, f32 = q.dtype, torch.float32
     code = _code(c, torch, q)
-    _want(state, "state", (batch, H, Dv, Dk), torch.float32, dev, index)
-    _want(q, "q", (batch, Hk, Dk), io, dev, index)
-    _want(k, "k", (batch, Hk, Dk), io, dev, index)
-    _want(v, "v", (batch, H, Dv), io, dev, index)
-    _want(log_decay, "log_decay", (H,), torch.float32, dev, index)
+    if not (k.shape == qs and v.shape == (batch, H, Dv) and state.shape == (batch, H, Dv, Dk)
+            and log_decay.shape == (H,) and k.dtype is io and v.dtype is io
+            and state.dtype is f32 and log_decay.dtype is f32 and k.get_device() == index
+            and v.get_device() == index and state.get_device() == index
+            and log_decay.get_device() == index and q.is_contiguous() and k.is_contiguous()
+            and v.is_contiguous() and state.is_contiguous() and log_decay.is_contiguous()):
+        dev = q.device
+        c._check(state, "state", (batch, H, Dv, Dk), f32, dev)
+        c._check(q, "q", (batch, Hk, Dk), io, dev)
+        c._check(k, "k", (batch, Hk, Dk), io, dev)
+        c._check(v, "v", (batch, H, Dv), io, dev)
+        c._check(log_decay, "log_decay", (H,), f32, dev)
     if o is None:
         o = torch.empty_like(v)
     else:
-        _want(o, "o", (batch, H, Dv), io, dev, index)
+        _want(o, "o", (batch, H, Dv), io, q.device, index)
     st = lib.ssm_linattn_step(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
                               Dk ** -0.5 if scale is None else scale, _ptr(o), batch, H, Hk, Dk,
                               Dv, code, _stream(torch, index))
@@ -266,9 +287,12 @@ def _group_norm_check(c, torch, x, groups, weight, bias, z, act):
     if groups < 1 or C < 1 or C % groups != 0:
         raise ValueError(f"groups: {groups} does not divide {C} channels")
     _want(x, "x", (batch, rows, C), io, dev, index)
-    _want(weight, "weight", (C,), torch.float32, dev, index)
-    _want(bias, "bias", (C,), torch.float32, dev, index)
-    _want(z, "z", (batch, rows, C), io, dev, index)
+    if weight is not None:
+        _want(weight, "weight", (C,), torch.float32, dev, index)
+    if bias is not None:
+        _want(bias, "bias", (C,), torch.float32, dev, index)
+    if z is not None:
+        _want(z, "z", (batch, rows, C), io, dev, index)
     return batch, rows, C, dev, index, code
 
 
@@ -350,31 +374,36 @@ def clip_grad_norm(grads, max_norm, outs=None, workspace=None):
     if not grads[0].is_cuda:
         raise ValueError("tensors must be on the GPU")
     dev, index = grads[0].device, grads[0].get_device()
-    codes = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
-    types = [codes.get(t.dtype) for t in grads]
-    # one pass over the list each; the loops that name a culprit run only if there is one
-    if None in types:
-        i = types.index(None)
-        raise TypeError(f"grads[{i}]: expected float32 or bfloat16, got {grads[i].dtype}")
-    for i, t in enumerate(grads):
-        if t.get_device() != index or not t.is_contiguous():
-            if t.device != dev:
-                raise ValueError(f"grads[{i}]: expected device {dev}, got {t.device}")
-            raise ValueError(f"grads[{i}]: must be contiguous")
-    if outs is not grads:
-        for i, (t, o) in enumerate(zip(grads, outs)):
-            if (o.shape != t.shape or o.dtype is not t.dtype or o.get_device() != index
-                    or not o.is_contiguous()):
-                raise ValueError(f"outs[{i}]: expected a contiguous {t.dtype} tensor of shape "
-                                 f"{tuple(t.shape)} on {dev}")
-    pointers, counts = ctypes.c_void_p * n, ctypes.c_int64 * n
-    src = pointers(*[t.data_ptr() for t in grads])
-    dst = src if outs is grads else pointers(*[o.data_ptr() for o in outs])
+    # whole lists at a time; the loops that name a culprit run only if there is one
+    tensor = torch.Tensor
+    types = [t.dtype for t in grads]
+    if not set(types) <= {torch.float32, torch.bfloat16}:
+        i = next(i for i, t in enumerate(types) if t not in (torch.float32, torch.bfloat16))
+        raise TypeError(f"grads[{i}]: expected float32 or bfloat16, got {types[i]}")
+    if set(map(tensor.get_device, grads)) != {index}:
+        i = next(i for i, t in enumerate(grads) if t.device != dev)
+        raise ValueError(f"grads[{i}]: expected device {dev}, got {grads[i].device}")
+    if not all(map(tensor.is_contiguous, grads)):
+        i = next(i for i, t in enumerate(grads) if not t.is_contiguous())
+        raise ValueError(f"grads[{i}]: must be contiguous")
+    if outs is not grads and not ([o.shape for o in outs] == [t.shape for t in grads]
+                                  and [o.dtype for o in outs] == types
+                                  and set(map(tensor.get_device, outs)) == {index}
+                                  and all(map(tensor.is_contiguous, outs))):
+        i = next(i for i, (t, o) in enumerate(zip(grads, outs))
+                 if o.shape != t.shape or o.dtype != t.dtype or o.device != dev
+                 or not o.is_contiguous())
+        raise ValueError(f"outs[{i}]: expected a contiguous {types[i]} tensor of shape "
+                         f"{tuple(grads[i].shape)} on {dev}")
+    src = array("Q", map(tensor.data_ptr, grads))
+    dst = src if outs is grads else array("Q", map(tensor.data_ptr, outs))
+    counts = array("q", map(tensor.numel, grads))
+    codes = array("i", [SSM_F32 if t is torch.float32 else SSM_BF16 for t in types])
     norm = torch.empty((), dtype=torch.float32, device=dev)
-    ws, size = _workspace(torch, workspace, int(lib.ssm_clip_grad_norm_workspace_size(n)), dev)
-    st = lib.ssm_clip_grad_norm(src, dst, counts(*[t.numel() for t in grads]),
-                                (ctypes.c_int32 * n)(*types), n, max_norm, _ptr(norm), _ptr(ws),
-                                size, _stream(torch, index))
+    ws, size = _workspace(torch, workspace, _clip_ws(n), dev)
+    st = lib.ssm_clip_grad_norm(src.buffer_info()[0], dst.buffer_info()[0],
+                                counts.buffer_info()[0], codes.buffer_info()[0], n, max_norm,
+                                _ptr(norm), _ptr(ws), size, _stream(torch, index))
     if st != 0:
         raise c.SsmError(st, "ssm_clip_grad_norm")
     return norm
