@@ -13,7 +13,9 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 int64_t chunks_of(int64_t L) { return (L + kChunk - 1) / kChunk; }
 
-int padded(int K) { return K <= 64 ? 64 : (K <= 128 ? 128 : 256); }
+// Row widths that a kernel is made for.  Only fp32 rows have one of 96, where
+// all of a chunk's work grows with the width.
+int padded(int K, bool f32) { return K <= 64 ? 64 : (f32 && K <= 96 ? 96 : (K <= 128 ? 128 : 256)); }
 
 // How a walk is laid out.
 //
@@ -36,7 +38,7 @@ struct Walk {
 };
 Walk plan(const Problem& p, int K, int V, bool dg) {
   Walk w;
-  const int KP = padded(K);
+  const int KP = padded(K, p.f32);
   const int64_t pairs = p.batch * p.H;
   const int64_t n64 = pairs * ((V + 63) / 64);
   w.tile.KP = w.state_tile.KP = KP;

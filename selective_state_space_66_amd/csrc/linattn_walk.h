@@ -137,13 +137,16 @@ __device__ __forceinline__ f32x4 mfma_parts(const bf16x8 (&a)[PA], const bf16x8 
 // b and the state sit in LDS in rows of KP bf16, 16-byte piece c of row r at
 // c ^ swz(r): 16-byte reads of one piece over rows r .. r + 15 and transposing
 // reads of 32 bytes from each of rows r .. r + 3 both spread over the banks.
+// Rows of 96 do the same as they stand, 52 banks apart.
+template <int KP>
+constexpr int kRow = KP == 96 ? 104 : KP;
 template <int KP>
 __device__ __forceinline__ constexpr int swz(int r) {
   return (((r << 1) & 6) | ((r >> 2) & 1)) ^ (((r >> 3) & 1) * (KP >= 128 ? 8 : 2));
 }
 template <int KP>
 __device__ __forceinline__ constexpr int sw(int r, int col) {
-  return (((col >> 3) ^ swz<KP>(r)) << 3) | (col & 7);
+  return KP == 96 ? col : (((col >> 3) ^ swz<KP>(r)) << 3) | (col & 7);
 }
 // c's rows of VB bf16 are only read by the transposing reads (32 bytes from
 // each of four rows at a time, over 64 banks of 4 bytes): where one row or two
@@ -183,12 +186,13 @@ struct Shape {
   // the fp32 form with 256-wide rows keeps two parts of T: three do not fit the LDS
   static constexpr int PT = (STATE || !DG) ? 0 : (NP == 3 && KP == 256 ? 2 : 3);
   static constexpr int PW = 3;                                    // parts of the weighted c
-  static constexpr int kB = NP * kQ * KP;                         // one buffer of b
+  static constexpr int KS = kRow<KP>;
+  static constexpr int kB = NP * kQ * KS;                         // one buffer of b
   static constexpr int kC = STATE ? 0 : NP * kQ * VB;             // one buffer of c
   static constexpr int kW = PW * kQ * VB;
   static constexpr int kW2 = DG ? kW : 0;
-  static constexpr int kS = PS * VB * KP;
-  static constexpr int kT = PT * VB * KP;
+  static constexpr int kS = PS * VB * KS;
+  static constexpr int kT = PT * VB * KS;
   static constexpr int kLds = 160 * 1024;                         // of a CU
   static constexpr int kRows = kB + kC;                           // one buffer of rows
   static constexpr int kRest = kW + kW2 + kS + kT;                // one of weighted c and state
@@ -199,14 +203,15 @@ struct Shape {
   static constexpr int kBytes = bytes(NROWS, NREST);
   static constexpr bool kFits = kBytes <= kLds;
   // Waves of a group: eight for 64 columns, where a block has its CU to itself
-  // and only more waves of its own hide its latencies.  WV of them lie along
-  // the columns v; group B's others along the rows kappa, group A's along the
-  // four token blocks.
+  // and only more waves of its own hide its latencies.  WVA or WVB of them lie
+  // along the columns v; group B's others along the rows kappa, group A's along
+  // the four token blocks.
   static constexpr int NW = (VB >= 64 && !STATE && !DG) || VB == 128 ? 8 : 4;
-  static constexpr int WV = NW / 4;         // group A has a wave for every token block
-  static constexpr int WK = NW / WV;
-  static constexpr int NVW = VB / 16 / WV;  // column tiles of a wave
-  static constexpr int JK = KP / 16 / WK;   // row tiles of the state of a group B wave
+  static constexpr int WVA = NW / 4;                // group A has a wave for every token block
+  static constexpr int WVB = KP == 96 ? 2 : WVA;    // and 96 rows are three tiles for each of two waves
+  static constexpr int NVA = VB / 16 / WVA;         // column tiles of a wave
+  static constexpr int NVB = VB / 16 / WVB;
+  static constexpr int JK = KP / 16 / (NW / WVB);   // row tiles of the state of a group B wave
   static constexpr int kGroup = 64 * NW;
   static constexpr int kThreads = STATE ? kGroup : 2 * kGroup;
   // waves per SIMD that the registers are shared out for: what the LDS lets in
@@ -234,11 +239,13 @@ void walk_kernel(const WalkArgs p) {
   constexpr int PRC = VB / EPP;                // pieces in a row of c
   constexpr int RB = kQ * PRB / Sh::kGroup;    // pieces of b per thread of group B
   constexpr int RC = kQ * PRC / Sh::kGroup;
+  constexpr int PB = KP == 96 ? 8 : PRB;       // pieces of a row of b that threads lie along
+  constexpr int RR = kQ * PB / Sh::kGroup;     // rows of b per thread
   constexpr int NK = KP / 32;                  // k-steps of a . b
-  constexpr int NVW = Sh::NVW;                 // column tiles of a wave
+  constexpr int KS = Sh::KS;
   constexpr int NROWS = Sh::NROWS, NREST = Sh::NREST;
-  static_assert(RB >= 1 && RC >= 1 && NVW >= 1 && Sh::JK >= 1, "tile too small");
-  static_assert(NP == 3 || NVW % 2 == 0, "bf16 outputs leave two tiles at a time");
+  static_assert(RB >= 1 && RC >= 1 && Sh::NVA >= 1 && Sh::NVB >= 1 && Sh::JK >= 1, "tile too small");
+  static_assert(NP == 3 || Sh::NVA % 2 == 0, "bf16 outputs leave two tiles at a time");
 
   __shared__ __align__(16) __bf16 lds[NROWS * Sh::kRows + NREST * Sh::kRest];
   // chunk i's rows (b, c) and the rest (c weighted for S, for T; parts of S, of T)
@@ -315,10 +322,11 @@ void walk_kernel(const WalkArgs p) {
 
   if (!STATE && group_a) {
     // ================================================== group A: the outputs
+    constexpr int NVW = Sh::NVA;
     constexpr int PP = NP == 3 ? 3 : 2;  // parts of the scores that lead to out
     constexpr int RA = NP == 1 ? NK : 2 * NK;
-    const int vw = 16 * NVW * (w % Sh::WV);                             // first column of the wave in the slice
-    const int blk = __builtin_amdgcn_readfirstlane(w / Sh::WV);         // its token block
+    const int vw = 16 * NVW * (w % Sh::WVA);                             // first column of the wave in the slice
+    const int blk = __builtin_amdgcn_readfirstlane(w / Sh::WVA);         // its token block
     const int t = 16 * blk + lr;                                        // this lane's token in a chunk
     const uint32_t rsa = (uint32_t)p.Ha * K * ES;
     const char* const pa = (const char*)p.a + (bL * p.Ha + h / (p.H / p.Ha)) * (int64_t)K * ES;
@@ -408,12 +416,12 @@ void walk_kernel(const WalkArgs p) {
         bf16x8 sF[NVW][Sh::PS > 0 ? Sh::PS : 1], tF[DG ? NVW : 1][Sh::PT > 0 ? Sh::PT : 1];
 #pragma unroll
         for (int vt = 0; vt < NVW; ++vt) {
-          const int at = (vw + 16 * vt + lr) * KP + sw<KP>(lr, kcol<NP>(k, lk));
+          const int at = (vw + 16 * vt + lr) * KS + sw<KP>(lr, kcol<NP>(k, lk));
 #pragma unroll
-          for (int e = 0; e < Sh::PS; ++e) sF[vt][e] = *(const bf16x8*)(Ss + e * VB * KP + at);
+          for (int e = 0; e < Sh::PS; ++e) sF[vt][e] = *(const bf16x8*)(Ss + e * VB * KS + at);
           if constexpr (DG) {
 #pragma unroll
-            for (int e = 0; e < Sh::PT; ++e) tF[vt][e] = *(const bf16x8*)(Ts + e * VB * KP + at);
+            for (int e = 0; e < Sh::PT; ++e) tF[vt][e] = *(const bf16x8*)(Ts + e * VB * KS + at);
           }
         }
 #pragma unroll
@@ -460,7 +468,7 @@ void walk_kernel(const WalkArgs p) {
           bf16x8 bF[NP];
 #pragma unroll
           for (int e = 0; e < NP; ++e)
-            bF[e] = *(const bf16x8*)(Bs + e * kQ * KP + (16 * sb + lr) * KP + sw<KP>(lr, kcol<NP>(k, lk)));
+            bF[e] = *(const bf16x8*)(Bs + e * kQ * KS + (16 * sb + lr) * KS + sw<KP>(lr, kcol<NP>(k, lk)));
           g[sb] = mfma_parts(bF, aF[k], g[sb]);
         }
       settle(g);
@@ -639,6 +647,7 @@ void walk_kernel(const WalkArgs p) {
     }
   } else {
     // ======================================= group B: b, c and the state
+    constexpr int NVW = Sh::NVB;
     const uint32_t rsb = (uint32_t)p.Hb * K * ES;
     const char* const pb = (const char*)p.b + (bL * p.Hb + h / (p.H / p.Hb)) * (int64_t)K * ES;
     const char* const pc = (const char*)p.c + ((bL * p.Hc + h / (p.H / p.Hc)) * (int64_t)V + v0) * ES;
@@ -646,7 +655,10 @@ void walk_kernel(const WalkArgs p) {
 
     u32x4 rB[RB], rC[RC];
     uint32_t rR = 0;
-    const int rowB = tid / PRB, pieceB = tid % PRB;
+    const int rowB = tid / PB, pieceB = tid % PB;
+    // piece j of this thread
+    auto b_row = [&](int j) { return rowB + (RR == RB ? j : j % RR) * (GT / PB); };
+    auto b_piece = [&](int j) { return RR == RB ? pieceB : pieceB + j / RR * PB; };
     const int rowC = tid / PRC, pieceC = tid % PRC;
     auto load_bc = [&](int c) {
       const int n = live_in(c);
@@ -655,7 +667,7 @@ void walk_kernel(const WalkArgs p) {
       const bool inb = pieceB * EPP < K, inc = v0 + pieceC * EPP < V;
 #pragma unroll
       for (int j = 0; j < RB; ++j)
-        rB[j] = load16(qb, inb ? (uint32_t)(rowB + j * (GT / PRB)) * rsb + pieceB * 16u : kOutside);
+        rB[j] = load16(qb, (RR == RB ? inb : b_piece(j) * EPP < K) ? (uint32_t)b_row(j) * rsb + b_piece(j) * 16u : kOutside);
 #pragma unroll
       for (int j = 0; j < RC; ++j)
         rC[j] = load16(qc, inc ? (uint32_t)(rowC + j * (GT / PRC)) * rsc + pieceC * 16u : kOutside);
@@ -720,8 +732,8 @@ void walk_kernel(const WalkArgs p) {
       cR = rR;
 #pragma unroll
       for (int j = 0; j < RB; ++j) {
-        const int row = rowB + j * (GT / PRB), col = pieceB * EPP;
-        __bf16* const d = Bs + row * KP + sw<KP>(row, col);
+        const int row = b_row(j), col = b_piece(j) * EPP;
+        __bf16* const d = Bs + row * KS + sw<KP>(row, col);
         if constexpr (NP == 1) {
           *(u32x4*)d = rB[j];
         } else {
@@ -729,7 +741,7 @@ void walk_kernel(const WalkArgs p) {
           split2<3>(__uint_as_float(rB[j][0]), __uint_as_float(rB[j][1]), p0);
           split2<3>(__uint_as_float(rB[j][2]), __uint_as_float(rB[j][3]), p1);
 #pragma unroll
-          for (int q = 0; q < 3; ++q) *(u32x2*)(d + q * kQ * KP) = u32x2{p0[q], p1[q]};
+          for (int q = 0; q < 3; ++q) *(u32x2*)(d + q * kQ * KS) = u32x2{p0[q], p1[q]};
         }
       }
       if constexpr (!STATE) {
@@ -753,7 +765,7 @@ void walk_kernel(const WalkArgs p) {
     // the state, fp32, in the matrix cores' result layout: lane value i of tile
     // (j, vt) is W[v = vw + 16 vt + lr][kappa = kw + 16 j + 4 lk + i]
     constexpr int JK = Sh::JK;
-    const int vw = 16 * NVW * (w % Sh::WV), kw = 16 * JK * (w / Sh::WV);
+    const int vw = 16 * NVW * (w % Sh::WVB), kw = 16 * JK * (w / Sh::WVB);
     f32x4 S[JK][NVW], D[DG ? JK : 1][DG ? NVW : 1];
 #pragma unroll
     for (int j = 0; j < JK; ++j)
@@ -777,20 +789,20 @@ void walk_kernel(const WalkArgs p) {
         for (int j = 0; j < JK; ++j)
 #pragma unroll
           for (int vt = 0; vt < NVW; ++vt) {
-            const int at = (vw + 16 * vt + lr) * KP + sw<KP>(lr, kw + 16 * j + 4 * lk);
+            const int at = (vw + 16 * vt + lr) * KS + sw<KP>(lr, kw + 16 * j + 4 * lk);
             {
               uint32_t p0[Sh::PS], p1[Sh::PS];
               split2<Sh::PS>(S[j][vt][0], S[j][vt][1], p0);
               split2<Sh::PS>(S[j][vt][2], S[j][vt][3], p1);
 #pragma unroll
-              for (int q = 0; q < Sh::PS; ++q) *(u32x2*)(Ss + q * VB * KP + at) = u32x2{p0[q], p1[q]};
+              for (int q = 0; q < Sh::PS; ++q) *(u32x2*)(Ss + q * VB * KS + at) = u32x2{p0[q], p1[q]};
             }
             if constexpr (DG) {
               uint32_t p0[Sh::PT], p1[Sh::PT];
               split2<Sh::PT>(D[j][vt][0], D[j][vt][1], p0);
               split2<Sh::PT>(D[j][vt][2], D[j][vt][3], p1);
 #pragma unroll
-              for (int q = 0; q < Sh::PT; ++q) *(u32x2*)(Ts + q * VB * KP + at) = u32x2{p0[q], p1[q]};
+              for (int q = 0; q < Sh::PT; ++q) *(u32x2*)(Ts + q * VB * KS + at) = u32x2{p0[q], p1[q]};
             }
           }
       }
@@ -827,8 +839,8 @@ void walk_kernel(const WalkArgs p) {
 #pragma unroll
           for (int e = 0; e < NP; ++e) {
             const int col = kw + 16 * j + 4 * qq;
-            bF[j][e] = join(tr_read(Bs + e * kQ * KP + ra * KP + sw<KP>(ra, col)),
-                            tr_read(Bs + e * kQ * KP + rb * KP + sw<KP>(rb, col)));
+            bF[j][e] = join(tr_read(Bs + e * kQ * KS + ra * KS + sw<KP>(ra, col)),
+                            tr_read(Bs + e * kQ * KS + rb * KS + sw<KP>(rb, col)));
           }
 #pragma unroll
         for (int vt = 0; vt < NVW; ++vt) {
