@@ -200,7 +200,10 @@ struct Shape {
   // buffers of each, as the LDS allows
   static constexpr int NREST = !STATE && bytes(2, 2) <= kLds ? 2 : 1;
   static constexpr int NROWS = (STATE ? 2 : 1) * bytes(2, NREST) <= kLds ? 2 : 1;
-  static constexpr int kBytes = bytes(NROWS, NREST);
+  // b's rows are only read up to the scores; with two of c's, group B writes the
+  // next chunk's while group A multiplies the scores with c
+  static constexpr int NC = NROWS == 2 ? 2 : (!STATE && bytes(1, 1) + 2 * kC <= kLds ? 2 : 1);
+  static constexpr int kBytes = bytes(NROWS, NREST) + 2 * (NC - NROWS) * kC;
   static constexpr bool kFits = kBytes <= kLds;
   // Waves of a group: eight for 64 columns, where a block has its CU to itself
   // and only more waves of its own hide its latencies.  WVA or WVB of them lie
@@ -243,15 +246,18 @@ void walk_kernel(const WalkArgs p) {
   constexpr int RR = kQ * PB / Sh::kGroup;     // rows of b per thread
   constexpr int NK = KP / 32;                  // k-steps of a . b
   constexpr int KS = Sh::KS;
-  constexpr int NROWS = Sh::NROWS, NREST = Sh::NREST;
+  constexpr int NROWS = Sh::NROWS, NC = Sh::NC, NREST = Sh::NREST;
   static_assert(RB >= 1 && RC >= 1 && Sh::NVA >= 1 && Sh::NVB >= 1 && Sh::JK >= 1, "tile too small");
   static_assert(NP == 3 || Sh::NVA % 2 == 0, "bf16 outputs leave two tiles at a time");
 
-  __shared__ __align__(16) __bf16 lds[NROWS * Sh::kRows + NREST * Sh::kRest];
-  // chunk i's rows (b, c) and the rest (c weighted for S, for T; parts of S, of T)
-  constexpr int kCs = Sh::kB, kCw2 = Sh::kW, kSs = kCw2 + Sh::kW2, kTs = kSs + Sh::kS;
-  auto rows_at = [&](int i) { return lds + (NROWS == 2 ? (i & 1) * Sh::kRows : 0); };
-  auto rest_at = [&](int i) { return lds + NROWS * Sh::kRows + (NREST == 2 ? (i & 1) * Sh::kRest : 0); };
+  __shared__ __align__(16) __bf16 lds[NROWS * Sh::kB + NC * Sh::kC + NREST * Sh::kRest];
+  // chunk i's rows of b, of c and the rest (c weighted for S, for T; parts of S, of T)
+  constexpr int kCw2 = Sh::kW, kSs = kCw2 + Sh::kW2, kTs = kSs + Sh::kS;
+  auto b_at = [&](int i) { return lds + (NROWS == 2 ? (i & 1) * Sh::kB : 0); };
+  auto c_at = [&](int i) { return lds + NROWS * Sh::kB + (NC == 2 ? (i & 1) * Sh::kC : 0); };
+  auto rest_at = [&](int i) {
+    return lds + NROWS * Sh::kB + NC * Sh::kC + (NREST == 2 ? (i & 1) * Sh::kRest : 0);
+  };
 
   // Consecutive block ids go round-robin to the 8 XCDs; each XCD gets a
   // contiguous run of (entry, head, span, slice), so the slices that read the
@@ -475,7 +481,7 @@ void walk_kernel(const WalkArgs p) {
       // Group B may write the rest.  Here the two halves of a chunk are alike in
       // both groups: staging and update beside state part and scores (f32, 128
       // keys: 63 us for 3 x 1537 x 12 heads; with the barrier before the scores 78).
-      if (NREST == 1 && NROWS == 2) lds_barrier();
+      if (NREST == 1 && NC == 2) lds_barrier();
 #pragma unroll
       for (int pair = REV ? W / 2 : 0; pair <= (REV ? 1 : W / 2); ++pair) {
         const int ra = 32 * pair + 4 * g4 + kk, rb = ra + 16;
@@ -554,7 +560,7 @@ void walk_kernel(const WalkArgs p) {
     lds_barrier();
     for (int i = first; i < last; ++i) {
       const int c = chunk_of(i), n = live_in(c);
-      const __bf16* const rows = rows_at(i);
+      const __bf16 *const Bs = b_at(i), *const Cs = c_at(i);
       const __bf16* const rest = rest_at(i);
       if constexpr (DG) {  // x of this lane's outputs
         const __amdgpu_buffer_rsrc_t r = rows_of(px, (int64_t)c * kQ, rsc, n, V - v0);
@@ -571,10 +577,10 @@ void walk_kernel(const WalkArgs p) {
         }
       }
       state_part(n, rest + kSs, rest + kTs);
-      if (blk == 0) chunk_part(std::integral_constant<int, 0>{}, rows, rows + kCs);
-      else if (blk == 1) chunk_part(std::integral_constant<int, 1>{}, rows, rows + kCs);
-      else if (blk == 2) chunk_part(std::integral_constant<int, 2>{}, rows, rows + kCs);
-      else chunk_part(std::integral_constant<int, 3>{}, rows, rows + kCs);
+      if (blk == 0) chunk_part(std::integral_constant<int, 0>{}, Bs, Cs);
+      else if (blk == 1) chunk_part(std::integral_constant<int, 1>{}, Bs, Cs);
+      else if (blk == 2) chunk_part(std::integral_constant<int, 2>{}, Bs, Cs);
+      else chunk_part(std::integral_constant<int, 3>{}, Bs, Cs);
       if constexpr (DG) {
 #pragma unroll
         for (int vt = 0; vt < NVW; ++vt)
@@ -585,7 +591,7 @@ void walk_kernel(const WalkArgs p) {
             dg = t < n ? fmaf(acc2[vt][e], x, dg) : dg;
           }
       }
-      if (NROWS == 1) lds_barrier();  // group B may write both
+      if (NC == 1) lds_barrier();  // group B may write everything
       // the next chunk's a, from loads a chunk old, and the loads after it
       // (before the stores, so that no wait for loads is one for stores)
       if (i + 1 < last) {
@@ -903,7 +909,7 @@ void walk_kernel(const WalkArgs p) {
     }
     int any_start = 0;
     if (first < last) {
-      stage_rows(rows_at(first), rows_at(first) + kCs);
+      stage_rows(b_at(first), c_at(first));
       if (first + 1 < last) load_bc(chunk_of(first + 1));
       __bf16* const rest = rest_at(first);
       stage_weighted(live_in(chunk_of(first)), rest, rest + kCw2);
@@ -915,12 +921,12 @@ void walk_kernel(const WalkArgs p) {
       __bf16* const next = rest_at(i + 1);
       const bool more = i + 1 < last;
       auto stage_next = [&]() {
-        stage_rows(rows_at(i + 1), rows_at(i + 1) + kCs);
+        stage_rows(b_at(i + 1), c_at(i + 1));
         if (i + 2 < last) load_bc(chunk_of(i + 2));  // a chunk ahead of its use
       };
       any_start |= starts != 0;
       if (NROWS == 2 && more) stage_next();
-      update(live_in(chunk_of(i)), rows_at(i), rest, rest + kCw2);
+      update(live_in(chunk_of(i)), b_at(i), rest, rest + kCw2);
       if (NREST == 1) lds_barrier();  // what update read may be written
       if (NROWS == 1 && more) stage_next();
       if (more) {
