@@ -363,18 +363,39 @@ __device__ __forceinline__ float block_sum(float v, float* scratch) {
   return scratch[0] + scratch[1] + scratch[2] + scratch[3];
 }
 
-// One block per (entry, group): the group's mean and rstd from the means and
-// squares of its channels' pieces.
-__global__ __launch_bounds__(256) void merge_stats_kernel(const Args p, float* mean_out, float* rstd_out) {
-  __shared__ float scratch[4];
+// What a merge takes of the partial sums: slice blockIdx.y of one group's pieces.
+struct Slice {
+  const float2* part;
+  int64_t piece0, rows, m;  // first piece, rows, entries (pieces x channels of the group)
+  int g, cg;
+};
+__device__ __forceinline__ Slice slice_of(const Args& p, int slice_pieces) {
+  Slice l;
   const int64_t n = blockIdx.x / (uint32_t)p.groups;
-  const int g = blockIdx.x % (uint32_t)p.groups;
-  const int cg = p.C / p.groups;
-  const float2* const part = (const float2*)p.ws + n * p.pieces * p.C + g * cg;
-  const int64_t m = (int64_t)p.pieces * cg;
-  const float total = (float)p.rows * (float)cg;
+  l.g = blockIdx.x % (uint32_t)p.groups;
+  l.cg = p.C / p.groups;
+  l.piece0 = (int64_t)blockIdx.y * slice_pieces;
+  const int64_t left = p.pieces - l.piece0, pieces = left < slice_pieces ? left : slice_pieces;
+  l.part = (const float2*)p.ws + (n * p.pieces + l.piece0) * p.C + l.g * l.cg;
+  l.m = pieces * l.cg;
+  const int64_t row0 = l.piece0 * p.piece_rows, row1 = row0 + pieces * p.piece_rows;
+  l.rows = (row1 < p.rows ? row1 : p.rows) - row0;
+  return l;
+}
+
+// One block per (entry, group) and slice: the mean and the squares about it from
+// the means and squares of the channels' pieces; the group's mean and rstd where
+// one slice is all, else the slice's moments for join_stats_kernel.
+__global__ __launch_bounds__(256) void merge_stats_kernel(const Args p, int slice_pieces, float4* moments,
+                                                          float* mean_out, float* rstd_out) {
+  __shared__ float scratch[4];
+  const Slice sl = slice_of(p, slice_pieces);
+  const int cg = sl.cg;
+  const float2* const part = sl.part;
+  const int64_t m = sl.m;
+  const float total = (float)sl.rows * (float)cg;
   auto count = [&](int64_t piece) {
-    const int64_t left = p.rows - piece * p.piece_rows;
+    const int64_t left = p.rows - (sl.piece0 + piece) * p.piece_rows;
     return (float)(left < p.piece_rows ? left : p.piece_rows);
   };
   // about the first channel's mean, so that a common offset cancels exactly;
@@ -410,12 +431,32 @@ __global__ __launch_bounds__(256) void merge_stats_kernel(const Args p, float* m
     const float d = e.x - mean;
     q += fmaf(count(piece) * d, d, e.y);
   }
-  const float var = block_sum(q, scratch) / total;
-  if (threadIdx.x == 0) {
-    const float rstd = 1.0f / sqrtf(var + p.eps);
+  q = block_sum(q, scratch);
+  if (threadIdx.x != 0) return;
+  if (gridDim.y > 1) {
+    moments[(int64_t)blockIdx.x * gridDim.y + blockIdx.y] = make_float4(total, mean, q, 0.0f);
+  } else {
     mean_out[blockIdx.x] = mean;
-    rstd_out[blockIdx.x] = rstd;
+    rstd_out[blockIdx.x] = 1.0f / sqrtf(q / total + p.eps);
   }
+}
+
+// One thread per (entry, group): its slices in order, about the first one's mean.
+__global__ __launch_bounds__(256) void join_stats_kernel(const float4* moments, int slices, int64_t n,
+                                                         float eps, float* mean_out, float* rstd_out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const float4* const e = moments + i * slices;
+  const float base = e[0].y;
+  float total = 0.0f, s = 0.0f, q = 0.0f;
+  for (int k = 0; k < slices; ++k) {
+    total += e[k].x;
+    s = fmaf(e[k].x, e[k].y - base, s);
+  }
+  const float mean = base + s / total;
+  for (int k = 0; k < slices; ++k) q += fmaf(e[k].x * (e[k].y - mean), e[k].y - mean, e[k].z);
+  mean_out[i] = mean;
+  rstd_out[i] = 1.0f / sqrtf(q / total + eps);
 }
 
 template <typename T, int VEC, bool SILU, bool GATE>
@@ -503,14 +544,14 @@ __global__ __launch_bounds__(256) void piece_grads_kernel(const Args p, int tile
   }
 }
 
-// One block per (entry, group): sum dn / M and sum(dn xh) / M.
-__global__ __launch_bounds__(256) void merge_grads_kernel(const Args p, float2* out) {
+// One block per (entry, group) and slice: sum dn / M and sum(dn xh) / M, M the
+// whole group's.
+__global__ __launch_bounds__(256) void merge_grads_kernel(const Args p, int slice_pieces, float2* out) {
   __shared__ float scratch[4];
-  const int64_t n = blockIdx.x / (uint32_t)p.groups;
-  const int g = blockIdx.x % (uint32_t)p.groups;
-  const int cg = p.C / p.groups;
-  const float2* const part = (const float2*)p.ws + n * p.pieces * p.C + g * cg;
-  const int64_t m = (int64_t)p.pieces * cg;
+  const Slice sl = slice_of(p, slice_pieces);
+  const int g = sl.g, cg = sl.cg;
+  const float2* const part = sl.part;
+  const int64_t m = sl.m;
   float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll 8
   for (int64_t i = threadIdx.x; i < m; i += 256) {
@@ -524,7 +565,19 @@ __global__ __launch_bounds__(256) void merge_grads_kernel(const Args p, float2* 
   const float inv = 1.0f / ((float)p.rows * (float)cg);
   s1 = block_sum(s1, scratch) * inv;
   s2 = block_sum(s2, scratch) * inv;
-  if (threadIdx.x == 0) out[blockIdx.x] = make_float2(s1, s2);
+  if (threadIdx.x == 0) out[(int64_t)blockIdx.x * gridDim.y + blockIdx.y] = make_float2(s1, s2);
+}
+
+__global__ __launch_bounds__(256) void join_grads_kernel(const float2* part, int slices, int64_t n, float2* out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float2 a = part[i * slices];
+  for (int k = 1; k < slices; ++k) {
+    const float2 e = part[i * slices + k];
+    a.x += e.x;
+    a.y += e.y;
+  }
+  out[i] = a;
 }
 
 template <typename T, int VEC, bool SILU, bool GATE>
@@ -605,6 +658,7 @@ struct Plan {
   int64_t blocks;       // one-row form: blocks down the entries
   int pieces;           // otherwise: pieces of an entry's rows
   int64_t piece_rows;
+  int slices, slice_pieces;  // of a group's pieces, merged apart and joined
 };
 
 // channels of the widest access (at most `cap`) that the pointers and a run of
@@ -657,6 +711,15 @@ Plan plan(const Args& p, bool f32, bool bwd, int cap = 8) {
   if (l.piece_rows < 1) l.piece_rows = 1;
   l.pieces = (int)((p.rows + l.piece_rows - 1) / l.piece_rows);
   if (l.pieces < 1) l.pieces = 1;
+  // Few wide groups leave their merge to a few blocks with much to read (32
+  // groups of 256 channels, 256 pieces: 184 us forwards in one slice, 52 in
+  // 16): about 4096 entries to a slice.  Below 8192 the second launch costs more.
+  const int64_t entries = (int64_t)l.pieces * cg;
+  int64_t slices = entries > 8192 ? (entries + 4095) / 4096 : 1;
+  if (slices > 32) slices = 32;
+  if (slices > l.pieces) slices = l.pieces;
+  l.slice_pieces = (int)((l.pieces + slices - 1) / slices);
+  l.slices = (int)((l.pieces + l.slice_pieces - 1) / l.slice_pieces);
   return l;
 }
 
@@ -699,7 +762,7 @@ hipError_t run_rows_lpg(const Args& p, const Plan& l, bool bwd, hipStream_t s) {
   }
 }
 
-// the parts of a workspace: partial sums, then the groups' two numbers
+// the parts of a workspace: partial sums, the groups' two numbers, the slices'
 size_t parts_bytes(const Args& p, const Plan& l, bool bwd) {
   if (l.rows) return bwd ? up256((size_t)l.blocks * p.C * 8) : 0;
   return up256((size_t)p.batch * l.pieces * p.C * 8);
@@ -711,24 +774,34 @@ hipError_t run_pieces(const Args& q, const Plan& l, bool bwd, hipStream_t s) {
   p.pieces = l.pieces;
   p.piece_rows = l.piece_rows;
   const dim3 grid((uint32_t)(p.batch * l.pieces), (uint32_t)l.tiles);
-  const dim3 groups((uint32_t)(p.batch * p.groups));
+  const int64_t ng = p.batch * p.groups;
+  const dim3 groups((uint32_t)ng, (uint32_t)l.slices), join((uint32_t)((ng + 255) / 256));
   const int threads = (l.tile * l.rpb + 63) / 64 * 64;
   char* const extra = (char*)p.ws + parts_bytes(p, l, bwd);
+  void* const slices = extra + up256((size_t)ng * 8);
   hipError_t e;
   if (!bwd) {
     piece_stats_kernel<T, VEC><<<grid, threads, 0, s>>>(p, l.tile, l.rpb);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     float* const mean = p.mean ? p.mean : (float*)extra;
     float* const rstd = p.rstd ? p.rstd : (float*)extra + (size_t)p.batch * p.groups;
-    merge_stats_kernel<<<groups, 256, 0, s>>>(p, mean, rstd);
+    merge_stats_kernel<<<groups, 256, 0, s>>>(p, l.slice_pieces, (float4*)slices, mean, rstd);
     if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (l.slices > 1) {
+      join_stats_kernel<<<join, 256, 0, s>>>((const float4*)slices, l.slices, ng, p.eps, mean, rstd);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     apply_fwd_kernel<T, VEC, SILU, GATE><<<grid, threads, 0, s>>>(p, mean, rstd, l.tile, l.rpb);
     return hipGetLastError();
   }
   piece_grads_kernel<T, VEC, SILU, GATE><<<grid, threads, 0, s>>>(p, l.tile, l.rpb);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  merge_grads_kernel<<<groups, 256, 0, s>>>(p, (float2*)extra);
+  merge_grads_kernel<<<groups, 256, 0, s>>>(p, l.slice_pieces, (float2*)(l.slices > 1 ? slices : extra));
   if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (l.slices > 1) {
+    join_grads_kernel<<<join, 256, 0, s>>>((const float2*)slices, l.slices, ng, (float2*)extra);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   apply_bwd_kernel<T, VEC, SILU, GATE><<<grid, threads, 0, s>>>(p, (const float2*)extra, l.tile, l.rpb);
   return hipGetLastError();
 }
@@ -751,7 +824,10 @@ hipError_t run(const Args& p, const Plan& l, bool bwd, hipStream_t s) {
 }
 
 size_t total_bytes(const Args& p, const Plan& l, bool bwd) {
-  return parts_bytes(p, l, bwd) + (l.rows ? 0 : up256((size_t)p.batch * p.groups * 8));
+  return parts_bytes(p, l, bwd) + (l.rows ? 0
+                                               : up256((size_t)p.batch * p.groups * 8) +
+                                                     (l.slices > 1 ? up256((size_t)p.batch * p.groups * l.slices * 16)
+                                                                   : 0));
 }
 
 }  // namespace

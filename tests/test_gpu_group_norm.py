@@ -133,6 +133,13 @@ def test_many_entries_and_wide():
     check(14, 2, 5, 6000, 2, torch.float32, act="silu")
 
 
+@pytest.mark.parametrize("io", IOS)
+def test_few_wide_groups(io):
+    """Groups whose pieces are merged in slices and joined."""
+    check(15, 1, 900, 2048, 8, io, act="silu", gate=True)
+    check(16, 2, 1201, 1028, 2, io, act="silu", offset=30.0 if io == torch.float32 else 0.0)
+
+
 def test_constant_values():
     """Nothing varies: the variance is zero, y is the bias and dx finite."""
     x = torch.full((4, 3, 32), 2.5, device=DEV)
