@@ -884,27 +884,48 @@ void walk_kernel(const WalkArgs p) {
           for (int i = 0; i < 4; ++i) S[j][vt][i] = s0[v * p.state_sv + (k + i) * p.state_sk];
         });
       }
-      // the states that the pieces of the walk before this span add, in order
-      for (int m = 0; m < i0 / p.piece_chunks; ++m) {
-        const float* loc = p.ws + ((int64_t)m * p.batch * p.H + bh) * (DG ? 2 : 1) * state_elems;
-        // real tokens of the piece
-        const int m0 = m * p.piece_chunks, m1 = m0 + p.piece_chunks - 1;
-        const int64_t ca = chunk_of(REV ? m1 : m0), cb = chunk_of(REV ? m0 : m1) + 1;
-        const int64_t hi = cb * kQ < len ? cb * kQ : len;
-        const int64_t n = hi > ca * kQ ? hi - ca * kQ : 0;
-        const bool cut = p.piece_cut[(int64_t)m * p.batch + b] != 0;
-        const float d = n == 0 ? 1.0f : exp2_hw(g2 * (float)n);
-        for_state([&](int j, int vt, int v, int k) {
-          const f32x4 av = *(const f32x4*)(loc + (int64_t)v * K + k);
-          if constexpr (DG) {
-            const f32x4 tv = *(const f32x4*)(loc + state_elems + (int64_t)v * K + k);
+      // the states that the pieces of the walk before this span add, in order; U
+      // of them loaded at once (one at a time, each costs a trip to memory: 412 us
+      // against 351 for 2 x 14447 tokens of 2 heads, 128 x 80, with all gradients)
+      constexpr int U = JK * NVW * (DG ? 2 : 1) <= 4 ? 4 : 2;
+      const int np = i0 / p.piece_chunks;
+      for (int m = 0; m < np; m += U) {
+        f32x4 av[U][JK][NVW], tv[U][DG ? JK : 1][DG ? NVW : 1];
+        int cut[U];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              D[j][vt][i] = cut ? tv[i] : d * (D[j][vt][i] + (float)n * S[j][vt][i]) + tv[i];
-          }
+        for (int u = 0; u < U; ++u) {
+          const int mu = m + u < np ? m + u : np - 1;
+          const float* loc = p.ws + ((int64_t)mu * p.batch * p.H + bh) * (DG ? 2 : 1) * state_elems;
+          cut[u] = p.piece_cut[(int64_t)mu * p.batch + b];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) S[j][vt][i] = cut ? av[i] : d * S[j][vt][i] + av[i];
-        });
+          for (int j = 0; j < JK; ++j)
+#pragma unroll
+            for (int vt = 0; vt < NVW; ++vt) {
+              const int v = v0 + vw + 16 * vt + lr, k = kw + 16 * j + 4 * lk;
+              const int64_t at = v < V && k < K ? (int64_t)v * K + k : 0;  // the rest is not used
+              av[u][j][vt] = *(const f32x4*)(loc + at);
+              if constexpr (DG) tv[u][j][vt] = *(const f32x4*)(loc + state_elems + at);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (m + u >= np) break;
+          // real tokens of the piece
+          const int m0 = (m + u) * p.piece_chunks, m1 = m0 + p.piece_chunks - 1;
+          const int64_t ca = chunk_of(REV ? m1 : m0), cb = chunk_of(REV ? m0 : m1) + 1;
+          const int64_t hi = cb * kQ < len ? cb * kQ : len;
+          const int64_t n = hi > ca * kQ ? hi - ca * kQ : 0;
+          const float d = n == 0 ? 1.0f : exp2_hw(g2 * (float)n);
+          for_state([&](int j, int vt, int, int) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (DG)
+                D[j][vt][i] = cut[u] ? tv[u][j][vt][i]
+                                     : d * (D[j][vt][i] + (float)n * S[j][vt][i]) + tv[u][j][vt][i];
+              S[j][vt][i] = cut[u] ? av[u][j][vt][i] : d * S[j][vt][i] + av[u][j][vt][i];
+            }
+          });
+        }
       }
     }
     int any_start = 0;
