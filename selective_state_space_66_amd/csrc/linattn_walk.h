@@ -62,7 +62,7 @@
 // the log-decay's gradient 233 to 255 us at the same size (19% of the matrix
 // cycles, 38% of the vector ones and 45% of the LDS's are used; without group
 // A's products 180, without B's 237, without both 97), fp32 rows of 72 and 96
-// with 3 x 1537 tokens of 12 heads 60.
+// with 3 x 1537 tokens of 12 heads 52.
 #pragma once
 
 #include "linattn_launch.h"
