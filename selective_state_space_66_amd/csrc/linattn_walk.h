@@ -657,7 +657,10 @@ void walk_kernel(const WalkArgs p) {
     const uint32_t rsb = (uint32_t)p.Hb * K * ES;
     const char* const pb = (const char*)p.b + (bL * p.Hb + h / (p.H / p.Hb)) * (int64_t)K * ES;
     const char* const pc = (const char*)p.c + ((bL * p.Hc + h / (p.H / p.Hc)) * (int64_t)V + v0) * ES;
-    const float lam64 = power(g2, kQ);
+    // lam^64 in two parts: its error, also that of rounding it to fp32, would
+    // come in once per chunk, and 100 chunks of a slow decay made 1e-6 of it
+    const double lam64d = exp(64.0 * (double)p.log_decay[h]);
+    const float lam64 = (float)lam64d, lam64_lo = lam64 > 0.0f ? (float)(lam64d - (double)lam64) : 0.0f;
 
     u32x4 rB[RB], rC[RC];
     uint32_t rR = 0;
@@ -816,7 +819,7 @@ void walk_kernel(const WalkArgs p) {
     // the state at the walk's end of the staged chunk
     auto update = [&](int n, const __bf16* Bs, const __bf16* Cw, const __bf16* Cw2) {
       const bool cut = starts != 0;
-      const float d = n == kQ ? lam64 : power(g2, n);
+      const float d = n == kQ ? lam64 : power(g2, n), dl = n == kQ ? lam64_lo : 0.0f;
       const float nf = (float)n;
 #pragma unroll
       for (int j = 0; j < JK; ++j)
@@ -824,8 +827,11 @@ void walk_kernel(const WalkArgs p) {
         for (int vt = 0; vt < NVW; ++vt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if constexpr (DG) D[j][vt][i] = d * (D[j][vt][i] + nf * S[j][vt][i]);
-            S[j][vt][i] *= d;
+            if constexpr (DG) {
+              const float t = D[j][vt][i] + nf * S[j][vt][i];
+              D[j][vt][i] = fmaf(t, d, t * dl);
+            }
+            S[j][vt][i] = fmaf(S[j][vt][i], d, S[j][vt][i] * dl);
           }
       if (cut) {
 #pragma unroll
