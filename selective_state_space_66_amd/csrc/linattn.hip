@@ -71,7 +71,7 @@ Walk plan(const Problem& p, int K, int V, bool dg) {
   w.pieces = (int)((w.nspan - 1) * split);
   w.state_bytes = up256((size_t)w.pieces * pairs * (dg ? 2 : 1) * (size_t)K * V * 4);
   w.cut_bytes = up256((size_t)w.pieces * p.batch * 4);
-  w.part_bytes = dg ? up256((size_t)pairs * w.nsl * w.nspan * 4) : 0;
+  w.part_bytes = dg ? up256((size_t)pairs * w.nsl * w.nspan * 8) : 0;
   return w;
 }
 
@@ -162,10 +162,10 @@ hipError_t sum_heads(const Problem& p, const float* part, void* out, hipStream_t
 
 // the gradient of each head's log-decay: its blocks' sums, in a fixed order, in
 // fp64 (a few hundred numbers: 5 us, of which a launch is 4)
-__global__ __launch_bounds__(64) void sum_parts_kernel(const float* part, float* out, int64_t n) {
-  const float* src = part + (int64_t)blockIdx.x * n;
+__global__ __launch_bounds__(64) void sum_parts_kernel(const double* part, float* out, int64_t n) {
+  const double* src = part + (int64_t)blockIdx.x * n;
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += 64) s += (double)src[i];
+  for (int64_t i = threadIdx.x; i < n; i += 64) s += src[i];
   __shared__ double all[64];
   all[threadIdx.x] = s;
   __syncthreads();
@@ -201,7 +201,7 @@ hipError_t backward(const Problem& p, const BwdArgs& g, void* workspace, hipStre
   const bool dg = g.dlog_decay != nullptr;
   const BwdLayout l = bwd_layout(p, dg);
   char* const ws = (char*)workspace;
-  float* const parts = (float*)(ws + l.states + l.cuts);
+  double* const parts = (double*)(ws + l.states + l.cuts);
   float* const shared = (float*)(ws + l.states + l.cuts + l.parts);
   const WalkArgs common = walk_args(p, ws, l.states);
   hipError_t e;

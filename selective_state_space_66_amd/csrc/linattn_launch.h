@@ -26,7 +26,7 @@ struct WalkArgs {
   const int32_t* seq_lens;   // nullable (batch)
   const uint8_t* reset;      // nullable (batch, L)
   const float* dlast;        // nullable: the gradient of g's last term, (batch, H, K, V)
-  float* dg_part;            // (H, batch * slices * spans)
+  double* dg_part;           // (H, batch * slices * spans)
   int64_t batch, L;
   int H, Ha, Hb, Hc, K, V;
   int64_t state_sv, state_sk;

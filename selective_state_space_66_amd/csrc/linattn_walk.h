@@ -324,7 +324,8 @@ void walk_kernel(const WalkArgs p) {
     return __builtin_amdgcn_raw_buffer_load_b8(r, lane, 0, 0);
   };
 
-  float dg = 0.0f;
+  float dg = 0.0f;       // of one chunk
+  double dg_sum = 0.0;   // its sums cancel over the chunks, so they are held in 64 bits
 
   if (!STATE && group_a) {
     // ================================================== group A: the outputs
@@ -590,6 +591,8 @@ void walk_kernel(const WalkArgs p) {
                                     : __uint_as_float(rX[vt][e]);
             dg = t < n ? fmaf(acc2[vt][e], x, dg) : dg;
           }
+        dg_sum += (double)dg;
+        dg = 0.0f;
       }
       if (NC == 1) lds_barrier();  // group B may write everything
       // the next chunk's a, from loads a chunk old, and the loads after it
@@ -990,13 +993,14 @@ void walk_kernel(const WalkArgs p) {
 
   if constexpr (DG && !STATE) {
     // the block's sum, in a fixed order
-    __shared__ float sums[16];
+    __shared__ double sums[2 * Sh::NW];
+    dg_sum += (double)dg;  // <dlast, T>
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) dg += __shfl_xor(dg, m);
-    if (lane == 0) sums[threadIdx.x >> 6] = dg;
+    for (int m = 32; m > 0; m >>= 1) dg_sum += __shfl_xor(dg_sum, m);
+    if (lane == 0) sums[threadIdx.x >> 6] = dg_sum;
     __syncthreads();
     if (threadIdx.x == 0) {
-      float s = 0.0f;
+      double s = 0.0;
 #pragma unroll
       for (int i = 0; i < 2 * Sh::NW; ++i) s += sums[i];
       p.dg_part[(int64_t)h * p.batch * p.nsl * p.nspan + ((int64_t)b * p.nsl + sl) * p.nspan + span] = s;
