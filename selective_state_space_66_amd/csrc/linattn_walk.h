@@ -35,12 +35,13 @@
 // parts whose sizes matter (hi hi; hi mid, mid hi; hi lo, mid mid, lo hi).
 // fp32 tensors travel as three parts.  With bf16 tensors the weighted c of
 // the state update has three parts, so the state (an fp32 output) is exact to
-// fp32 rounding.  Where they lead to a bf16 output, the scores have two parts
-// and the state that multiplies a_t one: its rounding adds in quadrature to
-// the output's own (2.3e-3 relative RMS where the state is all there is,
-// against 1.7e-3), and a second part costs the LDS traffic of the longest
-// step twice.  Where they lead to g's gradient, an fp32 sum, both have three.
-// Everything is accumulated in fp32.
+// fp32 rounding.  Where they lead to a bf16 output, the scores and the state
+// that multiplies a_t have two parts: 2^-18 of a value is left out, and the
+// output's error is that of its one rounding to four digits (8 x 2048 tokens of
+// 24 heads, 128 keys, 64 values: 1.6586e-3 relative RMS, as the exact result's
+// rounding; with one part of the state 2.2859e-3 and 75 us for 82, with three
+// parts of both 96 us).  Where they lead to g's gradient, an fp32 sum, both have
+// three.  Everything is accumulated in fp32.
 //
 // Work split.  A block owns one entry, head, span of the tokens and VB columns
 // of c.  A chunk's steps form a chain (state, outputs, next state), and with
@@ -182,7 +183,7 @@ struct Io<3> { typedef float T; };
 
 template <int NP, int KP, int VB, bool DG, bool STATE>
 struct Shape {
-  static constexpr int PS = STATE ? 0 : (NP == 3 || DG ? 3 : 1);  // parts of the state
+  static constexpr int PS = STATE ? 0 : (NP == 3 || DG ? 3 : 2);  // parts of the state
   // the fp32 form with 256-wide rows keeps two parts of T: three do not fit the LDS
   static constexpr int PT = (STATE || !DG) ? 0 : (NP == 3 && KP == 256 ? 2 : 3);
   static constexpr int PW = 3;                                    // parts of the weighted c
@@ -197,8 +198,11 @@ struct Shape {
   static constexpr int kRows = kB + kC;                           // one buffer of rows
   static constexpr int kRest = kW + kW2 + kS + kT;                // one of weighted c and state
   static constexpr int bytes(int rows, int rest) { return 2 * (rows * kRows + rest * kRest) + (DG ? 1024 : 0); }
-  // buffers of each, as the LDS allows
-  static constexpr int NREST = !STATE && bytes(2, 2) <= kLds ? 2 : 1;
+  // buffers of each, as the LDS allows.  Where one of the weighted c and the state
+  // lets two blocks into a CU, that is worth more than a second buffer (bf16, 32
+  // columns; 8 x 2048 x 24 heads of 128 x 128: 150 to 157 us against 169).
+  static constexpr int kRestLds = NP == 1 && !DG && VB == 32 && 2 * bytes(2, 1) <= kLds ? kLds / 2 : kLds;
+  static constexpr int NREST = !STATE && bytes(2, 2) <= kRestLds ? 2 : 1;
   static constexpr int NROWS = (STATE ? 2 : 1) * bytes(2, NREST) <= kLds ? 2 : 1;
   // b's rows are only read up to the scores; with two of c's, group B writes the
   // next chunk's while group A multiplies the scores with c

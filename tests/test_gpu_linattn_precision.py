@@ -1,0 +1,50 @@
+"""bf16 outputs of linear attention carry one rounding to bf16 and nothing else that shows.
+
+Bound.  Let x be the exact output and e the error before the last rounding.  The distance from
+a number to the nearest bf16 one changes by no more than the number does, so the result is off
+by at most |rounding of x| + 2 |e|, in RMS too.  e: two operands on the way to an output (the
+scores, the state) are held in two bf16 parts, 2^-18 of each value left out, and the fp32 sums
+add 6e-6 (a hundred roundings): 2 * 2^-18 + 6e-6 = 1.4e-5 of the output's RMS, twice that 2.8e-5.
+"""
+import numpy as np
+import pytest
+import torch
+
+import linattn_ref as R
+import selective_state_space_66_amd as ssm
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def dev(x, bf16=False):
+    t = torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+    return t.to(torch.bfloat16) if bf16 else t
+
+
+def rms(x):
+    return float(np.sqrt((x * x).mean()))
+
+
+# heads of each tile of the bf16 walks: rows of 64, 128 and 256, slices of 32 and 64 columns
+@pytest.mark.parametrize("H,Hk,Dk,Dv", [(2, 2, 64, 64), (2, 2, 128, 64), (2, 1, 64, 128), (3, 1, 32, 32),
+                                        (2, 2, 128, 32), (1, 1, 256, 64), (1, 1, 64, 256)])
+def test_one_rounding(H, Hk, Dk, Dv):
+    x = R.inputs(700 + Dk + Dv, 1, 150, H, Hk, Dk, Dv, "bf16")
+    print(f"[linattn] precision H{H}/{Hk} D{Dk}x{Dv}", flush=True)
+    q, k, v, do = (dev(x[n], True) for n in ("q", "k", "v", "do"))
+    g, h0, dlast = dev(x["g"]), dev(x["h0"]), dev(x["dlast"])
+    got = ssm.linattn_bwd(q, k, v, g, do, scale=0.25, h0=h0, dlast=dlast)
+    got["o"] = ssm.linattn_fwd(q, k, v, g, scale=0.25, h0=h0)[0]
+    plain = ssm.linattn_bwd(q, k, v, g, do, scale=0.25, h0=h0, dlast=dlast, need_dlog_decay=False)
+    torch.cuda.synchronize()
+    x = {n: a.astype(np.float64) for n, a in x.items()}
+    want = R.backward(x["q"], x["k"], x["v"], x["g"], x["do"], 0.25, x["h0"], x["dlast"])
+    want["o"] = R.forward(x["q"], x["k"], x["v"], x["g"], 0.25, x["h0"])[0]
+    for n in ("o", "dq", "dk", "dv"):
+        ref = want[n]
+        once = rms(torch.from_numpy(ref).to(torch.bfloat16).double().numpy() - ref)
+        results = [got[n]] + ([plain[n]] if n != "o" else [])
+        for y in results:
+            err = rms(y.double().cpu().numpy() - ref)
+            assert err <= once + 2.8e-5 * rms(ref), (n, err / rms(ref), once / rms(ref))
