@@ -53,7 +53,9 @@
 // earlier, into the other of two buffers: one barrier per chunk.  Where the LDS
 // does not hold two of everything, the rows of b and c have two and the
 // weighted c and the state one, written after a second barrier behind their
-// readers; or everything has one.
+// readers; or everything has one.  fp32 rows of 256 with the log-decay's
+// gradient fill the LDS even so: there c lies where T's last part was, brought
+// in between two barriers of its own once group A has read T.
 // Chunks of 64 tokens: the starts of documents fit one ballot.
 //
 // What bounds it.  About 60 flops per byte of bf16 rows: at the rates of a
@@ -184,12 +186,13 @@ struct Io<3> { typedef float T; };
 template <int NP, int KP, int VB, bool DG, bool STATE>
 struct Shape {
   static constexpr int PS = STATE ? 0 : (NP == 3 || DG ? 3 : 2);  // parts of the state
-  // the fp32 form with 256-wide rows keeps two parts of T: three do not fit the LDS
-  static constexpr int PT = (STATE || !DG) ? 0 : (NP == 3 && KP == 256 ? 2 : 3);
+  static constexpr int PT = (STATE || !DG) ? 0 : 3;
   static constexpr int PW = 3;                                    // parts of the weighted c
   static constexpr int KS = kRow<KP>;
   static constexpr int kB = NP * kQ * KS;                         // one buffer of b
-  static constexpr int kC = STATE ? 0 : NP * kQ * VB;             // one buffer of c
+  // c in the place of T's last part: with one of its own this shape takes 162 KB
+  static constexpr bool kShared = NP == 3 && KP == 256 && DG && !STATE;
+  static constexpr int kC = STATE || kShared ? 0 : NP * kQ * VB;  // one buffer of c
   static constexpr int kW = PW * kQ * VB;
   static constexpr int kW2 = DG ? kW : 0;
   static constexpr int kS = PS * VB * KS;
@@ -206,9 +209,10 @@ struct Shape {
   static constexpr int NROWS = (STATE ? 2 : 1) * bytes(2, NREST) <= kLds ? 2 : 1;
   // b's rows are only read up to the scores; with two of c's, group B writes the
   // next chunk's while group A multiplies the scores with c
-  static constexpr int NC = NROWS == 2 ? 2 : (!STATE && bytes(1, 1) + 2 * kC <= kLds ? 2 : 1);
+  static constexpr int NC = NROWS == 2 ? 2 : (!STATE && !kShared && bytes(1, 1) + 2 * kC <= kLds ? 2 : 1);
   static constexpr int kBytes = bytes(NROWS, NREST) + 2 * (NC - NROWS) * kC;
   static constexpr bool kFits = kBytes <= kLds;
+  static_assert(!kShared || (NREST == 1 && NROWS == 1 && NP * kQ * VB <= VB * KS), "c in T's last part");
   // Waves of a group: eight for 64 columns, where a block has its CU to itself
   // and only more waves of its own hide its latencies.  WVA or WVB of them lie
   // along the columns v; group B's others along the rows kappa, group A's along
@@ -258,7 +262,9 @@ void walk_kernel(const WalkArgs p) {
   // chunk i's rows of b, of c and the rest (c weighted for S, for T; parts of S, of T)
   constexpr int kCw2 = Sh::kW, kSs = kCw2 + Sh::kW2, kTs = kSs + Sh::kS;
   auto b_at = [&](int i) { return lds + (NROWS == 2 ? (i & 1) * Sh::kB : 0); };
-  auto c_at = [&](int i) { return lds + NROWS * Sh::kB + (NC == 2 ? (i & 1) * Sh::kC : 0); };
+  auto c_at = [&](int i) {
+    return lds + NROWS * Sh::kB + (Sh::kShared ? kTs + (Sh::PT - 1) * VB * KS : NC == 2 ? (i & 1) * Sh::kC : 0);
+  };
   auto rest_at = [&](int i) {
     return lds + NROWS * Sh::kB + NC * Sh::kC + (NREST == 2 ? (i & 1) * Sh::kRest : 0);
   };
@@ -486,7 +492,7 @@ void walk_kernel(const WalkArgs p) {
       // Group B may write the rest.  Here the two halves of a chunk are alike in
       // both groups: staging and update beside state part and scores (f32, 128
       // keys: 63 us for 3 x 1537 x 12 heads; with the barrier before the scores 78).
-      if (NREST == 1 && NC == 2) lds_barrier();
+      if ((NREST == 1 && NC == 2) || Sh::kShared) lds_barrier();
 #pragma unroll
       for (int pair = REV ? W / 2 : 0; pair <= (REV ? 1 : W / 2); ++pair) {
         const int ra = 32 * pair + 4 * g4 + kk, rb = ra + 16;
@@ -582,6 +588,7 @@ void walk_kernel(const WalkArgs p) {
         }
       }
       state_part(n, rest + kSs, rest + kTs);
+      if (Sh::kShared) lds_barrier();  // group B may write c over T's last part
       if (blk == 0) chunk_part(std::integral_constant<int, 0>{}, Bs, Cs);
       else if (blk == 1) chunk_part(std::integral_constant<int, 1>{}, Bs, Cs);
       else if (blk == 2) chunk_part(std::integral_constant<int, 2>{}, Bs, Cs);
@@ -742,25 +749,30 @@ void walk_kernel(const WalkArgs p) {
         }
       }
     };
-    auto stage_rows = [&](__bf16* Bs, __bf16* Cs) {
+    // rows of the loaded chunk: b's and c's, or c's alone, late (kShared)
+    constexpr std::true_type kLate{};
+    constexpr std::false_type kOnTime{};
+    auto stage_rows = [&](__bf16* Bs, __bf16* Cs, auto late) {
+      if constexpr (!late) {
 #pragma unroll
-      for (int j = 0; j < RC; ++j) cC[j] = rC[j];
-      cR = rR;
+        for (int j = 0; j < RC; ++j) cC[j] = rC[j];
+        cR = rR;
 #pragma unroll
-      for (int j = 0; j < RB; ++j) {
-        const int row = b_row(j), col = b_piece(j) * EPP;
-        __bf16* const d = Bs + row * KS + sw<KP>(row, col);
-        if constexpr (NP == 1) {
-          *(u32x4*)d = rB[j];
-        } else {
-          uint32_t p0[3], p1[3];
-          split2<3>(__uint_as_float(rB[j][0]), __uint_as_float(rB[j][1]), p0);
-          split2<3>(__uint_as_float(rB[j][2]), __uint_as_float(rB[j][3]), p1);
+        for (int j = 0; j < RB; ++j) {
+          const int row = b_row(j), col = b_piece(j) * EPP;
+          __bf16* const d = Bs + row * KS + sw<KP>(row, col);
+          if constexpr (NP == 1) {
+            *(u32x4*)d = rB[j];
+          } else {
+            uint32_t p0[3], p1[3];
+            split2<3>(__uint_as_float(rB[j][0]), __uint_as_float(rB[j][1]), p0);
+            split2<3>(__uint_as_float(rB[j][2]), __uint_as_float(rB[j][3]), p1);
 #pragma unroll
-          for (int q = 0; q < 3; ++q) *(u32x2*)(d + q * kQ * KS) = u32x2{p0[q], p1[q]};
+            for (int q = 0; q < 3; ++q) *(u32x2*)(d + q * kQ * KS) = u32x2{p0[q], p1[q]};
+          }
         }
       }
-      if constexpr (!STATE) {
+      if constexpr (!STATE && late == Sh::kShared) {
 #pragma unroll
         for (int j = 0; j < RC; ++j) {
           const int row = rowC + j * (GT / PRC), col = pieceC * EPP;
@@ -943,7 +955,7 @@ void walk_kernel(const WalkArgs p) {
     }
     int any_start = 0;
     if (first < last) {
-      stage_rows(b_at(first), c_at(first));
+      stage_rows(b_at(first), c_at(first), kOnTime);
       if (first + 1 < last) load_bc(chunk_of(first + 1));
       __bf16* const rest = rest_at(first);
       stage_weighted(live_in(chunk_of(first)), rest, rest + kCw2);
@@ -955,12 +967,17 @@ void walk_kernel(const WalkArgs p) {
       __bf16* const next = rest_at(i + 1);
       const bool more = i + 1 < last;
       auto stage_next = [&]() {
-        stage_rows(b_at(i + 1), c_at(i + 1));
+        stage_rows(b_at(i + 1), c_at(i + 1), kOnTime);
         if (i + 2 < last) load_bc(chunk_of(i + 2));  // a chunk ahead of its use
       };
       any_start |= starts != 0;
       if (NROWS == 2 && more) stage_next();
       update(live_in(chunk_of(i)), b_at(i), rest, rest + kCw2);
+      if constexpr (Sh::kShared) {
+        lds_barrier();
+        stage_rows(nullptr, c_at(i), kLate);
+        lds_barrier();
+      }
       if (NREST == 1) lds_barrier();  // what update read may be written
       if (NROWS == 1 && more) stage_next();
       if (more) {

@@ -48,3 +48,21 @@ def test_one_rounding(H, Hk, Dk, Dv):
         for y in results:
             err = rms(y.double().cpu().numpy() - ref)
             assert err <= once + 2.8e-5 * rms(ref), (n, err / rms(ref), once / rms(ref))
+
+
+@pytest.mark.parametrize("Dv", [64, 96, 128, 256])
+def test_log_decay_gradient_in_24_bits(Dv):
+    """A case in whole numbers, so that fp32 is exact: with a decay of one, a single value S =
+    2796203 (22 bits, every second one set) enters at token 62 and is looked at once, at token
+    64.  dS/dg there is 2 S, of which one half comes through the derivative of the state.  Two
+    bf16 parts would hold S to 11, 2e-6 of the sum."""
+    f = dict(dtype=torch.float32, device=DEV)
+    q, k = torch.zeros((1, 70, 1, 8), **f), torch.zeros((1, 70, 1, 8), **f)
+    v, do = torch.zeros((1, 70, 1, Dv), **f), torch.zeros((1, 70, 1, Dv), **f)
+    for row in (0, Dv - 1):
+        v.zero_(), do.zero_()
+        v[0, 62, 0, row], k[0, 62, 0, 3] = 2796203.0, 1.0
+        do[0, 64, 0, row], q[0, 64, 0, 3] = 1.0, 1.0
+        g = ssm.linattn_bwd(q, k, v, torch.zeros(1, **f), do, scale=1.0)
+        assert float(g["dlog_decay"]) == 2 * 2796203.0, row
+        assert float(g["dq"][0, 64, 0, 3]) == 2796203.0 and float(g["dk"][0, 62, 0, 3]) == 2796203.0
