@@ -489,6 +489,10 @@ void walk_kernel(const WalkArgs p) {
           g[sb] = mfma_parts(bF, aF[k], g[sb]);
         }
       settle(g);
+      if (starts) {  // group B clears rows of b (clear_cut)
+        lds_barrier();
+        lds_barrier();
+      }
       // Group B may write the rest.  Here the two halves of a chunk are alike in
       // both groups: staging and update beside state part and scores (f32, 128
       // keys: 63 us for 3 x 1537 x 12 heads; with the barrier before the scores 78).
@@ -523,7 +527,8 @@ void walk_kernel(const WalkArgs p) {
             float y = g[sb][i] * (m == 0 ? wd[i] : w1[i]);
             if (m == 2) y *= lam16;
             if (m == 3) y *= lam32;
-            // a token that t does not see leaves nothing, whatever it holds
+            // a token that t does not see leaves nothing, whatever its score (a NaN in
+            // its row of c does: the product takes the whole chunk)
             if (m == 0) y = (REV ? 4 * lk + i >= lr : 4 * lk + i <= lr) ? y : 0.0f;
             x[i] = y;
           }
@@ -710,6 +715,8 @@ void walk_kernel(const WalkArgs p) {
     auto c_value = [&](int j, int i) {
       return NP == 1 ? ((i & 1) ? hi_bf(cC[j][i / 2]) : lo_bf(cC[j][i / 2])) : __uint_as_float(cC[j][i % 4]);
     };
+    // whether row's document reaches the chunk's end (in the walk's direction)
+    auto to_end = [](uint64_t s, int row) { return REV ? (s & low_bits(row + 1)) == 0 : ((s >> row) >> 1) == 0; };
     // the weighted c of the loaded chunk
     auto stage_weighted = [&](int n, __bf16* Cw, __bf16* Cw2) {
       starts = __ballot((cR & 0xffu) != 0);
@@ -724,7 +731,7 @@ void walk_kernel(const WalkArgs p) {
           in = row < n;
           if (!REV) wt = in ? p.s_state * power(g2, e) : 0.0f;
         }
-        if (starts) in = in && (REV ? (starts & low_bits(row + 1)) == 0 : ((starts >> row) >> 1) == 0);
+        if (starts) in = in && to_end(starts, row);
         wt = in ? wt : 0.0f;
 #pragma unroll
         for (int which = 0; which < (DG ? 2 : 1); ++which) {
@@ -733,7 +740,7 @@ void walk_kernel(const WalkArgs p) {
           uint32_t pt[EPP / 2][3];
 #pragma unroll
           for (int i = 0; i < EPP / 2; ++i) split2<3>(c_value(j, 2 * i) * wq, c_value(j, 2 * i + 1) * wq, pt[i]);
-          if (starts) {  // a token that does not reach the end leaves nothing, whatever it holds
+          if (starts) {  // as b's rows in clear_cut
 #pragma unroll
             for (int i = 0; i < EPP / 2; ++i)
 #pragma unroll
@@ -757,6 +764,14 @@ void walk_kernel(const WalkArgs p) {
 #pragma unroll
         for (int j = 0; j < RC; ++j) cC[j] = rC[j];
         cR = rR;
+        if constexpr (STATE) {  // b is only read for the state (see clear_cut)
+          const uint64_t s = __ballot((rR & 0xffu) != 0);
+          if (s) {
+#pragma unroll
+            for (int j = 0; j < RB; ++j)
+              if (!to_end(s, b_row(j))) rB[j] = u32x4{0u, 0u, 0u, 0u};
+          }
+        }
 #pragma unroll
         for (int j = 0; j < RB; ++j) {
           const int row = b_row(j), col = b_piece(j) * EPP;
@@ -785,6 +800,27 @@ void walk_kernel(const WalkArgs p) {
             split2<3>(c_value(j, 2), c_value(j, 3), p1);
 #pragma unroll
             for (int q = 0; q < 3; ++q) *(u32x2*)(d + q * kQ * VB) = u32x2{p0[q], p1[q]};
+          }
+        }
+      }
+    };
+
+    // A token that does not reach the chunk's end leaves nothing in the state,
+    // whatever it holds.  A weight of zero is not enough for a NaN, so in a chunk
+    // with document starts b's rows are cleared too, once the scores are done (3 x
+    // 1537 tokens of 12 heads in documents of 500, fp32: 314 -> 327 us; clearing the
+    // operands in registers 321, but 2 to 8% of every walk without documents).
+    auto clear_cut = [&](__bf16* Bs) {
+#pragma unroll
+      for (int j = 0; j < RB; ++j) {
+        const int row = b_row(j), col = b_piece(j) * EPP;
+        __bf16* const d = Bs + row * KS + sw<KP>(row, col);
+        if (!to_end(starts, row)) {
+          if constexpr (NP == 1) {
+            *(u32x4*)d = u32x4{0u, 0u, 0u, 0u};
+          } else {
+#pragma unroll
+            for (int q = 0; q < 3; ++q) *(u32x2*)(d + q * kQ * KS) = u32x2{0u, 0u};
           }
         }
       }
@@ -972,12 +1008,19 @@ void walk_kernel(const WalkArgs p) {
       };
       any_start |= starts != 0;
       if (NROWS == 2 && more) stage_next();
-      update(live_in(chunk_of(i)), b_at(i), rest, rest + kCw2);
       if constexpr (Sh::kShared) {
         lds_barrier();
         stage_rows(nullptr, c_at(i), kLate);
-        lds_barrier();
       }
+      if constexpr (!STATE) {
+        if (starts) {
+          lds_barrier();
+          clear_cut(b_at(i));
+          lds_barrier();
+        }
+      }
+      if constexpr (Sh::kShared) lds_barrier();
+      update(live_in(chunk_of(i)), b_at(i), rest, rest + kCw2);
       if (NREST == 1) lds_barrier();  // what update read may be written
       if (NROWS == 1 && more) stage_next();
       if (more) {
