@@ -950,6 +950,11 @@ void walk_kernel(const WalkArgs p) {
       // against 351 for 2 x 14447 tokens of 2 heads, 128 x 80, with all gradients)
       constexpr int U = JK * NVW * (DG ? 2 : 1) <= 4 ? 4 : 2;
       const int np = i0 / p.piece_chunks;
+      // the decay over a whole piece in two parts, as over a chunk (one fp32 factor
+      // for each of hundreds of pieces: 1.5e-5 of a slow decay)
+      const int64_t whole = (int64_t)p.piece_chunks * kQ;
+      const double lampd = np > 0 ? exp((double)whole * (double)p.log_decay[h]) : 0.0;
+      const float lamp = (float)lampd, lamp_lo = lamp > 0.0f ? (float)(lampd - (double)lamp) : 0.0f;
       for (int m = 0; m < np; m += U) {
         f32x4 av[U][JK][NVW], tv[U][DG ? JK : 1][DG ? NVW : 1];
         int cut[U];
@@ -976,14 +981,16 @@ void walk_kernel(const WalkArgs p) {
           const int64_t ca = chunk_of(REV ? m1 : m0), cb = chunk_of(REV ? m0 : m1) + 1;
           const int64_t hi = cb * kQ < len ? cb * kQ : len;
           const int64_t n = hi > ca * kQ ? hi - ca * kQ : 0;
-          const float d = n == 0 ? 1.0f : exp2_hw(g2 * (float)n);
+          const float d = n == whole ? lamp : n == 0 ? 1.0f : exp2_hw(g2 * (float)n);
+          const float dl = n == whole ? lamp_lo : 0.0f;
           for_state([&](int j, int vt, int, int) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if constexpr (DG)
-                D[j][vt][i] = cut[u] ? tv[u][j][vt][i]
-                                     : d * (D[j][vt][i] + (float)n * S[j][vt][i]) + tv[u][j][vt][i];
-              S[j][vt][i] = cut[u] ? av[u][j][vt][i] : d * S[j][vt][i] + av[u][j][vt][i];
+              if constexpr (DG) {
+                const float t = D[j][vt][i] + (float)n * S[j][vt][i];
+                D[j][vt][i] = cut[u] ? tv[u][j][vt][i] : fmaf(t, d, fmaf(t, dl, tv[u][j][vt][i]));
+              }
+              S[j][vt][i] = cut[u] ? av[u][j][vt][i] : fmaf(S[j][vt][i], d, fmaf(S[j][vt][i], dl, av[u][j][vt][i]));
             }
           });
         }

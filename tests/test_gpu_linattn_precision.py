@@ -66,3 +66,26 @@ def test_log_decay_gradient_in_24_bits(Dv):
         g = ssm.linattn_bwd(q, k, v, torch.zeros(1, **f), do, scale=1.0)
         assert float(g["dlog_decay"]) == 2 * 2796203.0, row
         assert float(g["dq"][0, 64, 0, 3]) == 2796203.0 and float(g["dk"][0, 62, 0, 3]) == 2796203.0
+
+
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("g", [-1e-6, -3e-5, -2e-4])
+def test_slow_decay_over_many_pieces(g, io):
+    """One head with a long memory over a long axis, where the walk runs in many spans.  With
+    keys of zero the state only decays: last = h0 e^(g L) and, backwards, dh0 = dlast e^(g L).
+    Every chunk or piece (2048 of them at most) rounds each value once to fp32, in its own
+    direction: sqrt(2048) 2^-24 / sqrt(3) = 1.6e-6 in RMS; the RMS over 64 values may be a quarter
+    above it: 2e-6.  A factor rounded to fp32 would err in the same direction every time."""
+    L = 131072
+    x = torch.zeros((1, L, 1, 8), dtype=io, device=DEV)
+    rng = np.random.default_rng(int(-g * 1e7))
+    h0, dlast = (torch.from_numpy(rng.normal(size=(1, 1, 8, 8)).astype(np.float32)).to(DEV) for _ in range(2))
+    log_decay = torch.full((1,), g, dtype=torch.float32, device=DEV)
+    lam = float(np.exp(float(log_decay.double()[0]) * L))
+    last = ssm.linattn_fwd(x, x, x, log_decay, h0=h0)[1]
+    dh0 = ssm.linattn_bwd(x, x, x, log_decay, x, h0=h0, dlast=dlast)["dh0"]
+    for got, was in ((last, h0), (dh0, dlast)):
+        want = was.double() * lam
+        err = float((got.double() - want).norm() / want.norm())
+        print(f"[linattn] g {g} {io}: {err:.2e}", flush=True)
+        assert err <= 2e-6
