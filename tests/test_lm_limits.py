@@ -1,0 +1,28 @@
+"""Limits of the calls of include/ssm66_lm.h, from the sizes alone (no GPU): one size on each
+side of every limit, and what the plans behind the workspaces promise."""
+import ctypes
+import os
+
+import pytest
+
+import selective_state_space_66_amd as ssm
+
+OK, NULL, SHAPE, DTYPE, FLAG, ALIGN, UNSUPPORTED = range(7)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(ssm.LIB_PATH):
+        from selective_state_space_66_amd import build
+        build.build()
+    return ssm.load_library()
+
+
+@pytest.mark.parametrize("io", [0, 1])
+@pytest.mark.parametrize("Dk,Dv", [(8, 8), (32, 32), (64, 64), (128, 64), (128, 128), (256, 256)])
+def test_a_cut_walk_has_at_most_64_pieces(lib, Dk, Dv, io):
+    """The forward's workspace is the states of its pieces and a word per piece and entry."""
+    for batch, H in ((1, 1), (1, 2), (1, 3), (2, 2), (1, 16), (8, 24)):
+        for L in (64, 1024, 5000, 14447, 32768, 131072, 1 << 20, 1 << 23):
+            size = lib.ssm_linattn_fwd_workspace_size(batch, L, H, H, Dk, Dv, io)
+            assert size <= 64 * (batch * H * Dk * Dv * 4) + 64 * batch * 4 + 512, (batch, H, L)
