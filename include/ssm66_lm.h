@@ -110,9 +110,10 @@ int ssm_linattn_step(float* state, const void* q, const void* k, const void* v,
  *   weight, bias : (channels) float32, or NULL (one, zero)
  *   mean, rstd   : (batch, groups) float32, or NULL: what ssm_group_norm_bwd
  *                  takes
- * groups divides channels; channels at most 2^22.  Tensors are aligned to
- * their element size (to 16 bytes, and with channels / groups a multiple of
- * 16 bytes, is fastest).  y may be x or z.  Zero batch or rows is a no-op.
+ * groups divides channels; channels at most 2^22, batch * groups below 2^31
+ * (else SSM_ERR_UNSUPPORTED).  Tensors are aligned to their element size (to 16
+ * bytes, and with channels / groups a multiple of 16 bytes, is fastest).  y may
+ * be x or z.  Zero batch or rows is a no-op.
  * workspace: ssm_group_norm_workspace_size(..., 0, ...) bytes, 256-byte
  * aligned.  Repeated calls give identical bits.
  */

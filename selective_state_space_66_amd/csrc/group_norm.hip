@@ -31,6 +31,7 @@
 // Infinity Cache), the merges and the channel sums little above a launch.
 // All sums are fp32 in a fixed order (no atomics).
 #include "group_norm_launch.h"
+#include "lm_grid.h"
 #include "ssm_device.h"
 
 namespace ssm66 {
@@ -259,9 +260,13 @@ __global__ __launch_bounds__(256) void rows_bwd_kernel(const Args p, int tile, i
 // ---- any number of rows -------------------------------------------------------
 //
 // A block takes `tile` vector columns (blockIdx.y) of one piece of the rows of
-// one entry (blockIdx.x = entry * pieces + piece), 256 / tile rows at a time.
+// one entry (block_of() = entry * pieces + piece), 256 / tile rows at a time.
+
+// the number of a block along x and z
+__device__ __forceinline__ uint32_t block_of() { return blockIdx.z * gridDim.x + blockIdx.x; }
 
 struct Where {
+  uint32_t block;
   int64_t n, row0, row1;
   int r0, col;
   bool here;
@@ -269,8 +274,9 @@ struct Where {
 template <int VEC>
 __device__ __forceinline__ Where where(const Args& p, int tile, int rpb) {
   Where w;
-  w.n = blockIdx.x / (uint32_t)p.pieces;
-  const int64_t piece = blockIdx.x % (uint32_t)p.pieces;
+  w.block = block_of();
+  w.n = w.block / (uint32_t)p.pieces;
+  const int64_t piece = w.block % (uint32_t)p.pieces;
   w.row0 = piece * p.piece_rows;
   w.row1 = w.row0 + p.piece_rows < p.rows ? w.row0 + p.piece_rows : p.rows;
   w.r0 = (int)threadIdx.x / tile;
@@ -312,6 +318,7 @@ __device__ __forceinline__ Moments merge(Moments a, Moments b) {
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void piece_stats_kernel(const Args p, int tile, int rpb) {
   const Where w = where<VEC>(p, tile, rpb);
+  if (w.n >= p.batch) return;
   const T* const x = (const T*)p.x + w.n * p.rows * p.C + w.col;
   float first[VEC], s[VEC], q[VEC];
   float cnt = 0.0f;
@@ -333,7 +340,7 @@ __global__ __launch_bounds__(256) void piece_stats_kernel(const Args p, int tile
                }, buf);
   }
   __shared__ float3 all[256];
-  float2* const part = (float2*)p.ws + (int64_t)blockIdx.x * p.C;
+  float2* const part = (float2*)p.ws + (int64_t)w.block * p.C;
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
     const float inv = cnt > 0.0f ? 1.0f / cnt : 0.0f;
@@ -365,18 +372,20 @@ __device__ __forceinline__ float block_sum(float v, float* scratch) {
 
 // What a merge takes of the partial sums: slice blockIdx.y of one group's pieces.
 struct Slice {
+  uint32_t group;  // entry * groups + group of the entry
   const float2* part;
-  int64_t piece0, rows, m;  // first piece, rows, entries (pieces x channels of the group)
+  int64_t n, piece0, rows, m;  // entry, first piece, rows, partial sums (pieces x channels of the group)
   int g, cg;
 };
 __device__ __forceinline__ Slice slice_of(const Args& p, int slice_pieces) {
   Slice l;
-  const int64_t n = blockIdx.x / (uint32_t)p.groups;
-  l.g = blockIdx.x % (uint32_t)p.groups;
+  l.group = block_of();
+  l.n = l.group / (uint32_t)p.groups;
+  l.g = l.group % (uint32_t)p.groups;
   l.cg = p.C / p.groups;
   l.piece0 = (int64_t)blockIdx.y * slice_pieces;
   const int64_t left = p.pieces - l.piece0, pieces = left < slice_pieces ? left : slice_pieces;
-  l.part = (const float2*)p.ws + (n * p.pieces + l.piece0) * p.C + l.g * l.cg;
+  l.part = (const float2*)p.ws + (l.n * p.pieces + l.piece0) * p.C + l.g * l.cg;
   l.m = pieces * l.cg;
   const int64_t row0 = l.piece0 * p.piece_rows, row1 = row0 + pieces * p.piece_rows;
   l.rows = (row1 < p.rows ? row1 : p.rows) - row0;
@@ -390,6 +399,7 @@ __global__ __launch_bounds__(256) void merge_stats_kernel(const Args p, int slic
                                                           float* mean_out, float* rstd_out) {
   __shared__ float scratch[4];
   const Slice sl = slice_of(p, slice_pieces);
+  if (sl.n >= p.batch) return;
   const int cg = sl.cg;
   const float2* const part = sl.part;
   const int64_t m = sl.m;
@@ -434,10 +444,10 @@ __global__ __launch_bounds__(256) void merge_stats_kernel(const Args p, int slic
   q = block_sum(q, scratch);
   if (threadIdx.x != 0) return;
   if (gridDim.y > 1) {
-    moments[(int64_t)blockIdx.x * gridDim.y + blockIdx.y] = make_float4(total, mean, q, 0.0f);
+    moments[(int64_t)sl.group * gridDim.y + blockIdx.y] = make_float4(total, mean, q, 0.0f);
   } else {
-    mean_out[blockIdx.x] = mean;
-    rstd_out[blockIdx.x] = 1.0f / sqrtf(q / total + p.eps);
+    mean_out[sl.group] = mean;
+    rstd_out[sl.group] = 1.0f / sqrtf(q / total + p.eps);
   }
 }
 
@@ -463,7 +473,7 @@ template <typename T, int VEC, bool SILU, bool GATE>
 __global__ __launch_bounds__(256) void apply_fwd_kernel(const Args p, const float* mean, const float* rstd,
                                                         int tile, int rpb) {
   const Where w = where<VEC>(p, tile, rpb);
-  if (!w.here) return;
+  if (!w.here || w.n >= p.batch) return;
   const int cg = p.C / p.groups;
   // y = x a + b with the norm folded into a and b would lose the mean's
   // cancellation; x - mean comes first
@@ -494,6 +504,7 @@ __global__ __launch_bounds__(256) void apply_fwd_kernel(const Args p, const floa
 template <typename T, int VEC, bool SILU, bool GATE>
 __global__ __launch_bounds__(256) void piece_grads_kernel(const Args p, int tile, int rpb) {
   const Where w = where<VEC>(p, tile, rpb);
+  if (w.n >= p.batch) return;
   const int cg = p.C / p.groups;
   float mu[VEC], rs[VEC], wt[VEC], sh[VEC], s1[VEC], s2[VEC];
 #pragma unroll
@@ -525,7 +536,7 @@ __global__ __launch_bounds__(256) void piece_grads_kernel(const Args p, int tile
       }
     }, buf);
   __shared__ float2 all[256];
-  float2* const part = (float2*)p.ws + (int64_t)blockIdx.x * p.C;
+  float2* const part = (float2*)p.ws + (int64_t)w.block * p.C;
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
     float2 t = make_float2(s1[i], s2[i]);
@@ -549,6 +560,7 @@ __global__ __launch_bounds__(256) void piece_grads_kernel(const Args p, int tile
 __global__ __launch_bounds__(256) void merge_grads_kernel(const Args p, int slice_pieces, float2* out) {
   __shared__ float scratch[4];
   const Slice sl = slice_of(p, slice_pieces);
+  if (sl.n >= p.batch) return;
   const int g = sl.g, cg = sl.cg;
   const float2* const part = sl.part;
   const int64_t m = sl.m;
@@ -565,7 +577,7 @@ __global__ __launch_bounds__(256) void merge_grads_kernel(const Args p, int slic
   const float inv = 1.0f / ((float)p.rows * (float)cg);
   s1 = block_sum(s1, scratch) * inv;
   s2 = block_sum(s2, scratch) * inv;
-  if (threadIdx.x == 0) out[(int64_t)blockIdx.x * gridDim.y + blockIdx.y] = make_float2(s1, s2);
+  if (threadIdx.x == 0) out[(int64_t)sl.group * gridDim.y + blockIdx.y] = make_float2(s1, s2);
 }
 
 __global__ __launch_bounds__(256) void join_grads_kernel(const float2* part, int slices, int64_t n, float2* out) {
@@ -583,7 +595,7 @@ __global__ __launch_bounds__(256) void join_grads_kernel(const float2* part, int
 template <typename T, int VEC, bool SILU, bool GATE>
 __global__ __launch_bounds__(256) void apply_bwd_kernel(const Args p, const float2* sums, int tile, int rpb) {
   const Where w = where<VEC>(p, tile, rpb);
-  if (!w.here) return;
+  if (!w.here || w.n >= p.batch) return;
   const int cg = p.C / p.groups;
   float mu[VEC], rs[VEC], wt[VEC], sh[VEC], a1[VEC], a2[VEC];
 #pragma unroll
@@ -773,10 +785,11 @@ hipError_t run_pieces(const Args& q, const Plan& l, bool bwd, hipStream_t s) {
   Args p = q;
   p.pieces = l.pieces;
   p.piece_rows = l.piece_rows;
-  const dim3 grid((uint32_t)(p.batch * l.pieces), (uint32_t)l.tiles);
-  const int64_t ng = p.batch * p.groups;
-  const dim3 groups((uint32_t)ng, (uint32_t)l.slices), join((uint32_t)((ng + 255) / 256));
   const int threads = (l.tile * l.rpb + 63) / 64 * 64;
+  const int64_t ng = p.batch * p.groups;
+  const Grid gp = grid_of(p.batch * l.pieces, threads), gg = grid_of(ng, 256);
+  const dim3 grid(gp.x, (uint32_t)l.tiles, gp.more);
+  const dim3 groups(gg.x, (uint32_t)l.slices, gg.more), join((uint32_t)((ng + 255) / 256));
   char* const extra = (char*)p.ws + parts_bytes(p, l, bwd);
   void* const slices = extra + up256((size_t)ng * 8);
   hipError_t e;

@@ -1,0 +1,47 @@
+"""Calls whose launches need 2^32 threads or more: more than one dimension of a grid holds.
+Many small entries, against the formulas in 64 bits on the GPU; bounds as in the tests of the
+ordinary sizes."""
+import pytest
+import torch
+
+import selective_state_space_66_amd as ssm
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def normal(seed, shape, io):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return torch.randn(shape, generator=g, device=DEV).to(io)
+
+
+def close(got, want, tol, what, terms=None):
+    assert got.shape == want.shape and torch.isfinite(got).all(), what
+    err = float((got.double() - want).norm() / (want if terms is None else terms).norm())
+    assert err <= tol, f"{what}: {err:.2e}"
+
+
+# 19.2 million (entry, group) pairs, and 17 million entries
+@pytest.mark.parametrize("N,C,groups,io", [(600000, 64, 32, torch.float32), (17000000, 4, 1, torch.bfloat16)])
+def test_group_norm(N, C, groups, io):
+    print(f"[group norm] {N}x2x{C}/{groups} {io}", flush=True)
+    x, dy = normal(1, (N, 2, C), io), normal(2, (N, 2, C), io)
+    w = normal(3, (C,), torch.float32)
+    y, mean, rstd = ssm.group_norm_fwd(x, groups, weight=w)
+    g = ssm.group_norm_bwd(x, groups, dy, mean, rstd, weight=w)
+    torch.cuda.synchronize()
+    tol = 1e-5 + (2.0 ** -8 if io == torch.bfloat16 else 0.0)
+    xs = x.double().view(N, 2, groups, -1)
+    mu = xs.mean((1, 3), keepdim=True)
+    rs = ((xs - mu).square().mean((1, 3), keepdim=True) + 1e-5).rsqrt()
+    xh = (xs - mu) * rs
+    close(rstd, rs[:, 0, :, 0], 1e-5, "rstd")
+    wd = w.double().view(groups, -1)
+    close(y, (xh * wd).view(N, 2, C), tol, "y")
+    du = dy.double().view(N, 2, groups, -1)
+    close(g["dweight"], (du * xh).sum((0, 1)).view(C), 1e-5, "dweight",
+          terms=(du * xh).square().sum((0, 1)).sqrt().view(C))
+    dn = du * wd
+    dx = rs * (dn - dn.mean((1, 3), keepdim=True) - xh * (dn * xh).mean((1, 3), keepdim=True))
+    close(g["dx"], dx.view(N, 2, C), tol, "dx", terms=(rs * dn).view(N, 2, C))

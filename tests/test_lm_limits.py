@@ -26,3 +26,27 @@ def test_a_cut_walk_has_at_most_64_pieces(lib, Dk, Dv, io):
         for L in (64, 1024, 5000, 14447, 32768, 131072, 1 << 20, 1 << 23):
             size = lib.ssm_linattn_fwd_workspace_size(batch, L, H, H, Dk, Dv, io)
             assert size <= 64 * (batch * H * Dk * Dv * 4) + 64 * batch * 4 + 512, (batch, H, L)
+
+
+# Never dereferenced: every call below ends at a check.  Inside the limits that is the one for
+# the workspace's size.
+P = ctypes.c_void_p(0x10000)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_group_norm_limits(lib, backward):
+    def call(batch, C, groups, rows=2):
+        if backward:
+            return lib.ssm_group_norm_bwd(P, None, None, None, 0, P, P, P, P, None, None, None, P, 1,
+                                          batch, rows, C, groups, 0, None)
+        return lib.ssm_group_norm_fwd(P, None, None, None, 0, 1e-5, P, None, None, P, 1, batch, rows,
+                                      C, groups, 0, None)
+
+    assert call(1, 1 << 22, 1) == SHAPE and call(1, (1 << 22) + 1, 1) == UNSUPPORTED
+    for groups in (1, 2, 32):
+        most = ((1 << 31) - 1) // groups
+        size = lib.ssm_group_norm_workspace_size
+        assert call(most, 32, groups) == SHAPE and size(most, 2, 32, groups, int(backward), 0) > 0
+        assert call(most + 1, 32, groups) == UNSUPPORTED
+        assert size(most + 1, 2, 32, groups, int(backward), 0) == 0
+        assert call(most + 1, 32, groups, rows=1) == UNSUPPORTED
