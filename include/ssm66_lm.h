@@ -41,8 +41,9 @@ extern "C" {
  *   last_state : (batch, nheads, dv, dk) float32, or NULL; must not overlap h0
  * kheads divides nheads; dk and dv are multiples of 8, at most 256; q, k, v
  * and o are 16-byte aligned, and so are h0 and last_state; nheads * dv and
- * kheads * dk at most 2^22 (else SSM_ERR_UNSUPPORTED).  Zero batch or nheads
- * is a no-op; seqlen == 0 copies h0 (or zero) to last_state.
+ * kheads * dk at most 2^22, batch * nheads below 2^21, seqlen at most 2^29 - 64
+ * (else SSM_ERR_UNSUPPORTED).  Zero batch or nheads is a no-op; seqlen == 0
+ * copies h0 (or zero) to last_state.
  * workspace: ssm_linattn_fwd_workspace_size(...) bytes, 256-byte aligned,
  * contents not needed before or after (NULL where the size is 0).
  * Values are not checked.  A NaN or infinity in a real token reaches all outputs

@@ -2,6 +2,7 @@
 // (linattn_walk.h) are laid out, the sums over heads that share keys, and the
 // single-token step.
 #include "linattn_launch.h"
+#include "lm_grid.h"
 #include "ssm_device.h"
 
 namespace ssm66 {
@@ -134,7 +135,7 @@ WalkArgs walk_args(const Problem& p, char* ws, size_t cuts_at) {
 template <typename T>
 __global__ __launch_bounds__(256) void sum_heads_kernel(const float* part, T* out, int64_t n4, int Hk,
                                                         int rep, int D4) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
   if (i >= n4) return;
   const int64_t row = i / ((int64_t)Hk * D4);
   const int rest = (int)(i - row * Hk * D4), g = rest / D4, d = rest - g * D4;
@@ -157,7 +158,8 @@ __global__ __launch_bounds__(256) void sum_heads_kernel(const float* part, T* ou
 hipError_t sum_heads(const Problem& p, const float* part, void* out, hipStream_t stream) {
   const int64_t n4 = p.batch * p.L * p.Hk * (p.Dk / 4);
   if (n4 == 0) return hipSuccess;
-  const dim3 grid((uint32_t)((n4 + 255) / 256));
+  const Grid g = grid_of((n4 + 255) / 256, 256);
+  const dim3 grid(g.x, g.more);
   if (p.f32)
     sum_heads_kernel<float><<<grid, 256, 0, stream>>>(part, (float*)out, n4, p.Hk, p.H / p.Hk, p.Dk / 4);
   else

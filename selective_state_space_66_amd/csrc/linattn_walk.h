@@ -69,6 +69,7 @@
 #pragma once
 
 #include "linattn_launch.h"
+#include "lm_grid.h"
 #include "ssm_device.h"
 
 namespace ssm66 {
@@ -273,8 +274,9 @@ void walk_kernel(const WalkArgs p) {
   // contiguous run of (entry, head, span, slice), so the slices that read the
   // same a and b meet in its L2.
   const uint32_t per = (p.nblk + 7u) / 8u;
-  const uint32_t logical = (blockIdx.x % 8u) * per + blockIdx.x / 8u;
-  if (logical >= p.nblk) return;
+  const uint32_t id = blockIdx.y * gridDim.x + blockIdx.x;  // y: more blocks than x holds
+  const uint32_t logical = (id % 8u) * per + id / 8u;
+  if (id / 8u >= per || logical >= p.nblk) return;
   uint32_t rest = logical;
   const int sl = (int)(rest % (uint32_t)p.nsl);
   rest /= (uint32_t)p.nsl;
@@ -1088,18 +1090,18 @@ hipError_t launch_walk(const WalkArgs& args, bool rev, bool dg, bool state, hipS
   const int64_t n = (int64_t)a.batch * a.H * a.nsl * a.nspan_run;
   if (n == 0) return hipSuccess;
   a.nblk = (uint32_t)n;
-  const dim3 grid((uint32_t)((n + 7) / 8 * 8));
   // the kernels that a plan can choose: the outputs' walk takes 64 columns at
   // most, and 32 with the log-decay's gradient, whose state walk takes 64
-#define SSM_WALK(REV, DG, STATE)                                                                       \
-  do {                                                                                                 \
-    if constexpr (VB <= (STATE ? (DG ? 64 : 128) : (DG ? 32 : 64)))                                    \
-      static_assert(Shape<NP, KP, VB, DG, STATE>::kFits, "more than the LDS of a CU");                  \
-    if constexpr (VB <= (STATE ? (DG ? 64 : 128) : (DG ? 32 : 64)))                                              \
-      walk_kernel<NP, KP, VB, REV, DG, STATE>                                                          \
-          <<<grid, dim3(Shape<NP, KP, VB, DG, STATE>::kThreads), 0, stream>>>(a);                      \
-    else                                                                                               \
-      return hipErrorInvalidValue;                                                                     \
+#define SSM_WALK(REV, DG, STATE)                                                                      \
+  do {                                                                                                \
+    if constexpr (VB <= (STATE ? (DG ? 64 : 128) : (DG ? 32 : 64))) {                                 \
+      static_assert(Shape<NP, KP, VB, DG, STATE>::kFits, "more than the LDS of a CU");                \
+      constexpr int kThreads = Shape<NP, KP, VB, DG, STATE>::kThreads;                                \
+      const Grid g = grid_of((n + 7) / 8 * 8, kThreads);                                              \
+      walk_kernel<NP, KP, VB, REV, DG, STATE><<<dim3(g.x, g.more), dim3(kThreads), 0, stream>>>(a);   \
+    } else {                                                                                          \
+      return hipErrorInvalidValue;                                                                    \
+    }                                                                                                 \
   } while (0)
   if (state && rev) SSM_WALK(true, false, true);
   else if (state && dg) SSM_WALK(false, true, true);

@@ -45,3 +45,24 @@ def test_group_norm(N, C, groups, io):
     dn = du * wd
     dx = rs * (dn - dn.mean((1, 3), keepdim=True) - xh * (dn * xh).mean((1, 3), keepdim=True))
     close(g["dx"], dx.view(N, 2, C), tol, "dx", terms=(rs * dn).view(N, 2, C))
+
+
+def test_linear_attention():
+    """2097151 single tokens of one head: 16.8 million blocks of 512 threads where the values
+    are wide.  bf16 outputs: 4e-3, as in the tests of the ordinary sizes."""
+    B, Dk, Dv = (1 << 21) - 1, 8, 256
+    print(f"[linattn] {B}x1x1 {Dk}x{Dv}", flush=True)
+    io = torch.bfloat16
+    q, k = normal(4, (B, 1, 1, Dk), io), normal(5, (B, 1, 1, Dk), io)
+    v, do = normal(6, (B, 1, 1, Dv), io), normal(7, (B, 1, 1, Dv), io)
+    g = torch.full((1,), -0.1, device=DEV)
+    o = ssm.linattn_fwd(q, k, v, g, scale=0.5, return_last_state=False)[0]
+    grads = ssm.linattn_bwd(q, k, v, g, do, scale=0.5, need_dlog_decay=False)
+    torch.cuda.synchronize()
+    for a in range(0, B, 1 << 18):
+        s = slice(a, a + (1 << 18))
+        qd, kd, vd, dd = (t[s].double() for t in (q, k, v, do))
+        close(o[s], 0.5 * (qd * kd).sum(-1, keepdim=True) * vd, 4e-3, "o")
+        close(grads["dv"][s], 0.5 * (qd * kd).sum(-1, keepdim=True) * dd, 4e-3, "dv")
+        close(grads["dq"][s], 0.5 * (dd * vd).sum(-1, keepdim=True) * kd, 4e-3, "dq")
+        close(grads["dk"][s], 0.5 * (dd * vd).sum(-1, keepdim=True) * qd, 4e-3, "dk")

@@ -50,3 +50,30 @@ def test_group_norm_limits(lib, backward):
         assert call(most + 1, 32, groups) == UNSUPPORTED
         assert size(most + 1, 2, 32, groups, int(backward), 0) == 0
         assert call(most + 1, 32, groups, rows=1) == UNSUPPORTED
+
+
+ODD = ctypes.c_void_p(0x10008)  # not aligned as a workspace, which is looked at after the limits
+
+
+def linattn_calls(lib):
+    def fwd(batch, L, H, Hk, Dk, Dv, io=1):
+        return lib.ssm_linattn_fwd(P, P, P, P, 1.0, None, None, None, P, None, ODD, 1 << 60, batch, L,
+                                   H, Hk, Dk, Dv, io, None)
+
+    def bwd(batch, L, H, Hk, Dk, Dv, io=1):
+        return lib.ssm_linattn_bwd(P, P, P, P, 1.0, None, None, None, P, None, P, P, P, None, None, ODD,
+                                   1 << 60, batch, L, H, Hk, Dk, Dv, io, None)
+    return fwd, bwd
+
+
+@pytest.mark.parametrize("io", [0, 1])
+def test_linattn_limits(lib, io):
+    for call in linattn_calls(lib):
+        for inside, outside in (((1, 1, 1, 1, 256, 256), (1, 1, 1, 1, 264, 256)),
+                                ((1, 1, 1, 1, 8, 256), (1, 1, 1, 1, 8, 264)),
+                                (((1 << 21) - 1, 1, 1, 1, 8, 256), (1 << 21, 1, 1, 1, 8, 256)),
+                                ((1, (1 << 29) - 64, 1, 1, 8, 8), (1, (1 << 29) - 63, 1, 1, 8, 8)),
+                                ((1, 1, 1 << 14, 1 << 14, 256, 8), (1, 1, (1 << 14) + 1, (1 << 14) + 1, 256, 8)),
+                                ((1, 1, 1 << 14, 1, 8, 256), (1, 1, (1 << 14) + 1, 1, 8, 256))):
+            assert call(*inside, io) == ALIGN, inside
+            assert call(*outside, io) == UNSUPPORTED, outside
