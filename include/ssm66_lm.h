@@ -71,8 +71,8 @@ int ssm_linattn_fwd(const void* q, const void* k, const void* v, const float* lo
  * Outputs are overwritten.  A token sees no gradient from after the next
  * document start.  workspace: ssm_linattn_bwd_workspace_size(...) bytes,
  * 256-byte aligned (need_dlog_decay says whether dlog_decay is asked for).
- * Alignment and limits as for ssm_linattn_fwd.  All sums are taken in a fixed
- * order: repeated calls give identical bits.
+ * Alignment and limits as for ssm_linattn_fwd, and nheads * dk at most 2^22.
+ * All sums are taken in a fixed order: repeated calls give identical bits.
  */
 size_t ssm_linattn_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads,
                                       int64_t kheads, int64_t dk, int64_t dv,

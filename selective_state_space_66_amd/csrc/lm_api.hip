@@ -40,12 +40,14 @@ int linattn_shape(int64_t batch, int64_t seqlen, int64_t nheads, int64_t kheads,
 }
 
 int linattn_limits(int64_t batch, int64_t seqlen, int64_t nheads, int64_t kheads, int64_t dk,
-                   int64_t dv) {
+                   int64_t dv, bool backward) {
   // 16-byte pieces of a row, the widest tile of the kernels, 32-bit offsets
   // within a chunk, 32-bit block numbers (at most 64 spans and 16 slices)
   if (dk % 8 != 0 || dv % 8 != 0 || dk > 256 || dv > 256) return SSM_ERR_UNSUPPORTED;
   const int64_t widest = (int64_t)1 << 22;
-  if (nheads > widest || nheads * dv > widest || nheads * dk > widest) return SSM_ERR_UNSUPPORTED;
+  if (nheads > widest || nheads * dv > widest || kheads * dk > widest) return SSM_ERR_UNSUPPORTED;
+  // gradients of shared keys have a row per head before they are added
+  if (backward && nheads * dk > widest) return SSM_ERR_UNSUPPORTED;
   if (batch > 0x7fffffff || batch * nheads > 0x7fffffff / 1024) return SSM_ERR_UNSUPPORTED;
   if (seqlen > (int64_t)64 * 0x7fffff) return SSM_ERR_UNSUPPORTED;
   // the sums over shared heads: one thread for four columns
@@ -183,7 +185,7 @@ int ssm_clip_grad_norm(const void* const* grads, void* const* outs, const int64_
 size_t ssm_linattn_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads,
                                       int64_t kheads, int64_t dk, int64_t dv, int io_dtype) {
   if (linattn_shape(batch, seqlen, nheads, kheads, dk, dv, io_dtype) != SSM_OK ||
-      linattn_limits(batch, seqlen, nheads, kheads, dk, dv) != SSM_OK)
+      linattn_limits(batch, seqlen, nheads, kheads, dk, dv, false) != SSM_OK)
     return 0;
   return ssm66::linattn::fwd_workspace(problem(nullptr, nullptr, nullptr, nullptr, 1.0f, nullptr,
                                                nullptr, nullptr, batch, seqlen, nheads, kheads, dk,
@@ -194,7 +196,7 @@ size_t ssm_linattn_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nhe
                                       int64_t kheads, int64_t dk, int64_t dv,
                                       int need_dlog_decay, int io_dtype) {
   if (linattn_shape(batch, seqlen, nheads, kheads, dk, dv, io_dtype) != SSM_OK ||
-      linattn_limits(batch, seqlen, nheads, kheads, dk, dv) != SSM_OK)
+      linattn_limits(batch, seqlen, nheads, kheads, dk, dv, true) != SSM_OK)
     return 0;
   return ssm66::linattn::bwd_workspace(problem(nullptr, nullptr, nullptr, nullptr, 1.0f, nullptr,
                                                nullptr, nullptr, batch, seqlen, nheads, kheads, dk,
@@ -211,7 +213,7 @@ int ssm_linattn_fwd(const void* q, const void* k, const void* v, const float* lo
   if (st != SSM_OK) return st;
   if (batch == 0 || nheads == 0) return SSM_OK;
   if (!log_decay || (seqlen > 0 && (!q || !k || !v || !o))) return SSM_ERR_NULL;
-  if ((st = linattn_limits(batch, seqlen, nheads, kheads, dk, dv)) != SSM_OK) return st;
+  if ((st = linattn_limits(batch, seqlen, nheads, kheads, dk, dv, false)) != SSM_OK) return st;
   const void* p16[6] = {q, k, v, o, h0, last_state};
   for (const void* x : p16)
     if (!aligned(x, 16)) return SSM_ERR_ALIGN;
@@ -236,7 +238,7 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* lo
   if (nheads == 0) return SSM_OK;
   if (batch > 0 && !log_decay) return SSM_ERR_NULL;
   if (batch > 0 && seqlen > 0 && (!q || !k || !v || !do_ || !dq || !dk_ || !dv_)) return SSM_ERR_NULL;
-  if ((st = linattn_limits(batch, seqlen, nheads, kheads, dk, dv)) != SSM_OK) return st;
+  if ((st = linattn_limits(batch, seqlen, nheads, kheads, dk, dv, true)) != SSM_OK) return st;
   const void* p16[10] = {q, k, v, do_, dq, dk_, dv_, h0, dlast, dh0};
   for (const void* x : p16)
     if (!aligned(x, 16)) return SSM_ERR_ALIGN;

@@ -66,3 +66,21 @@ def test_linear_attention():
         close(grads["dv"][s], 0.5 * (qd * kd).sum(-1, keepdim=True) * dd, 4e-3, "dv")
         close(grads["dq"][s], 0.5 * (dd * vd).sum(-1, keepdim=True) * kd, 4e-3, "dq")
         close(grads["dk"][s], 0.5 * (dd * vd).sum(-1, keepdim=True) * qd, 4e-3, "dk")
+
+
+def test_many_heads_on_one_key_head():
+    """32768 heads that share keys of 256: as many columns of keys, forwards, as one head has."""
+    import linattn_ref as R
+    H, Dk, Dv, L = 32768, 256, 8, 70
+    print(f"[linattn] 1x{L}x{H}/1 {Dk}x{Dv}", flush=True)
+    io = torch.bfloat16
+    q, k = normal(8, (1, L, 1, Dk), io), normal(9, (1, L, 1, Dk), io)
+    v = normal(10, (1, L, H, Dv), io)
+    g = -torch.rand(H, generator=torch.Generator(device=DEV).manual_seed(11), device=DEV) * 0.1
+    o, last = ssm.linattn_fwd(q, k, v, g)
+    torch.cuda.synchronize()
+    for h in (0, 1, 12345, H - 1):
+        n = [t.double().cpu().numpy() for t in (q, k, v[:, :, h:h + 1], g[h:h + 1])]
+        want, state = R.forward(*n, Dk ** -0.5)
+        close(o[:, :, h:h + 1].cpu(), torch.from_numpy(want), 4e-3, f"o of head {h}")
+        close(last[:, h:h + 1].cpu(), torch.from_numpy(state), 1e-5, f"state of head {h}")

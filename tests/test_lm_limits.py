@@ -77,3 +77,12 @@ def test_linattn_limits(lib, io):
                                 ((1, 1, 1 << 14, 1, 8, 256), (1, 1, (1 << 14) + 1, 1, 8, 256))):
             assert call(*inside, io) == ALIGN, inside
             assert call(*outside, io) == UNSUPPORTED, outside
+
+
+def test_heads_that_share_keys(lib):
+    """Forwards only the keys' own heads count, backwards every head has a row of gradients."""
+    fwd, bwd = linattn_calls(lib)
+    assert fwd(1, 1, 1 << 19, 1, 256, 8) == ALIGN and fwd(1, 1, (1 << 19) + 1, 1, 256, 8) == UNSUPPORTED
+    assert bwd(1, 1, 1 << 14, 1, 256, 8) == ALIGN and bwd(1, 1, (1 << 14) + 1, 1, 256, 8) == UNSUPPORTED
+    assert lib.ssm_linattn_bwd_workspace_size(1, 64, 1 << 14, 1, 256, 8, 0, 1) > 0
+    assert lib.ssm_linattn_bwd_workspace_size(1, 64, (1 << 14) + 1, 1, 256, 8, 0, 1) == 0
