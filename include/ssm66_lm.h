@@ -87,8 +87,9 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* lo
 /*
  * One token against a state cache (batch, nheads, dv, dk) float32, updated in
  * place: S = lam S + v k^T, o = scale S q.  q, k: (batch, kheads, dk);
- * v, o: (batch, nheads, dv), io dtype.  dk is a multiple of 8, at most 256;
- * dv any positive size; state, q and k are 16-byte aligned, v and o to their
+ * v, o: (batch, nheads, dv), io dtype.  dk is a multiple of 8, at most 256; dv
+ * any positive size up to 2^30, batch * nheads * ceil(dv / 4) below 2^31 (else
+ * SSM_ERR_UNSUPPORTED); state, q and k are 16-byte aligned, v and o to their
  * element size.
  */
 int ssm_linattn_step(float* state, const void* q, const void* k, const void* v,

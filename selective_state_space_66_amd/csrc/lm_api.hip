@@ -266,7 +266,8 @@ int ssm_linattn_step(float* state, const void* q, const void* k, const void* v,
   if (!state || !q || !k || !v || !log_decay || !o) return SSM_ERR_NULL;
   if (dk % 8 != 0 || dk > 256) return SSM_ERR_UNSUPPORTED;
   const int64_t most = 0x7fffffff;
-  if (dv > most || nheads > most || batch * nheads > most / ((dv + 3) / 4)) return SSM_ERR_UNSUPPORTED;
+  if (dv > 1 << 30) return SSM_ERR_UNSUPPORTED;  // rows of a block past the last one stay 32-bit
+  if (nheads > most || batch * nheads > most / ((dv + 3) / 4)) return SSM_ERR_UNSUPPORTED;
   const size_t es = io_dtype == SSM_BF16 ? 2 : 4;
   if (!aligned(state, 16) || !aligned(q, 16) || !aligned(k, 16)) return SSM_ERR_ALIGN;
   if (!aligned(v, es) || !aligned(o, es) || !aligned(log_decay, 4)) return SSM_ERR_ALIGN;

@@ -86,3 +86,18 @@ def test_heads_that_share_keys(lib):
     assert bwd(1, 1, 1 << 14, 1, 256, 8) == ALIGN and bwd(1, 1, (1 << 14) + 1, 1, 256, 8) == UNSUPPORTED
     assert lib.ssm_linattn_bwd_workspace_size(1, 64, 1 << 14, 1, 256, 8, 0, 1) > 0
     assert lib.ssm_linattn_bwd_workspace_size(1, 64, (1 << 14) + 1, 1, 256, 8, 0, 1) == 0
+
+
+def test_step_limits(lib):
+    def call(batch, H, Dk, Dv):
+        return lib.ssm_linattn_step(ctypes.c_void_p(0x10008), P, P, P, P, 1.0, P, batch, H, 1, Dk, Dv, 0, None)
+
+    most = (1 << 31) - 1
+    for inside, outside in (((1, 1, 256, 1), (1, 1, 264, 1)),
+                            ((1, 1, 8, 1 << 30), (1, 1, 8, (1 << 30) + 1)),
+                            ((most, 1, 8, 4), (most + 1, 1, 8, 4)), ((1, most, 8, 1), (1, most + 1, 8, 1)),
+                            ((most // 16, 1, 8, 64), (most // 16 + 1, 1, 8, 64))):
+        assert call(*inside) == ALIGN, inside
+        assert call(*outside) == UNSUPPORTED, outside
+    for Dv in (most, most - 1, 1 << 31):
+        assert call(1, 1, 8, Dv) == UNSUPPORTED
