@@ -283,7 +283,9 @@ __device__ __forceinline__ f32x4 load4(const T* p) {
 template <typename T, int LPR, int R>
 __global__ __launch_bounds__(256) void linattn_step_kernel(const StepArgs p, int nb) {
   constexpr int kRows = 64 / LPR;  // rows of a wave's load
-  const uint32_t bh = blockIdx.x / (uint32_t)nb, part = blockIdx.x % (uint32_t)nb;
+  const uint32_t id = blockIdx.y * gridDim.x + blockIdx.x;  // y: more blocks than x holds
+  const uint32_t bh = id / (uint32_t)nb, part = id % (uint32_t)nb;
+  if (bh >= (uint32_t)(p.batch * p.H)) return;
   const uint32_t b = bh / (uint32_t)p.H, h = bh - b * (uint32_t)p.H;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int col = 4 * (lane % LPR);
@@ -333,7 +335,8 @@ hipError_t step_rows(const StepArgs& a, hipStream_t stream) {
   const int nb = (a.Dv + per - 1) / per;
   const int64_t n = heads * nb;
   if (n > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid((uint32_t)n);
+  const Grid g = grid_of(n, 256);
+  const dim3 grid(g.x, g.more);
   if (many) linattn_step_kernel<T, LPR, 4><<<grid, 256, 0, stream>>>(a, nb);
   else linattn_step_kernel<T, LPR, 1><<<grid, 256, 0, stream>>>(a, nb);
   return hipGetLastError();

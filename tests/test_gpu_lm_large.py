@@ -84,3 +84,23 @@ def test_many_heads_on_one_key_head():
         want, state = R.forward(*n, Dk ** -0.5)
         close(o[:, :, h:h + 1].cpu(), torch.from_numpy(want), 4e-3, f"o of head {h}")
         close(last[:, h:h + 1].cpu(), torch.from_numpy(state), 1e-5, f"state of head {h}")
+
+
+@pytest.mark.parametrize("B,H", [(17000000, 1), (4250000, 4)])
+def test_step(B, H):
+    """17 million heads of one value, a block each.  fp32: 1e-5, as in the tests of the ordinary
+    sizes."""
+    Dk, Dv = 8, 1
+    print(f"[linattn] step {B}x{H} {Dk}x{Dv}", flush=True)
+    f = torch.float32
+    state = normal(12, (B, H, Dv, Dk), f)
+    q, k, v = normal(13, (B, 1, Dk), f), normal(14, (B, 1, Dk), f), normal(15, (B, H, Dv), f)
+    was = state.clone()
+    o = ssm.linattn_step(state, q, k, v, torch.full((H,), -0.2, device=DEV), scale=0.5)
+    torch.cuda.synchronize()
+    lam = float(torch.tensor(-0.2).double().exp())
+    for a in range(0, B, 1 << 22):
+        s = slice(a, a + (1 << 22))
+        want = lam * was[s].double() + v[s].double()[..., None] * k[s].double()[:, :, None, :]
+        close(state[s], want, 1e-5, "state")
+        close(o[s], 0.5 * (want * q[s].double()[:, :, None, :]).sum(-1), 1e-5, "o")
