@@ -134,7 +134,9 @@ __global__ __launch_bounds__(256) void rows_fwd_kernel(const Args p, int tile, i
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < VEC; ++i) s += v[j][i];
-    // the mean, and what its rounding left (a common offset is large beside it)
+    // the mean, and what its rounding left (a common offset is large beside it);
+    // then the squares about both (those about the first part alone less the
+    // second's square can fall below zero where little varies)
     const float m0 = group_sum<LPG>(s) * inv;
     float q = 0.0f, left = 0.0f;
 #pragma unroll
@@ -144,19 +146,27 @@ __global__ __launch_bounds__(256) void rows_fwd_kernel(const Args p, int tile, i
       for (int i = 0; i < VEC; ++i) {
         v[j][i] = in ? v[j][i] - m0 : 0.0f;
         left += v[j][i];
-        q = fmaf(v[j][i], v[j][i], q);
       }
     }
     left = group_sum<LPG>(left) * inv;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = (l + j * LPG) * VEC < cg;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        v[j][i] = in ? v[j][i] - left : 0.0f;
+        q = fmaf(v[j][i], v[j][i], q);
+      }
+    }
     const float mean = m0 + left;
-    const float rstd = 1.0f / sqrtf(fmaf(group_sum<LPG>(q), inv, p.eps - left * left));
+    const float rstd = 1.0f / sqrtf(fmaf(group_sum<LPG>(q), inv, p.eps));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (l + j * LPG) * VEC;
       float y[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
-        y[i] = Point<SILU, GATE>::forward(fmaf((v[j][i] - left) * rstd, w[j][i], b[j][i]), gz[j][i]);
+        y[i] = Point<SILU, GATE>::forward(fmaf(v[j][i] * rstd, w[j][i], b[j][i]), gz[j][i]);
       if (c < cg) store_vec<T, VEC>((T*)p.y + at + c, y);
     }
     if (l == 0) {
