@@ -26,11 +26,12 @@ int padded(int K, bool f32) { return K <= 64 ? 64 : (f32 && K <= 96 ? 96 : (K <=
 // How a walk is laid out.
 //
 // Tile.  A block takes 64 columns where its CU is its own (bf16 rows of up to
-// 128; 75.8 us against 78.4 with 32 for 192 (entry, head) pairs of 64 columns,
-// 128 keys, 2048 tokens), but 32, two blocks to a CU, where 64 would leave a
-// second round of blocks partly filled (112 against 121 us for 192 pairs of
-// 128 columns, 64 keys).  fp32 rows and the walk with the log-decay's gradient
-// have three parts of most operands and take 32, fp32 rows of 256 take 16.
+// 128; 2048 tokens: 77 us against 83 with 32 for 192 (entry, head) pairs of 64
+// columns, 128 keys, 134 against 153 for 512 pairs, 64 keys), but 32, two blocks
+// to a CU, where 64 would leave half of the second round of blocks empty or more
+// (97 against 114 us for 192 pairs of 128 columns, 64 keys; 150 against 160 with
+// 128 keys).  fp32 rows and the walk with the log-decay's gradient have three
+// parts of most operands and take 32, fp32 rows of 256 take 16.
 //
 // Spans.  Too few blocks for one round are cut along the tokens as often as
 // fills it; each span then needs the state before it, from a walk that reads b
@@ -49,7 +50,7 @@ Walk plan(const Problem& p, int K, int V, bool dg) {
   const int64_t n64 = pairs * ((V + 63) / 64);
   w.tile.KP = w.state_tile.KP = KP;
   if (p.f32) w.tile.VB = KP == 256 ? 16 : 32;
-  else w.tile.VB = !dg && KP <= 128 && V > 32 && n64 <= 256 ? 64 : 32;
+  else w.tile.VB = !dg && KP <= 128 && V > 32 && (n64 <= 256 || n64 > 384) ? 64 : 32;
   w.nsl = (V + w.tile.VB - 1) / w.tile.VB;
   const int64_t blocks = pairs * w.nsl;
   const int64_t round = !p.f32 && !dg && KP <= 128 && w.tile.VB == 32 ? 512 : 256;
