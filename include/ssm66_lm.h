@@ -45,11 +45,13 @@ extern "C" {
  * (else SSM_ERR_UNSUPPORTED).  Zero batch or nheads is a no-op; seqlen == 0
  * copies h0 (or zero) to last_state.
  * workspace: ssm_linattn_fwd_workspace_size(...) bytes, 256-byte aligned,
- * contents not needed before or after (NULL where the size is 0).
+ * contents not needed before or after (NULL where the size is 0).  Outputs and
+ * workspace overlap no input.
  * Values are not checked.  A NaN or infinity in a real token reaches all outputs
  * of its own chunk of 64 tokens (tokens before it and other documents too), the
  * later ones of its document and the state, if the document lasts to its end; no
- * other.  Repeated calls give identical bits.
+ * other.  float32 values of a magnitude over 3.396e38 (half a unit past bf16's
+ * largest) count as infinities.  Repeated calls give identical bits.
  */
 size_t ssm_linattn_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads,
                                       int64_t kheads, int64_t dk, int64_t dv, int io_dtype);

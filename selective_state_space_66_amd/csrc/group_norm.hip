@@ -24,10 +24,10 @@
 //   two passes around the sums of du and du xh.
 //
 // Measured (a copy reaches 5.2 TB/s).  One row: 16384 tokens x 1536 channels in
-// 24 groups with gate, bf16: forwards 33.9 us (4.5 TB/s), backwards 56.8 (4.4)
-// and 4.9 for the channel sums.  Pieces: 6 x 4095 x 320 in 32 groups with silu,
-// fp32: forwards 8.8 + 5.3 + 12.1 us, backwards 13.4 + 5.4 + 16.6 + 3.9; the
-// passes over the tensors run at 3.6 to 5.7 TB/s (the second finds x in the
+// 24 groups with gate, bf16: forwards 33.8 us (4.5 TB/s), backwards 54.5 (4.6)
+// and 4.8 for the channel sums.  Pieces: 6 x 4095 x 320 in 32 groups with silu,
+// fp32: forwards 9.8 + 5.4 + 11.9 us, backwards 13.2 + 5.8 + 16.2 + 3.9; the
+// passes over the tensors run at 3.2 to 5.8 TB/s (the second finds x in the
 // Infinity Cache), the merges and the channel sums little above a launch.
 // All sums are fp32 in a fixed order (no atomics).
 #include "group_norm_launch.h"
@@ -724,7 +724,10 @@ Plan plan(const Args& p, bool f32, bool bwd, int cap = 8) {
   l.rpb = 256 / l.tile;
   // pieces: about 1024 blocks (four per CU), and at least 8 rows for each thread
   // of one, so that the partial sums (8 bytes per channel and piece) stay well
-  // below the tensor's own bytes
+  // below the tensor's own bytes.  An entry of fewer rows is one piece all the
+  // same: one row of a group too wide for the registers of a wave (over 2048 bf16
+  // or 1024 fp32 channels, over 256 of an odd number) moves 22 bytes a bf16
+  // channel forwards where 4 are needed.
   int64_t pieces = (1024 + p.batch * l.tiles - 1) / (p.batch * l.tiles);
   const int64_t most = (p.rows + 8 * l.rpb - 1) / (8 * l.rpb);
   if (pieces > most) pieces = most;

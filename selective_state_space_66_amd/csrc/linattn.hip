@@ -35,9 +35,9 @@ int padded(int K, bool f32) { return K <= 64 ? 64 : (f32 && K <= 96 ? 96 : (K <=
 //
 // Spans.  Too few blocks for one round are cut along the tokens as often as
 // fills it; each span then needs the state before it, from a walk that reads b
-// and c once more (1 x 65536 x 16 heads of 128: 8 spans, 333 us and 137 us for
-// the states).  Cutting two thirds of a round costs more than it gives (119 +
-// 33 against 76 us for the 192 pairs above), and so do sequences under 16 chunks.
+// and c once more (1 x 65536 x 16 heads of 128: 8 spans, 369 us and 149 us for
+// the states).  Cutting two thirds of a round costs more than it gives (94 + 27
+// against 87 us for the 192 pairs above), and so do sequences under 16 chunks.
 struct Walk {
   Tile tile, state_tile;
   int nsl, nspan, span_chunks, pieces, piece_chunks;
@@ -131,7 +131,7 @@ WalkArgs walk_args(const Problem& p, char* ws, size_t cuts_at) {
 }
 
 // dq and dk of keys shared by `rep` heads: the heads' fp32 parts added in
-// order, rounded once.  Four columns per thread; HBM or caches bound it (5.3 us
+// order, rounded once.  Four columns per thread; HBM or caches bound it (5.4 us
 // for 3 x 1537 x 12 heads of 72, 4 TB/s).
 template <typename T>
 __global__ __launch_bounds__(256) void sum_heads_kernel(const float* part, T* out, int64_t n4, int Hk,

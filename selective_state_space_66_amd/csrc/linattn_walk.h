@@ -60,12 +60,12 @@
 //
 // What bounds it.  About 60 flops per byte of bf16 rows: at the rates of a
 // large copy and a large product the bytes take longer.  8 x 2048 tokens of 24
-// heads, 128 keys and 64 values, bf16: 75 us (4.1 TB/s; a copy of these bytes
-// takes 59).  The other walks are bound by the latency of a chunk's chain: with
-// the log-decay's gradient 233 to 255 us at the same size (19% of the matrix
-// cycles, 38% of the vector ones and 45% of the LDS's are used; without group
-// A's products 180, without B's 237, without both 97), fp32 rows of 72 and 96
-// with 3 x 1537 tokens of 12 heads 52.
+// heads, 128 keys and 64 values, bf16: 77 to 86 us (3.6 to 4.0 TB/s; a copy of
+// these bytes takes 59), a third of the matrix cycles used.  The other walks are
+// bound by the latency of a chunk's chain: with the log-decay's gradient 230 to
+// 255 us at the same size (19% of the matrix cycles, 38% of the vector ones and
+// 45% of the LDS's are used; without group A's products 180, without B's 237,
+// without both 97), fp32 rows of 72 and 96 with 3 x 1537 tokens of 12 heads 54.
 #pragma once
 
 #include "linattn_launch.h"
@@ -139,9 +139,9 @@ __device__ __forceinline__ f32x4 mfma_parts(const bf16x8 (&a)[PA], const bf16x8 
 }
 
 // b and the state sit in LDS in rows of KP bf16, 16-byte piece c of row r at
-// c ^ swz(r): 16-byte reads of one piece over rows r .. r + 15 and transposing
-// reads of 32 bytes from each of rows r .. r + 3 both spread over the banks.
-// Rows of 96 do the same as they stand, 52 banks apart.
+// c ^ swz(r), for 16-byte reads of one piece over rows r .. r + 15 and
+// transposing reads of 32 bytes from each of rows r .. r + 3.  Rows of 96 need
+// no exchange, 52 banks apart.
 template <int KP>
 constexpr int kRow = KP == 96 ? 104 : KP;
 template <int KP>
@@ -154,7 +154,10 @@ __device__ __forceinline__ constexpr int sw(int r, int col) {
 }
 // c's rows of VB bf16 are only read by the transposing reads (32 bytes from
 // each of four rows at a time, over 64 banks of 4 bytes): where one row or two
-// fill the banks, the others change places by pairs of pieces
+// fill the banks, the others change places by pairs of pieces.  Rows of 32 stay
+// as they are, and a read of theirs meets half of the banks: of the LDS's active
+// cycles 41% are conflicts in a walk of 32 columns, 43% with the log-decay's
+// gradient, 26% in one of 64 columns.
 template <int VB>
 __device__ __forceinline__ constexpr int swc(int r, int col) {
   return VB >= 64 ? (((col >> 3) ^ ((VB == 128 ? r & 3 : (r >> 1) & 1) << 1)) << 3) | (col & 7) : col;

@@ -358,7 +358,8 @@ def clip_grad_norm(grads, max_norm, outs=None, workspace=None):
     """The global norm of many gradients on the GPU, and the gradients clipped to it.
 
     grads: a list of contiguous float32 or bfloat16 tensors of any shapes, all on one GPU;
-    outs: optional tensors like them for the clipped gradients (in place when omitted).
+    outs: optional tensors like them for the clipped gradients (in place when omitted); no
+    memory is listed twice.
     out = grad * min(1, max_norm / (norm + 1e-6)).  Returns the norm before clipping, a
     float32 tensor with no dimensions, on the GPU (nothing waits for it).
     """
