@@ -876,33 +876,50 @@ void walk_kernel(const WalkArgs p) {
           }
       }
     };
-    // the state at the walk's end of the staged chunk
+    // The state at the walk's end of the staged chunk.  Where its last bits matter
+    // (fp32 results, and the state and T behind the log-decay's gradient), the
+    // chunk's own part is added up by itself: a slow head's state is large beside
+    // it, and each product that adds to it rounds to its size, 6 or 12 times a chunk
+    // (T after 2000 tokens with a memory of 4096: 3.8e-7 to 6.4e-7 instead of 1.2e-7
+    // to 1.9e-7).  Rows of 256 then leave the two steps of the products a loop: unrolled,
+    // the kernel outgrows the instruction cache (2 x 2048 x 24 heads of 64 x 256, bf16,
+    // with all gradients 381 us against 341).
+    constexpr bool APART = DG || NP == 3;
+    constexpr bool ROLL = APART && KP == 256;
     auto update = [&](int n, const __bf16* Bs, const __bf16* Cw, const __bf16* Cw2) {
       const bool cut = starts != 0;
       const float d = n == kQ ? lam64 : power(g2, n), dl = n == kQ ? lam64_lo : 0.0f;
       const float nf = (float)n;
-#pragma unroll
-      for (int j = 0; j < JK; ++j)
-#pragma unroll
-        for (int vt = 0; vt < NVW; ++vt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (DG) {
-              const float t = D[j][vt][i] + nf * S[j][vt][i];
-              D[j][vt][i] = fmaf(t, d, t * dl);
-            }
-            S[j][vt][i] = fmaf(S[j][vt][i], d, S[j][vt][i] * dl);
-          }
-      if (cut) {
+      if constexpr (!APART) {
 #pragma unroll
         for (int j = 0; j < JK; ++j)
 #pragma unroll
-          for (int vt = 0; vt < NVW; ++vt) {
-            S[j][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if constexpr (DG) D[j][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-          }
-      }
+          for (int vt = 0; vt < NVW; ++vt)
 #pragma unroll
+            for (int i = 0; i < 4; ++i) S[j][vt][i] = fmaf(S[j][vt][i], d, S[j][vt][i] * dl);
+        if (cut) {
+#pragma unroll
+          for (int j = 0; j < JK; ++j)
+#pragma unroll
+            for (int vt = 0; vt < NVW; ++vt) S[j][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+      }
+      f32x4 P[JK][NVW], PD[DG ? JK : 1][DG ? NVW : 1];
+#pragma unroll
+      for (int j = 0; j < JK; ++j)
+#pragma unroll
+        for (int vt = 0; vt < NVW; ++vt) {
+          P[j][vt] = APART ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : S[j][vt];
+          if constexpr (DG) PD[j][vt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+      auto settle_all = [&]() {
+#pragma unroll
+        for (int j = 0; j < JK; ++j) {
+          settle(P[j]);
+          if constexpr (DG) settle(PD[j]);
+        }
+      };
+#pragma unroll(ROLL ? 1 : 2)
       for (int ks = 0; ks < 2; ++ks) {
         const int ra = 32 * ks + 8 * g4 + kk, rb = ra + 4;
         bf16x8 bF[JK][NP];
@@ -929,16 +946,26 @@ void walk_kernel(const WalkArgs p) {
           }
 #pragma unroll
           for (int j = 0; j < JK; ++j) {
-            S[j][vt] = mfma_parts(bF[j], cF, S[j][vt]);
-            if constexpr (DG) D[j][vt] = mfma_parts(bF[j], cF2, D[j][vt]);
+            P[j][vt] = mfma_parts(bF[j], cF, P[j][vt]);
+            if constexpr (DG) PD[j][vt] = mfma_parts(bF[j], cF2, PD[j][vt]);
           }
         }
+        if constexpr (ROLL) settle_all();  // before the loop's branch
       }
+      settle_all();
 #pragma unroll
-      for (int j = 0; j < JK; ++j) {
-        settle(S[j]);
-        if constexpr (DG) settle(D[j]);
-      }
+      for (int j = 0; j < JK; ++j)
+#pragma unroll
+        for (int vt = 0; vt < NVW; ++vt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (DG) {
+              const float t = D[j][vt][i] + nf * S[j][vt][i];
+              D[j][vt][i] = cut ? PD[j][vt][i] : fmaf(t, d, fmaf(t, dl, PD[j][vt][i]));
+            }
+            const float s = S[j][vt][i];
+            S[j][vt][i] = !APART || cut ? P[j][vt][i] : fmaf(s, d, fmaf(s, dl, P[j][vt][i]));
+          }
     };
 
     if (first < last) load_bc(chunk_of(first));

@@ -89,3 +89,33 @@ def test_slow_decay_over_many_pieces(g, io):
         err = float((got.double() - want).norm() / want.norm())
         print(f"[linattn] g {g} {io}: {err:.2e}", flush=True)
         assert err <= 2e-6
+
+
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (64, 128), (16, 256)])
+def test_derivative_of_a_slow_state(Dk, Dv, io):
+    """64 heads of one decay, 1 - 2^-12, see the same 2000 tokens; head h's log-decay gradient is
+    one element of dS/dg after them, picked by dlast.  It is a sum over the tokens, of
+    terms of either sign, held in fp32 over 32 chunks.  A chunk rounds it twice at its size (as
+    it decays, as the chunk's own part joins) and the state once: sqrt(64) 2^-24 / sqrt(3) =
+    2.8e-7, and as much over sqrt(2) through the state, in quadrature 3.4e-7 of the root of the
+    terms' squares, in RMS over the heads; 3.5e-7."""
+    H, L = 64, 2000
+    gen = torch.Generator(device=DEV).manual_seed(Dk + Dv)
+    k1 = (torch.randn((L, Dk), generator=gen, device=DEV) * Dk ** -0.5).to(io)
+    v1 = torch.randn((L, Dv), generator=gen, device=DEV).to(io)
+    k = k1[None, :, None].contiguous()
+    v = v1[None, :, None].expand(1, L, H, Dv).contiguous()
+    q, do = torch.zeros_like(k), torch.zeros_like(v)
+    g = torch.full((H,), float(np.log1p(-2.0 ** -12)), device=DEV)
+    rng = np.random.default_rng(Dv)
+    rows, cols = torch.from_numpy(rng.integers(0, Dv, H)), torch.from_numpy(rng.integers(0, Dk, H))
+    dlast = torch.zeros((1, H, Dv, Dk), device=DEV)
+    dlast[0, torch.arange(H), rows, cols] = 1.0
+    got = ssm.linattn_bwd(q, k, v, g, do, scale=1.0, dlast=dlast)["dlog_decay"].double().cpu()
+    age = torch.arange(L - 1, -1, -1, dtype=torch.float64)
+    weight = age * torch.exp(g.double().cpu()[0] * age)
+    terms = weight[:, None] * v1.double().cpu()[:, rows] * k1.double().cpu()[:, cols]
+    err = (got - terms.sum(0)) / terms.square().sum(0).sqrt()
+    print(f"[linattn] dS/dg {Dk}x{Dv} {io}: {float(err.square().mean().sqrt()):.2e}", flush=True)
+    assert float(err.square().mean().sqrt()) <= 3.5e-7
