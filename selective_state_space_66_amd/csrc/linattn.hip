@@ -35,7 +35,7 @@ int padded(int K, bool f32) { return K <= 64 ? 64 : (f32 && K <= 96 ? 96 : (K <=
 //
 // Spans.  Too few blocks for one round are cut along the tokens as often as
 // fills it; each span then needs the state before it, from a walk that reads b
-// and c once more (1 x 65536 x 16 heads of 128: 8 spans, 369 us and 149 us for
+// and c once more (1 x 65536 x 16 heads of 128: 8 spans, 370 us and 152 us for
 // the states).  Cutting two thirds of a round costs more than it gives (94 + 27
 // against 87 us for the 192 pairs above), and so do sequences under 16 chunks.
 struct Walk {
