@@ -21,12 +21,17 @@ missing, every call raises.
 
 The operators of a linear-attention layer and of its training step (lm.py) are
 reached from here too: linattn_fwd, linattn_bwd, linattn_step, group_norm_fwd,
-group_norm_bwd, clip_grad_norm.
+group_norm_bwd, clip_grad_norm.  So are the gated linear recurrence and what
+stands around a mixer in a layer (layer.py): gated_scan_fwd, gated_scan_bwd,
+gated_scan_step.
 """
 import ctypes
 import os
 
+from . import layer as _layer
 from . import lm as _lm
+from .layer import (gated_scan_bwd, gated_scan_fwd, gated_scan_step,  # noqa: F401
+                    gated_scan_workspace_size)
 from .lm import (clip_grad_norm, group_norm_bwd, group_norm_fwd,  # noqa: F401
                  group_norm_workspace_size, linattn_bwd, linattn_bwd_workspace_size, linattn_fwd,
                  linattn_fwd_workspace_size, linattn_step)
@@ -102,6 +107,7 @@ def load_library():
     lib.ssm_abi_version.restype = ci
     lib.ssm_abi_version.argtypes = []
     _lm.declare(lib)
+    _layer.declare(lib)
     _lib = lib
     return lib
 
