@@ -9,6 +9,12 @@
  *   ssm_gated_scan_fwd, ssm_gated_scan_bwd, ssm_gated_scan_step
  *       a recurrence of one state per channel whose decay and input are gated
  *       by the data: sequences, gradients, one token.
+ *   ssm_add_norm_fwd, ssm_add_norm_bwd
+ *       a residual, a dropped-out branch and the layer or RMS norm of their sum.
+ *   ssm_dropout
+ *       dropout from a counter-based generator, the mask never stored.
+ *   ssm_rotary
+ *       rotary positions of queries and keys, and their gradients.
  */
 #ifndef SSM66_LAYER_H
 #define SSM66_LAYER_H
@@ -80,6 +86,97 @@ int ssm_gated_scan_bwd(const void* x, const void* r, const void* i, const float*
 int ssm_gated_scan_step(float* state, const void* x, const void* r, const void* i,
                         const float* decay, void* y, int64_t batch, int64_t dim, int io_dtype,
                         void* stream);
+
+/*
+ * Random numbers of ssm_dropout and the add_norm calls: Philox4x32 with ten
+ * rounds under the key rng[0] (low word first).  Value e of a tensor (its place
+ * in row-major order) takes word e % 4 of the block with the 128-bit counter
+ * (e / 4, rng[1] + site), low words first; it is dropped where word < p 2^32
+ * (rounded down), else multiplied with 1 / (1 - p).  rng lies in device memory,
+ * so that a captured graph draws anew when the program moves rng[1] on; a
+ * backward call takes the rng and site of its forward.
+ *   rng  : (2) int64, device: seed and offset; may be NULL where p is 0
+ *   site : added to the offset: one number for each place that drops
+ *   p    : 0 <= p < 1
+ *
+ * Dropout: y = dropout(x) + residual (NULL: none).
+ *   x           : (n) io_dtype
+ *   residual, y : (n) out_dtype; y may be x (of one type) or residual
+ * The gradient of x is ssm_dropout of dy, without a residual, from out_dtype to
+ * io_dtype.  Tensors are aligned to their element size (16 bytes is fastest);
+ * zero n is a no-op.  A dropped value counts as 0 whatever it is.
+ */
+int ssm_dropout(const void* x, const void* residual, const int64_t* rng, int64_t site, float p,
+                void* y, int64_t n, int io_dtype, int out_dtype, void* stream);
+
+/* norms of ssm_add_norm_fwd */
+#define SSM_NORM_LAYER 0
+#define SSM_NORM_RMS 1
+
+/*
+ * A residual stream, a branch that joins it, and the norm of their sum:
+ *   h = residual + dropout(x)   (rounded to h's type; the norm is of that),
+ *   y = (h - mean) / sqrt(var + eps) weight + bias       (SSM_NORM_LAYER),
+ *   y = h / sqrt(mean of squares + eps) weight + bias    (SSM_NORM_RMS)
+ * over each row, the variance over the same values (not one less).
+ *   x, y         : (rows, dim), io_dtype
+ *   residual, h  : (rows, dim), h_dtype, which is io_dtype or SSM_F32; either
+ *                  may be NULL (no residual; h not kept).  h may be residual
+ *   weight, bias : (dim) float32, or NULL (one, zero)
+ *   mean, rstd   : (rows) float32, or NULL: what ssm_add_norm_bwd takes (mean
+ *                  is not written by the RMS norm)
+ * y may be x.  dim at most 16384 (else SSM_ERR_UNSUPPORTED).  Tensors are
+ * aligned to their element size (to 16 bytes, and with dim a multiple of 8, is
+ * fastest).  Zero rows is a no-op.
+ */
+int ssm_add_norm_fwd(const void* x, const void* residual, const float* weight, const float* bias,
+                     int norm, float eps, float p, const int64_t* rng, int64_t site, void* y,
+                     void* h, float* mean, float* rstd, int64_t rows, int64_t dim, int io_dtype,
+                     int h_dtype, void* stream);
+
+/*
+ * Gradients of ssm_add_norm_fwd, from the h, mean and rstd it wrote (without a
+ * residual and with p = 0, h is x).
+ *   dy             : (rows, dim), io_dtype
+ *   dh             : (rows, dim), h_dtype, the gradient of h from elsewhere, or
+ *                    NULL (zero)
+ *   dx             : (rows, dim), io_dtype
+ *   dresidual      : (rows, dim), h_dtype, or NULL
+ *   dweight, dbias : (dim) float32, or NULL
+ * Outputs are overwritten; dx may be dy, dresidual may be dh.  workspace:
+ * ssm_add_norm_workspace_size(...) bytes, 256-byte aligned (NULL and 0 where
+ * neither dweight nor dbias is asked for).  Zero rows writes zeros to dweight
+ * and dbias.  All sums are taken in a fixed order: repeated calls give identical
+ * bits.
+ */
+size_t ssm_add_norm_workspace_size(int64_t rows, int64_t dim);
+int ssm_add_norm_bwd(const void* h, const void* dy, const void* dh, const float* weight, int norm,
+                     const float* mean, const float* rstd, float p, const int64_t* rng,
+                     int64_t site, void* dx, void* dresidual, float* dweight, float* dbias,
+                     void* workspace, size_t workspace_bytes, int64_t rows, int64_t dim,
+                     int io_dtype, int h_dtype, void* stream);
+
+/*
+ * Rotary positions.  Pair j of each head is turned by the angle t = position
+ * freqs[j] and scaled:
+ *   (a, b) -> mscale (a cos t - b sin t, b cos t + a sin t),
+ * a and b the elements 2j and 2j + 1 of the head (interleaved != 0) or j and
+ * j + rot / 2.  The elements from rot on are copied.
+ *   q, q_out  : (batch, seqlen, heads, dim), io dtype
+ *   k, k_out  : (batch, seqlen, kheads, dim), or NULL with kheads = 0
+ *   freqs     : (rot / 2) float32, taken as exact (the angle is formed in 64 bits)
+ *   positions : (batch, seqlen) int32, or NULL: 0 .. seqlen - 1 in each entry
+ *   inverse   : nonzero turns by -t, which is the gradient of the call without
+ * q_out may be q and k_out may be k.  rot is even, 2 <= rot <= dim.  Tensors are
+ * aligned to their element size (16 bytes, with dim and rot -- halves: rot / 2 --
+ * multiples of 16 bytes, is fastest).  heads, kheads and dim at most 2^20, batch
+ * * seqlen * (heads + kheads) * dim below 2^38, seqlen below 2^31 (else
+ * SSM_ERR_UNSUPPORTED).  Zero batch or seqlen is a no-op.
+ */
+int ssm_rotary(const void* q, const void* k, const float* freqs, const int32_t* positions,
+               float mscale, int interleaved, int inverse, void* q_out, void* k_out, int64_t batch,
+               int64_t seqlen, int64_t heads, int64_t kheads, int64_t dim, int64_t rot,
+               int io_dtype, void* stream);
 
 #ifdef __cplusplus
 }

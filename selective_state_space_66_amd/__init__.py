@@ -23,15 +23,17 @@ The operators of a linear-attention layer and of its training step (lm.py) are
 reached from here too: linattn_fwd, linattn_bwd, linattn_step, group_norm_fwd,
 group_norm_bwd, clip_grad_norm.  So are the gated linear recurrence and what
 stands around a mixer in a layer (layer.py): gated_scan_fwd, gated_scan_bwd,
-gated_scan_step.
+gated_scan_step, add_norm_fwd, add_norm_bwd, dropout_fwd, dropout_bwd,
+rotary_freqs, rotary_fwd, rotary_bwd.
 """
 import ctypes
 import os
 
 from . import layer as _layer
 from . import lm as _lm
-from .layer import (gated_scan_bwd, gated_scan_fwd, gated_scan_step,  # noqa: F401
-                    gated_scan_workspace_size)
+from .layer import (add_norm_bwd, add_norm_fwd, add_norm_workspace_size,  # noqa: F401
+                    dropout_bwd, dropout_fwd, gated_scan_bwd, gated_scan_fwd, gated_scan_step,
+                    gated_scan_workspace_size, rotary_bwd, rotary_freqs, rotary_fwd)
 from .lm import (clip_grad_norm, group_norm_bwd, group_norm_fwd,  # noqa: F401
                  group_norm_workspace_size, linattn_bwd, linattn_bwd_workspace_size, linattn_fwd,
                  linattn_fwd_workspace_size, linattn_step)

@@ -14,7 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libssm66_hip.so")
 SOURCES = ["ssm_api.hip", "scan_fwd.hip", "scan_tpar.hip", "scan_wave8.hip", "scan_bwd.hip", "scan_bwd_wave.hip", "step.hip", "conv1d.hip", "ssd.hip",
            "probe.hip", "lm_api.hip", "linattn.hip", "linattn_bf16.hip", "linattn_f32.hip",
-           "group_norm.hip", "grad_clip.hip", "layer_api.hip", "gated_scan.hip"]
+           "group_norm.hip", "grad_clip.hip", "layer_api.hip", "gated_scan.hip", "add_norm.hip",
+           "dropout.hip", "rotary.hip"]
 
 HIPCC_FLAGS = [
     "-O3", "-std=c++17", "-fPIC",

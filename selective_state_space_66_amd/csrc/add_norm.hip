@@ -1,0 +1,378 @@
+// add_norm.hip -- a residual, a dropped-out branch, and the norm of their sum.
+//
+//   h = residual + dropout(x),  in h's type,
+//   layer: xh = (h - mean) rstd, rstd = 1 / sqrt(sum (h - mean)^2 / n + eps);
+//   RMS:   xh = h rstd,          rstd = 1 / sqrt(sum h^2 / n + eps);
+//   y = xh w + b.
+// Backwards, with dn = dy w and dh what reaches h from elsewhere,
+//   dH = rstd (dn - [sum dn / n] - xh sum(dn xh) / n) + dh   ([]: layer only),
+//   dresidual = dH,  dx = dropout's map of dH,  dw = sum dy xh,  db = sum dy.
+//
+// HBM bounds all of it.  A row is read once and held by 16 to 64 lanes or by two
+// to sixteen waves, eight neighbouring values a lane (sixteen past 8192); the
+// sums go over the lanes by shuffles and over the waves through LDS.  A thread
+// keeps its columns over all the rows it takes, so the backward adds dw and db
+// in registers; a block leaves one row of partial sums, added up in a fixed
+// order by a kernel of its own.  All sums are fp32, those over the rows' blocks
+// fp64.
+#include "add_norm_launch.h"
+#include "vec_io.h"
+
+namespace ssm66 {
+namespace add_norm {
+
+namespace {
+
+// LPR lanes hold a row, CNT values each, VEC neighbouring ones at a time
+// (VEC == 1: dims that are no multiple of eight, tensors off 16 bytes).
+template <int LPR, int CNT, int VEC>
+struct Form {
+  static constexpr int kThreads = LPR > 128 ? LPR : 256;
+  static constexpr int kRows = kThreads / LPR;  // of a block at a time
+  static constexpr int kVecs = CNT / VEC;
+};
+
+// Sums of two values over the lanes of a row, to all of them.  `part` has room
+// for the waves of a block; a second call uses the other half.
+template <int LPR>
+__device__ __forceinline__ void row_sums(float& a, float& b, float2* part) {
+#pragma unroll
+  for (int m = (LPR < 64 ? LPR : 64) / 2; m > 0; m >>= 1) {
+    a += __shfl_xor(a, m);
+    b += __shfl_xor(b, m);
+  }
+  if constexpr (LPR > 64) {
+    constexpr int N = LPR / 64;
+    const int w = (int)threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) part[w] = make_float2(a, b);
+    __syncthreads();
+    const float2* const mine = part + w / N * N;
+    a = b = 0.0f;
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      a += mine[q].x;
+      b += mine[q].y;
+    }
+  }
+}
+
+template <typename T, typename TH, int LPR, int CNT, int VEC>
+__global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void fwd_kernel(const Args p) {
+  typedef Form<LPR, CNT, VEC> F;
+  __shared__ float2 part[2][16];
+  const int l = (int)threadIdx.x % LPR;
+  const int64_t r0 = (int64_t)blockIdx.x * F::kRows + (int)threadIdx.x / LPR;
+  const int64_t step = (int64_t)gridDim.x * F::kRows;
+  const float inv = 1.0f / (float)p.dim;
+  uint64_t seed = 0, offset = 0;
+  if (p.drop.rng) {
+    seed = (uint64_t)p.drop.rng[0];
+    offset = (uint64_t)p.drop.rng[1] + p.drop.site;
+  }
+  float w[F::kVecs][VEC], b[F::kVecs][VEC];
+#pragma unroll
+  for (int j = 0; j < F::kVecs; ++j) {
+    const int c = (l + j * LPR) * VEC;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      w[j][k] = p.weight && c < p.dim ? p.weight[c + k] : 1.0f;
+      b[j][k] = p.bias && c < p.dim ? p.bias[c + k] : 0.0f;
+    }
+  }
+  // whole blocks stay for the barriers: the rows past the last are empty
+  const int64_t rounds = (p.rows + step - 1) / step;
+  for (int64_t q = 0; q < rounds; ++q) {
+    const int64_t row = r0 + q * step;
+    const bool real = row < p.rows;
+    const int64_t base = row * p.dim;
+    float v[F::kVecs][VEC];
+    float s = 0.0f, sq = 0.0f;
+#pragma unroll
+    for (int j = 0; j < F::kVecs; ++j) {
+      const int c = (l + j * LPR) * VEC;
+      if (real && c < p.dim) {
+        float res[VEC];
+        load_n<VEC>((const T*)p.x + base + c, v[j]);
+        if (p.residual) load_n<VEC>((const TH*)p.residual + base + c, res);
+        if (p.drop.rng) {
+          float f[VEC];
+          drop_factors<VEC>(p.drop, seed, offset, base + c, f);
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) v[j][k] = dropped(v[j][k], f[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          if (p.residual) v[j][k] += res[k];
+          v[j][k] = as_stored(v[j][k], (const TH*)nullptr);
+        }
+        if (p.h) store_n<VEC>((TH*)p.h + base + c, v[j]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[j][k] = 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        s += v[j][k];
+        sq = fmaf(v[j][k], v[j][k], sq);
+      }
+    }
+    row_sums<LPR>(s, sq, part[0]);
+    float mean = 0.0f, var = sq * inv;
+    if (!p.rms) {
+      // the squares about the mean as rounded, and what the rounding left of it
+      mean = s * inv;
+      float left = 0.0f;
+      sq = 0.0f;
+#pragma unroll
+      for (int j = 0; j < F::kVecs; ++j) {
+        const bool in = (l + j * LPR) * VEC < p.dim;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          v[j][k] = in ? v[j][k] - mean : 0.0f;
+          left += v[j][k];
+          sq = fmaf(v[j][k], v[j][k], sq);
+        }
+      }
+      row_sums<LPR>(left, sq, part[1]);
+      left *= inv;
+      var = fmaf(-left, left, sq * inv);
+      var = var < 0.0f ? 0.0f : var;  // (a NaN stays one)
+      mean += left;
+#pragma unroll
+      for (int j = 0; j < F::kVecs; ++j)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[j][k] -= left;
+    }
+    const float rstd = 1.0f / sqrtf(var + p.eps);
+#pragma unroll
+    for (int j = 0; j < F::kVecs; ++j) {
+      const int c = (l + j * LPR) * VEC;
+      if (real && c < p.dim) {
+        float y[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) y[k] = fmaf(v[j][k] * rstd, w[j][k], b[j][k]);
+        store_n<VEC>((T*)p.y + base + c, y);
+      }
+    }
+    if (real && l == 0) {
+      if (p.mean && !p.rms) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+    if constexpr (LPR > 64) __syncthreads();  // part[0] has been read
+  }
+}
+
+template <typename T, typename TH, int LPR, int CNT, int VEC>
+__global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void bwd_kernel(const Args p) {
+  typedef Form<LPR, CNT, VEC> F;
+  __shared__ float2 part[2][16];
+  const int l = (int)threadIdx.x % LPR;
+  const int64_t r0 = (int64_t)blockIdx.x * F::kRows + (int)threadIdx.x / LPR;
+  const int64_t step = (int64_t)gridDim.x * F::kRows;
+  const float inv = 1.0f / (float)p.dim;
+  uint64_t seed = 0, offset = 0;
+  if (p.drop.rng) {
+    seed = (uint64_t)p.drop.rng[0];
+    offset = (uint64_t)p.drop.rng[1] + p.drop.site;
+  }
+  float w[F::kVecs][VEC], dw[F::kVecs][VEC], db[F::kVecs][VEC];
+#pragma unroll
+  for (int j = 0; j < F::kVecs; ++j) {
+    const int c = (l + j * LPR) * VEC;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      w[j][k] = p.weight && c < p.dim ? p.weight[c + k] : 1.0f;
+      dw[j][k] = db[j][k] = 0.0f;
+    }
+  }
+  const int64_t rounds = (p.rows + step - 1) / step;
+  for (int64_t q = 0; q < rounds; ++q) {
+    const int64_t row = r0 + q * step;
+    const bool real = row < p.rows;
+    const int64_t base = row * p.dim;
+    float xh[F::kVecs][VEC], dy[F::kVecs][VEC], dh[F::kVecs][VEC];
+#pragma unroll
+    for (int j = 0; j < F::kVecs; ++j) {
+      const int c = (l + j * LPR) * VEC;
+      if (real && c < p.dim) {
+        load_n<VEC>((const TH*)p.h + base + c, xh[j]);
+        load_n<VEC>((const T*)p.dy + base + c, dy[j]);
+        if (p.dh) load_n<VEC>((const TH*)p.dh + base + c, dh[j]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) xh[j][k] = dy[j][k] = 0.0f;
+      }
+    }
+    const float mean = real && !p.rms ? p.mean[row] : 0.0f, rstd = real ? p.rstd[row] : 0.0f;
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < F::kVecs; ++j)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        xh[j][k] = (xh[j][k] - mean) * rstd;  // past the row's end dy is 0
+        dw[j][k] = fmaf(dy[j][k], xh[j][k], dw[j][k]);
+        db[j][k] += dy[j][k];
+        dy[j][k] *= w[j][k];
+        s1 += dy[j][k];
+        s2 = fmaf(dy[j][k], xh[j][k], s2);
+      }
+    row_sums<LPR>(s1, s2, part[q & 1]);
+    s1 = p.rms ? 0.0f : s1 * inv;
+    s2 *= inv;
+#pragma unroll
+    for (int j = 0; j < F::kVecs; ++j) {
+      const int c = (l + j * LPR) * VEC;
+      if (real && c < p.dim) {
+        float g[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          g[k] = rstd * (dy[j][k] - s1 - xh[j][k] * s2);
+          if (p.dh) g[k] += dh[j][k];
+        }
+        if (p.dresidual) store_n<VEC>((TH*)p.dresidual + base + c, g);
+        if (p.drop.rng) {
+          float f[VEC];
+          drop_factors<VEC>(p.drop, seed, offset, base + c, f);
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) g[k] = dropped(g[k], f[k]);
+        }
+        store_n<VEC>((T*)p.dx + base + c, g);
+      }
+    }
+  }
+  if (!p.part) return;
+  // the block's rows added in order, then one row of partial sums (dw, db)
+  __shared__ float2 sums[F::kThreads];
+#pragma unroll
+  for (int j = 0; j < F::kVecs; ++j)
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      const int c = (l + j * LPR) * VEC + k;
+      float2 t = make_float2(dw[j][k], db[j][k]);
+      if (F::kRows > 1) {
+        __syncthreads();
+        sums[threadIdx.x] = t;
+        __syncthreads();
+        if ((int)threadIdx.x < LPR)
+          for (int r = 1; r < F::kRows; ++r) {
+            t.x += sums[threadIdx.x + r * LPR].x;
+            t.y += sums[threadIdx.x + r * LPR].y;
+          }
+      }
+      if ((int)threadIdx.x < LPR && c < p.dim) p.part[(int64_t)blockIdx.x * p.dim + c] = t;
+    }
+}
+
+// dw and db from the blocks' partial sums: 16 columns of a block, 16 groups of
+// lanes that take every 16th row, added in fp64 in a fixed order
+__global__ __launch_bounds__(256) void column_sum_kernel(const float2* part, float* dw, float* db,
+                                                         int blocks, int dim) {
+  __shared__ double2 sums[16][16];
+  const int l = (int)threadIdx.x & 15, g = (int)threadIdx.x >> 4;
+  const int c = (int)blockIdx.x * 16 + l;
+  double x = 0.0, y = 0.0;
+  if (c < dim) {
+    int r = g;
+    for (; r + 112 < blocks; r += 128) {
+      float2 t[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) t[q] = part[(int64_t)(r + 16 * q) * dim + c];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        x += t[q].x;
+        y += t[q].y;
+      }
+    }
+    for (; r < blocks; r += 16) {
+      const float2 t = part[(int64_t)r * dim + c];
+      x += t.x;
+      y += t.y;
+    }
+  }
+  sums[g][l] = make_double2(x, y);
+  __syncthreads();
+  if (g == 0 && c < dim) {
+    for (int q = 1; q < 16; ++q) {
+      x += sums[q][l].x;
+      y += sums[q][l].y;
+    }
+    if (dw) dw[c] = (float)x;
+    if (db) db[c] = (float)y;
+  }
+}
+
+constexpr int64_t kBackThreads = 196608;  // of the backward's blocks together
+
+struct Call {
+  Args p;
+  bool back;
+  hipStream_t s;
+  int* blocks;  // how many were launched
+};
+
+template <typename T, typename TH, int LPR, int CNT, int VEC>
+hipError_t launch(const Call& c) {
+  typedef Form<LPR, CNT, VEC> F;
+  int64_t n = (c.p.rows + F::kRows - 1) / F::kRows;
+  const int64_t most = c.back ? kBackThreads / F::kThreads : 2 * kBackThreads / F::kThreads;
+  if (n > most) n = most;
+  *c.blocks = (int)n;
+  if (c.back) bwd_kernel<T, TH, LPR, CNT, VEC><<<(unsigned)n, F::kThreads, 0, c.s>>>(c.p);
+  else fwd_kernel<T, TH, LPR, CNT, VEC><<<(unsigned)n, F::kThreads, 0, c.s>>>(c.p);
+  return hipGetLastError();
+}
+
+template <typename T, typename TH>
+hipError_t pick(const Call& c) {
+  const Args& p = c.p;
+  const uintptr_t all = (uintptr_t)p.x | (uintptr_t)p.residual | (uintptr_t)p.y | (uintptr_t)p.h |
+                        (uintptr_t)p.dy | (uintptr_t)p.dh | (uintptr_t)p.dx | (uintptr_t)p.dresidual;
+  const int d = p.dim;
+  if (all % 16 == 0 && d % 8 == 0) {
+    if (d <= 128) return launch<T, TH, 16, 8, 8>(c);
+    if (d <= 256) return launch<T, TH, 32, 8, 8>(c);
+    if (d <= 512) return launch<T, TH, 64, 8, 8>(c);
+    if (d <= 1024) return launch<T, TH, 128, 8, 8>(c);
+    if (d <= 1536) return launch<T, TH, 192, 8, 8>(c);
+    if (d <= 2048) return launch<T, TH, 256, 8, 8>(c);
+    if (d <= 4096) return launch<T, TH, 512, 8, 8>(c);
+    if (d <= 8192) return launch<T, TH, 1024, 8, 8>(c);
+    return launch<T, TH, 1024, 16, 8>(c);
+  }
+  if (d <= 512) return launch<T, TH, 64, 8, 1>(c);
+  if (d <= 2048) return launch<T, TH, 256, 8, 1>(c);
+  if (d <= 8192) return launch<T, TH, 1024, 8, 1>(c);
+  return launch<T, TH, 1024, 16, 1>(c);
+}
+
+hipError_t run(const Call& c, bool x_f32, bool h_f32) {
+  if (x_f32) return pick<float, float>(c);
+  return h_f32 ? pick<bf16_bits, float>(c) : pick<bf16_bits, bf16_bits>(c);
+}
+
+}  // namespace
+
+size_t workspace_bytes(int64_t rows, int64_t dim) {
+  // a block takes a row at least, and 192 threads
+  const int64_t most = kBackThreads / 192, n = rows < most ? rows : most;
+  return (size_t)((n * dim * 8 + 255) / 256 * 256);
+}
+
+hipError_t forward(const Args& p, bool x_f32, bool h_f32, hipStream_t s) {
+  int blocks;
+  return run(Call{p, false, s, &blocks}, x_f32, h_f32);
+}
+
+hipError_t backward(const Args& p, bool x_f32, bool h_f32, hipStream_t s) {
+  int blocks = 0;
+  if (p.rows > 0) {
+    const hipError_t e = run(Call{p, true, s, &blocks}, x_f32, h_f32);
+    if (e != hipSuccess) return e;
+  }
+  if (!p.dweight && !p.dbias) return hipSuccess;
+  column_sum_kernel<<<(p.dim + 15) / 16, 256, 0, s>>>(p.part, p.dweight, p.dbias, blocks, p.dim);
+  return hipGetLastError();
+}
+
+}  // namespace add_norm
+}  // namespace ssm66

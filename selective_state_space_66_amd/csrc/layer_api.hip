@@ -5,7 +5,10 @@
 #include <initializer_list>
 
 #include "../../include/ssm66_layer.h"
+#include "add_norm_launch.h"
+#include "dropout_launch.h"
 #include "gated_scan_launch.h"
+#include "rotary_launch.h"
 
 namespace {
 
@@ -44,6 +47,19 @@ ssm66::gated_scan::Args scan_args(const void* x, const void* r, const void* i, c
   a.x = x; a.r = r; a.i = i; a.decay = decay; a.seq_lens = seq_lens; a.reset = reset;
   a.batch = batch; a.L = seqlen; a.dim = (int)dim; a.ws = ws;
   return a;
+}
+
+bool io_type(int t) { return t == SSM_F32 || t == SSM_BF16; }
+
+// sizes, types, rate and norm of the add_norm calls
+int norm_args(int64_t rows, int64_t dim, int norm, float p, int io_dtype, int h_dtype) {
+  if (rows < 0 || dim < 1) return SSM_ERR_SHAPE;
+  if (!io_type(io_dtype) || !io_type(h_dtype)) return SSM_ERR_DTYPE;
+  if (io_dtype == SSM_F32 && h_dtype != SSM_F32) return SSM_ERR_DTYPE;
+  if (norm != SSM_NORM_LAYER && norm != SSM_NORM_RMS) return SSM_ERR_FLAG;
+  if (!(p >= 0.0f && p < 1.0f)) return SSM_ERR_FLAG;
+  if (!product_fits({rows, dim})) return SSM_ERR_SHAPE;
+  return dim > ssm66::add_norm::kMostDim ? SSM_ERR_UNSUPPORTED : SSM_OK;
 }
 
 }  // namespace
@@ -115,6 +131,99 @@ int ssm_gated_scan_step(float* state, const void* x, const void* r, const void* 
   ssm66::gated_scan::StepArgs a;
   a.state = state; a.x = x; a.r = r; a.i = i; a.decay = decay; a.y = y; a.batch = batch; a.dim = (int)dim;
   return status(ssm66::gated_scan::step(a, io_dtype == SSM_F32, (hipStream_t)stream));
+}
+
+int ssm_dropout(const void* x, const void* residual, const int64_t* rng, int64_t site, float p,
+                void* y, int64_t n, int io_dtype, int out_dtype, void* stream) {
+  if (n < 0 || !product_fits({n})) return SSM_ERR_SHAPE;
+  if (!io_type(io_dtype) || !io_type(out_dtype)) return SSM_ERR_DTYPE;
+  if (!(p >= 0.0f && p < 1.0f)) return SSM_ERR_FLAG;
+  if (n == 0) return SSM_OK;
+  if (!x || !y || (p > 0.0f && !rng)) return SSM_ERR_NULL;
+  if (!aligned(x, width(io_dtype)) || !aligned_all(width(out_dtype), {residual, y}) || !aligned(rng, 8))
+    return SSM_ERR_ALIGN;
+  if (x == y && io_dtype != out_dtype) return SSM_ERR_FLAG;  // written before its neighbours are read
+  ssm66::dropout::Args a;
+  a.x = x; a.residual = residual; a.y = y; a.n = n; a.drop = ssm66::drop_of(p, rng, site);
+  return status(ssm66::dropout::run(a, io_dtype == SSM_F32, out_dtype == SSM_F32, (hipStream_t)stream));
+}
+
+int ssm_add_norm_fwd(const void* x, const void* residual, const float* weight, const float* bias,
+                     int norm, float eps, float p, const int64_t* rng, int64_t site, void* y,
+                     void* h, float* mean, float* rstd, int64_t rows, int64_t dim, int io_dtype,
+                     int h_dtype, void* stream) {
+  const int st = norm_args(rows, dim, norm, p, io_dtype, h_dtype);
+  if (st != SSM_OK) return st;
+  if (rows == 0) return SSM_OK;
+  if (!x || !y || (p > 0.0f && !rng)) return SSM_ERR_NULL;
+  if (!aligned_all(width(io_dtype), {x, y}) || !aligned_all(width(h_dtype), {residual, h}) ||
+      !aligned_all(4, {weight, bias, mean, rstd}) || !aligned(rng, 8))
+    return SSM_ERR_ALIGN;
+  if (h == y || (h == x && io_dtype != h_dtype) || (residual == y && residual)) return SSM_ERR_FLAG;
+  ssm66::add_norm::Args a = {};
+  a.x = x; a.residual = residual; a.weight = weight; a.bias = bias; a.y = y; a.h = h;
+  a.mean = mean; a.rstd = rstd; a.drop = ssm66::drop_of(p, rng, site);
+  a.rows = rows; a.dim = (int)dim; a.rms = norm == SSM_NORM_RMS; a.eps = eps;
+  return status(ssm66::add_norm::forward(a, io_dtype == SSM_F32, h_dtype == SSM_F32, (hipStream_t)stream));
+}
+
+size_t ssm_add_norm_workspace_size(int64_t rows, int64_t dim) {
+  if (norm_args(rows, dim, SSM_NORM_LAYER, 0.0f, SSM_F32, SSM_F32) != SSM_OK) return 0;
+  return ssm66::add_norm::workspace_bytes(rows, dim);
+}
+
+int ssm_add_norm_bwd(const void* h, const void* dy, const void* dh, const float* weight, int norm,
+                     const float* mean, const float* rstd, float p, const int64_t* rng,
+                     int64_t site, void* dx, void* dresidual, float* dweight, float* dbias,
+                     void* workspace, size_t workspace_bytes, int64_t rows, int64_t dim,
+                     int io_dtype, int h_dtype, void* stream) {
+  const int st = norm_args(rows, dim, norm, p, io_dtype, h_dtype);
+  if (st != SSM_OK) return st;
+  if (rows > 0 && (!h || !dy || !dx || !rstd || (norm == SSM_NORM_LAYER && !mean) || (p > 0.0f && !rng)))
+    return SSM_ERR_NULL;
+  if (!aligned_all(width(io_dtype), {dy, dx}) || !aligned_all(width(h_dtype), {h, dh, dresidual}) ||
+      !aligned_all(4, {weight, mean, rstd, dweight, dbias}) || !aligned(rng, 8) || !aligned(workspace, 256))
+    return SSM_ERR_ALIGN;
+  if (rows > 0 && (dx == dresidual || dx == h || dresidual == h || (dx == dh && io_dtype != h_dtype) ||
+                   (dresidual == dy && io_dtype != h_dtype)))
+    return SSM_ERR_FLAG;
+  const bool sums = dweight || dbias;
+  const size_t need = sums ? ssm66::add_norm::workspace_bytes(rows, dim) : 0;
+  if (need > 0 && !workspace) return SSM_ERR_NULL;
+  if (workspace_bytes < need) return SSM_ERR_SHAPE;
+  ssm66::add_norm::Args a = {};
+  a.h = (void*)h; a.dy = dy; a.dh = dh; a.weight = weight; a.mean = (float*)mean; a.rstd = (float*)rstd;
+  a.drop = ssm66::drop_of(p, rng, site); a.dx = dx; a.dresidual = dresidual;
+  a.dweight = dweight; a.dbias = dbias; a.part = sums ? (float2*)workspace : nullptr;
+  a.rows = rows; a.dim = (int)dim; a.rms = norm == SSM_NORM_RMS;
+  return status(ssm66::add_norm::backward(a, io_dtype == SSM_F32, h_dtype == SSM_F32, (hipStream_t)stream));
+}
+
+int ssm_rotary(const void* q, const void* k, const float* freqs, const int32_t* positions,
+               float mscale, int interleaved, int inverse, void* q_out, void* k_out, int64_t batch,
+               int64_t seqlen, int64_t heads, int64_t kheads, int64_t dim, int64_t rot,
+               int io_dtype, void* stream) {
+  if (batch < 0 || seqlen < 0 || heads < 1 || kheads < 0 || dim < 1) return SSM_ERR_SHAPE;
+  if (rot < 2 || rot % 2 != 0 || rot > dim) return SSM_ERR_SHAPE;
+  if (!io_type(io_dtype)) return SSM_ERR_DTYPE;
+  const int64_t most = (int64_t)1 << 20;
+  if (!product_fits({batch, seqlen}) || !product_fits({batch, seqlen, heads, dim}) ||
+      !product_fits({batch, seqlen, kheads, dim}))
+    return SSM_ERR_SHAPE;
+  if (batch == 0 || seqlen == 0) return SSM_OK;
+  if (!q || !q_out || !freqs || (kheads > 0 && (!k || !k_out))) return SSM_ERR_NULL;
+  if (heads > most || kheads > most || dim > most || seqlen > 0x7fffffff ||
+      !ssm66::rotary::fits(batch * seqlen, (int)(heads + kheads), (int)dim))
+    return SSM_ERR_UNSUPPORTED;
+  if (!aligned_all(width(io_dtype), {q, k, q_out, k_out}) || !aligned_all(4, {freqs, positions}))
+    return SSM_ERR_ALIGN;
+  if (kheads > 0 && (q_out == k || k_out == q || q_out == k_out)) return SSM_ERR_FLAG;
+  ssm66::rotary::Args a = {};
+  a.q = q; a.k = kheads > 0 ? k : nullptr; a.qo = q_out; a.ko = kheads > 0 ? k_out : nullptr;
+  a.freqs = freqs; a.positions = positions; a.tokens = batch * seqlen; a.L = seqlen;
+  a.H = (int)heads; a.Hk = (int)kheads; a.D = (int)dim; a.pairs = (int)(rot / 2);
+  a.mscale = mscale; a.sign = inverse ? -1.0f : 1.0f; a.interleaved = interleaved != 0;
+  return status(ssm66::rotary::run(a, io_dtype == SSM_F32, (hipStream_t)stream));
 }
 
 }  // extern "C"

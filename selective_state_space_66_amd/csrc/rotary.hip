@@ -1,0 +1,148 @@
+// rotary.hip -- rotary positions of queries and keys.
+//
+// Pair j of a head is turned by the angle t = position * freqs[j]:
+//   (a, b) -> mscale (a cos t - b sin t, b cos t + a sin t),
+// a and b the elements 2j and 2j + 1 (interleaved) or j and j + pairs (halves).
+// The gradient is the turn by -t.
+//
+// HBM bounds it.  A thread keeps the cosines and sines of its pairs of one token
+// and goes over the heads of queries and keys with them, 16 bytes an access (the
+// two halves of a pair are two); few tokens are spread over the heads too.
+//
+// Angles: position * freqs / 2 pi in fp64 (2^31 positions leave 6e-8 of a turn),
+// less the nearest quarter turn, then the series of sine and cosine up to an
+// eighth of a turn in fp32, which leave out less than 2e-9.
+#include "lm_grid.h"
+#include "rotary_launch.h"
+#include "vec_io.h"
+
+namespace ssm66 {
+namespace rotary {
+
+namespace {
+
+__device__ __forceinline__ void turn_of(int position, float freq, float* c, float* s) {
+  const double rev = (double)position * (double)freq * 0.15915494309189535;
+  const double quarter = rint(rev * 4.0);
+  const float x = (float)((rev - quarter * 0.25) * 6.283185307179586);
+  const int k = (int)((int64_t)quarter & 3);
+  const float z = x * x;
+  float sn = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
+  sn = fmaf(z, sn, 8.3333333e-3f);
+  sn = fmaf(z, sn, -1.6666667e-1f);
+  sn = fmaf(x * z, sn, x);
+  float cs = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
+  cs = fmaf(z, cs, -1.3888889e-3f);
+  cs = fmaf(z, cs, 4.1666667e-2f);
+  cs = fmaf(z, cs, -0.5f);
+  cs = fmaf(z, cs, 1.0f);
+  const float a = k & 1 ? sn : cs, b = k & 1 ? cs : sn;
+  *c = k == 1 || k == 2 ? -a : a;
+  *s = k >= 2 ? -b : b;
+}
+
+// VEC elements an access.  Interleaved: a thread has one access, VEC / 2 pairs
+// (VEC == 1: one pair as two elements).  Halves: two accesses, VEC pairs.  The
+// threads past the pairs copy what is not turned.
+template <typename T, int VEC, bool INTER>
+__global__ __launch_bounds__(256) void rotary_kernel(const Args p) {
+  constexpr int W = INTER ? (VEC == 1 ? 2 : VEC) : VEC;      // elements from one thread to the next
+  constexpr int PAIRS = INTER ? W / 2 : VEC;
+  const int64_t n = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+  const int lane = (int)(n % p.lanes);
+  const int64_t rest = n / p.lanes;
+  const int split = (int)(rest % p.splits);
+  const int64_t tok = rest / p.splits;
+  if (tok >= p.tokens) return;
+  const int turning = INTER ? 2 * p.pairs / W : p.pairs / VEC;
+  const int heads = p.H + p.Hk, each = (heads + p.splits - 1) / p.splits;
+  const int h0 = split * each, h1 = h0 + each < heads ? h0 + each : heads;
+  if (lane >= turning) {
+    const int at = 2 * p.pairs + (lane - turning) * VEC;
+    for (int h = h0; h < h1; ++h) {
+      const bool isq = h < p.H;
+      const int64_t row = isq ? (tok * p.H + h) * p.D : (tok * p.Hk + h - p.H) * p.D;
+      float v[VEC];
+      load_n<VEC>((const T*)(isq ? p.q : p.k) + row + at, v);
+      store_n<VEC>((T*)(isq ? p.qo : p.ko) + row + at, v);
+    }
+    return;
+  }
+  const int position = p.positions ? p.positions[tok] : (int)(tok % p.L);
+  float c[PAIRS], s[PAIRS];
+#pragma unroll
+  for (int j = 0; j < PAIRS; ++j) {
+    turn_of(position, p.freqs[lane * PAIRS + j], &c[j], &s[j]);
+    c[j] *= p.mscale;
+    s[j] *= p.mscale * p.sign;
+  }
+  for (int h = h0; h < h1; ++h) {
+    const bool isq = h < p.H;
+    const int64_t row = isq ? (tok * p.H + h) * p.D : (tok * p.Hk + h - p.H) * p.D;
+    const T* const in = (const T*)(isq ? p.q : p.k) + row + lane * W;
+    T* const out = (T*)(isq ? p.qo : p.ko) + row + lane * W;
+    if constexpr (INTER) {
+      float v[W];
+      load_n<W>(in, v);
+#pragma unroll
+      for (int j = 0; j < PAIRS; ++j) {
+        const float a = v[2 * j], b = v[2 * j + 1];
+        v[2 * j] = fmaf(a, c[j], -(b * s[j]));
+        v[2 * j + 1] = fmaf(b, c[j], a * s[j]);
+      }
+      store_n<W>(out, v);
+    } else {
+      float a[VEC], b[VEC];
+      load_n<VEC>(in, a);
+      load_n<VEC>(in + p.pairs, b);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float u = a[j];
+        a[j] = fmaf(u, c[j], -(b[j] * s[j]));
+        b[j] = fmaf(b[j], c[j], u * s[j]);
+      }
+      store_n<VEC>(out, a);
+      store_n<VEC>(out + p.pairs, b);
+    }
+  }
+}
+
+template <typename T, int VEC, bool INTER>
+hipError_t launch(Args p, hipStream_t s) {
+  constexpr int W = INTER ? (VEC == 1 ? 2 : VEC) : VEC;
+  const bool in_place = p.q == p.qo && p.k == p.ko;
+  p.lanes = (INTER ? 2 * p.pairs / W : p.pairs / VEC) + (in_place ? 0 : (p.D - 2 * p.pairs) / VEC);
+  // threads for eight waves a CU before a thread takes more than one head
+  const int heads = p.H + p.Hk;
+  const int64_t wide = p.tokens * p.lanes, want = 256 * 8 * 64;
+  int64_t splits = (want + wide - 1) / wide;
+  if (splits > heads) splits = heads;
+  const int each = (int)((heads + splits - 1) / splits);
+  p.splits = (heads + each - 1) / each;
+  const Grid g = grid_of((wide * p.splits + 255) / 256, 256);
+  rotary_kernel<T, VEC, INTER><<<dim3(g.x, g.more), 256, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t pick(const Args& p, hipStream_t s) {
+  constexpr int VEC = 16 / sizeof(T);
+  const bool wide = (((uintptr_t)p.q | (uintptr_t)p.k | (uintptr_t)p.qo | (uintptr_t)p.ko) & 15) == 0 &&
+                    p.D % VEC == 0 && (p.interleaved ? 2 * p.pairs : p.pairs) % VEC == 0;
+  if (p.interleaved) return wide ? launch<T, VEC, true>(p, s) : launch<T, 1, true>(p, s);
+  return wide ? launch<T, VEC, false>(p, s) : launch<T, 1, false>(p, s);
+}
+
+}  // namespace
+
+bool fits(int64_t tokens, int heads, int D) {
+  // one thread an element at most, 32-bit block numbers
+  return (__int128)tokens * heads * D < (__int128)1 << 38;
+}
+
+hipError_t run(const Args& p, bool f32, hipStream_t s) {
+  return f32 ? pick<float>(p, s) : pick<bf16_bits>(p, s);
+}
+
+}  // namespace rotary
+}  // namespace ssm66

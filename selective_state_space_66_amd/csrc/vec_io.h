@@ -1,0 +1,63 @@
+// vec_io.h -- N neighbouring io values in one or two 16-byte accesses, or in one
+// of their own size (gfx950 device code).
+#pragma once
+
+#include "ssm_device.h"
+
+namespace ssm66 {
+
+template <int N>
+__device__ __forceinline__ void load_n(const float* p, float (&f)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) {
+      const float4 v = ((const float4*)p)[q];
+      f[4 * q] = v.x; f[4 * q + 1] = v.y; f[4 * q + 2] = v.z; f[4 * q + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) f[k] = p[k];
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_n(const bf16_bits* p, float (&f)[N]) {
+  if constexpr (N == 8) {
+    const uint4 v = *(const uint4*)p;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      f[2 * q] = __uint_as_float(w[q] << 16);
+      f[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) f[k] = to_f32(p[k]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_n(float* p, const float (&f)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q)
+      ((float4*)p)[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) p[k] = f[k];
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_n(bf16_bits* p, const float (&f)[N]) {
+  if constexpr (N == 8) {
+    *(uint4*)p = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                            pack_bf16x2(f[6], f[7]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) store_io(p + k, f[k]);
+  }
+}
+
+// the value as it will be read back from memory of its type
+__device__ __forceinline__ float as_stored(float v, const float*) { return v; }
+__device__ __forceinline__ float as_stored(float v, const bf16_bits*) { return (float)(__bf16)v; }
+
+}  // namespace ssm66

@@ -6,12 +6,27 @@ step of the computation runs in the library's HIP kernels.
                                            return_states=False)
     grads = gated_scan_bwd(x, r, i, decay, dy, states, dlast=None, seq_lens=None, reset=None)
     y = gated_scan_step(state, x, r, i, decay)                   # state updated in place
+    y, h, mean, rstd = add_norm_fwd(x, residual=None, weight=None, bias=None, kind="layer",
+                                    eps=1e-5, p=0.0, rng=None, site=0)
+    grads = add_norm_bwd(h, dy, mean, rstd, weight=None, kind="layer", dh=None, p=0.0, rng=None,
+                         site=0)
+    y = dropout_fwd(x, p, rng, site=0, residual=None)
+    dx = dropout_bwd(dy, p, rng, site=0)
+    freqs, mscale = rotary_freqs(rot_dim, theta=10000.0, scaling="none", device="cuda")
+    q, k = rotary_fwd(q, k, freqs, positions=None, mscale=1.0, interleaved=False)
+    dq, dk = rotary_bwd(dq, dk, freqs, positions=None, mscale=1.0, interleaved=False)
+
+rng is a tensor of two int64 on the GPU, seed and offset of a counter-based generator; the
+program moves the offset on from step to step (rng[1] += number of sites), a backward call
+takes its forward's rng and site.
 """
 import ctypes
 import functools
+import math
 
-from .lm import _code, _core, _flags, _on_gpu, _ptr, _stream, _want, _workspace
+from .lm import SSM_BF16, SSM_F32, _code, _core, _flags, _on_gpu, _ptr, _stream, _want, _workspace
 
+_NORMS = {"layer": 0, "rms": 1}
 _CHUNK = 128  # tokens from one kept state of the recurrence to the next
 
 
@@ -26,6 +41,18 @@ def declare(lib):
     lib.ssm_gated_scan_bwd.argtypes = [vp] * 15 + [sz] + [i64] * 3 + [ci, vp]
     lib.ssm_gated_scan_step.restype = ci
     lib.ssm_gated_scan_step.argtypes = [vp] * 6 + [i64] * 2 + [ci, vp]
+    cf = ctypes.c_float
+    lib.ssm_dropout.restype = ci
+    lib.ssm_dropout.argtypes = [vp] * 3 + [i64, cf, vp, i64, ci, ci, vp]
+    lib.ssm_add_norm_workspace_size.restype = sz
+    lib.ssm_add_norm_workspace_size.argtypes = [i64, i64]
+    lib.ssm_add_norm_fwd.restype = ci
+    lib.ssm_add_norm_fwd.argtypes = [vp] * 4 + [ci, cf, cf, vp, i64] + [vp] * 4 + [i64, i64, ci, ci, vp]
+    lib.ssm_add_norm_bwd.restype = ci
+    lib.ssm_add_norm_bwd.argtypes = [vp] * 4 + [ci, vp, vp, cf, vp, i64] + [vp] * 5 + \
+        [sz, i64, i64, ci, ci, vp]
+    lib.ssm_rotary.restype = ci
+    lib.ssm_rotary.argtypes = [vp] * 4 + [cf, ci, ci, vp, vp] + [i64] * 6 + [ci, vp]
 
 
 def _call(c, torch, index, name, *args):
@@ -154,3 +181,243 @@ def gated_scan_step(state, x, r, i, decay, y=None):
     _call(c, torch, index, "ssm_gated_scan_step", _ptr(state), _ptr(x), _ptr(r), _ptr(i),
           _ptr(decay), _ptr(y), batch, dim, code)
     return y
+
+
+def _rng(torch, p, rng, device, index):
+    if not 0.0 <= p < 1.0:
+        raise ValueError(f"p: expected a rate in [0, 1), got {p}")
+    if rng is not None:
+        _want(rng, "rng", (2,), torch.int64, device, index)
+    elif p > 0.0:
+        raise ValueError("rng: two int64 on the GPU (seed, offset) are needed where p is not 0")
+
+
+def _dense(c, torch, x, name):
+    """The GPU's index of a contiguous io tensor, and its type's code."""
+    if not x.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return x.get_device(), _code(c, torch, x)
+
+
+def _dropout(x, p, rng, site, residual, y, dtype, name):
+    c, torch = _core()
+    index, code = _dense(c, torch, x, name)
+    _rng(torch, p, rng, x.device, index)
+    if residual is not None:
+        if residual.dtype != x.dtype and residual.dtype is not torch.float32:
+            raise TypeError(f"residual: expected {x.dtype} or float32, got {residual.dtype}")
+        dtype = residual.dtype
+        _want(residual, "residual", x.shape, dtype, x.device, index)
+    if y is None:
+        y = torch.empty_like(x, dtype=dtype)
+    else:
+        _want(y, "dx" if name == "dy" else "y", x.shape, dtype, x.device, index)
+    _call(c, torch, index, "ssm_dropout", _ptr(x), _ptr(residual), _ptr(rng), site, p, _ptr(y),
+          x.numel(), code, _code(c, torch, y))
+    return y
+
+
+def dropout_fwd(x, p, rng, site=0, residual=None, y=None):
+    """Dropout on the GPU, from a counter-based generator: the mask is never stored.
+
+    x: any shape, float32 or bfloat16; p: the rate, 0 <= p < 1; rng: two int64 on the GPU, seed
+    and offset (None where p is 0); site: a number for each place that drops, added to the
+    offset; residual: optional tensor like x, of x's type or float32, which is added.
+    Returns dropout(x) + residual, of the residual's type (else x's); y may be given, and may
+    be x (of one type) or residual.
+    """
+    return _dropout(x, p, rng, site, residual, y, x.dtype, "x")
+
+
+def dropout_bwd(dy, p, rng, site=0, dtype=None, dx=None):
+    """Gradient of dropout_fwd's x (the residual's is dy), with its p, rng and site.
+
+    dtype: x's type, where it is not dy's.
+    """
+    return _dropout(dy, p, rng, site, None, dx, dtype or dy.dtype, "dy")
+
+
+def _norm_check(c, torch, x, name, kind, weight, bias, p, rng):
+    index, code = _dense(c, torch, x, name)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"{name} must be (..., dim)")
+    if kind not in _NORMS:
+        raise ValueError(f"kind: expected one of {sorted(_NORMS)}, got {kind!r}")
+    dim = x.shape[-1]
+    _want(weight, "weight", (dim,), torch.float32, x.device, index)
+    _want(bias, "bias", (dim,), torch.float32, x.device, index)
+    _rng(torch, p, rng, x.device, index)
+    return x.numel() // dim, dim, index, code
+
+
+@functools.lru_cache(maxsize=512)
+def add_norm_workspace_size(rows, dim):
+    """Bytes of workspace add_norm_bwd needs where dweight or dbias is asked for."""
+    return int(_core()[0].load_library().ssm_add_norm_workspace_size(rows, dim))
+
+
+def add_norm_fwd(x, residual=None, weight=None, bias=None, kind="layer", eps=1e-5, p=0.0, rng=None,
+                 site=0, y=None, h=None, return_stats=True):
+    """A residual, a dropped-out branch and the norm of their sum, on the GPU.
+
+    h = residual + dropout(x), y = norm(h) weight + bias over the last dimension (at most
+    16384); kind: "layer" or "rms".
+    x: (..., dim) float32 or bfloat16; residual: optional, like x, of x's type or float32;
+    weight, bias: optional (dim,) float32; p, rng, site: as for dropout_fwd.
+    h is rounded to the residual's type (else x's), and the norm is of that.
+    Returns (y like x, h, mean, rstd): h is x itself where there is nothing to add or drop; mean
+    and rstd (...) float32 are what add_norm_bwd takes (None if not requested, mean also with
+    "rms").  y may be given, and may be x; h may be given, and may be residual.
+    """
+    c, torch = _core()
+    rows, dim, index, code = _norm_check(c, torch, x, "x", kind, weight, bias, p, rng)
+    f32 = torch.float32
+    h_dtype = x.dtype
+    if residual is not None:
+        if residual.dtype != x.dtype and residual.dtype is not f32:
+            raise TypeError(f"residual: expected {x.dtype} or float32, got {residual.dtype}")
+        h_dtype = residual.dtype
+        _want(residual, "residual", x.shape, h_dtype, x.device, index)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _want(y, "y", x.shape, x.dtype, x.device, index)
+    same = h is None and residual is None and p == 0.0
+    if h is not None:
+        _want(h, "h", x.shape, h_dtype, x.device, index)
+    elif not same:
+        h = torch.empty_like(x, dtype=h_dtype)
+    elif y is x:
+        raise ValueError("y: may be x only where h is a tensor of its own")
+    mean = rstd = None
+    if return_stats:
+        rstd = torch.empty(x.shape[:-1], dtype=f32, device=x.device)
+        mean = torch.empty_like(rstd) if kind == "layer" else None
+    _call(c, torch, index, "ssm_add_norm_fwd", _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias),
+          _NORMS[kind], eps, p, _ptr(rng), site, _ptr(y), _ptr(h), _ptr(mean), _ptr(rstd), rows, dim,
+          code, SSM_F32 if h_dtype is f32 else SSM_BF16)
+    return y, x if same else h, mean, rstd
+
+
+def add_norm_bwd(h, dy, mean, rstd, weight=None, kind="layer", dh=None, p=0.0, rng=None, site=0,
+                 need_dweight=None, need_dbias=False, need_dresidual=True, workspace=None):
+    """Gradients of add_norm_fwd on the GPU, from the h, mean and rstd it returned.
+
+    dy: like y; dh: optional, like h, the gradient that reaches h from elsewhere.
+    Returns a dict: dx (dy's type), dresidual (h's type), dweight and dbias (float32), None where
+    not needed; dweight is needed where weight is given, unless need_dweight says otherwise.
+    """
+    c, torch = _core()
+    rows, dim, index, code = _norm_check(c, torch, dy, "dy", kind, weight, None, p, rng)
+    f32, dev = torch.float32, dy.device
+    if h.dtype != dy.dtype and h.dtype is not f32:
+        raise TypeError(f"h: expected {dy.dtype} or float32, got {h.dtype}")
+    _want(h, "h", dy.shape, h.dtype, dev, index)
+    _want(dh, "dh", dy.shape, h.dtype, dev, index)
+    _want(rstd, "rstd", dy.shape[:-1], f32, dev, index)
+    if kind == "layer":
+        _want(mean, "mean", dy.shape[:-1], f32, dev, index)
+    if need_dweight is None:
+        need_dweight = weight is not None
+    g = dict(dx=torch.empty_like(dy), dresidual=torch.empty_like(h) if need_dresidual else None,
+             dweight=torch.empty((dim,), dtype=f32, device=dev) if need_dweight else None,
+             dbias=torch.empty((dim,), dtype=f32, device=dev) if need_dbias else None)
+    need = add_norm_workspace_size(rows, dim) if need_dweight or need_dbias else 0
+    ws, size = _workspace(torch, workspace, need, dev)
+    _call(c, torch, index, "ssm_add_norm_bwd", _ptr(h), _ptr(dy), _ptr(dh), _ptr(weight),
+          _NORMS[kind], _ptr(mean) if kind == "layer" else None, _ptr(rstd), p, _ptr(rng), site,
+          _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(ws), size,
+          rows, dim, code, SSM_F32 if h.dtype is f32 else SSM_BF16)
+    return g
+
+
+def rotary_freqs(rot_dim, theta=10000.0, scaling="none", factor=1.0, original_length=None,
+                 beta_fast=32.0, beta_slow=1.0, device=None):
+    """The angle per position of each pair, (rot_dim / 2,) float32, and the factor mscale of the
+    outputs: what rotary_fwd takes, computed once.
+
+    theta ** (-2 j / rot_dim), and for contexts `factor` times longer than those trained on
+      "linear": all divided by the factor;
+      "ntk": theta times factor ** (rot_dim / (rot_dim - 2)), so that the slowest pair is;
+      "yarn": divided for the pairs that turn less than beta_slow times in original_length
+      positions, kept for those that turn more than beta_fast times, with a ramp between, and
+      mscale = 1 + 0.1 log(factor).
+    """
+    _, torch = _core()
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError(f"rot_dim: expected an even size of at least 2, got {rot_dim}")
+    if scaling not in ("none", "linear", "ntk", "yarn"):
+        raise ValueError(f"scaling: expected none, linear, ntk or yarn, got {scaling!r}")
+    if not theta > 1.0 or not factor >= 1.0:
+        raise ValueError("theta: expected more than 1, and factor: at least 1")
+    pairs, mscale = rot_dim // 2, 1.0
+    if scaling == "ntk" and rot_dim > 2:
+        theta = theta * factor ** (rot_dim / (rot_dim - 2))
+    freqs = [theta ** (-2.0 * j / rot_dim) for j in range(pairs)]
+    if scaling == "linear":
+        freqs = [f / factor for f in freqs]
+    if scaling == "yarn":
+        if not original_length or original_length < 1:
+            raise ValueError("original_length: needed for scaling='yarn'")
+
+        def pair_of(turns):  # the pair that turns so often in original_length positions
+            return rot_dim * math.log(original_length / (turns * 2.0 * math.pi)) / (2.0 * math.log(theta))
+
+        low = max(math.floor(pair_of(beta_fast)), 0)
+        high = min(math.ceil(pair_of(beta_slow)), rot_dim - 1)
+        ramp = [min(max((j - low) / max(high - low, 1e-3), 0.0), 1.0) for j in range(pairs)]
+        freqs = [f / factor * t + f * (1.0 - t) for f, t in zip(freqs, ramp)]
+        mscale = 1.0 + 0.1 * math.log(factor)
+    return torch.tensor(freqs, dtype=torch.float64).float().to(device or "cuda"), mscale
+
+
+def _rotary(q, k, freqs, positions, mscale, interleaved, inverse, q_out, k_out, names):
+    c, torch = _core()
+    index = _on_gpu(q, names[0], 4, "(batch, L, heads, dim)")
+    batch, L, H, D = q.shape
+    dev, code, Hk = q.device, _code(c, torch, q), 0
+    _same(c, q, q.shape, index, **{names[0]: q})
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError(f"{names[1]} must be (batch, L, kheads, dim)")
+        Hk = k.shape[2]
+        _same(c, q, (batch, L, Hk, D), index, **{names[1]: k})
+    if freqs.dim() != 1 or not 1 <= freqs.shape[0] <= D // 2:
+        raise ValueError(f"freqs: expected 1 to {D // 2} values, got {tuple(freqs.shape)}")
+    _want(freqs, "freqs", freqs.shape, torch.float32, dev, index)
+    _want(positions, "positions", (batch, L), torch.int32, dev, index)
+    if H < 1:
+        raise ValueError(f"{names[0]}: at least one head is needed")
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    else:
+        _want(q_out, "q_out", q.shape, q.dtype, dev, index)
+    if k is None:
+        k_out = None
+    elif k_out is None:
+        k_out = torch.empty_like(k)
+    else:
+        _want(k_out, "k_out", k.shape, q.dtype, dev, index)
+    _call(c, torch, index, "ssm_rotary", _ptr(q), _ptr(k), _ptr(freqs), _ptr(positions), mscale,
+          int(bool(interleaved)), inverse, _ptr(q_out), _ptr(k_out), batch, L, H, Hk, D,
+          2 * freqs.shape[0], code)
+    return q_out, k_out
+
+
+def rotary_fwd(q, k, freqs, positions=None, mscale=1.0, interleaved=False, q_out=None, k_out=None):
+    """Rotary positions of queries and keys on the GPU.
+
+    q: (batch, L, heads, dim), k: (batch, L, kheads, dim) or None, float32 or bfloat16;
+    freqs: (rot / 2,) float32, the angle per position of each pair (rotary_freqs); the elements
+    of a head from rot on are left as they are; positions: optional (batch, L) int32 (0 .. L - 1
+    when omitted); interleaved: pairs are neighbours, else they lie rot / 2 apart.
+    Returns (q_out, k_out), which may be given, and may be q and k (in place).
+    """
+    return _rotary(q, k, freqs, positions, mscale, interleaved, 0, q_out, k_out, ("q", "k"))
+
+
+def rotary_bwd(dq, dk, freqs, positions=None, mscale=1.0, interleaved=False, q_out=None, k_out=None):
+    """Gradients of rotary_fwd's q and k from those of its outputs (same arguments)."""
+    return _rotary(dq, dk, freqs, positions, mscale, interleaved, 1, q_out, k_out, ("dq", "dk"))
