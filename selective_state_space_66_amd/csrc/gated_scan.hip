@@ -15,7 +15,7 @@
 // (V, H): h -> exp(-V) h + H, V the sum of its v.  Pairs are joined over the
 // waves in LDS and over the chunks through memory: a block publishes the pair
 // of its chunk as one 64-bit word, waits for the words of the chunks before it
-// in its group of 32 chunks and for the state before the group, and goes on
+// in its group of 16 chunks and for the state before the group, and goes on
 // with its tokens, which never left the registers.  The order of every join is
 // fixed by the chunk's number, so repeated calls give identical bits.
 //
@@ -39,7 +39,7 @@ namespace gated_scan {
 
 namespace {
 
-constexpr int kGroup = 32;                     // chunks from one published state to the next
+constexpr int kGroup = 16;                     // chunks from one published state to the next
 constexpr uint64_t kEmpty = ~(uint64_t)0;      // a word that is not there yet
 constexpr float kCut = __builtin_inff();       // V of a stretch where a document starts
 
@@ -58,73 +58,85 @@ __device__ __forceinline__ float exp_f(float x) {
 // within what e^x can hold (a NaN stays one)
 __device__ __forceinline__ float held(float x) { return x > 87.0f ? 87.0f : x < -87.0f ? -87.0f : x; }
 
-// sigmoid(z) and 1 - sigmoid(z), both to a few units in the last place
-template <bool PRECISE>
-__device__ __forceinline__ void sigmoid2(float z, float* s, float* rest) {
-  const float e = exp_f<PRECISE>(held(-z));
-  *s = rcp_hw(1.0f + e);
-  *rest = e * *s;
-}
 template <bool PRECISE>
 __device__ __forceinline__ float sigmoid1(float z) {
   return rcp_hw(1.0f + exp_f<PRECISE>(PRECISE ? held(-z) : -z));
 }
+// sigmoid(z) and 1 - sigmoid(z), both to a few units in the last place
+template <bool PRECISE>
+__device__ __forceinline__ void sigmoid2(float z, float* s, float* rest) {
+  const float e = exp_f<PRECISE>(PRECISE ? held(-fabsf(z)) : -fabsf(z));
+  const float r = rcp_hw(1.0f + e), er = e * r;
+  *s = z > 0.0f ? r : er;
+  *rest = z > 0.0f ? er : r;
+}
 
 // 1 - e^-v from v and a = e^-v: the series where it leaves out less than half a
 // unit (its last term), the difference above, where it has lost at most a bit
-template <bool PRECISE>
 __device__ __forceinline__ float one_minus(float v, float a) {
-  if (PRECISE) {
-    float s = fmaf(v, -1.0f / 3628800.0f, 1.0f / 362880.0f);
-    s = fmaf(v, -s, 1.0f / 40320.0f);
-    s = fmaf(v, -s, 1.0f / 5040.0f);
-    s = fmaf(v, -s, 1.0f / 720.0f);
-    s = fmaf(v, -s, 1.0f / 120.0f);
-    s = fmaf(v, -s, 1.0f / 24.0f);
-    s = fmaf(v, -s, 1.0f / 6.0f);
-    s = fmaf(v, -s, 0.5f);
-    s = fmaf(v, -s, 1.0f);
-    return v < 0.6931472f ? v * s : 1.0f - a;
-  }
-  float s = fmaf(v, -1.0f / 120.0f, 1.0f / 24.0f);
+  float s = fmaf(v, -1.0f / 3628800.0f, 1.0f / 362880.0f);
+  s = fmaf(v, -s, 1.0f / 40320.0f);
+  s = fmaf(v, -s, 1.0f / 5040.0f);
+  s = fmaf(v, -s, 1.0f / 720.0f);
+  s = fmaf(v, -s, 1.0f / 120.0f);
+  s = fmaf(v, -s, 1.0f / 24.0f);
   s = fmaf(v, -s, 1.0f / 6.0f);
   s = fmaf(v, -s, 0.5f);
   s = fmaf(v, -s, 1.0f);
-  return v < 0.125f ? v * s : 1.0f - a;
+  return v < 0.6931472f ? v * s : 1.0f - a;
 }
 
-// The factor of a state: a itself, or (PRECISE, where a is near 1) -b with the
-// sign bit set, which stands for 1 - b.
+// What a token's gate r does: V is v in the unit of the sums (natural where
+// PRECISE, of log2 else, so that a is one exp2), f the factor of the state, m
+// the root of 1 - a^2.  f is a itself, or (PRECISE, where a is near 1) -b with
+// the sign bit set, which stands for 1 - b.
+struct Gate { float V, f, m; };
 template <bool PRECISE>
-__device__ __forceinline__ float factor(float v, float a, float b) {
-  return PRECISE && v < 0.6931472f ? -b : a;
+__device__ __forceinline__ float sum_unit(float decay) { return PRECISE ? decay : decay * kLog2e; }
+template <bool PRECISE>
+__device__ __forceinline__ Gate gate_of(float d, float r) {  // d: sum_unit(decay)
+  Gate g;
+  g.V = d * sigmoid1<PRECISE>(r);
+  if (PRECISE) {
+    const float a = exp_f<true>(-g.V), b = one_minus(g.V, a);
+    g.f = g.V < 0.6931472f ? -b : a;
+    g.m = __builtin_amdgcn_sqrtf(b * (2.0f - b));
+  } else {
+    // 1 - a^2: four terms of its series below v = 0.05, which leave out 8e-7 of
+    // it; a's rounding is 6e-7 of the difference above
+    g.f = exp2_hw(-g.V);
+    float s = fmaf(g.V, -0.15388844f, 0.44403291f);
+    s = fmaf(g.V, s, -0.96090603f);
+    s = fmaf(g.V, s, 1.38629436f);
+    const float m2 = g.V < 0.07f ? g.V * s : fmaf(-g.f, g.f, 1.0f);
+    g.m = __builtin_amdgcn_sqrtf(m2);
+  }
+  return g;
 }
 template <bool PRECISE>
 __device__ __forceinline__ float times(float f, float h) {
-  if (!PRECISE) return f * h;
   const float t = f * h;
-  return __float_as_int(f) < 0 ? t + h : t;
+  return PRECISE && __float_as_int(f) < 0 ? t + h : t;
 }
 template <bool PRECISE>
 __device__ __forceinline__ float advance(float f, float h, float u) {
   const float t = fmaf(f, h, u);
-  if (!PRECISE) return t;
-  return __float_as_int(f) < 0 ? t + h : t;
+  return PRECISE && __float_as_int(f) < 0 ? t + h : t;
 }
 
-// What a stretch does to a state, its factor instead of V (kCut: a document
-// starts in it, nothing of the state before is read, a NaN neither).
+// What a stretch of tokens does to a state, its factor instead of V (kCut: a
+// document starts in it, nothing of the state before is read, a NaN neither).
 template <bool PRECISE>
 __device__ __forceinline__ float stretch_factor(float V) {
   if (V == kCut) return kCut;
-  const float a = exp_f<PRECISE>(-V);
-  return PRECISE ? factor<true>(V, a, one_minus<true>(V, a)) : a;
+  if (!PRECISE) return exp2_hw(-V);
+  const float a = exp_f<true>(-V);
+  return V < 0.6931472f ? -one_minus(V, a) : a;
 }
 template <bool PRECISE>
 __device__ __forceinline__ float over(float f, float h, float add) {
   return f == kCut ? add : advance<PRECISE>(f, h, add);
 }
-
 // V of two stretches together
 __device__ __forceinline__ float joint(float V, float W) { return V == kCut || W == kCut ? kCut : V + W; }
 
@@ -180,103 +192,102 @@ struct Spot {
   int64_t b, t0;
   int c;
   bool here;
+  int last;          // from t0 to the last token that may be read (negative past it)
   int real, inside;  // of the wave's tokens, those before the length and before L
   uint32_t cuts;     // bit j: a document starts at the wave's token j
 
   __device__ __forceinline__ Spot(const Args& p, uint32_t n, bool backward) {
-    const uint32_t rows = p.blocks / (uint32_t)p.chunks;
-    at = (int)(n / rows);
-    const uint32_t row = n % rows;
-    b = row / (uint32_t)p.tiles;
+    // quotients come from the vector unit; the rest is to stay on the scalar one
+    const uint32_t rows = (uint32_t)__builtin_amdgcn_readfirstlane((int)(p.blocks / (uint32_t)p.chunks));
+    at = __builtin_amdgcn_readfirstlane((int)(n / rows));
+    const uint32_t row = n - (uint32_t)at * rows;
+    const int entry = __builtin_amdgcn_readfirstlane((int)(row / (uint32_t)p.tiles));
+    b = entry;
     chunk = backward ? p.chunks - 1 - at : at;
     lane = (int)threadIdx.x & 63;
     w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    c = ((int)(row % (uint32_t)p.tiles) * 64 + lane) * VEC;
+    c = ((int)(row - (uint32_t)entry * (uint32_t)p.tiles) * 64 + lane) * VEC;
     here = c < p.dim;
     t0 = (int64_t)chunk * (TOK * W) + w * TOK;
     int64_t len = p.L;
     if (p.seq_lens) {
-      len = p.seq_lens[b];
+      len = __builtin_amdgcn_readfirstlane(p.seq_lens[b]);
       len = len < 0 ? 0 : len > p.L ? p.L : len;
     }
     const int64_t left = len - t0, out = p.L - t0;
     real = left <= 0 ? 0 : left >= TOK ? TOK : (int)left;
     inside = out <= 0 ? 0 : out >= TOK ? TOK : (int)out;
+    last = left > TOK ? TOK - 1 : left < 1 ? (int)((len > 0 ? len - 1 : 0) - t0) : (int)left - 1;
     cuts = 0;
     if (p.reset && real > 0) {
       const bool start = lane < real && p.reset[b * p.L + t0 + lane] != 0;
       cuts = (uint32_t)__ballot(start);
     }
   }
-  __device__ __forceinline__ int64_t offset(const Args& p) const { return (b * p.L + t0) * p.dim + c; }
+  // the wave's row j of a tensor: a scalar base and the thread's offset in bytes
+  template <typename T>
+  __device__ __forceinline__ const char* row(const Args& p, const void* t, int j) const {
+    return (const char*)t + ((b * p.L + t0 + j) * p.dim) * (int64_t)sizeof(T);
+  }
+  template <typename T>
+  __device__ __forceinline__ uint32_t bytes() const { return (uint32_t)c * (uint32_t)sizeof(T); }
 };
 
-// The wave's tokens of one tensor; what is not there is zero.
+// The wave's tokens of one tensor.  In the place of what is not there stand the
+// last real token and the first channel: loads without a branch, and what is
+// made of them is left out of the sums and not stored.
 template <typename T, int VEC, int TOK, int W>
 __device__ __forceinline__ void load_tokens(const Args& p, const Spot<VEC, TOK, W>& s, const void* from,
                                             typename Raw<T, VEC>::type (&raw)[TOK]) {
   typedef typename Raw<T, VEC>::type R;
-  const T* const at = (const T*)from + s.offset(p);
-  if (s.real == TOK && s.here) {
+  const uint32_t at = s.here ? s.template bytes<T>() : 0u;
 #pragma unroll
-    for (int j = 0; j < TOK; ++j) raw[j] = *(const R*)(at + (int64_t)j * p.dim);
-  } else {
-#pragma unroll
-    for (int j = 0; j < TOK; ++j)
-      raw[j] = s.here && j < s.real ? *(const R*)(at + (int64_t)j * p.dim) : (R)0;
-  }
+  for (int j = 0; j < TOK; ++j)
+    raw[j] = *(const R*)(s.template row<T>(p, from, j < s.last ? j : s.last) + at);
 }
 
 // ---- the chunks before a block's own --------------------------------------------
-//
-// Called by all threads of a block between two barriers: wave w joins its share
-// of the words and leaves (factor, H) in `joined`; the wave behind the last
-// word's returns the state before the group, through `start`.
 
-template <bool PRECISE, int VEC, int W>
-__device__ __forceinline__ void join_before(const Args& p, int at, int64_t row0, bool here, int w,
-                                            int lane, float2* joined, float* start) {
+// The state before chunk `at` of its row in the order of the chunks, by one
+// wave: from the state before its group of chunks (`begin`: before the first)
+// over the words of those between.
+template <bool PRECISE, int VEC>
+__device__ __forceinline__ void state_before(const Args& p, int at, int64_t row0,
+                                             const float (&begin)[VEC], float (&h)[VEC]) {
   const int first = at / kGroup * kGroup, n = at - first;
   const int64_t stride = p.batch * (int64_t)p.dim;
-  constexpr int kShare = (kGroup + W - 1) / W;  // chunks of a wave
-  if (here) {
-    float V[VEC], H[VEC];
+  constexpr int kAhead = 8;  // words on their way at a time
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) V[k] = H[k] = 0.0f;
-    const int64_t base = (int64_t)(first + w * kShare) * stride + row0;
-    uint64_t word[kShare][VEC];
+  for (int k = 0; k < VEC; ++k) h[k] = begin[k];
+  if (first > 0) {
+    const uint64_t* const g = p.groups + (int64_t)(first / kGroup - 1) * stride + row0;
 #pragma unroll
-    for (int q = 0; q < kShare; ++q)
+    for (int k = 0; k < VEC; ++k) {
+      uint64_t word = look(g + k);
+      while (word == kEmpty) {
+        __builtin_amdgcn_s_sleep(1);
+        word = look(g + k);
+      }
+      h[k] = lo_of(word);
+    }
+  }
+  for (int q0 = 0; q0 < n; q0 += kAhead) {
+    const uint64_t* const at0 = p.sums + (int64_t)(first + q0) * stride + row0;
+    uint64_t word[kAhead][VEC];
 #pragma unroll
-      for (int k = 0; k < VEC; ++k)
-        word[q][k] = w * kShare + q < n ? look(p.sums + base + q * stride + k) : 0;
+    for (int q = 0; q < kAhead; ++q)
 #pragma unroll
-    for (int q = 0; q < kShare; ++q) {
-      if (w * kShare + q >= n) break;
+      for (int k = 0; k < VEC; ++k) word[q][k] = q0 + q < n ? look(at0 + q * stride + k) : 0;
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      if (q0 + q >= n) break;
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
         while (word[q][k] == kEmpty) {
           __builtin_amdgcn_s_sleep(1);
-          word[q][k] = look(p.sums + base + q * stride + k);
+          word[q][k] = look(at0 + q * stride + k);
         }
-        const float f = stretch_factor<PRECISE>(hi_of(word[q][k]));
-        H[k] = over<PRECISE>(f, H[k], lo_of(word[q][k]));
-        V[k] = joint(V[k], hi_of(word[q][k]));
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < VEC; ++k)
-      joined[w * (64 * VEC) + lane * VEC + k] = make_float2(stretch_factor<PRECISE>(V[k]), H[k]);
-    if (w == W - 1 && first > 0) {
-      const uint64_t* const g = p.groups + (int64_t)(first / kGroup - 1) * stride + row0;
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        uint64_t s = look(g + k);
-        while (s == kEmpty) {
-          __builtin_amdgcn_s_sleep(1);
-          s = look(g + k);
-        }
-        start[lane * VEC + k] = lo_of(s);
+        h[k] = over<PRECISE>(stretch_factor<PRECISE>(hi_of(word[q][k])), h[k], lo_of(word[q][k]));
       }
     }
   }
@@ -293,26 +304,83 @@ __device__ __forceinline__ uint32_t block_number(const Args& p) {
   return __builtin_amdgcn_readfirstlane(number);
 }
 
+// H of the wave's tokens, from a state of zero (or of `h`).
+template <bool PRECISE, bool PLAIN, int VEC, int TOK>
+__device__ __forceinline__ void run_tokens(int real, uint32_t cuts, const float (&f)[TOK][VEC],
+                                           const float (&u)[TOK][VEC], float (&h)[VEC]) {
+#pragma unroll
+  for (int j = 0; j < TOK; ++j)
+    if (PLAIN || j < real)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        const float t = advance<PRECISE>(f[j][k], h[k], u[j][k]);
+        h[k] = !PLAIN && (cuts >> j & 1) ? u[j][k] : t;
+      }
+}
+
+// What the wave's tokens add to the adjoint from their right.
+template <typename T, bool PLAIN, int VEC, int TOK>
+__device__ __forceinline__ void run_back(int real, uint32_t cuts, const float (&f)[TOK][VEC],
+                                         const typename Raw<T, VEC>::type (&rd)[TOK], float (&c)[VEC]) {
+#pragma unroll
+  for (int j = TOK - 1; j >= 0; --j)
+    if (PLAIN || j < real) {
+      float dy[VEC];
+      Raw<T, VEC>::get(rd[j], dy);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        const float t = times<sizeof(T) == 4>(f[j][k], dy[k] + c[k]);
+        c[k] = !PLAIN && (cuts >> j & 1) ? 0.0f : t;
+      }
+    }
+}
+
+// The states before each token, in the place of what the tokens add; h: the
+// state before the first.
+template <bool PRECISE, bool PLAIN, int VEC, int TOK>
+__device__ __forceinline__ void states_before(int real, uint32_t cuts, const float (&f)[TOK][VEC],
+                                              float (&u)[TOK][VEC], float (&h)[VEC]) {
+#pragma unroll
+  for (int j = 0; j < TOK; ++j) {
+    const bool cut = !PLAIN && (cuts >> j & 1);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      const float add = u[j][k];
+      u[j][k] = cut ? 0.0f : h[k];
+      const float t = advance<PRECISE>(f[j][k], h[k], add);
+      if (PLAIN || j < real) h[k] = cut ? add : t;
+    }
+  }
+}
+
 // ---- forwards -----------------------------------------------------------------
+//
+// Between the two barriers wave 0 joins the block's waves (what stands before
+// each of them, and the block's own word) while wave 1 looks at the chunks
+// before.
 
 template <typename T, int VEC, int TOK, int W, bool MANY>
 __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
   constexpr bool PRECISE = sizeof(T) == 4;
+  constexpr int N = 64 * VEC;
   typedef Raw<T, VEC> IO;
-  __shared__ float2 pair[W * 64 * VEC], joined[W * 64 * VEC];
-  __shared__ float vsum[W * 64 * VEC], start[64 * VEC];
+  __shared__ float2 pair[W][N];  // (V, H) of each wave, then (factor, H) of the waves before it
+  __shared__ float start[N];
   const uint32_t n = block_number<MANY>(p);
   if (n >= p.blocks) return;
   const Spot<VEC, TOK, W> s(p, n, false);
   const int64_t row = s.b * p.dim + s.c;
+  const int slot = s.lane * VEC;
 
-  typename IO::type rx[TOK], rr[TOK], ri[TOK];
-  load_tokens<T>(p, s, p.r, rr);
-  load_tokens<T>(p, s, p.i, ri);
-  load_tokens<T>(p, s, p.x, rx);
+  typename IO::type rx[TOK] = {}, rr[TOK] = {}, ri[TOK] = {};
+  if (MANY || p.L > 0) {
+    load_tokens<T>(p, s, p.r, rr);
+    load_tokens<T>(p, s, p.i, ri);
+    load_tokens<T>(p, s, p.x, rx);
+  }
   float d[VEC];
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) d[k] = s.here ? p.decay[s.c + k] : 0.0f;
+  for (int k = 0; k < VEC; ++k) d[k] = sum_unit<PRECISE>(s.here ? p.decay[s.c + k] : 0.0f);
 
   float f[TOK][VEC], u[TOK][VEC], V[VEC], H[VEC];
 #pragma unroll
@@ -325,89 +393,70 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
     IO::get(ri[j], i);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      const float v = d[k] * sigmoid1<PRECISE>(r[k]);
-      const float a = exp_f<PRECISE>(-v);
-      const float b = one_minus<PRECISE>(v, a);
-      f[j][k] = factor<PRECISE>(v, a, b);
-      u[j][k] = __builtin_amdgcn_sqrtf(b * (2.0f - b)) * sigmoid1<PRECISE>(i[k]) * x[k];
-      if (j < s.real) V[k] += v;
+      const Gate g = gate_of<PRECISE>(d[k], r[k]);
+      f[j][k] = g.f;
+      u[j][k] = g.m * sigmoid1<PRECISE>(i[k]) * x[k];
+      V[k] += j < s.real ? g.V : 0.0f;
     }
   }
   const bool plain = s.real == TOK && s.cuts == 0;  // the whole wave alike
-  if (plain) {
+  if (plain) run_tokens<PRECISE, true>(s.real, s.cuts, f, u, H);
+  else run_tokens<PRECISE, false>(s.real, s.cuts, f, u, H);
 #pragma unroll
-    for (int j = 0; j < TOK; ++j)
+  for (int k = 0; k < VEC; ++k) pair[s.w][slot + k] = make_float2(s.cuts ? kCut : V[k], H[k]);
+  lds_barrier();
+
+  if (s.w == 0) {
+    float2 e[W][VEC];
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) H[k] = advance<PRECISE>(f[j][k], H[k], u[j][k]);
-  } else {
+    for (int q = 0; q < W; ++q)
 #pragma unroll
-    for (int j = 0; j < TOK; ++j)
-      if (j < s.real) {
-        const bool cut = s.cuts >> j & 1;
+      for (int k = 0; k < VEC; ++k) e[q][k] = pair[q][slot + k];
 #pragma unroll
-        for (int k = 0; k < VEC; ++k)
-          H[k] = cut ? u[j][k] : advance<PRECISE>(f[j][k], H[k], u[j][k]);
+    for (int k = 0; k < VEC; ++k) {
+      float Vb = 0.0f, Hb = 0.0f;
+#pragma unroll
+      for (int q = 0; q < W; ++q) {
+        pair[q][slot + k] = make_float2(stretch_factor<PRECISE>(Vb), Hb);
+        Hb = over<PRECISE>(stretch_factor<PRECISE>(e[q][k].x), Hb, e[q][k].y);
+        Vb = joint(Vb, e[q][k].x);
       }
-    if (s.cuts)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) V[k] = kCut;
+      // the last chunk of a group publishes the state instead, and nobody reads the last one's
+      if (MANY && s.here && s.at + 1 < p.chunks && s.at % kGroup != kGroup - 1)
+        publish(p.sums + (int64_t)s.at * (p.batch * p.dim) + row + k, Vb, Hb);
+    }
   }
-  const int slot = s.w * (64 * VEC) + s.lane * VEC;
+  if (s.w == (W > 1 ? 1 : 0)) {
+    float begin[VEC], h[VEC];
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) {
-    pair[slot + k] = make_float2(stretch_factor<PRECISE>(V[k]), H[k]);
-    vsum[slot + k] = V[k];
+    for (int k = 0; k < VEC; ++k) h[k] = begin[k] = s.here && p.h0 ? p.h0[row + k] : 0.0f;
+    if (s.here) {
+      if (MANY) state_before<PRECISE, VEC>(p, s.at, row, begin, h);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        start[slot + k] = h[k];
+      }
+    }
   }
   lds_barrier();
 
   float h[VEC];
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) h[k] = s.here && p.h0 ? p.h0[row + k] : 0.0f;
-  if (MANY) {
-    const int first = s.at / kGroup * kGroup;
-    if (s.w == 0 && s.here && s.at + 1 < p.chunks && s.at + 1 < first + kGroup) {
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        float Vb = 0.0f, Hb = 0.0f;
-#pragma unroll
-        for (int q = 0; q < W; ++q) {
-          const float2 e = pair[q * (64 * VEC) + s.lane * VEC + k];
-          Hb = over<PRECISE>(e.x, Hb, e.y);
-          Vb = joint(Vb, vsum[q * (64 * VEC) + s.lane * VEC + k]);
-        }
-        publish(p.sums + (int64_t)s.at * (p.batch * p.dim) + row + k, Vb, Hb);
-      }
-    }
-    join_before<PRECISE, VEC, W>(p, s.at, row, s.here, s.w, s.lane, joined, start);
-    lds_barrier();
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      if (first > 0) h[k] = start[s.lane * VEC + k];
-#pragma unroll
-      for (int q = 0; q < W; ++q) {
-        const float2 e = joined[q * (64 * VEC) + s.lane * VEC + k];
-        h[k] = over<PRECISE>(e.x, h[k], e.y);
-      }
-    }
+  for (int k = 0; k < VEC; ++k) {
+    const float2 e = pair[s.w][slot + k];
+    h[k] = over<PRECISE>(e.x, start[slot + k], e.y);
   }
-  if (s.w == 0 && s.here && p.states)
+  if (p.states && s.here && s.w * TOK % kKeep == 0 && s.t0 < p.L)
 #pragma unroll
     for (int k = 0; k < VEC; ++k)
-      p.states[(s.b * p.chunks + s.chunk) * p.dim + s.c + k] = h[k];
-  for (int q = 0; q < s.w; ++q)
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      const float2 e = pair[q * (64 * VEC) + s.lane * VEC + k];
-      h[k] = over<PRECISE>(e.x, h[k], e.y);
-    }
-
-  typename IO::type* out = (typename IO::type*)((T*)p.y + s.offset(p));
+      p.states[(s.b * p.kept + s.t0 / kKeep) * p.dim + s.c + k] = h[k];
   if (plain) {
 #pragma unroll
     for (int j = 0; j < TOK; ++j) {
 #pragma unroll
       for (int k = 0; k < VEC; ++k) h[k] = advance<PRECISE>(f[j][k], h[k], u[j][k]);
-      if (s.here) *(typename IO::type*)((T*)out + (int64_t)j * p.dim) = IO::put(h);
+      if (s.here)
+        *(typename IO::type*)((char*)s.template row<T>(p, p.y, j) + s.template bytes<T>()) = IO::put(h);
     }
   } else {
 #pragma unroll
@@ -419,7 +468,8 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
         if (j < s.real) h[k] = cut ? u[j][k] : advance<PRECISE>(f[j][k], h[k], u[j][k]);
         o[k] = j < s.real ? h[k] : 0.0f;
       }
-      if (s.here && j < s.inside) *(typename IO::type*)((T*)out + (int64_t)j * p.dim) = IO::put(o);
+      if (s.here && j < s.inside)
+        *(typename IO::type*)((char*)s.template row<T>(p, p.y, j) + s.template bytes<T>()) = IO::put(o);
     }
   }
   if (s.w == W - 1 && s.here) {
@@ -438,29 +488,78 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
 // A block computes its gates and, from the state before its chunk, its states
 // again; the adjoint comes from the right as the state does from the left.
 
+// The gradients of the wave's tokens, from the last to the first; before[j] is
+// the state before token j, c the adjoint from the right, P the sum of P_t.
+template <typename T, bool PLAIN, int VEC, int TOK, int W>
+__device__ __forceinline__ void token_gradients(
+    const Args& p, const Spot<VEC, TOK, W>& s, const typename Raw<T, VEC>::type (&rx)[TOK],
+    const typename Raw<T, VEC>::type (&rr)[TOK], const typename Raw<T, VEC>::type (&ri)[TOK],
+    const typename Raw<T, VEC>::type (&rd)[TOK], const float (&f)[TOK][VEC],
+    const float (&m)[TOK][VEC], const float (&before)[TOK][VEC], const float (&decay)[VEC],
+    float (&c)[VEC], float (&P)[VEC]) {
+  constexpr bool PRECISE = sizeof(T) == 4;
+  typedef Raw<T, VEC> IO;
+  typedef typename IO::type R;
+#pragma unroll
+  for (int j = TOK - 1; j >= 0; --j) {
+    float x[VEC], r[VEC], i[VEC], dy[VEC], dx[VEC], dr[VEC], di[VEC];
+    IO::get(rx[j], x);
+    IO::get(rr[j], r);
+    IO::get(ri[j], i);
+    IO::get(rd[j], dy);
+    const bool real = PLAIN || j < s.real, cut = !PLAIN && (s.cuts >> j & 1);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      float sr, rest_r, g, rest_g;
+      sigmoid2<PRECISE>(r[k], &sr, &rest_r);
+      sigmoid2<PRECISE>(i[k], &g, &rest_g);
+      const float v = decay[k] * sr, lam = dy[k] + c[k];
+      const float al = times<PRECISE>(f[j][k], lam);
+      const float gx = g * x[k], lm = lam * m[j][k];
+      // a v / m: 0 where v is (m is the root of about 2 v there)
+      const float avm = times<PRECISE>(f[j][k], v * rcp_hw(fmaxf(m[j][k], 1e-30f)));
+      const float q = fmaf(gx, avm, -(v * before[j][k])) * al;
+      dx[k] = real ? lm * g : 0.0f;
+      di[k] = real ? lm * gx * rest_g : 0.0f;
+      dr[k] = real ? q * rest_r : 0.0f;
+      if (real) {
+        P[k] += q;
+        c[k] = cut ? 0.0f : al;
+      }
+    }
+    if (s.here && (PLAIN || j < s.inside)) {
+      *(R*)((char*)s.template row<T>(p, p.dx, j) + s.template bytes<T>()) = IO::put(dx);
+      *(R*)((char*)s.template row<T>(p, p.dr, j) + s.template bytes<T>()) = IO::put(dr);
+      *(R*)((char*)s.template row<T>(p, p.di, j) + s.template bytes<T>()) = IO::put(di);
+    }
+  }
+}
+
 template <typename T, int VEC, int TOK, int W, bool MANY>
 __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
   constexpr bool PRECISE = sizeof(T) == 4;
+  constexpr int N = 64 * VEC;
   typedef Raw<T, VEC> IO;
-  // (factor, H) forwards and D, what a stretch adds to the adjoint, of each wave
-  __shared__ float2 pair[W * 64 * VEC], joined[W * 64 * VEC];
-  __shared__ float back[W * 64 * VEC], vsum[W * 64 * VEC], start[64 * VEC];
+  // (V, H) of each wave, and D, what it adds to the adjoint; then the state
+  // before each wave, and (factor, D) of the waves behind it
+  __shared__ float2 pair[W][N], behind[W][N];
+  __shared__ float back[W][N], first[W][N], start[N];
   const uint32_t n = block_number<MANY>(p);
   if (n >= p.blocks) return;
   const Spot<VEC, TOK, W> s(p, n, true);
   const int64_t row = s.b * p.dim + s.c;
+  const int slot = s.lane * VEC;
 
-  typename IO::type rx[TOK], rr[TOK], ri[TOK], rd[TOK];
-  load_tokens<T>(p, s, p.r, rr);
-  load_tokens<T>(p, s, p.i, ri);
-  load_tokens<T>(p, s, p.x, rx);
-  load_tokens<T>(p, s, p.dy, rd);
-  float d[VEC], h[VEC];
-#pragma unroll
-  for (int k = 0; k < VEC; ++k) {
-    d[k] = s.here ? p.decay[s.c + k] : 0.0f;
-    h[k] = s.here && p.states ? p.states[(s.b * p.chunks + s.chunk) * p.dim + s.c + k] : 0.0f;
+  typename IO::type rx[TOK] = {}, rr[TOK] = {}, ri[TOK] = {}, rd[TOK] = {};
+  if (MANY || p.L > 0) {
+    load_tokens<T>(p, s, p.r, rr);
+    load_tokens<T>(p, s, p.i, ri);
+    load_tokens<T>(p, s, p.x, rx);
+    load_tokens<T>(p, s, p.dy, rd);
   }
+  float decay[VEC];
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) decay[k] = s.here ? p.decay[s.c + k] : 0.0f;
 
   float f[TOK][VEC], u[TOK][VEC], m[TOK][VEC], V[VEC], H[VEC], D[VEC];
 #pragma unroll
@@ -473,101 +572,75 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
     IO::get(ri[j], i);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      const float v = d[k] * sigmoid1<PRECISE>(r[k]);
-      const float a = exp_f<PRECISE>(-v);
-      const float b = one_minus<PRECISE>(v, a);
-      f[j][k] = factor<PRECISE>(v, a, b);
-      m[j][k] = __builtin_amdgcn_sqrtf(b * (2.0f - b));
-      u[j][k] = m[j][k] * sigmoid1<PRECISE>(i[k]) * x[k];
-      if (j < s.real) V[k] += v;
+      const Gate g = gate_of<PRECISE>(sum_unit<PRECISE>(decay[k]), r[k]);
+      f[j][k] = g.f;
+      m[j][k] = g.m;
+      u[j][k] = g.m * sigmoid1<PRECISE>(i[k]) * x[k];
+      V[k] += j < s.real ? g.V : 0.0f;
     }
   }
   const bool plain = s.real == TOK && s.cuts == 0;
   if (plain) {
-#pragma unroll
-    for (int j = 0; j < TOK; ++j)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) H[k] = advance<PRECISE>(f[j][k], H[k], u[j][k]);
-#pragma unroll
-    for (int j = TOK - 1; j >= 0; --j) {
-      float dy[VEC];
-      IO::get(rd[j], dy);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) D[k] = times<PRECISE>(f[j][k], dy[k] + D[k]);
-    }
+    run_tokens<PRECISE, true>(s.real, s.cuts, f, u, H);
+    run_back<T, true>(s.real, s.cuts, f, rd, D);
   } else {
-#pragma unroll
-    for (int j = 0; j < TOK; ++j)
-      if (j < s.real) {
-        const bool cut = s.cuts >> j & 1;
-#pragma unroll
-        for (int k = 0; k < VEC; ++k)
-          H[k] = cut ? u[j][k] : advance<PRECISE>(f[j][k], H[k], u[j][k]);
-      }
-#pragma unroll
-    for (int j = TOK - 1; j >= 0; --j)
-      if (j < s.real) {
-        const bool cut = s.cuts >> j & 1;
-        float dy[VEC];
-        IO::get(rd[j], dy);
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) D[k] = cut ? 0.0f : times<PRECISE>(f[j][k], dy[k] + D[k]);
-      }
-    if (s.cuts)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) V[k] = kCut;
+    run_tokens<PRECISE, false>(s.real, s.cuts, f, u, H);
+    run_back<T, false>(s.real, s.cuts, f, rd, D);
   }
-  const int slot = s.w * (64 * VEC) + s.lane * VEC;
 #pragma unroll
   for (int k = 0; k < VEC; ++k) {
-    pair[slot + k] = make_float2(stretch_factor<PRECISE>(V[k]), H[k]);
-    back[slot + k] = D[k];
-    vsum[slot + k] = V[k];
+    pair[s.w][slot + k] = make_float2(s.cuts ? kCut : V[k], H[k]);
+    back[s.w][slot + k] = D[k];
   }
   lds_barrier();
 
-  float c[VEC];
-#pragma unroll
-  for (int k = 0; k < VEC; ++k) c[k] = s.here && p.dlast ? p.dlast[row + k] : 0.0f;
-  if (MANY) {
-    const int first = s.at / kGroup * kGroup;
-    if (s.w == 0 && s.here && s.at + 1 < p.chunks && s.at + 1 < first + kGroup) {
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        float Vb = 0.0f, Db = 0.0f;
-#pragma unroll
-        for (int q = W - 1; q >= 0; --q) {
-          const int o = q * (64 * VEC) + s.lane * VEC + k;
-          Db = over<PRECISE>(pair[o].x, Db, back[o]);
-          Vb = joint(Vb, vsum[o]);
-        }
-        publish(p.sums + (int64_t)s.at * (p.batch * p.dim) + row + k, Vb, Db);
-      }
-    }
-    join_before<PRECISE, VEC, W>(p, s.at, row, s.here, s.w, s.lane, joined, start);
-    lds_barrier();
+  // wave 0: the states before the waves; then, in turn, what stands behind them
+  // and the block's own word (wave 1), and the chunks behind (wave 2)
+  if (s.w == 0) {
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      if (first > 0) c[k] = start[s.lane * VEC + k];
+      float h = s.here && p.states ? p.states[(s.b * p.kept + s.t0 / kKeep) * p.dim + s.c + k] : 0.0f;
 #pragma unroll
       for (int q = 0; q < W; ++q) {
-        const float2 e = joined[q * (64 * VEC) + s.lane * VEC + k];
-        c[k] = over<PRECISE>(e.x, c[k], e.y);
+        const float2 e = pair[q][slot + k];
+        first[q][slot + k] = h;
+        h = over<PRECISE>(stretch_factor<PRECISE>(e.x), h, e.y);
       }
     }
   }
-  for (int q = 0; q < s.w; ++q)
+  if (s.w == 1 % W) {
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      const float2 e = pair[q * (64 * VEC) + s.lane * VEC + k];
-      h[k] = over<PRECISE>(e.x, h[k], e.y);
-    }
-  for (int q = W - 1; q > s.w; --q)
+      float Vb = 0.0f, Db = 0.0f;
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      const int o = q * (64 * VEC) + s.lane * VEC + k;
-      c[k] = over<PRECISE>(pair[o].x, c[k], back[o]);
+      for (int q = W - 1; q >= 0; --q) {
+        const float Vq = pair[q][slot + k].x, Dq = back[q][slot + k];
+        behind[q][slot + k] = make_float2(stretch_factor<PRECISE>(Vb), Db);
+        Db = over<PRECISE>(stretch_factor<PRECISE>(Vq), Db, Dq);
+        Vb = joint(Vb, Vq);
+      }
+      if (MANY && s.here && s.at + 1 < p.chunks && s.at % kGroup != kGroup - 1)
+        publish(p.sums + (int64_t)s.at * (p.batch * p.dim) + row + k, Vb, Db);
     }
+  }
+  if (s.w == 2 % W) {
+    float begin[VEC], c[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) c[k] = begin[k] = s.here && p.dlast ? p.dlast[row + k] : 0.0f;
+    if (s.here) {
+      if (MANY) state_before<PRECISE, VEC>(p, s.at, row, begin, c);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) start[slot + k] = c[k];
+    }
+  }
+  lds_barrier();
+  float h[VEC], c[VEC];
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) {
+    h[k] = first[s.w][slot + k];
+    const float2 e = behind[s.w][slot + k];
+    c[k] = over<PRECISE>(e.x, start[slot + k], e.y);
+  }
 
   // the gates are computed again rather than kept: what the compiler may not
   // know to be the same words as above
@@ -578,53 +651,15 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
     asm volatile("" : "+v"(rx[j]));
     asm volatile("" : "+v"(rd[j]));
   }
-  // the states before each token, in the place of what the tokens add
-#pragma unroll
-  for (int j = 0; j < TOK; ++j) {
-    const bool cut = s.cuts >> j & 1;
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      const float before = cut ? 0.0f : h[k];
-      if (j < s.real) h[k] = cut ? u[j][k] : advance<PRECISE>(f[j][k], h[k], u[j][k]);
-      u[j][k] = before;
-    }
-  }
   float P[VEC];
 #pragma unroll
   for (int k = 0; k < VEC; ++k) P[k] = 0.0f;
-  const int64_t at = s.offset(p);
-#pragma unroll
-  for (int j = TOK - 1; j >= 0; --j) {
-    float x[VEC], r[VEC], i[VEC], dy[VEC], dx[VEC], dr[VEC], di[VEC];
-    IO::get(rx[j], x);
-    IO::get(rr[j], r);
-    IO::get(ri[j], i);
-    IO::get(rd[j], dy);
-    const bool real = j < s.real, cut = s.cuts >> j & 1;
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      float sr, rest_r, g, rest_g;
-      sigmoid2<PRECISE>(r[k], &sr, &rest_r);
-      sigmoid2<PRECISE>(i[k], &g, &rest_g);
-      const float v = d[k] * sr, lam = dy[k] + c[k];
-      const float al = times<PRECISE>(f[j][k], lam);
-      const float gx = g * x[k], lm = lam * m[j][k];
-      // a v / m: 0 where v is (m is the root of about 2 v there)
-      const float avm = times<PRECISE>(f[j][k], v * rcp_hw(fmaxf(m[j][k], 1e-30f)));
-      const float q = fmaf(gx, avm, -v * u[j][k]) * al;
-      dx[k] = real ? lm * g : 0.0f;
-      di[k] = real ? lm * gx * rest_g : 0.0f;
-      dr[k] = real ? q * rest_r : 0.0f;
-      if (real) {
-        P[k] += q;
-        c[k] = cut ? 0.0f : al;
-      }
-    }
-    if (s.here && j < s.inside) {
-      *(typename IO::type*)((T*)p.dx + at + (int64_t)j * p.dim) = IO::put(dx);
-      *(typename IO::type*)((T*)p.dr + at + (int64_t)j * p.dim) = IO::put(dr);
-      *(typename IO::type*)((T*)p.di + at + (int64_t)j * p.dim) = IO::put(di);
-    }
+  if (plain) {
+    states_before<PRECISE, true>(s.real, s.cuts, f, u, h);
+    token_gradients<T, true>(p, s, rx, rr, ri, rd, f, m, u, decay, c, P);
+  } else {
+    states_before<PRECISE, false>(s.real, s.cuts, f, u, h);
+    token_gradients<T, false>(p, s, rx, rr, ri, rd, f, m, u, decay, c, P);
   }
   if (s.w == 0 && s.here) {
     if (MANY && s.at % kGroup == kGroup - 1 && s.at + 1 < p.chunks)
@@ -636,16 +671,16 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
       for (int k = 0; k < VEC; ++k) p.dh0[row + k] = c[k];
   }
   if (!p.part) return;
-  lds_barrier();  // vsum has been read
+  // each wave read its own row of `first` alone, and that before this
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) vsum[slot + k] = P[k];
+  for (int k = 0; k < VEC; ++k) first[s.w][slot + k] = P[k];
   lds_barrier();
   if (s.w == 0 && s.here)
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
       float t = 0.0f;
 #pragma unroll
-      for (int q = 0; q < W; ++q) t += vsum[q * (64 * VEC) + s.lane * VEC + k];
+      for (int q = 0; q < W; ++q) t += first[q][slot + k];
       p.part[((int64_t)s.chunk * p.batch + s.b) * p.dim + s.c + k] = t;
     }
 }
@@ -696,11 +731,8 @@ __global__ __launch_bounds__(256) void step_kernel(const StepArgs p) {
     for (int k = 0; k < VEC; ++k) h[k] = p.state[at + k];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      const float v = p.decay[c + k] * sigmoid1<PRECISE>(r[k]);
-      const float a = exp_f<PRECISE>(-v);
-      const float b = one_minus<PRECISE>(v, a);
-      const float u = __builtin_amdgcn_sqrtf(b * (2.0f - b)) * sigmoid1<PRECISE>(i[k]) * x[k];
-      h[k] = advance<PRECISE>(factor<PRECISE>(v, a, b), h[k], u);
+      const Gate g = gate_of<PRECISE>(sum_unit<PRECISE>(p.decay[c + k]), r[k]);
+      h[k] = advance<PRECISE>(g.f, h[k], g.m * sigmoid1<PRECISE>(i[k]) * x[k]);
       p.state[at + k] = h[k];
     }
     *(R*)((T*)p.y + at) = IO::put(h);
@@ -709,12 +741,23 @@ __global__ __launch_bounds__(256) void step_kernel(const StepArgs p) {
 
 // ---- launches -------------------------------------------------------------------
 
-int64_t chunks_of(int64_t L) { return L > 0 ? (L + kChunk - 1) / kChunk : 1; }
+#ifndef FT
+#define FT 16
+#define FW 8
+#define BT 8
+#define BW 8
+#define GT 16
+#define GW 8
+#define HT 8
+#define HW 8
+#endif
+int64_t pieces_of(int64_t L, int64_t n) { return L > 0 ? (L + n - 1) / n : 1; }
 int64_t up(int64_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout { int64_t ticket, sums, groups, part, bytes; };
-Layout layout(int64_t batch, int64_t L, int64_t dim, bool need_part) {
-  const int64_t chunks = chunks_of(L), rows = batch * dim;
+// chunk: tokens of a block
+Layout layout(int64_t batch, int64_t L, int64_t dim, int chunk, bool need_part) {
+  const int64_t chunks = pieces_of(L, chunk), rows = batch * dim;
   Layout a = {};
   int64_t at = 0;
   if (chunks > 1) {
@@ -728,10 +771,11 @@ Layout layout(int64_t batch, int64_t L, int64_t dim, bool need_part) {
   return a;
 }
 
-void place(Args& p, int vec) {
-  const Layout a = layout(p.batch, p.L, p.dim, p.ddecay != nullptr);
+void place(Args& p, int vec, int chunk) {
+  const Layout a = layout(p.batch, p.L, p.dim, chunk, p.ddecay != nullptr);
   char* const ws = (char*)p.ws;
-  p.chunks = (int)chunks_of(p.L);
+  p.chunks = (int)pieces_of(p.L, chunk);
+  p.kept = (int)pieces_of(p.L, kKeep);
   p.tiles = (p.dim + 64 * vec - 1) / (64 * vec);
   p.blocks = (uint32_t)(p.batch * p.tiles * p.chunks);
   p.ticket = (uint32_t*)(ws + a.ticket);
@@ -750,8 +794,8 @@ hipError_t clear(const Args& p, hipStream_t s) {
 
 template <typename T, int VEC, int TOK, int W, bool BWD>
 hipError_t launch(Args p, hipStream_t s) {
-  static_assert(TOK * W == kChunk, "states are kept every kChunk tokens");
-  place(p, VEC);
+  static_assert(TOK * W % kKeep == 0 && (TOK >= kKeep || kKeep % TOK == 0), "states are kept by whole waves");
+  place(p, VEC, TOK * W);
   const Grid g = grid_of(p.blocks, 64 * W);
   const dim3 grid(g.x, g.more), block(64 * W);
   if (p.chunks > 1) {
@@ -781,31 +825,32 @@ bool pairs(int dim, std::initializer_list<const void*> ptrs) {
 
 bool fits(int64_t batch, int64_t L, int64_t dim) {
   // block numbers are 32-bit, and so are chunk numbers and channels
-  const __int128 blocks = (__int128)batch * ((dim + 63) / 64) * chunks_of(L);
-  return dim <= (1 << 24) && chunks_of(L) < (1 << 24) && blocks < 0x7fffffff;
+  const __int128 blocks = (__int128)batch * ((dim + 63) / 64) * pieces_of(L, kKeep);
+  return dim <= (1 << 24) && L <= 0x7fffff00 && blocks < 0x7fffffff;
 }
 
 size_t workspace_bytes(int64_t batch, int64_t L, int64_t dim, bool backward, bool need_ddecay) {
-  return (size_t)layout(batch, L, dim, backward && need_ddecay).bytes;
+  // the smaller chunk needs more
+  return (size_t)layout(batch, L, dim, kKeep, backward && need_ddecay).bytes;
 }
 
 hipError_t forward(const Args& p, bool f32, hipStream_t s) {
-  if (f32) return launch<float, 1, 16, 8, false>(p, s);
-  if (pairs(p.dim, {p.x, p.r, p.i, p.y})) return launch<bf16_bits, 2, 16, 8, false>(p, s);
-  return launch<bf16_bits, 1, 16, 8, false>(p, s);
+  if (f32) return launch<float, 1, GT, GW, false>(p, s);
+  if (pairs(p.dim, {p.x, p.r, p.i, p.y})) return launch<bf16_bits, 2, FT, FW, false>(p, s);
+  return launch<bf16_bits, 1, GT, GW, false>(p, s);
 }
 
 hipError_t backward(const Args& p, bool f32, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (p.batch == 0) {
-  } else if (f32) e = launch<float, 1, 8, 16, true>(p, s);
+  } else if (f32) e = launch<float, 1, HT, HW, true>(p, s);
   else if (pairs(p.dim, {p.x, p.r, p.i, p.dy, p.dx, p.dr, p.di}))
-    e = launch<bf16_bits, 2, 8, 16, true>(p, s);
-  else e = launch<bf16_bits, 1, 8, 16, true>(p, s);
+    e = launch<bf16_bits, 2, BT, BW, true>(p, s);
+  else e = launch<bf16_bits, 1, HT, HW, true>(p, s);
   if (e != hipSuccess || !p.ddecay) return e;
-  const Layout a = layout(p.batch, p.L, p.dim, true);
+  const Layout a = layout(p.batch, p.L, p.dim, BT * BW, true);
   decay_sum_kernel<<<(p.dim + 63) / 64, 1024, 0, s>>>((const float*)((const char*)p.ws + a.part), p.decay,
-                                                      p.ddecay, chunks_of(p.L) * p.batch, p.dim);
+                                                      p.ddecay, pieces_of(p.L, BT * BW) * p.batch, p.dim);
   return hipGetLastError();
 }
 

@@ -7,7 +7,7 @@
 namespace ssm66 {
 namespace gated_scan {
 
-constexpr int kChunk = 128;  // tokens of a block, and from one kept state to the next
+constexpr int kKeep = 64;  // tokens from one kept state to the next
 
 struct Args {
   const void *x, *r, *i;     // (batch, L, dim) io dtype
@@ -20,7 +20,7 @@ struct Args {
   // forwards
   void* y;
   float* last_state;         // nullable (batch, dim)
-  float* states;             // (batch, chunks, dim): the state before each chunk; nullable forwards
+  float* states;             // (batch, kept, dim): the state before every kKeep tokens; nullable forwards
   // backwards
   const void* dy;
   const float* dlast;        // nullable (batch, dim)
@@ -32,7 +32,7 @@ struct Args {
   uint32_t* ticket;
   uint64_t *sums, *groups;   // (chunks, batch, dim), (groups of chunks, batch, dim)
   float* part;               // (chunks * batch, dim)
-  int chunks, tiles;
+  int chunks, kept, tiles;
   uint32_t blocks;
 };
 

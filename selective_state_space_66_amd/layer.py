@@ -27,7 +27,7 @@ import math
 from .lm import SSM_BF16, SSM_F32, _code, _core, _flags, _on_gpu, _ptr, _stream, _want, _workspace
 
 _NORMS = {"layer": 0, "rms": 1}
-_CHUNK = 128  # tokens from one kept state of the recurrence to the next
+_CHUNK = 64   # tokens from one kept state of the recurrence to the next
 
 
 def declare(lib):
@@ -113,7 +113,7 @@ def gated_scan_fwd(x, r, i, decay, h0=None, seq_lens=None, reset=None, y=None, l
     seq_lens: optional (batch,) int32 real lengths (y = 0 past them, the state kept);
     reset: optional (batch, L) bool or uint8, state zeroed before each flagged token.
     Returns (y like x, last_state (batch, dim) float32 or None, states or None): with
-    return_states the state before every 128th token, (batch, ceil(L / 128), dim) float32,
+    return_states the state before every 64th token, (batch, ceil(L / 64), dim) float32,
     which gated_scan_bwd takes.
     """
     c, torch = _core()
