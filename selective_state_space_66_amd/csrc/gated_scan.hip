@@ -39,7 +39,7 @@ namespace gated_scan {
 
 namespace {
 
-constexpr int kGroup = 16;                     // chunks from one published state to the next
+constexpr int kGroup = 4;                     // chunks from one published state to the next
 constexpr uint64_t kEmpty = ~(uint64_t)0;      // a word that is not there yet
 constexpr float kCut = __builtin_inff();       // V of a stretch where a document starts
 
@@ -62,13 +62,20 @@ template <bool PRECISE>
 __device__ __forceinline__ float sigmoid1(float z) {
   return rcp_hw(1.0f + exp_f<PRECISE>(PRECISE ? held(-z) : -z));
 }
-// sigmoid(z) and 1 - sigmoid(z), both to a few units in the last place
+// sigmoid(z) and 1 - sigmoid(z).  PRECISE: both to a few units in the last
+// place.  Else the second is a difference, off by 2^-24 at most: half a unit of
+// a bf16 gradient where the gate is within 3e-5 of open, more of smaller ones.
 template <bool PRECISE>
 __device__ __forceinline__ void sigmoid2(float z, float* s, float* rest) {
-  const float e = exp_f<PRECISE>(PRECISE ? held(-fabsf(z)) : -fabsf(z));
-  const float r = rcp_hw(1.0f + e), er = e * r;
-  *s = z > 0.0f ? r : er;
-  *rest = z > 0.0f ? er : r;
+  if (PRECISE) {
+    const float e = exp_f<true>(held(-fabsf(z)));
+    const float r = rcp_hw(1.0f + e), er = e * r;
+    *s = z > 0.0f ? r : er;
+    *rest = z > 0.0f ? er : r;
+  } else {
+    *s = sigmoid1<false>(z);
+    *rest = 1.0f - *s;
+  }
 }
 
 // 1 - e^-v from v and a = e^-v: the series where it leaves out less than half a
@@ -90,13 +97,14 @@ __device__ __forceinline__ float one_minus(float v, float a) {
 // PRECISE, of log2 else, so that a is one exp2), f the factor of the state, m
 // the root of 1 - a^2.  f is a itself, or (PRECISE, where a is near 1) -b with
 // the sign bit set, which stands for 1 - b.
-struct Gate { float V, f, m; };
+struct Gate { float V, f, m, s, rest; };
 template <bool PRECISE>
 __device__ __forceinline__ float sum_unit(float decay) { return PRECISE ? decay : decay * kLog2e; }
 template <bool PRECISE>
 __device__ __forceinline__ Gate gate_of(float d, float r) {  // d: sum_unit(decay)
   Gate g;
-  g.V = d * sigmoid1<PRECISE>(r);
+  sigmoid2<PRECISE>(r, &g.s, &g.rest);
+  g.V = d * g.s;
   if (PRECISE) {
     const float a = exp_f<true>(-g.V), b = one_minus(g.V, a);
     g.f = g.V < 0.6931472f ? -b : a;
@@ -219,81 +227,86 @@ struct Spot {
     inside = out <= 0 ? 0 : out >= TOK ? TOK : (int)out;
     last = left > TOK ? TOK - 1 : left < 1 ? (int)((len > 0 ? len - 1 : 0) - t0) : (int)left - 1;
     cuts = 0;
-    if (p.reset && real > 0) {
-      const bool start = lane < real && p.reset[b * p.L + t0 + lane] != 0;
-      cuts = (uint32_t)__ballot(start);
-    }
   }
-  // the wave's row j of a tensor: a scalar base and the thread's offset in bytes
+  __device__ __forceinline__ void read_cuts(const Args& p) {
+    if (!p.reset || real <= 0) return;
+    const bool start = lane < real && p.reset[b * p.L + t0 + lane] != 0;
+    cuts = (uint32_t)__ballot(start);
+  }
+  // A tensor's rows of the wave: a scalar base and 32-bit offsets, that of row j
+  // to be loaded and to be stored.  In the place of a token that is not there
+  // the last real one is loaded, and the first channel: loads without a branch,
+  // and what is made of them is left out of the sums and not stored.
   template <typename T>
-  __device__ __forceinline__ const char* row(const Args& p, const void* t, int j) const {
-    return (const char*)t + ((b * p.L + t0 + j) * p.dim) * (int64_t)sizeof(T);
+  __device__ __forceinline__ const char* from(const Args& p, const void* t) const {
+    return (const char*)t + ((b * p.L + t0 + (last < 0 ? last : 0)) * p.dim) * (int64_t)sizeof(T);
   }
   template <typename T>
-  __device__ __forceinline__ uint32_t bytes() const { return (uint32_t)c * (uint32_t)sizeof(T); }
+  __device__ __forceinline__ uint32_t load_at(const Args& p, int j) const {
+    const int q = j < last ? j : last < 0 ? 0 : last;
+    return (here ? (uint32_t)c * (uint32_t)sizeof(T) : 0u) + (uint32_t)q * ((uint32_t)p.dim * (uint32_t)sizeof(T));
+  }
+  template <typename T>
+  __device__ __forceinline__ char* to(const Args& p, void* t) const {
+    return (char*)t + ((b * p.L + t0) * p.dim) * (int64_t)sizeof(T);
+  }
+  template <typename T>
+  __device__ __forceinline__ uint32_t store_at(const Args& p, int j) const {
+    return (uint32_t)c * (uint32_t)sizeof(T) + (uint32_t)j * ((uint32_t)p.dim * (uint32_t)sizeof(T));
+  }
 };
-
-// The wave's tokens of one tensor.  In the place of what is not there stand the
-// last real token and the first channel: loads without a branch, and what is
-// made of them is left out of the sums and not stored.
-template <typename T, int VEC, int TOK, int W>
-__device__ __forceinline__ void load_tokens(const Args& p, const Spot<VEC, TOK, W>& s, const void* from,
-                                            typename Raw<T, VEC>::type (&raw)[TOK]) {
-  typedef typename Raw<T, VEC>::type R;
-  const uint32_t at = s.here ? s.template bytes<T>() : 0u;
-#pragma unroll
-  for (int j = 0; j < TOK; ++j)
-    raw[j] = *(const R*)(s.template row<T>(p, from, j < s.last ? j : s.last) + at);
-}
 
 // ---- the chunks before a block's own --------------------------------------------
 
 // The state before chunk `at` of its row in the order of the chunks, by one
-// wave: from the state before its group of chunks (`begin`: before the first)
-// over the words of those between.
+// wave: the words of the chunks between its group's start and itself, joined,
+// over the state before the group (`begin`: before the first).  The chain from
+// group to group is what a long row waits for, so nothing but one step stands
+// between a group's state and the next one's.
 template <bool PRECISE, int VEC>
 __device__ __forceinline__ void state_before(const Args& p, int at, int64_t row0,
                                              const float (&begin)[VEC], float (&h)[VEC]) {
   const int first = at / kGroup * kGroup, n = at - first;
   const int64_t stride = p.batch * (int64_t)p.dim;
-  constexpr int kAhead = 8;  // words on their way at a time
+  const uint64_t* const group = p.groups + (int64_t)(first / kGroup - 1) * stride + row0;
+  uint64_t state[VEC];
+  float V[VEC], H[VEC];
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) h[k] = begin[k];
-  if (first > 0) {
-    const uint64_t* const g = p.groups + (int64_t)(first / kGroup - 1) * stride + row0;
+  for (int k = 0; k < VEC; ++k) {
+    state[k] = first > 0 ? look(group + k) : 0;
+    V[k] = H[k] = 0.0f;
+  }
+  const uint64_t* const sums = p.sums + (int64_t)first * stride + row0;
+  uint64_t word[kGroup - 1][VEC];
+#pragma unroll
+  for (int q = 0; q < kGroup - 1; ++q)
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) word[q][k] = q < n ? look(sums + q * stride + k) : 0;
+#pragma unroll
+  for (int q = 0; q < kGroup - 1; ++q) {
+    if (q >= n) break;
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      uint64_t word = look(g + k);
-      while (word == kEmpty) {
+      while (word[q][k] == kEmpty) {
         __builtin_amdgcn_s_sleep(1);
-        word = look(g + k);
+        word[q][k] = look(sums + q * stride + k);
       }
-      h[k] = lo_of(word);
+      H[k] = over<PRECISE>(stretch_factor<PRECISE>(hi_of(word[q][k])), H[k], lo_of(word[q][k]));
+      V[k] = joint(V[k], hi_of(word[q][k]));
     }
   }
-  for (int q0 = 0; q0 < n; q0 += kAhead) {
-    const uint64_t* const at0 = p.sums + (int64_t)(first + q0) * stride + row0;
-    uint64_t word[kAhead][VEC];
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) word[q][k] = q0 + q < n ? look(at0 + q * stride + k) : 0;
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
-      if (q0 + q >= n) break;
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        while (word[q][k] == kEmpty) {
-          __builtin_amdgcn_s_sleep(1);
-          word[q][k] = look(at0 + q * stride + k);
-        }
-        h[k] = over<PRECISE>(stretch_factor<PRECISE>(hi_of(word[q][k])), h[k], lo_of(word[q][k]));
-      }
+  for (int k = 0; k < VEC; ++k) {
+    const float f = stretch_factor<PRECISE>(V[k]);
+    while (state[k] == kEmpty) {
+      __builtin_amdgcn_s_sleep(1);
+      state[k] = look(group + k);
     }
+    h[k] = over<PRECISE>(f, first > 0 ? lo_of(state[k]) : begin[k], H[k]);
   }
 }
 
-// The block's number.
+// The block's number: the next of the counter.
 template <bool MANY>
 __device__ __forceinline__ uint32_t block_number(const Args& p) {
   if (!MANY) return blockIdx.y * gridDim.x + blockIdx.x;
@@ -364,20 +377,25 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
   constexpr bool PRECISE = sizeof(T) == 4;
   constexpr int N = 64 * VEC;
   typedef Raw<T, VEC> IO;
-  __shared__ float2 pair[W][N];  // (V, H) of each wave, then (factor, H) of the waves before it
+  // (V, H) of each wave, then (factor, H) of the waves before it, and the state
+  // before the chunk
+  __shared__ float2 pair[W][N], ahead[W][N];
   __shared__ float start[N];
   const uint32_t n = block_number<MANY>(p);
   if (n >= p.blocks) return;
-  const Spot<VEC, TOK, W> s(p, n, false);
-  const int64_t row = s.b * p.dim + s.c;
-  const int slot = s.lane * VEC;
+  Spot<VEC, TOK, W> s(p, n, false);
 
   typename IO::type rx[TOK] = {}, rr[TOK] = {}, ri[TOK] = {};
-  if (MANY || p.L > 0) {
-    load_tokens<T>(p, s, p.r, rr);
-    load_tokens<T>(p, s, p.i, ri);
-    load_tokens<T>(p, s, p.x, rx);
-  }
+  if (MANY || p.L > 0)
+#pragma unroll
+    for (int j = 0; j < TOK; ++j) {
+      rr[j] = *(const typename IO::type*)(s.template from<T>(p, p.r) + s.template load_at<T>(p, j));
+      ri[j] = *(const typename IO::type*)(s.template from<T>(p, p.i) + s.template load_at<T>(p, j));
+      rx[j] = *(const typename IO::type*)(s.template from<T>(p, p.x) + s.template load_at<T>(p, j));
+    }
+  s.read_cuts(p);
+  const int64_t row = s.b * p.dim + s.c;
+  const int slot = s.lane * VEC;
   float d[VEC];
 #pragma unroll
   for (int k = 0; k < VEC; ++k) d[k] = sum_unit<PRECISE>(s.here ? p.decay[s.c + k] : 0.0f);
@@ -407,19 +425,15 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
   lds_barrier();
 
   if (s.w == 0) {
-    float2 e[W][VEC];
-#pragma unroll
-    for (int q = 0; q < W; ++q)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) e[q][k] = pair[q][slot + k];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
       float Vb = 0.0f, Hb = 0.0f;
-#pragma unroll
+#pragma unroll 2
       for (int q = 0; q < W; ++q) {
-        pair[q][slot + k] = make_float2(stretch_factor<PRECISE>(Vb), Hb);
-        Hb = over<PRECISE>(stretch_factor<PRECISE>(e[q][k].x), Hb, e[q][k].y);
-        Vb = joint(Vb, e[q][k].x);
+        const float2 e = pair[q][slot + k];
+        ahead[q][slot + k] = make_float2(stretch_factor<PRECISE>(Vb), Hb);
+        Hb = over<PRECISE>(stretch_factor<PRECISE>(e.x), Hb, e.y);
+        Vb = joint(Vb, e.x);
       }
       // the last chunk of a group publishes the state instead, and nobody reads the last one's
       if (MANY && s.here && s.at + 1 < p.chunks && s.at % kGroup != kGroup - 1)
@@ -430,10 +444,29 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
     float begin[VEC], h[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) h[k] = begin[k] = s.here && p.h0 ? p.h0[row + k] : 0.0f;
+    const bool ends = MANY && s.at % kGroup == kGroup - 1 && s.at + 1 < p.chunks;
+    float fb[VEC], Hb[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) fb[k] = Hb[k] = 0.0f;
+    if (ends)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        float Vb = 0.0f;
+#pragma unroll 2
+        for (int q = 0; q < W; ++q) {
+          const float2 e = pair[q][slot + k];
+          Hb[k] = over<PRECISE>(stretch_factor<PRECISE>(e.x), Hb[k], e.y);
+          Vb = joint(Vb, e.x);
+        }
+        fb[k] = stretch_factor<PRECISE>(Vb);
+      }
     if (s.here) {
       if (MANY) state_before<PRECISE, VEC>(p, s.at, row, begin, h);
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
+        if (ends)
+          publish(p.groups + (int64_t)(s.at / kGroup) * (p.batch * p.dim) + row + k, 0.0f,
+                  over<PRECISE>(fb[k], h[k], Hb[k]));
         start[slot + k] = h[k];
       }
     }
@@ -443,7 +476,7 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
   float h[VEC];
 #pragma unroll
   for (int k = 0; k < VEC; ++k) {
-    const float2 e = pair[s.w][slot + k];
+    const float2 e = ahead[s.w][slot + k];
     h[k] = over<PRECISE>(e.x, start[slot + k], e.y);
   }
   if (p.states && s.here && s.w * TOK % kKeep == 0 && s.t0 < p.L)
@@ -456,7 +489,7 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
 #pragma unroll
       for (int k = 0; k < VEC; ++k) h[k] = advance<PRECISE>(f[j][k], h[k], u[j][k]);
       if (s.here)
-        *(typename IO::type*)((char*)s.template row<T>(p, p.y, j) + s.template bytes<T>()) = IO::put(h);
+        *(typename IO::type*)(s.template to<T>(p, p.y) + s.template store_at<T>(p, j)) = IO::put(h);
     }
   } else {
 #pragma unroll
@@ -469,55 +502,55 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
         o[k] = j < s.real ? h[k] : 0.0f;
       }
       if (s.here && j < s.inside)
-        *(typename IO::type*)((char*)s.template row<T>(p, p.y, j) + s.template bytes<T>()) = IO::put(o);
+        *(typename IO::type*)(s.template to<T>(p, p.y) + s.template store_at<T>(p, j)) = IO::put(o);
     }
   }
-  if (s.w == W - 1 && s.here) {
-    if (MANY && s.at % kGroup == kGroup - 1 && s.at + 1 < p.chunks)
+  if (s.w == W - 1 && s.here && p.last_state && s.chunk == p.chunks - 1)
 #pragma unroll
-      for (int k = 0; k < VEC; ++k)
-        publish(p.groups + (int64_t)(s.at / kGroup) * (p.batch * p.dim) + row + k, 0.0f, h[k]);
-    if (p.last_state && s.chunk == p.chunks - 1)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) p.last_state[row + k] = h[k];
-  }
+    for (int k = 0; k < VEC; ++k) p.last_state[row + k] = h[k];
 }
+
 
 // ---- backwards ----------------------------------------------------------------
 //
 // A block computes its gates and, from the state before its chunk, its states
-// again; the adjoint comes from the right as the state does from the left.
+// again; the adjoint comes from the right as the state does from the left.  The
+// gates stay in registers, x and dy wait in LDS meanwhile.
+
+// What a block keeps of a token's gates: f, m, sigmoid(r), sigmoid(i), and of
+// fp32 also what is left of both to 1.
+template <bool PRECISE, int VEC, int TOK>
+struct Gates {
+  float f[TOK][VEC], m[TOK][VEC], r[TOK][VEC], i[TOK][VEC];
+  float rest_r[PRECISE ? TOK : 1][VEC], rest_i[PRECISE ? TOK : 1][VEC];
+};
 
 // The gradients of the wave's tokens, from the last to the first; before[j] is
 // the state before token j, c the adjoint from the right, P the sum of P_t.
 template <typename T, bool PLAIN, int VEC, int TOK, int W>
 __device__ __forceinline__ void token_gradients(
-    const Args& p, const Spot<VEC, TOK, W>& s, const typename Raw<T, VEC>::type (&rx)[TOK],
-    const typename Raw<T, VEC>::type (&rr)[TOK], const typename Raw<T, VEC>::type (&ri)[TOK],
-    const typename Raw<T, VEC>::type (&rd)[TOK], const float (&f)[TOK][VEC],
-    const float (&m)[TOK][VEC], const float (&before)[TOK][VEC], const float (&decay)[VEC],
-    float (&c)[VEC], float (&P)[VEC]) {
+    const Args& p, const Spot<VEC, TOK, W>& s, const typename Raw<T, VEC>::type* stash,
+    const Gates<sizeof(T) == 4, VEC, TOK>& gate,
+    const float (&before)[TOK][VEC], const float (&decay)[VEC], float (&c)[VEC], float (&P)[VEC]) {
   constexpr bool PRECISE = sizeof(T) == 4;
   typedef Raw<T, VEC> IO;
   typedef typename IO::type R;
 #pragma unroll
   for (int j = TOK - 1; j >= 0; --j) {
-    float x[VEC], r[VEC], i[VEC], dy[VEC], dx[VEC], dr[VEC], di[VEC];
-    IO::get(rx[j], x);
-    IO::get(rr[j], r);
-    IO::get(ri[j], i);
-    IO::get(rd[j], dy);
+    float x[VEC], dy[VEC], dx[VEC], dr[VEC], di[VEC];
+    IO::get(stash[j * (64 * W)], x);
+    IO::get(stash[(TOK + j) * (64 * W)], dy);
     const bool real = PLAIN || j < s.real, cut = !PLAIN && (s.cuts >> j & 1);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      float sr, rest_r, g, rest_g;
-      sigmoid2<PRECISE>(r[k], &sr, &rest_r);
-      sigmoid2<PRECISE>(i[k], &g, &rest_g);
+      const float sr = gate.r[j][k], g = gate.i[j][k], f = gate.f[j][k], m = gate.m[j][k];
+      const float rest_r = PRECISE ? gate.rest_r[PRECISE ? j : 0][k] : 1.0f - sr;
+      const float rest_g = PRECISE ? gate.rest_i[PRECISE ? j : 0][k] : 1.0f - g;
       const float v = decay[k] * sr, lam = dy[k] + c[k];
-      const float al = times<PRECISE>(f[j][k], lam);
-      const float gx = g * x[k], lm = lam * m[j][k];
+      const float al = times<PRECISE>(f, lam);
+      const float gx = g * x[k], lm = lam * m;
       // a v / m: 0 where v is (m is the root of about 2 v there)
-      const float avm = times<PRECISE>(f[j][k], v * rcp_hw(fmaxf(m[j][k], 1e-30f)));
+      const float avm = times<PRECISE>(f, v * rcp_hw(fmaxf(m, 1e-30f)));
       const float q = fmaf(gx, avm, -(v * before[j][k])) * al;
       dx[k] = real ? lm * g : 0.0f;
       di[k] = real ? lm * gx * rest_g : 0.0f;
@@ -528,9 +561,9 @@ __device__ __forceinline__ void token_gradients(
       }
     }
     if (s.here && (PLAIN || j < s.inside)) {
-      *(R*)((char*)s.template row<T>(p, p.dx, j) + s.template bytes<T>()) = IO::put(dx);
-      *(R*)((char*)s.template row<T>(p, p.dr, j) + s.template bytes<T>()) = IO::put(dr);
-      *(R*)((char*)s.template row<T>(p, p.di, j) + s.template bytes<T>()) = IO::put(di);
+      *(R*)(s.template to<T>(p, p.dx) + s.template store_at<T>(p, j)) = IO::put(dx);
+      *(R*)(s.template to<T>(p, p.dr) + s.template store_at<T>(p, j)) = IO::put(dr);
+      *(R*)(s.template to<T>(p, p.di) + s.template store_at<T>(p, j)) = IO::put(di);
     }
   }
 }
@@ -544,24 +577,31 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
   // before each wave, and (factor, D) of the waves behind it
   __shared__ float2 pair[W][N], behind[W][N];
   __shared__ float back[W][N], first[W][N], start[N];
+  // each thread's own x and dy: the registers are for the gates
+  __shared__ typename IO::type stashes[2 * TOK * 64 * W];
+  typename IO::type* const stash = stashes + threadIdx.x;
   const uint32_t n = block_number<MANY>(p);
   if (n >= p.blocks) return;
-  const Spot<VEC, TOK, W> s(p, n, true);
-  const int64_t row = s.b * p.dim + s.c;
-  const int slot = s.lane * VEC;
+  Spot<VEC, TOK, W> s(p, n, true);
 
   typename IO::type rx[TOK] = {}, rr[TOK] = {}, ri[TOK] = {}, rd[TOK] = {};
-  if (MANY || p.L > 0) {
-    load_tokens<T>(p, s, p.r, rr);
-    load_tokens<T>(p, s, p.i, ri);
-    load_tokens<T>(p, s, p.x, rx);
-    load_tokens<T>(p, s, p.dy, rd);
-  }
+  if (MANY || p.L > 0)
+#pragma unroll
+    for (int j = 0; j < TOK; ++j) {
+      rr[j] = *(const typename IO::type*)(s.template from<T>(p, p.r) + s.template load_at<T>(p, j));
+      ri[j] = *(const typename IO::type*)(s.template from<T>(p, p.i) + s.template load_at<T>(p, j));
+      rx[j] = *(const typename IO::type*)(s.template from<T>(p, p.x) + s.template load_at<T>(p, j));
+      rd[j] = *(const typename IO::type*)(s.template from<T>(p, p.dy) + s.template load_at<T>(p, j));
+    }
+  s.read_cuts(p);
+  const int64_t row = s.b * p.dim + s.c;
+  const int slot = s.lane * VEC;
   float decay[VEC];
 #pragma unroll
   for (int k = 0; k < VEC; ++k) decay[k] = s.here ? p.decay[s.c + k] : 0.0f;
 
-  float f[TOK][VEC], u[TOK][VEC], m[TOK][VEC], V[VEC], H[VEC], D[VEC];
+  Gates<PRECISE, VEC, TOK> gate;
+  float u[TOK][VEC], V[VEC], H[VEC], D[VEC];
 #pragma unroll
   for (int k = 0; k < VEC; ++k) V[k] = H[k] = D[k] = 0.0f;
 #pragma unroll
@@ -573,19 +613,31 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
       const Gate g = gate_of<PRECISE>(sum_unit<PRECISE>(decay[k]), r[k]);
-      f[j][k] = g.f;
-      m[j][k] = g.m;
-      u[j][k] = g.m * sigmoid1<PRECISE>(i[k]) * x[k];
+      gate.f[j][k] = g.f;
+      gate.m[j][k] = g.m;
+      gate.r[j][k] = g.s;
+      float rest;
+      sigmoid2<PRECISE>(i[k], &gate.i[j][k], &rest);
+      if (PRECISE) {
+        gate.rest_r[PRECISE ? j : 0][k] = g.rest;
+        gate.rest_i[PRECISE ? j : 0][k] = rest;
+      }
+      u[j][k] = g.m * gate.i[j][k] * x[k];
       V[k] += j < s.real ? g.V : 0.0f;
     }
   }
+#pragma unroll
+  for (int j = 0; j < TOK; ++j) {
+    stash[j * (64 * W)] = rx[j];
+    stash[(TOK + j) * (64 * W)] = rd[j];
+  }
   const bool plain = s.real == TOK && s.cuts == 0;
   if (plain) {
-    run_tokens<PRECISE, true>(s.real, s.cuts, f, u, H);
-    run_back<T, true>(s.real, s.cuts, f, rd, D);
+    run_tokens<PRECISE, true>(s.real, s.cuts, gate.f, u, H);
+    run_back<T, true>(s.real, s.cuts, gate.f, rd, D);
   } else {
-    run_tokens<PRECISE, false>(s.real, s.cuts, f, u, H);
-    run_back<T, false>(s.real, s.cuts, f, rd, D);
+    run_tokens<PRECISE, false>(s.real, s.cuts, gate.f, u, H);
+    run_back<T, false>(s.real, s.cuts, gate.f, rd, D);
   }
 #pragma unroll
   for (int k = 0; k < VEC; ++k) {
@@ -594,13 +646,13 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
   }
   lds_barrier();
 
-  // wave 0: the states before the waves; then, in turn, what stands behind them
-  // and the block's own word (wave 1), and the chunks behind (wave 2)
+  // wave 0: the states before the waves; wave 1: what stands behind them, and
+  // the block's own word; wave 2: the chunks behind
   if (s.w == 0) {
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
       float h = s.here && p.states ? p.states[(s.b * p.kept + s.t0 / kKeep) * p.dim + s.c + k] : 0.0f;
-#pragma unroll
+#pragma unroll 2
       for (int q = 0; q < W; ++q) {
         const float2 e = pair[q][slot + k];
         first[q][slot + k] = h;
@@ -612,7 +664,7 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
       float Vb = 0.0f, Db = 0.0f;
-#pragma unroll
+#pragma unroll 2
       for (int q = W - 1; q >= 0; --q) {
         const float Vq = pair[q][slot + k].x, Dq = back[q][slot + k];
         behind[q][slot + k] = make_float2(stretch_factor<PRECISE>(Vb), Db);
@@ -627,10 +679,31 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
     float begin[VEC], c[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) c[k] = begin[k] = s.here && p.dlast ? p.dlast[row + k] : 0.0f;
+    const bool ends = MANY && s.at % kGroup == kGroup - 1 && s.at + 1 < p.chunks;
+    float fb[VEC], Db[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) fb[k] = Db[k] = 0.0f;
+    if (ends)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        float Vb = 0.0f;
+#pragma unroll 2
+        for (int q = W - 1; q >= 0; --q) {
+          const float Vq = pair[q][slot + k].x;
+          Db[k] = over<PRECISE>(stretch_factor<PRECISE>(Vq), Db[k], back[q][slot + k]);
+          Vb = joint(Vb, Vq);
+        }
+        fb[k] = stretch_factor<PRECISE>(Vb);
+      }
     if (s.here) {
       if (MANY) state_before<PRECISE, VEC>(p, s.at, row, begin, c);
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) start[slot + k] = c[k];
+      for (int k = 0; k < VEC; ++k) {
+        if (ends)
+          publish(p.groups + (int64_t)(s.at / kGroup) * (p.batch * p.dim) + row + k, 0.0f,
+                  over<PRECISE>(fb[k], c[k], Db[k]));
+        start[slot + k] = c[k];
+      }
     }
   }
   lds_barrier();
@@ -642,47 +715,32 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
     c[k] = over<PRECISE>(e.x, start[slot + k], e.y);
   }
 
-  // the gates are computed again rather than kept: what the compiler may not
-  // know to be the same words as above
-#pragma unroll
-  for (int j = 0; j < TOK; ++j) {
-    asm volatile("" : "+v"(rr[j]));
-    asm volatile("" : "+v"(ri[j]));
-    asm volatile("" : "+v"(rx[j]));
-    asm volatile("" : "+v"(rd[j]));
-  }
   float P[VEC];
 #pragma unroll
   for (int k = 0; k < VEC; ++k) P[k] = 0.0f;
   if (plain) {
-    states_before<PRECISE, true>(s.real, s.cuts, f, u, h);
-    token_gradients<T, true>(p, s, rx, rr, ri, rd, f, m, u, decay, c, P);
+    states_before<PRECISE, true>(s.real, s.cuts, gate.f, u, h);
+    token_gradients<T, true>(p, s, stash, gate, u, decay, c, P);
   } else {
-    states_before<PRECISE, false>(s.real, s.cuts, f, u, h);
-    token_gradients<T, false>(p, s, rx, rr, ri, rd, f, m, u, decay, c, P);
+    states_before<PRECISE, false>(s.real, s.cuts, gate.f, u, h);
+    token_gradients<T, false>(p, s, stash, gate, u, decay, c, P);
   }
-  if (s.w == 0 && s.here) {
-    if (MANY && s.at % kGroup == kGroup - 1 && s.at + 1 < p.chunks)
+  if (s.w == 0 && s.here && p.dh0 && s.chunk == 0)
 #pragma unroll
-      for (int k = 0; k < VEC; ++k)
-        publish(p.groups + (int64_t)(s.at / kGroup) * (p.batch * p.dim) + row + k, 0.0f, c[k]);
-    if (p.dh0 && s.chunk == 0)
+    for (int k = 0; k < VEC; ++k) p.dh0[row + k] = c[k];
+  if (p.part) {
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) p.dh0[row + k] = c[k];
+    for (int k = 0; k < VEC; ++k) back[s.w][slot + k] = P[k];
+    lds_barrier();
+    if (s.w == 0 && s.here)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        float t = 0.0f;
+#pragma unroll
+        for (int q = 0; q < W; ++q) t += back[q][slot + k];
+        p.part[((int64_t)s.chunk * p.batch + s.b) * p.dim + s.c + k] = t;
+      }
   }
-  if (!p.part) return;
-  // each wave read its own row of `first` alone, and that before this
-#pragma unroll
-  for (int k = 0; k < VEC; ++k) first[s.w][slot + k] = P[k];
-  lds_barrier();
-  if (s.w == 0 && s.here)
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      float t = 0.0f;
-#pragma unroll
-      for (int q = 0; q < W; ++q) t += first[q][slot + k];
-      p.part[((int64_t)s.chunk * p.batch + s.b) * p.dim + s.c + k] = t;
-    }
 }
 
 // ddecay from the rows of partial sums, added in fp64 in a fixed order: 64
@@ -741,16 +799,6 @@ __global__ __launch_bounds__(256) void step_kernel(const StepArgs p) {
 
 // ---- launches -------------------------------------------------------------------
 
-#ifndef FT
-#define FT 16
-#define FW 8
-#define BT 8
-#define BW 8
-#define GT 16
-#define GW 8
-#define HT 8
-#define HW 8
-#endif
 int64_t pieces_of(int64_t L, int64_t n) { return L > 0 ? (L + n - 1) / n : 1; }
 int64_t up(int64_t n) { return (n + 255) / 256 * 256; }
 
@@ -835,22 +883,22 @@ size_t workspace_bytes(int64_t batch, int64_t L, int64_t dim, bool backward, boo
 }
 
 hipError_t forward(const Args& p, bool f32, hipStream_t s) {
-  if (f32) return launch<float, 1, GT, GW, false>(p, s);
-  if (pairs(p.dim, {p.x, p.r, p.i, p.y})) return launch<bf16_bits, 2, FT, FW, false>(p, s);
-  return launch<bf16_bits, 1, GT, GW, false>(p, s);
+  if (f32) return launch<float, 1, 16, 8, false>(p, s);
+  if (pairs(p.dim, {p.x, p.r, p.i, p.y})) return launch<bf16_bits, 2, 16, 8, false>(p, s);
+  return launch<bf16_bits, 1, 16, 8, false>(p, s);
 }
 
 hipError_t backward(const Args& p, bool f32, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (p.batch == 0) {
-  } else if (f32) e = launch<float, 1, HT, HW, true>(p, s);
+  } else if (f32) e = launch<float, 1, 8, 8, true>(p, s);
   else if (pairs(p.dim, {p.x, p.r, p.i, p.dy, p.dx, p.dr, p.di}))
-    e = launch<bf16_bits, 2, BT, BW, true>(p, s);
-  else e = launch<bf16_bits, 1, HT, HW, true>(p, s);
+    e = launch<bf16_bits, 2, 8, 8, true>(p, s);
+  else e = launch<bf16_bits, 1, 8, 8, true>(p, s);
   if (e != hipSuccess || !p.ddecay) return e;
-  const Layout a = layout(p.batch, p.L, p.dim, BT * BW, true);
+  const Layout a = layout(p.batch, p.L, p.dim, kKeep, true);
   decay_sum_kernel<<<(p.dim + 63) / 64, 1024, 0, s>>>((const float*)((const char*)p.ws + a.part), p.decay,
-                                                      p.ddecay, pieces_of(p.L, BT * BW) * p.batch, p.dim);
+                                                      p.ddecay, pieces_of(p.L, kKeep) * p.batch, p.dim);
   return hipGetLastError();
 }
 
