@@ -79,21 +79,42 @@ __global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void fwd_kernel(co
       b[j][k] = p.bias && c < p.dim ? p.bias[c + k] : 0.0f;
     }
   }
-  // whole blocks stay for the barriers: the rows past the last are empty
+  // whole blocks stay for the barriers: the rows past the last are empty.  A row
+  // is on its way while the one before it is worked on.
   const int64_t rounds = (p.rows + step - 1) / step;
+  RawN<T, VEC> nx[F::kVecs];
+  RawN<TH, VEC> nr[F::kVecs];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < F::kVecs; ++j) {
+      const int c = (l + j * LPR) * VEC;
+      nx[j] = RawN<T, VEC>{};
+      nr[j] = RawN<TH, VEC>{};
+      if (row < p.rows && c < p.dim) {
+        nx[j].load((const T*)p.x + row * p.dim + c);
+        if (p.residual) nr[j].load((const TH*)p.residual + row * p.dim + c);
+      }
+    }
+  };
+  constexpr bool kAhead = VEC > 1;  // (single values take too many registers)
+  if (kAhead) fetch(r0);
   for (int64_t q = 0; q < rounds; ++q) {
     const int64_t row = r0 + q * step;
     const bool real = row < p.rows;
     const int64_t base = row * p.dim;
-    float v[F::kVecs][VEC];
+    float v[F::kVecs][VEC], res[F::kVecs][VEC];
     float s = 0.0f, sq = 0.0f;
+    if (!kAhead) fetch(row);
+#pragma unroll
+    for (int j = 0; j < F::kVecs; ++j) {
+      nx[j].get(v[j]);
+      nr[j].get(res[j]);
+    }
+    if (kAhead) fetch(row + step);
 #pragma unroll
     for (int j = 0; j < F::kVecs; ++j) {
       const int c = (l + j * LPR) * VEC;
       if (real && c < p.dim) {
-        float res[VEC];
-        load_n<VEC>((const T*)p.x + base + c, v[j]);
-        if (p.residual) load_n<VEC>((const TH*)p.residual + base + c, res);
         if (p.drop.rng) {
           float f[VEC];
           drop_factors<VEC>(p.drop, seed, offset, base + c, f);
@@ -102,7 +123,7 @@ __global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void fwd_kernel(co
         }
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-          if (p.residual) v[j][k] += res[k];
+          if (p.residual) v[j][k] += res[j][k];
           v[j][k] = as_stored(v[j][k], (const TH*)nullptr);
         }
         if (p.h) store_n<VEC>((TH*)p.h + base + c, v[j]);
@@ -301,7 +322,13 @@ __global__ __launch_bounds__(256) void column_sum_kernel(const float2* part, flo
   }
 }
 
-constexpr int64_t kBackThreads = 196608;  // of the backward's blocks together
+// Blocks: as many as run at a time (256 CUs of about 1024 threads), so that each
+// has its share of the rows at once (8192 x 4096, bf16 with fp32 h: forwards 83 us;
+// 1.5 times as many blocks 94, a block a row 157).  Those of the backward each
+// leave a row of partial sums; four of 192 threads take 87 us for 16384 x 1536,
+// five 89.
+constexpr int64_t most_blocks(int threads) { return 256 * (1024 / threads); }
+constexpr int64_t back_most(int threads) { return 256 * (threads > 256 ? 1024 / threads : 4); }
 
 struct Call {
   Args p;
@@ -313,8 +340,9 @@ struct Call {
 template <typename T, typename TH, int LPR, int CNT, int VEC>
 hipError_t launch(const Call& c) {
   typedef Form<LPR, CNT, VEC> F;
+  static_assert(F::kThreads >= 192, "the workspace has room for blocks of 192 threads");
   int64_t n = (c.p.rows + F::kRows - 1) / F::kRows;
-  const int64_t most = c.back ? kBackThreads / F::kThreads : 2 * kBackThreads / F::kThreads;
+  const int64_t most = c.back ? back_most(F::kThreads) : most_blocks(F::kThreads);
   if (n > most) n = most;
   *c.blocks = (int)n;
   if (c.back) bwd_kernel<T, TH, LPR, CNT, VEC><<<(unsigned)n, F::kThreads, 0, c.s>>>(c.p);
@@ -354,7 +382,7 @@ hipError_t run(const Call& c, bool x_f32, bool h_f32) {
 
 size_t workspace_bytes(int64_t rows, int64_t dim) {
   // a block takes a row at least, and 192 threads
-  const int64_t most = kBackThreads / 192, n = rows < most ? rows : most;
+  const int64_t most = back_most(192), n = rows < most ? rows : most;
   return (size_t)((n * dim * 8 + 255) / 256 * 256);
 }
 

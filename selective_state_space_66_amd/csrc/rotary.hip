@@ -43,32 +43,38 @@ __device__ __forceinline__ void turn_of(int position, float freq, float* c, floa
 
 // VEC elements an access.  Interleaved: a thread has one access, VEC / 2 pairs
 // (VEC == 1: one pair as two elements).  Halves: two accesses, VEC pairs.  The
-// threads past the pairs copy what is not turned.
-template <typename T, int VEC, bool INTER>
+// threads past the pairs copy what is not turned.  N: unsigned of 32 bits where
+// the number of threads fits (a 64-bit quotient costs as much as four heads).
+template <typename T, int VEC, bool INTER, typename N>
 __global__ __launch_bounds__(256) void rotary_kernel(const Args p) {
   constexpr int W = INTER ? (VEC == 1 ? 2 : VEC) : VEC;      // elements from one thread to the next
   constexpr int PAIRS = INTER ? W / 2 : VEC;
-  const int64_t n = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
-  const int lane = (int)(n % p.lanes);
-  const int64_t rest = n / p.lanes;
-  const int split = (int)(rest % p.splits);
-  const int64_t tok = rest / p.splits;
+  constexpr int kAhead = INTER ? 4 : 2;  // heads loaded before the first is stored
+  const N n = ((N)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+  const N rest = n / (N)p.lanes;
+  const int lane = (int)(n - rest * (N)p.lanes);
+  const int64_t tok = (int64_t)(rest / (N)p.splits);
+  const int split = (int)(rest - (N)tok * (N)p.splits);
   if (tok >= p.tokens) return;
   const int turning = INTER ? 2 * p.pairs / W : p.pairs / VEC;
-  const int heads = p.H + p.Hk, each = (heads + p.splits - 1) / p.splits;
-  const int h0 = split * each, h1 = h0 + each < heads ? h0 + each : heads;
-  if (lane >= turning) {
-    const int at = 2 * p.pairs + (lane - turning) * VEC;
+  const int heads = p.H + p.Hk;
+  const int h0 = split * p.each, h1 = h0 + p.each < heads ? h0 + p.each : heads;
+  const bool turns = lane < turning;
+  const int col = turns ? lane * W : 2 * p.pairs + (lane - turning) * VEC;
+  const T* const q = (const T*)p.q + tok * p.H * p.D + col;
+  const T* const k = (const T*)p.k + tok * p.Hk * p.D + col;
+  T* const qo = (T*)p.qo + tok * p.H * p.D + col;
+  T* const ko = (T*)p.ko + tok * p.Hk * p.D + col;
+  if (!turns) {
     for (int h = h0; h < h1; ++h) {
-      const bool isq = h < p.H;
-      const int64_t row = isq ? (tok * p.H + h) * p.D : (tok * p.Hk + h - p.H) * p.D;
+      const int64_t at = (int64_t)(h < p.H ? h : h - p.H) * p.D;
       float v[VEC];
-      load_n<VEC>((const T*)(isq ? p.q : p.k) + row + at, v);
-      store_n<VEC>((T*)(isq ? p.qo : p.ko) + row + at, v);
+      load_n<VEC>((h < p.H ? q : k) + at, v);
+      store_n<VEC>((h < p.H ? qo : ko) + at, v);
     }
     return;
   }
-  const int position = p.positions ? p.positions[tok] : (int)(tok % p.L);
+  const int position = p.positions ? p.positions[tok] : (int)((N)tok % (N)p.L);
   float c[PAIRS], s[PAIRS];
 #pragma unroll
   for (int j = 0; j < PAIRS; ++j) {
@@ -76,33 +82,39 @@ __global__ __launch_bounds__(256) void rotary_kernel(const Args p) {
     c[j] *= p.mscale;
     s[j] *= p.mscale * p.sign;
   }
-  for (int h = h0; h < h1; ++h) {
-    const bool isq = h < p.H;
-    const int64_t row = isq ? (tok * p.H + h) * p.D : (tok * p.Hk + h - p.H) * p.D;
-    const T* const in = (const T*)(isq ? p.q : p.k) + row + lane * W;
-    T* const out = (T*)(isq ? p.qo : p.ko) + row + lane * W;
-    if constexpr (INTER) {
-      float v[W];
-      load_n<W>(in, v);
+  for (int g0 = h0; g0 < h1; g0 += kAhead) {
+    float a[kAhead][W], b[INTER ? 1 : kAhead][VEC];
 #pragma unroll
-      for (int j = 0; j < PAIRS; ++j) {
-        const float a = v[2 * j], b = v[2 * j + 1];
-        v[2 * j] = fmaf(a, c[j], -(b * s[j]));
-        v[2 * j + 1] = fmaf(b, c[j], a * s[j]);
-      }
-      store_n<W>(out, v);
-    } else {
-      float a[VEC], b[VEC];
-      load_n<VEC>(in, a);
-      load_n<VEC>(in + p.pairs, b);
+    for (int g = 0; g < kAhead; ++g) {
+      const int h = g0 + g;
+      if (h >= h1) break;
+      const T* const in = (h < p.H ? q : k) + (int64_t)(h < p.H ? h : h - p.H) * p.D;
+      load_n<W>(in, a[g]);
+      if constexpr (!INTER) load_n<VEC>(in + p.pairs, b[g]);
+    }
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float u = a[j];
-        a[j] = fmaf(u, c[j], -(b[j] * s[j]));
-        b[j] = fmaf(b[j], c[j], u * s[j]);
+    for (int g = 0; g < kAhead; ++g) {
+      const int h = g0 + g;
+      if (h >= h1) break;
+      T* const out = (h < p.H ? qo : ko) + (int64_t)(h < p.H ? h : h - p.H) * p.D;
+      if constexpr (INTER) {
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j) {
+          const float x = a[g][2 * j], y = a[g][2 * j + 1];
+          a[g][2 * j] = fmaf(x, c[j], -(y * s[j]));
+          a[g][2 * j + 1] = fmaf(y, c[j], x * s[j]);
+        }
+        store_n<W>(out, a[g]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float x = a[g][j], y = b[g][j];
+          a[g][j] = fmaf(x, c[j], -(y * s[j]));
+          b[g][j] = fmaf(y, c[j], x * s[j]);
+        }
+        store_n<VEC>(out, a[g]);
+        store_n<VEC>(out + p.pairs, b[g]);
       }
-      store_n<VEC>(out, a);
-      store_n<VEC>(out + p.pairs, b);
     }
   }
 }
@@ -112,15 +124,20 @@ hipError_t launch(Args p, hipStream_t s) {
   constexpr int W = INTER ? (VEC == 1 ? 2 : VEC) : VEC;
   const bool in_place = p.q == p.qo && p.k == p.ko;
   p.lanes = (INTER ? 2 * p.pairs / W : p.pairs / VEC) + (in_place ? 0 : (p.D - 2 * p.pairs) / VEC);
-  // threads for eight waves a CU before a thread takes more than one head
+  // a thread takes up to eight heads (the angles cost as much as three), fewer
+  // where that leaves less than eight waves a CU
   const int heads = p.H + p.Hk;
   const int64_t wide = p.tokens * p.lanes, want = 256 * 8 * 64;
   int64_t splits = (want + wide - 1) / wide;
+  if (splits < (heads + 7) / 8) splits = (heads + 7) / 8;
   if (splits > heads) splits = heads;
-  const int each = (int)((heads + splits - 1) / splits);
-  p.splits = (heads + each - 1) / each;
-  const Grid g = grid_of((wide * p.splits + 255) / 256, 256);
-  rotary_kernel<T, VEC, INTER><<<dim3(g.x, g.more), 256, 0, s>>>(p);
+  p.each = (int)((heads + splits - 1) / splits);
+  p.splits = (heads + p.each - 1) / p.each;
+  const int64_t n = wide * p.splits;
+  const Grid g = grid_of((n + 255) / 256, 256);
+  const dim3 grid(g.x, g.more);
+  if (n < 0xffff0000ll) rotary_kernel<T, VEC, INTER, uint32_t><<<grid, 256, 0, s>>>(p);
+  else rotary_kernel<T, VEC, INTER, uint64_t><<<grid, 256, 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -56,6 +56,42 @@ __device__ __forceinline__ void store_n(bf16_bits* p, const float (&f)[N]) {
   }
 }
 
+// N values as they lie in memory: on their way while the thread does other work
+template <typename T, int N> struct RawN {
+  T v[N];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = p[k];
+  }
+  __device__ __forceinline__ void get(float (&f)[N]) const {
+#pragma unroll
+    for (int k = 0; k < N; ++k) f[k] = to_f32(v[k]);
+  }
+};
+template <> struct RawN<bf16_bits, 8> {
+  uint4 v;
+  __device__ __forceinline__ void load(const bf16_bits* p) { v = *(const uint4*)p; }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      f[2 * q] = __uint_as_float(w[q] << 16);
+      f[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+    }
+  }
+};
+template <> struct RawN<float, 8> {
+  float4 v[2];
+  __device__ __forceinline__ void load(const float* p) {
+    v[0] = ((const float4*)p)[0];
+    v[1] = ((const float4*)p)[1];
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = v[0].x; f[1] = v[0].y; f[2] = v[0].z; f[3] = v[0].w;
+    f[4] = v[1].x; f[5] = v[1].y; f[6] = v[1].z; f[7] = v[1].w;
+  }
+};
+
 // the value as it will be read back from memory of its type
 __device__ __forceinline__ float as_stored(float v, const float*) { return v; }
 __device__ __forceinline__ float as_stored(float v, const bf16_bits*) { return (float)(__bf16)v; }

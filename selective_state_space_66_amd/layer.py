@@ -59,7 +59,7 @@ def _call(c, torch, index, name, *args):
     """One call on the current stream of GPU `index`, which a launch needs to be the current
     device."""
     fn = getattr(c.load_library(), name)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         st = fn(*args, _stream(torch, index))
     else:
         with torch.cuda.device(index):
@@ -68,13 +68,9 @@ def _call(c, torch, index, name, *args):
         raise c.SsmError(st, name)
 
 
-def _same(c, like, shape, index, **tensors):
-    """Tensors of one shape and type on one GPU."""
-    dtype = like.dtype
-    for name, t in tensors.items():
-        if not (t.shape == shape and t.dtype is dtype and t.get_device() == index
-                and t.is_contiguous()):
-            c._check(t, name, shape, dtype, like.device)
+def _fits(t, shape, dtype, index):
+    return (t.shape == shape and t.dtype is dtype and t.get_device() == index
+            and t.is_contiguous())
 
 
 # sizes alone decide a workspace
@@ -91,15 +87,19 @@ def gated_scan_workspace_size(batch, L, dim, backward=False, need_ddecay=True):
 
 def _scan_check(c, torch, x, r, i, decay, seq_lens, reset):
     index = _on_gpu(x, "x", 3, "(batch, L, dim)")
-    shape = batch, L, dim = x.shape
+    shape, io, dev = x.shape, x.dtype, x.device
+    batch, L, dim = shape
     code = _code(c, torch, x)
-    _same(c, x, shape, index, x=x, r=r, i=i)
-    _want(decay, "decay", (dim,), torch.float32, x.device, index)
+    if not (_fits(r, shape, io, index) and _fits(i, shape, io, index) and x.is_contiguous()
+            and _fits(decay, (dim,), torch.float32, index)):
+        for name, t in (("x", x), ("r", r), ("i", i)):
+            c._check(t, name, shape, io, dev)
+        c._check(decay, "decay", (dim,), torch.float32, dev)
     if seq_lens is not None:
-        _want(seq_lens, "seq_lens", (batch,), torch.int32, x.device, index)
+        _want(seq_lens, "seq_lens", (batch,), torch.int32, dev, index)
     if reset is not None:
-        _want(reset, "reset", (batch, L), torch.uint8, x.device, index)
-    return batch, L, dim, x.device, index, code
+        _want(reset, "reset", (batch, L), torch.uint8, dev, index)
+    return batch, L, dim, dev, index, code
 
 
 def gated_scan_fwd(x, r, i, decay, h0=None, seq_lens=None, reset=None, y=None, last_state=None,
@@ -129,9 +129,8 @@ def gated_scan_fwd(x, r, i, decay, h0=None, seq_lens=None, reset=None, y=None, l
     if last_state is not None:
         _want(last_state, "last_state", (batch, dim), f32, dev, index)
     elif return_last_state:
-        last_state = torch.empty((batch, dim), dtype=f32, device=dev)
-    states = torch.empty((batch, (L + _CHUNK - 1) // _CHUNK, dim), dtype=f32, device=dev) \
-        if return_states else None
+        last_state = decay.new_empty((batch, dim))
+    states = decay.new_empty((batch, (L + _CHUNK - 1) // _CHUNK, dim)) if return_states else None
     ws, size = _workspace(torch, workspace, _scan_ws(batch, L, dim, 0, 0), dev)
     _call(c, torch, index, "ssm_gated_scan_fwd", _ptr(x), _ptr(r), _ptr(i), _ptr(decay), _ptr(h0),
           _ptr(seq_lens), _ptr(reset), _ptr(y), _ptr(last_state), _ptr(states), _ptr(ws), size,
@@ -150,12 +149,12 @@ def gated_scan_bwd(x, r, i, decay, dy, states, dlast=None, seq_lens=None, reset=
     reset = _flags(torch, reset)
     batch, L, dim, dev, index, io = _scan_check(c, torch, x, r, i, decay, seq_lens, reset)
     f32 = torch.float32
-    _same(c, x, x.shape, index, dy=dy)
+    _want(dy, "dy", x.shape, x.dtype, dev, index)
     _want(states, "states", (batch, (L + _CHUNK - 1) // _CHUNK, dim), f32, dev, index)
     _want(dlast, "dlast", (batch, dim), f32, dev, index)
     g = dict(dx=torch.empty_like(x), dr=torch.empty_like(x), di=torch.empty_like(x),
              ddecay=torch.empty_like(decay) if need_ddecay else None,
-             dh0=torch.empty((batch, dim), dtype=f32, device=dev) if need_dh0 else None)
+             dh0=decay.new_empty((batch, dim)) if need_dh0 else None)
     ws, size = _workspace(torch, workspace, _scan_ws(batch, L, dim, 1, int(bool(need_ddecay))), dev)
     _call(c, torch, index, "ssm_gated_scan_bwd", _ptr(x), _ptr(r), _ptr(i), _ptr(decay),
           _ptr(states), _ptr(seq_lens), _ptr(reset), _ptr(dy), _ptr(dlast), _ptr(g["dx"]),
@@ -169,11 +168,16 @@ def gated_scan_step(state, x, r, i, decay, y=None):
     updated in place.  x, r, i: (batch, dim).  Returns y like x."""
     c, torch = _core()
     index = _on_gpu(x, "x", 2, "(batch, dim)")
-    shape = batch, dim = x.shape
+    shape, io, f32 = x.shape, x.dtype, torch.float32
+    batch, dim = shape
     code = _code(c, torch, x)
-    _same(c, x, shape, index, x=x, r=r, i=i)
-    _want(state, "state", shape, torch.float32, x.device, index)
-    _want(decay, "decay", (dim,), torch.float32, x.device, index)
+    if not (_fits(r, shape, io, index) and _fits(i, shape, io, index) and x.is_contiguous()
+            and _fits(state, shape, f32, index) and _fits(decay, (dim,), f32, index)):
+        dev = x.device
+        for name, t in (("x", x), ("r", r), ("i", i)):
+            c._check(t, name, shape, io, dev)
+        c._check(state, "state", shape, f32, dev)
+        c._check(decay, "decay", (dim,), f32, dev)
     if y is None:
         y = torch.empty_like(x)
     else:
@@ -184,6 +188,8 @@ def gated_scan_step(state, x, r, i, decay, y=None):
 
 
 def _rng(torch, p, rng, device, index):
+    if rng is None and p == 0.0:
+        return
     if not 0.0 <= p < 1.0:
         raise ValueError(f"p: expected a rate in [0, 1), got {p}")
     if rng is not None:
@@ -194,11 +200,12 @@ def _rng(torch, p, rng, device, index):
 
 def _dense(c, torch, x, name):
     """The GPU's index of a contiguous io tensor, and its type's code."""
-    if not x.is_cuda:
+    index = x.get_device()
+    if index < 0:
         raise ValueError("tensors must be on the GPU")
     if not x.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    return x.get_device(), _code(c, torch, x)
+    return index, _code(c, torch, x)
 
 
 def _dropout(x, p, rng, site, residual, y, dtype, name):
@@ -246,8 +253,10 @@ def _norm_check(c, torch, x, name, kind, weight, bias, p, rng):
     if kind not in _NORMS:
         raise ValueError(f"kind: expected one of {sorted(_NORMS)}, got {kind!r}")
     dim = x.shape[-1]
-    _want(weight, "weight", (dim,), torch.float32, x.device, index)
-    _want(bias, "bias", (dim,), torch.float32, x.device, index)
+    if weight is not None:
+        _want(weight, "weight", (dim,), torch.float32, x.device, index)
+    if bias is not None:
+        _want(bias, "bias", (dim,), torch.float32, x.device, index)
     _rng(torch, p, rng, x.device, index)
     return x.numel() // dim, dim, index, code
 
@@ -377,29 +386,31 @@ def _rotary(q, k, freqs, positions, mscale, interleaved, inverse, q_out, k_out, 
     c, torch = _core()
     index = _on_gpu(q, names[0], 4, "(batch, L, heads, dim)")
     batch, L, H, D = q.shape
-    dev, code, Hk = q.device, _code(c, torch, q), 0
-    _same(c, q, q.shape, index, **{names[0]: q})
+    io, dev, code, Hk = q.dtype, q.device, _code(c, torch, q), 0
+    if not q.is_contiguous():
+        raise ValueError(f"{names[0]}: must be contiguous")
     if k is not None:
         if k.dim() != 4:
             raise ValueError(f"{names[1]} must be (batch, L, kheads, dim)")
         Hk = k.shape[2]
-        _same(c, q, (batch, L, Hk, D), index, **{names[1]: k})
+        _want(k, names[1], (batch, L, Hk, D), io, dev, index)
     if freqs.dim() != 1 or not 1 <= freqs.shape[0] <= D // 2:
         raise ValueError(f"freqs: expected 1 to {D // 2} values, got {tuple(freqs.shape)}")
     _want(freqs, "freqs", freqs.shape, torch.float32, dev, index)
-    _want(positions, "positions", (batch, L), torch.int32, dev, index)
+    if positions is not None:
+        _want(positions, "positions", (batch, L), torch.int32, dev, index)
     if H < 1:
         raise ValueError(f"{names[0]}: at least one head is needed")
     if q_out is None:
         q_out = torch.empty_like(q)
     else:
-        _want(q_out, "q_out", q.shape, q.dtype, dev, index)
+        _want(q_out, "q_out", q.shape, io, dev, index)
     if k is None:
         k_out = None
     elif k_out is None:
         k_out = torch.empty_like(k)
     else:
-        _want(k_out, "k_out", k.shape, q.dtype, dev, index)
+        _want(k_out, "k_out", k.shape, io, dev, index)
     _call(c, torch, index, "ssm_rotary", _ptr(q), _ptr(k), _ptr(freqs), _ptr(positions), mscale,
           int(bool(interleaved)), inverse, _ptr(q_out), _ptr(k_out), batch, L, H, Hk, D,
           2 * freqs.shape[0], code)
