@@ -1,0 +1,181 @@
+"""The C ABI of include/ssm66_layer.h: every declared function is exported, arguments that the
+library must refuse come back as a status before anything touches a device, and one size stands
+on each side of every limit (no GPU)."""
+import ctypes
+import os
+import re
+
+import pytest
+
+import selective_state_space_66_amd as ssm
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+SRC = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "ssm66_layer.h")).read(), flags=re.S)
+OK, NULL, SHAPE, DTYPE, FLAG, ALIGN, UNSUPPORTED = range(7)
+# never dereferenced: every call below ends at a check
+P, P2, P3, P4, P5, P6, P7 = (ctypes.c_void_p(0x10000 * k) for k in range(1, 8))
+ODD = ctypes.c_void_p(0x10002)
+BYTE = ctypes.c_void_p(0x10001)
+HALF = ctypes.c_void_p(0x10008)    # 8-byte aligned only
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(ssm.LIB_PATH):
+        from selective_state_space_66_amd import build
+        build.build()
+    return ssm.load_library()
+
+
+def test_exports_every_declared_symbol(lib):
+    names = re.findall(r"^\s*(?:int|size_t)\s+(ssm_\w+)\s*\(", SRC, flags=re.M)
+    assert len(names) == 9
+    raw = ctypes.CDLL(ssm.LIB_PATH)
+    for n in names:
+        assert hasattr(raw, n), n
+    for n in ("gated_scan_fwd", "gated_scan_bwd", "gated_scan_step", "add_norm_fwd", "add_norm_bwd",
+              "dropout_fwd", "dropout_bwd", "rotary_freqs", "rotary_fwd", "rotary_bwd"):
+        assert callable(getattr(ssm, n))
+
+
+def caller(fn, **defaults):
+    def call(lib, **kw):
+        assert set(kw) <= set(defaults), kw
+        return getattr(lib, fn)(*{**defaults, **kw}.values(), None)
+    return call
+
+
+scan = caller("ssm_gated_scan_fwd", x=P, r=P, i=P, decay=P, h0=None, lens=None, reset=None, y=P, last=None,
+              states=None, ws=P, size=BIG, batch=2, L=300, dim=64, io=1)
+scan_bwd = caller("ssm_gated_scan_bwd", x=P, r=P, i=P, decay=P, states=P, lens=None, reset=None, dy=P,
+                  dlast=None, dx=P, dr=P, di=P, ddecay=None, dh0=None, ws=P, size=BIG, batch=2, L=300,
+                  dim=64, io=1)
+step = caller("ssm_gated_scan_step", state=P, x=P, r=P, i=P, decay=P, y=P, batch=2, dim=64, io=1)
+drop = caller("ssm_dropout", x=P, residual=None, rng=P, site=0, p=0.5, y=P, n=100, io=1, out=1)
+norm = caller("ssm_add_norm_fwd", x=P, residual=P2, weight=None, bias=None, norm=0, eps=1e-5, p=0.0, rng=None,
+              site=0, y=P3, h=P4, mean=None, rstd=None, rows=5, dim=64, io=1, ht=0)
+norm_bwd = caller("ssm_add_norm_bwd", h=P, dy=P2, dh=None, weight=None, norm=0, mean=P, rstd=P, p=0.0,
+                  rng=None, site=0, dx=P3, dresidual=P4, dweight=P5, dbias=None, ws=P6, size=BIG, rows=5,
+                  dim=64, io=1, ht=0)
+rotary = caller("ssm_rotary", q=P, k=P2, freqs=P, positions=None, mscale=1.0, inter=0, inverse=0, qo=P3, ko=P4,
+                batch=2, L=10, heads=4, kheads=2, dim=64, rot=32, io=1)
+
+
+@pytest.mark.parametrize("call", [scan, scan_bwd])
+def test_scan_refusals(lib, call):
+    for kw, want in ((dict(batch=-1), SHAPE), (dict(L=-1), SHAPE), (dict(dim=-1), SHAPE),
+                     (dict(batch=BIG, L=BIG), SHAPE), (dict(io=2), DTYPE), (dict(x=None), NULL),
+                     (dict(r=None), NULL), (dict(i=None), NULL), (dict(decay=None), NULL),
+                     (dict(x=BYTE), ALIGN), (dict(r=ODD, io=0), ALIGN), (dict(decay=ODD), ALIGN),
+                     (dict(lens=ODD), ALIGN), (dict(ws=HALF), ALIGN), (dict(ws=None), NULL),
+                     (dict(size=64), SHAPE), (dict(dim=(1 << 24) + 1, L=1), UNSUPPORTED),
+                     (dict(dim=1 << 24, L=1, size=0, x=BYTE), ALIGN),
+                     (dict(batch=1, L=0x7fffff01, dim=1), UNSUPPORTED),
+                     (dict(batch=1, L=0x7fffff00, dim=1, size=0), SHAPE)):
+        assert call(lib, **kw) == want, kw
+    # batch * tiles * chunks of 64: 2^31 - 1 is the first that is refused
+    most = ((1 << 31) - 2) // 5
+    assert call(lib, batch=most, L=300, size=0) == SHAPE
+    assert call(lib, batch=most + 1, L=300, size=0) == UNSUPPORTED
+    assert call(lib, dim=0) == OK
+
+
+def test_scan_own_refusals(lib):
+    assert scan(lib, y=None) == NULL and scan(lib, y=BYTE) == ALIGN
+    assert scan(lib, h0=P, last=P) == FLAG  # several blocks read h0
+    assert scan(lib, batch=0) == OK
+    for name in ("states", "dy", "dx", "dr", "di"):
+        assert scan_bwd(lib, **{name: None}) == NULL, name
+        assert scan_bwd(lib, **{name: BYTE}) == ALIGN, name
+    assert scan_bwd(lib, dlast=P, dh0=P) == FLAG
+    for name in ("dlast", "dh0", "ddecay"):
+        assert scan_bwd(lib, **{name: ODD}) == ALIGN, name
+
+
+def test_scan_workspace(lib):
+    size = lib.ssm_gated_scan_workspace_size
+    assert size(2, 64, 1000, 0, 0) == 0  # one chunk
+    assert size(2, 64, 1000, 1, 1) >= 2 * 1000 * 4
+    assert 0 < size(2, 300, 64, 0, 0) < size(2, 300, 64, 1, 1)
+    assert size(2, 300, 64, 1, 0) == size(2, 300, 64, 0, 0)
+    assert size(-1, 300, 64, 0, 0) == 0 and size(1, 1 << 31, 64, 0, 0) == 0 and size(2, 300, 0, 0, 0) == 0
+    need = size(2, 300, 64, 1, 1)
+    assert scan_bwd(lib, ddecay=P, size=need - 1) == SHAPE
+
+
+def test_step_refusals(lib):
+    for kw, want in ((dict(batch=-1), SHAPE), (dict(io=3), DTYPE), (dict(state=None), NULL), (dict(y=None), NULL),
+                     (dict(decay=None), NULL), (dict(x=BYTE), ALIGN), (dict(state=ODD), ALIGN),
+                     (dict(dim=(1 << 24) + 1), UNSUPPORTED), (dict(dim=1 << 24, x=BYTE), ALIGN)):
+        assert step(lib, **kw) == want, kw
+    assert step(lib, batch=0) == OK and step(lib, dim=0) == OK
+
+
+def test_dropout_refusals(lib):
+    for kw, want in ((dict(n=-1), SHAPE), (dict(n=1 << 62), SHAPE), (dict(io=2), DTYPE), (dict(out=-1), DTYPE),
+                     (dict(p=1.0), FLAG), (dict(p=-0.5), FLAG), (dict(p=float("nan")), FLAG), (dict(x=None), NULL),
+                     (dict(y=None), NULL), (dict(rng=None), NULL), (dict(x=BYTE), ALIGN), (dict(y=ODD, out=0), ALIGN),
+                     (dict(residual=BYTE), ALIGN), (dict(rng=ctypes.c_void_p(0x10004)), ALIGN),
+                     (dict(out=0), FLAG)):  # in place, from one type to another
+        assert drop(lib, **kw) == want, kw
+    assert drop(lib, n=0) == OK
+
+
+def test_norm_refusals(lib):
+    for call in (norm, norm_bwd):
+        for kw, want in ((dict(rows=-1), SHAPE), (dict(dim=0), SHAPE), (dict(rows=1 << 62), SHAPE), (dict(io=2), DTYPE),
+                         (dict(ht=2), DTYPE), (dict(io=0, ht=1), DTYPE), (dict(norm=2), FLAG), (dict(p=1.0), FLAG),
+                         (dict(p=0.5), NULL), (dict(dim=16385), UNSUPPORTED), (dict(weight=ODD), ALIGN),
+                         (dict(h=ODD), ALIGN), (dict(rstd=ODD), ALIGN)):
+            assert call(lib, **kw) == want, kw
+        assert call(lib, dim=16384, rstd=ODD) == ALIGN
+    assert norm(lib, x=None) == NULL and norm(lib, y=None) == NULL and norm(lib, rows=0) == OK
+    for kw in (dict(h=P3), dict(h=P), dict(residual=P3)):  # h over y, h over x of another type, y over residual
+        assert norm(lib, **kw) == FLAG, kw
+    for name in ("h", "dy", "dx", "mean", "rstd"):
+        assert norm_bwd(lib, **{name: None}) == NULL, name
+    assert norm_bwd(lib, norm=1, mean=None, ws=None) == NULL  # the RMS norm needs no mean
+    assert norm_bwd(lib, ws=HALF) == ALIGN and norm_bwd(lib, size=8) == SHAPE
+    for kw in (dict(dx=P4), dict(dx=P), dict(dresidual=P), dict(dresidual=P2), dict(dh=P3)):
+        assert norm_bwd(lib, **kw) == FLAG, kw
+    assert lib.ssm_add_norm_workspace_size(10, 16385) == 0
+    assert lib.ssm_add_norm_workspace_size(1, 64) > 0
+    # a row of partial sums for each block, however many rows there are
+    assert lib.ssm_add_norm_workspace_size(1 << 30, 64) == lib.ssm_add_norm_workspace_size(1 << 20, 64)
+
+
+def test_rotary_refusals(lib):
+    for kw, want in ((dict(batch=-1), SHAPE), (dict(heads=0), SHAPE), (dict(kheads=-1), SHAPE), (dict(rot=0), SHAPE),
+                     (dict(rot=31), SHAPE), (dict(rot=66), SHAPE), (dict(io=2), DTYPE), (dict(q=None), NULL),
+                     (dict(k=None), NULL), (dict(qo=None), NULL), (dict(ko=None), NULL), (dict(freqs=None), NULL),
+                     (dict(q=BYTE), ALIGN), (dict(freqs=ODD), ALIGN), (dict(positions=ODD), ALIGN),
+                     (dict(qo=P2), FLAG), (dict(ko=P), FLAG), (dict(ko=P3), FLAG),
+                     (dict(batch=BIG, L=BIG), SHAPE), (dict(L=1 << 31), UNSUPPORTED),
+                     (dict(dim=(1 << 20) + 2, q=BYTE), UNSUPPORTED), (dict(dim=1 << 20, q=BYTE), ALIGN),
+                     (dict(heads=(1 << 20) + 1), UNSUPPORTED), (dict(kheads=(1 << 20) + 1), UNSUPPORTED),
+                     (dict(batch=1 << 25, L=32, heads=2, q=BYTE), UNSUPPORTED),
+                     (dict(batch=(1 << 25) - 1, L=32, heads=2, q=BYTE), ALIGN)):
+        assert rotary(lib, **kw) == want, kw
+    assert rotary(lib, batch=0) == OK and rotary(lib, L=0) == OK
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_arguments(lib):
+    import torch
+    x, d = torch.zeros(1, 4, 8), torch.ones(8)
+    with pytest.raises(ValueError):
+        ssm.gated_scan_fwd(x, x, x, d)
+    with pytest.raises(ValueError):
+        ssm.gated_scan_bwd(x, x, x, d, x, torch.zeros(1, 1, 8))
+    with pytest.raises(ValueError):
+        ssm.gated_scan_step(x[:, 0], x[:, 0], x[:, 0], x[:, 0], d)
+    with pytest.raises(ValueError):
+        ssm.add_norm_fwd(x)
+    with pytest.raises(ValueError):
+        ssm.add_norm_bwd(x, x, None, torch.ones(1, 4))
+    with pytest.raises(ValueError):
+        ssm.dropout_fwd(x, 0.5, torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        ssm.dropout_bwd(x, 0.0, None)
+    with pytest.raises(ValueError):
+        ssm.rotary_fwd(torch.zeros(1, 2, 1, 8), None, torch.ones(4))
