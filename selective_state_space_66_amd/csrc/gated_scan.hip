@@ -32,14 +32,13 @@
 
 #include "gated_scan_launch.h"
 #include "lm_grid.h"
-#include "ssm_device.h"
+#include "vec_io.h"
 
 namespace ssm66 {
 namespace gated_scan {
 
 namespace {
 
-constexpr int kGroup = 4;                     // chunks from one published state to the next
 constexpr uint64_t kEmpty = ~(uint64_t)0;      // a word that is not there yet
 constexpr float kCut = __builtin_inff();       // V of a stretch where a document starts
 
@@ -260,6 +259,16 @@ struct Spot {
 
 // ---- the chunks before a block's own --------------------------------------------
 
+// Whether chunk `at` is the last of its group, and there are more: it publishes
+// the state behind it, the others (but the last of all, whom nobody reads) their
+// own word.
+__device__ __forceinline__ bool ends_group(const Args& p, int at) {
+  return (at & (p.group - 1)) == p.group - 1 && at + 1 < p.chunks;
+}
+__device__ __forceinline__ bool has_word(const Args& p, int at) {
+  return (at & (p.group - 1)) != p.group - 1 && at + 1 < p.chunks;
+}
+
 // The state before chunk `at` of its row in the order of the chunks, by one
 // wave: the words of the chunks between its group's start and itself, joined,
 // over the state before the group (`begin`: before the first).  The chain from
@@ -268,9 +277,10 @@ struct Spot {
 template <bool PRECISE, int VEC>
 __device__ __forceinline__ void state_before(const Args& p, int at, int64_t row0,
                                              const float (&begin)[VEC], float (&h)[VEC]) {
-  const int first = at / kGroup * kGroup, n = at - first;
+  constexpr int kAhead = 3;  // words on their way at a time
+  const int n = at & (p.group - 1), first = at - n;
   const int64_t stride = p.batch * (int64_t)p.dim;
-  const uint64_t* const group = p.groups + (int64_t)(first / kGroup - 1) * stride + row0;
+  const uint64_t* const group = p.groups + (int64_t)(first / p.group - 1) * stride + row0;
   uint64_t state[VEC];
   float V[VEC], H[VEC];
 #pragma unroll
@@ -278,23 +288,25 @@ __device__ __forceinline__ void state_before(const Args& p, int at, int64_t row0
     state[k] = first > 0 ? look(group + k) : 0;
     V[k] = H[k] = 0.0f;
   }
-  const uint64_t* const sums = p.sums + (int64_t)first * stride + row0;
-  uint64_t word[kGroup - 1][VEC];
+  for (int q0 = 0; q0 < n; q0 += kAhead) {
+    const uint64_t* const sums = p.sums + (int64_t)(first + q0) * stride + row0;
+    uint64_t word[kAhead][VEC];
 #pragma unroll
-  for (int q = 0; q < kGroup - 1; ++q)
+    for (int q = 0; q < kAhead; ++q)
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) word[q][k] = q < n ? look(sums + q * stride + k) : 0;
+      for (int k = 0; k < VEC; ++k) word[q][k] = q0 + q < n ? look(sums + q * stride + k) : 0;
 #pragma unroll
-  for (int q = 0; q < kGroup - 1; ++q) {
-    if (q >= n) break;
+    for (int q = 0; q < kAhead; ++q) {
+      if (q0 + q >= n) break;
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      while (word[q][k] == kEmpty) {
-        __builtin_amdgcn_s_sleep(1);
-        word[q][k] = look(sums + q * stride + k);
+      for (int k = 0; k < VEC; ++k) {
+        while (word[q][k] == kEmpty) {
+          __builtin_amdgcn_s_sleep(1);
+          word[q][k] = look(sums + q * stride + k);
+        }
+        H[k] = over<PRECISE>(stretch_factor<PRECISE>(hi_of(word[q][k])), H[k], lo_of(word[q][k]));
+        V[k] = joint(V[k], hi_of(word[q][k]));
       }
-      H[k] = over<PRECISE>(stretch_factor<PRECISE>(hi_of(word[q][k])), H[k], lo_of(word[q][k]));
-      V[k] = joint(V[k], hi_of(word[q][k]));
     }
   }
 #pragma unroll
@@ -437,8 +449,7 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
         Hb = over<PRECISE>(stretch_factor<PRECISE>(e.x), Hb, e.y);
         Vb = joint(Vb, e.x);
       }
-      // the last chunk of a group publishes the state instead, and nobody reads the last one's
-      if (MANY && s.here && s.at + 1 < p.chunks && s.at % kGroup != kGroup - 1)
+      if (MANY && s.here && has_word(p, s.at))
         publish(p.sums + (int64_t)s.at * (p.batch * p.dim) + row + k, Vb, Hb);
     }
   }
@@ -446,7 +457,7 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
     float begin[VEC], h[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) h[k] = begin[k] = s.here && p.h0 ? p.h0[row + k] : 0.0f;
-    const bool ends = MANY && s.at % kGroup == kGroup - 1 && s.at + 1 < p.chunks;
+    const bool ends = MANY && ends_group(p, s.at);
     float fb[VEC], Hb[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) fb[k] = Hb[k] = 0.0f;
@@ -467,7 +478,7 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
         if (ends)
-          publish(p.groups + (int64_t)(s.at / kGroup) * (p.batch * p.dim) + row + k, 0.0f,
+          publish(p.groups + (int64_t)(s.at / p.group) * (p.batch * p.dim) + row + k, 0.0f,
                   over<PRECISE>(fb[k], h[k], Hb[k]));
         start[slot + k] = h[k];
       }
@@ -673,7 +684,7 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
         Db = over<PRECISE>(stretch_factor<PRECISE>(Vq), Db, Dq);
         Vb = joint(Vb, Vq);
       }
-      if (MANY && s.here && s.at + 1 < p.chunks && s.at % kGroup != kGroup - 1)
+      if (MANY && s.here && has_word(p, s.at))
         publish(p.sums + (int64_t)s.at * (p.batch * p.dim) + row + k, Vb, Db);
     }
   }
@@ -681,7 +692,7 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
     float begin[VEC], c[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) c[k] = begin[k] = s.here && p.dlast ? p.dlast[row + k] : 0.0f;
-    const bool ends = MANY && s.at % kGroup == kGroup - 1 && s.at + 1 < p.chunks;
+    const bool ends = MANY && ends_group(p, s.at);
     float fb[VEC], Db[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) fb[k] = Db[k] = 0.0f;
@@ -702,7 +713,7 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
         if (ends)
-          publish(p.groups + (int64_t)(s.at / kGroup) * (p.batch * p.dim) + row + k, 0.0f,
+          publish(p.groups + (int64_t)(s.at / p.group) * (p.batch * p.dim) + row + k, 0.0f,
                   over<PRECISE>(fb[k], c[k], Db[k]));
         start[slot + k] = c[k];
       }
@@ -774,28 +785,29 @@ __global__ __launch_bounds__(1024) void decay_sum_kernel(const float* part, cons
 
 // ---- one token ----------------------------------------------------------------
 
+// A thread keeps its channels over the rows it takes.
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void step_kernel(const StepArgs p) {
   constexpr bool PRECISE = sizeof(T) == 4;
-  typedef Raw<T, VEC> IO;
-  typedef typename IO::type R;
-  const int64_t n = p.batch * p.dim / VEC, stride = (int64_t)gridDim.x * 256;
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += stride) {
-    const int64_t at = e * VEC;
-    const int c = (int)(at % p.dim);
-    float x[VEC], r[VEC], i[VEC], h[VEC];
-    IO::get(*(const R*)((const T*)p.x + at), x);
-    IO::get(*(const R*)((const T*)p.r + at), r);
-    IO::get(*(const R*)((const T*)p.i + at), i);
+  const int c = ((int)blockIdx.x * 256 + (int)threadIdx.x) * VEC;
+  if (c >= p.dim) return;
+  float d[VEC];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) h[k] = p.state[at + k];
+  for (int k = 0; k < VEC; ++k) d[k] = sum_unit<PRECISE>(p.decay[c + k]);
+  for (int64_t row = blockIdx.y; row < p.batch; row += gridDim.y) {
+    const int64_t at = row * p.dim + c;
+    float x[VEC], r[VEC], i[VEC], h[VEC];
+    load_n<VEC>((const T*)p.x + at, x);
+    load_n<VEC>((const T*)p.r + at, r);
+    load_n<VEC>((const T*)p.i + at, i);
+    load_n<VEC>(p.state + at, h);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      const Gate g = gate_of<PRECISE>(sum_unit<PRECISE>(p.decay[c + k]), r[k]);
+      const Gate g = gate_of<PRECISE>(d[k], r[k]);
       h[k] = advance<PRECISE>(g.f, h[k], g.m * sigmoid1<PRECISE>(i[k]) * x[k]);
-      p.state[at + k] = h[k];
     }
-    *(R*)((T*)p.y + at) = IO::put(h);
+    store_n<VEC>(p.state + at, h);
+    store_n<VEC>((T*)p.y + at, h);
   }
 }
 
@@ -804,16 +816,27 @@ __global__ __launch_bounds__(256) void step_kernel(const StepArgs p) {
 int64_t pieces_of(int64_t L, int64_t n) { return L > 0 ? (L + n - 1) / n : 1; }
 int64_t up(int64_t n) { return (n + 255) / 256 * 256; }
 
+// Chunks of a group.  Few rows wait for the chain from group to group (about a
+// microsecond a link), many for the words that each block reads.  Forwards and
+// backwards of 32768 tokens, bf16, with groups of 4, 8, 16 and 32:
+//   256 channels:  73 + 194, 49 + 112, 39 + 73, 37 + 60 us;
+//   512:           78 + 204, 56 + 121, 51 + 84, 55 + 89;
+//   2048:          132 + 295, 133 + 264, 141 + 275, 156 + 316;
+//   8 x 2048 x 1536: 51 + 101, 53 + 103, 54 + 107, 54 + 119.
+int group_of(int64_t rows, int chunk) {
+  return rows <= 256 ? 32 : rows <= 768 ? 16 : rows <= (chunk > kKeep ? 1536 : 2048) ? 8 : 4;
+}
+
 struct Layout { int64_t ticket, sums, groups, part, bytes; };
 // chunk: tokens of a block
 Layout layout(int64_t batch, int64_t L, int64_t dim, int chunk, bool need_part) {
-  const int64_t chunks = pieces_of(L, chunk), rows = batch * dim;
+  const int64_t chunks = pieces_of(L, chunk), rows = batch * dim, group = group_of(rows, chunk);
   Layout a = {};
   int64_t at = 0;
   if (chunks > 1) {
     a.ticket = at; at += 256;
     a.sums = at;   at += up(8 * chunks * rows);
-    a.groups = at; at += up(8 * ((chunks + kGroup - 1) / kGroup) * rows);
+    a.groups = at; at += up(8 * ((chunks + group - 1) / group) * rows);
   }
   a.part = at;
   if (need_part) at += up(4 * chunks * rows);
@@ -826,6 +849,7 @@ void place(Args& p, int vec, int chunk) {
   char* const ws = (char*)p.ws;
   p.chunks = (int)pieces_of(p.L, chunk);
   p.kept = (int)pieces_of(p.L, kKeep);
+  p.group = group_of(p.batch * p.dim, chunk);
   p.tiles = (p.dim + 64 * vec - 1) / (64 * vec);
   p.blocks = (uint32_t)(p.batch * p.tiles * p.chunks);
   p.ticket = (uint32_t*)(ws + a.ticket);
@@ -837,7 +861,7 @@ void place(Args& p, int vec, int chunk) {
 hipError_t clear(const Args& p, hipStream_t s) {
   // the words of the chunks and of the groups lie side by side, both rounded up to 256 bytes
   const int64_t n = (int64_t)(p.groups - p.sums) +
-                    up(8 * (((int64_t)p.chunks + kGroup - 1) / kGroup * (p.batch * p.dim))) / 8;
+                    up(8 * (((int64_t)p.chunks + p.group - 1) / p.group * (p.batch * p.dim))) / 8;
   const int64_t blocks = (n + 511) / 512;
   clear_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(p.ticket, p.sums, n);
   return hipGetLastError();
@@ -919,14 +943,20 @@ hipError_t backward(const Args& p, bool f32, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename T, int VEC>
+void launch_step(const StepArgs& p, hipStream_t s) {
+  const unsigned x = (unsigned)((p.dim / VEC + 255) / 256);
+  int64_t y = 8192 / x;
+  y = y < 1 ? 1 : y < p.batch ? y : p.batch;
+  step_kernel<T, VEC><<<dim3(x, (unsigned)y), 256, 0, s>>>(p);
+}
+
 hipError_t step(const StepArgs& p, bool f32, hipStream_t s) {
-  const bool two = !f32 && p.dim % 2 == 0 && aligned4({p.x, p.r, p.i, p.y});
-  const int64_t n = p.batch * p.dim / (two ? 2 : 1);
-  const int64_t blocks = (n + 255) / 256;
-  const unsigned g = (unsigned)(blocks < 8192 ? blocks : 8192);
-  if (f32) step_kernel<float, 1><<<g, 256, 0, s>>>(p);
-  else if (two) step_kernel<bf16_bits, 2><<<g, 256, 0, s>>>(p);
-  else step_kernel<bf16_bits, 1><<<g, 256, 0, s>>>(p);
+  // 16 bytes an access (8 of bf16) where rows and tensors allow it
+  const uintptr_t all = (uintptr_t)p.x | (uintptr_t)p.r | (uintptr_t)p.i | (uintptr_t)p.y;
+  const bool four = p.dim % 4 == 0 && (uintptr_t)p.state % 16 == 0 && all % (f32 ? 16 : 8) == 0;
+  if (f32) four ? launch_step<float, 4>(p, s) : launch_step<float, 1>(p, s);
+  else four ? launch_step<bf16_bits, 4>(p, s) : launch_step<bf16_bits, 1>(p, s);
   return hipGetLastError();
 }
 

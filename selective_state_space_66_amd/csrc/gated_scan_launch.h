@@ -33,6 +33,7 @@ struct Args {
   uint64_t *sums, *groups;   // (chunks, batch, dim), (groups of chunks, batch, dim)
   float* part;               // (chunks * batch, dim)
   int chunks, kept, tiles;
+  int group;                 // chunks from one published state to the next, a power of two
   uint32_t blocks;
 };
 

@@ -29,6 +29,12 @@ __device__ __forceinline__ void load_n(const bf16_bits* p, float (&f)[N]) {
       f[2 * q] = __uint_as_float(w[q] << 16);
       f[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
     }
+  } else if constexpr (N == 4) {
+    const uint2 v = *(const uint2*)p;
+    f[0] = __uint_as_float(v.x << 16);
+    f[1] = __uint_as_float(v.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.y << 16);
+    f[3] = __uint_as_float(v.y & 0xffff0000u);
   } else {
 #pragma unroll
     for (int k = 0; k < N; ++k) f[k] = to_f32(p[k]);
@@ -50,6 +56,8 @@ __device__ __forceinline__ void store_n(bf16_bits* p, const float (&f)[N]) {
   if constexpr (N == 8) {
     *(uint4*)p = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                             pack_bf16x2(f[6], f[7]));
+  } else if constexpr (N == 4) {
+    *(uint2*)p = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
   } else {
 #pragma unroll
     for (int k = 0; k < N; ++k) store_io(p + k, f[k]);
