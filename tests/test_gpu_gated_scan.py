@@ -137,6 +137,45 @@ def test_padding_and_documents_hold_a_nan_back():
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("every", [1, 7, 64, 128, 512])
+def test_documents_side_by_side(every, io):
+    """A document starts at every token, between waves, at chunks and at groups of chunks; each is
+    a sequence of its own, whatever the state before it."""
+    L = 1300
+    d, h0, dy, dlast, _ = inputs(2, L, 66, TYPES[io], 13, False)
+    reset = torch.zeros((2, L), dtype=torch.uint8, device=DEV)
+    reset[:, ::every] = 1
+    h0.fill_(float("nan"))
+    y, last, states = ssm.gated_scan_fwd(**d, h0=h0, reset=reset, return_states=True)
+    want = ref.forward(**d, reset=reset)
+    ref.check("y", y, want["y"], want["y_bound"], TYPES[io])
+    ref.check("last_state", last, want["last_state"], want["last_bound"])
+    g = ssm.gated_scan_bwd(**d, dy=dy, states=states, dlast=dlast, reset=reset, need_dh0=True)
+    want = ref.backward(**d, dy=dy, dlast=dlast, reset=reset)
+    for n in ("dx", "dr", "di"):
+        ref.check(n, g[n], want[n], want[n + "_bound"], TYPES[io])
+    ref.check("ddecay", g["ddecay"], want["ddecay"], want["ddecay_bound"])
+    assert not g["dh0"].any()
+
+
+@pytest.mark.parametrize("rows,dim", [(1, 200), (1, 700), (1, 1500), (2, 1030), (3, 1100)])
+def test_groups_of_every_size(rows, dim):
+    """Rows for groups of 32, 16, 8 and 4 chunks, forwards and backwards, a few groups long."""
+    d, h0, dy, dlast, kw = inputs(rows, 4500, dim, torch.bfloat16, 14, True)
+    y, last, states = ssm.gated_scan_fwd(**d, h0=h0, return_states=True, **kw)
+    g = ssm.gated_scan_bwd(**d, dy=dy, states=states, dlast=dlast, need_dh0=True, **kw)
+    torch.cuda.synchronize()
+    want = ref.backward(**d, dy=dy, dlast=dlast, h0=h0, **kw)
+    f = ref.forward(**d, h0=h0, **kw)
+    ref.check("y", y, f["y"], f["y_bound"], torch.bfloat16)
+    ref.check("last_state", last, f["last_state"], f["last_bound"])
+    for n in ("dx", "dr", "di"):
+        ref.check(n, g[n], want[n], want[n + "_bound"], torch.bfloat16)
+    for n in ("dh0", "ddecay"):
+        ref.check(n, g[n], want[n], want[n + "_bound"])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_steps_make_the_sequence(io):
     d, h0, _, _, _ = inputs(3, 40, 130, TYPES[io], 6, False)
     y, last, _ = ssm.gated_scan_fwd(**d, h0=h0)
