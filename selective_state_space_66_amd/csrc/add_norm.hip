@@ -284,39 +284,46 @@ __global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void bwd_kernel(co
     }
 }
 
-// dw and db from the blocks' partial sums: 16 columns of a block, 16 groups of
-// lanes that take every 16th row, added in fp64 in a fixed order
-__global__ __launch_bounds__(256) void column_sum_kernel(const float2* part, float* dw, float* db,
-                                                         int blocks, int dim) {
-  __shared__ double2 sums[16][16];
+// dw and db from the blocks' partial sums: 16 columns of a block, 64 groups of
+// lanes that take every 64th row, added in fp64 in a fixed order
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float2* part, float* dw, float* db,
+                                                          int blocks, int dim) {
+  constexpr int kGroups = 64;
+  __shared__ double2 sums[kGroups][16];
   const int l = (int)threadIdx.x & 15, g = (int)threadIdx.x >> 4;
   const int c = (int)blockIdx.x * 16 + l;
   double x = 0.0, y = 0.0;
   if (c < dim) {
     int r = g;
-    for (; r + 112 < blocks; r += 128) {
+    for (; r + 7 * kGroups < blocks; r += 8 * kGroups) {
       float2 t[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) t[q] = part[(int64_t)(r + 16 * q) * dim + c];
+      for (int q = 0; q < 8; ++q) t[q] = part[(int64_t)(r + kGroups * q) * dim + c];
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         x += t[q].x;
         y += t[q].y;
       }
     }
-    for (; r < blocks; r += 16) {
+    for (; r < blocks; r += kGroups) {
       const float2 t = part[(int64_t)r * dim + c];
       x += t.x;
       y += t.y;
     }
   }
-  sums[g][l] = make_double2(x, y);
-  __syncthreads();
-  if (g == 0 && c < dim) {
-    for (int q = 1; q < 16; ++q) {
-      x += sums[q][l].x;
-      y += sums[q][l].y;
+  for (int many = kGroups; many > 1; many /= 8) {  // 64, then 8 of them left
+    sums[g][l] = make_double2(x, y);
+    __syncthreads();
+    if (g < many / 8) {
+      for (int q = 1; q < 8; ++q) {
+        const double2 t = sums[g + q * (many / 8)][l];
+        x += t.x;
+        y += t.y;
+      }
     }
+    __syncthreads();
+  }
+  if (g == 0 && c < dim) {
     if (dw) dw[c] = (float)x;
     if (db) db[c] = (float)y;
   }
@@ -398,7 +405,7 @@ hipError_t backward(const Args& p, bool x_f32, bool h_f32, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (!p.dweight && !p.dbias) return hipSuccess;
-  column_sum_kernel<<<(p.dim + 15) / 16, 256, 0, s>>>(p.part, p.dweight, p.dbias, blocks, p.dim);
+  column_sum_kernel<<<(p.dim + 15) / 16, 1024, 0, s>>>(p.part, p.dweight, p.dbias, blocks, p.dim);
   return hipGetLastError();
 }
 

@@ -19,11 +19,12 @@
 // with its tokens, which never left the registers.  The order of every join is
 // fixed by the chunk's number, so repeated calls give identical bits.
 //
-// Why the waits end: a block takes its chunk's number from a counter, chunks of
-// every row in order, and waits only for words of smaller numbers.  The block
-// with the smallest unfinished number therefore waits for nothing that is not
-// there, and blocks that run are not taken off the chip before they end.  The
-// words are cleared to a pattern that no block writes by a kernel before.
+// Why the waits end: a block that has begun takes its chunk's number from a
+// counter, chunks of every row in order, and waits only for words of smaller
+// numbers of the same counter.  Of the numbers taken the smallest unfinished one
+// waits for nothing that is not there, and blocks that run are not taken off the
+// chip before they end.  The words are cleared to a pattern that no block writes
+// by a kernel before.
 //
 // 1 - a^2 is b (2 - b) with b = 1 - a from its series where v is small: long
 // memories have v of 1e-3 and less.  fp32 tensors also take h - b h instead of
@@ -185,12 +186,42 @@ __device__ __forceinline__ uint64_t look(const uint64_t* at) {
 __device__ __forceinline__ float hi_of(uint64_t w) { return __uint_as_float((uint32_t)(w >> 32)); }
 __device__ __forceinline__ float lo_of(uint64_t w) { return __uint_as_float((uint32_t)w); }
 
-// the counter to 0, n words (an even number, from a 16-byte boundary on) to kEmpty
-__global__ __launch_bounds__(256) void clear_kernel(uint32_t* ticket, uint64_t* words, int64_t n) {
+constexpr int kLine = 32;           // numbers from one counter to the next: 128 bytes
+constexpr uint32_t kCounters = 128;  // at most
+
+// the counters to 0, n words (an even number, from a 16-byte boundary on) to kEmpty
+__global__ __launch_bounds__(256) void clear_kernel(uint32_t* tickets, uint32_t counters,
+                                                    uint64_t* words, int64_t n) {
   const int64_t step = (int64_t)gridDim.x * 256;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
+  if (blockIdx.x == 0 && threadIdx.x < counters) tickets[threadIdx.x * kLine] = 0;
   for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n / 2; k += step)
     ((ulonglong2*)words)[k] = make_ulonglong2(kEmpty, kEmpty);
+}
+
+// The tile a block works on: a row (a tile of channels of one entry) and the
+// number of its chunk, in the order they are taken.
+struct Tile {
+  uint32_t row;
+  int at;
+  bool real;
+};
+// The rows are dealt out to the counters and a block asks that of its number.  Of
+// a counter's numbers the first belong to its rows' first chunks, and so on; a
+// block waits for smaller numbers of its own counter.
+template <bool MANY>
+__device__ __forceinline__ Tile take_tile(const Args& p) {
+  const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x;
+  if (!MANY) return Tile{block, 0, block < p.rows};
+  if (block >= p.blocks) return Tile{0, 0, false};
+  __shared__ uint32_t number;
+  const uint32_t g = (uint32_t)__builtin_amdgcn_readfirstlane((int)(block % p.counters));
+  if (threadIdx.x == 0)
+    number = __hip_atomic_fetch_add(p.tickets + g * kLine, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  const uint32_t n = (uint32_t)__builtin_amdgcn_readfirstlane((int)number);
+  const uint32_t mine = (p.rows - g + p.counters - 1) / p.counters;  // rows of this counter
+  const uint32_t at = (uint32_t)__builtin_amdgcn_readfirstlane((int)(n / mine));
+  return Tile{g + (n - at * mine) * p.counters, (int)at, at < (uint32_t)p.chunks};
 }
 
 // Which tokens and channels a thread has.  `at`: 0, 1, ... of the chunks in the
@@ -205,17 +236,15 @@ struct Spot {
   int real, inside;  // of the wave's tokens, those before the length and before L
   uint32_t cuts;     // bit j: a document starts at the wave's token j
 
-  __device__ __forceinline__ Spot(const Args& p, uint32_t n, bool backward) {
-    // quotients come from the vector unit; the rest is to stay on the scalar one
-    const uint32_t rows = (uint32_t)__builtin_amdgcn_readfirstlane((int)(p.blocks / (uint32_t)p.chunks));
-    at = __builtin_amdgcn_readfirstlane((int)(n / rows));
-    const uint32_t row = n - (uint32_t)at * rows;
-    const int entry = __builtin_amdgcn_readfirstlane((int)(row / (uint32_t)p.tiles));
+  __device__ __forceinline__ Spot(const Args& p, const Tile& t, bool backward) {
+    at = t.at;
+    // a quotient comes from the vector unit; the rest is to stay on the scalar one
+    const int entry = __builtin_amdgcn_readfirstlane((int)(t.row / (uint32_t)p.tiles));
     b = entry;
     chunk = backward ? p.chunks - 1 - at : at;
     lane = (int)threadIdx.x & 63;
     w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    c = ((int)(row - (uint32_t)entry * (uint32_t)p.tiles) * 64 + lane) * VEC;
+    c = ((int)(t.row - (uint32_t)entry * (uint32_t)p.tiles) * 64 + lane) * VEC;
     here = c < p.dim;
     t0 = (int64_t)chunk * (TOK * W) + w * TOK;
     int64_t len = p.L;
@@ -320,17 +349,6 @@ __device__ __forceinline__ void state_before(const Args& p, int at, int64_t row0
   }
 }
 
-// The block's number: the next of the counter.
-template <bool MANY>
-__device__ __forceinline__ uint32_t block_number(const Args& p) {
-  if (!MANY) return blockIdx.y * gridDim.x + blockIdx.x;
-  __shared__ uint32_t number;
-  if (threadIdx.x == 0)
-    number = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  return __builtin_amdgcn_readfirstlane(number);
-}
-
 // H of the wave's tokens, from a state of zero (or of `h`).
 template <bool PRECISE, bool PLAIN, int VEC, int TOK>
 __device__ __forceinline__ void run_tokens(int real, uint32_t cuts, const float (&f)[TOK][VEC],
@@ -395,9 +413,9 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
   // before the chunk
   __shared__ float2 pair[W][N], ahead[W][N];
   __shared__ float start[N];
-  const uint32_t n = block_number<MANY>(p);
-  if (n >= p.blocks) return;
-  Spot<VEC, TOK, W> s(p, n, false);
+  const Tile tile = take_tile<MANY>(p);
+  if (!tile.real) return;
+  Spot<VEC, TOK, W> s(p, tile, false);
 
   typename IO::type rx[TOK] = {}, rr[TOK] = {}, ri[TOK] = {};
   if (MANY || p.L > 0)
@@ -593,9 +611,9 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
   // each thread's own x and dy: the registers are for the gates
   __shared__ typename IO::type stashes[2 * TOK * 64 * W];
   typename IO::type* const stash = stashes + threadIdx.x;
-  const uint32_t n = block_number<MANY>(p);
-  if (n >= p.blocks) return;
-  Spot<VEC, TOK, W> s(p, n, true);
+  const Tile tile = take_tile<MANY>(p);
+  if (!tile.real) return;
+  Spot<VEC, TOK, W> s(p, tile, true);
 
   typename IO::type rx[TOK] = {}, rr[TOK] = {}, ri[TOK] = {}, rd[TOK] = {};
   if (MANY || p.L > 0)
@@ -766,12 +784,12 @@ __global__ __launch_bounds__(1024) void decay_sum_kernel(const float* part, cons
   double t = 0.0;
   if (c < dim) {
     int64_t r = w;
-    for (; r + 48 < rows; r += 64) {
-      float v[4];
+    for (; r + 112 < rows; r += 128) {
+      float v[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = part[(r + 16 * q) * dim + c];
+      for (int q = 0; q < 8; ++q) v[q] = part[(r + 16 * q) * dim + c];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) t += v[q];
+      for (int q = 0; q < 8; ++q) t += v[q];
     }
     for (; r < rows; r += 16) t += part[r * dim + c];
   }
@@ -834,7 +852,7 @@ Layout layout(int64_t batch, int64_t L, int64_t dim, int chunk, bool need_part) 
   Layout a = {};
   int64_t at = 0;
   if (chunks > 1) {
-    a.ticket = at; at += 256;
+    a.ticket = at; at += 4 * kLine * kCounters;
     a.sums = at;   at += up(8 * chunks * rows);
     a.groups = at; at += up(8 * ((chunks + group - 1) / group) * rows);
   }
@@ -851,8 +869,18 @@ void place(Args& p, int vec, int chunk) {
   p.kept = (int)pieces_of(p.L, kKeep);
   p.group = group_of(p.batch * p.dim, chunk);
   p.tiles = (p.dim + 64 * vec - 1) / (64 * vec);
-  p.blocks = (uint32_t)(p.batch * p.tiles * p.chunks);
-  p.ticket = (uint32_t*)(ws + a.ticket);
+  p.rows = (uint32_t)(p.batch * p.tiles);
+  // A counter gives 85 numbers a microsecond.  Blocks that all begin at once (3 x
+  // 1537 x 1000, fp32, forwards) take 26 us with a counter for each row, 29 with
+  // two and 30 with one; where there are more than run at a time, two keep them
+  // from loading in step (8 x 2048 x 1536, bf16, backwards: 94 us; a counter for
+  // each row 98; 32768 x 2048: 246 and 264).
+  const uint32_t most = (int64_t)p.rows * p.chunks <= 1024 ? kCounters : 2;
+  // rows of a counter, and as few counters as they need: hardly a block is left over
+  const uint32_t each = (p.rows + most - 1) / most;
+  p.counters = (p.rows + each - 1) / each;
+  p.blocks = p.counters * each * (uint32_t)p.chunks;
+  p.tickets = (uint32_t*)(ws + a.ticket);
   p.sums = (uint64_t*)(ws + a.sums);
   p.groups = (uint64_t*)(ws + a.groups);
   p.part = p.ddecay ? (float*)(ws + a.part) : nullptr;
@@ -863,7 +891,7 @@ hipError_t clear(const Args& p, hipStream_t s) {
   const int64_t n = (int64_t)(p.groups - p.sums) +
                     up(8 * (((int64_t)p.chunks + p.group - 1) / p.group * (p.batch * p.dim))) / 8;
   const int64_t blocks = (n + 511) / 512;
-  clear_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(p.ticket, p.sums, n);
+  clear_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(p.tickets, p.counters, p.sums, n);
   return hipGetLastError();
 }
 

@@ -29,12 +29,13 @@ struct Args {
   float* dh0;                // nullable (batch, dim)
   void* ws;
   // set by the launch
-  uint32_t* ticket;
+  uint32_t* tickets;         // one counter in 128 bytes
   uint64_t *sums, *groups;   // (chunks, batch, dim), (groups of chunks, batch, dim)
   float* part;               // (chunks * batch, dim)
   int chunks, kept, tiles;
   int group;                 // chunks from one published state to the next, a power of two
-  uint32_t blocks;
+  uint32_t rows;             // batch * tiles
+  uint32_t counters, blocks;
 };
 
 // whether the grid these sizes need exists
