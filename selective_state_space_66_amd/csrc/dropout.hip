@@ -5,7 +5,9 @@
 // is the same map of dy without the residual.
 //
 // A thread takes eight values: two calls of the generator and one or two 16-byte
-// accesses a tensor.  Tensors off a 16-byte boundary, and the last values, take
+// accesses a tensor.  HBM bounds it: 16384 x 1536, bf16, with a residual 26 us (151
+// MB, 5.8 TB/s, part of it from the Infinity Cache); its 27 vector instructions a
+// value, most of them the generator's, would take 17.  Tensors off a 16-byte boundary, and the last values, take
 // the same values one at a time.
 #include "dropout_launch.h"
 #include "vec_io.h"
