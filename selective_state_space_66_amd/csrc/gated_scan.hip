@@ -147,8 +147,9 @@ template <bool PRECISE>
 __device__ __forceinline__ float stretch_factor(float V) {
   if (V == kCut) return kCut;
   if (!PRECISE) return exp2_hw(-V);
+  // a stretch of nothing is the factor 1 (an infinite state passes it as it is)
   const float a = exp_f<true>(-V);
-  return V < 0.6931472f ? -one_minus(V, a) : a;
+  return V < 0.6931472f && V > 0.0f ? -one_minus(V, a) : a;
 }
 template <bool PRECISE>
 __device__ __forceinline__ float over(float f, float h, float add) {
@@ -480,7 +481,7 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
         publish(p.sums + (int64_t)s.at * (p.batch * p.dim) + row + k, Vb, Hb);
     }
   }
-  if (s.w == (W > 1 ? 1 : 0)) {
+  if (s.w == 1) {
     float begin[VEC], h[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) h[k] = begin[k] = s.here && p.h0 ? p.h0[row + k] : 0.0f;
@@ -549,7 +550,6 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
 #pragma unroll
     for (int k = 0; k < VEC; ++k) p.last_state[row + k] = h[k];
 }
-
 
 // ---- backwards ----------------------------------------------------------------
 //
@@ -700,7 +700,7 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
       }
     }
   }
-  if (s.w == 1 % W) {
+  if (s.w == 1) {
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
       float Vb = 0.0f, Db = 0.0f;
@@ -715,7 +715,7 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
         publish(p.sums + (int64_t)s.at * (p.batch * p.dim) + row + k, Vb, Db);
     }
   }
-  if (s.w == 2 % W) {
+  if (s.w == 2) {
     float begin[VEC], c[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) c[k] = begin[k] = s.here && p.dlast ? p.dlast[row + k] : 0.0f;
@@ -949,13 +949,13 @@ bool fits(int64_t batch, int64_t L, int64_t dim) {
 }
 
 size_t workspace_bytes(int64_t batch, int64_t L, int64_t dim, bool backward, bool need_ddecay) {
-  // the smaller chunk needs more
+  // the forward's chunks are longer and need less, however the groups fall
   return (size_t)layout(batch, L, dim, kKeep, backward && need_ddecay).bytes;
 }
 
 // Up to kKeep tokens: one chunk, and a kernel of few instructions, which are most
-// of what such a call waits for (33 tokens of 256 channels: 8.0 -> 4.9 us; 64 x 64 x 1024,
-// bf16: 16.1 -> 13.3).
+// of what such a call waits for (33 tokens of 256 channels: 4.9 us, by the kernel
+// for longer rows 8.0; 64 x 64 x 1024, bf16: 13.3 and 16.1).
 hipError_t forward(const Args& p, bool f32, hipStream_t s) {
   if (p.L <= kKeep)
     return f32 ? launch<float, 1, 4, 16, false, true>(p, s) : launch<bf16_bits, 1, 4, 16, false, true>(p, s);

@@ -237,6 +237,22 @@ def test_empty_calls():
     assert not ssm.gated_scan_bwd(none, none, none, decay, none, states)["ddecay"].any()
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("L", [0, 40, 1000])
+def test_a_state_without_tokens_is_kept_as_it_is(L, io):
+    """Rows of length 0 hand their state on bit for bit, an infinity and a tiny number too, and
+    the gradient of the last state back."""
+    d, h0, dy, dlast, _ = inputs(2, L, 8, TYPES[io], 15, False)
+    lens = torch.zeros(2, dtype=torch.int32, device=DEV)
+    h0[0] = torch.tensor([float("inf"), -float("inf"), 1e-38, 3e38, 0.0, -0.5, 1.0, 7e-20], device=DEV)
+    y, last, states = ssm.gated_scan_fwd(**d, h0=h0, seq_lens=lens, return_states=True)
+    assert torch.equal(last, h0) and not y.any()
+    g = ssm.gated_scan_bwd(**d, dy=dy, states=states, dlast=dlast, seq_lens=lens, need_dh0=True)
+    assert torch.equal(g["dh0"], dlast)
+    for n in ("dx", "dr", "di", "ddecay"):
+        assert not g[n].any()
+
+
 def test_same_bits_again_on_another_stream_and_beside_another_call():
     a, h0, dy, dlast, kw = inputs(4, 5000, 256, torch.bfloat16, 9, True)
     b = inputs(2, 7000, 192, torch.float32, 10, False)[0]
