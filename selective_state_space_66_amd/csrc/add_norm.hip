@@ -25,14 +25,38 @@ namespace add_norm {
 
 namespace {
 
-// LPR lanes hold a row, CNT values each, VEC neighbouring ones at a time
-// (VEC == 1: dims that are no multiple of eight, tensors off 16 bytes).
-template <int LPR, int CNT, int VEC>
+constexpr int VEC = 8;
+
+// LPR lanes hold a row, VECS times eight neighbouring values each.
+template <int LPR>
 struct Form {
   static constexpr int kThreads = LPR > 128 ? LPR : 256;
   static constexpr int kRows = kThreads / LPR;  // of a block at a time
-  static constexpr int kVecs = CNT / VEC;
 };
+
+// how many of the eight values from column c on the row has (EVEN: rows are
+// multiples of eight, all or none)
+template <bool EVEN>
+__device__ __forceinline__ int values_at(int c, int dim) {
+  return c < dim ? (EVEN || dim - c >= VEC ? VEC : dim - c) : 0;
+}
+template <bool EVEN, typename T>
+__device__ __forceinline__ void load(Raw8<T>& r, const T* p, int n) {
+  if constexpr (EVEN) {
+    if (n > 0) r.load(p, VEC);
+    else r = Raw8<T>{};
+  } else {
+    r.load(p, n);
+  }
+}
+
+// The factors of eight values of a row; rows of a multiple of four begin at one.
+template <bool EVEN>
+__device__ __forceinline__ void factors(const Args& p, uint64_t seed, uint64_t offset, int64_t at,
+                                        float (&f)[VEC]) {
+  if (EVEN || p.dim % 4 == 0) drop_factors(p.drop, seed, offset, at, f);
+  else drop_factors_any(p.drop, seed, offset, at, f);
+}
 
 // Sums of two values over the lanes of a row, to all of them.  `part` has room
 // for the waves of a block; a second call uses the other half.
@@ -58,9 +82,9 @@ __device__ __forceinline__ void row_sums(float& a, float& b, float2* part) {
   }
 }
 
-template <typename T, typename TH, int LPR, int CNT, int VEC>
-__global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void fwd_kernel(const Args p) {
-  typedef Form<LPR, CNT, VEC> F;
+template <typename T, typename TH, int LPR, int VECS, bool EVEN>
+__global__ __launch_bounds__(Form<LPR>::kThreads) void fwd_kernel(const Args p) {
+  typedef Form<LPR> F;
   __shared__ float2 part[2][16];
   const int l = (int)threadIdx.x % LPR;
   const int64_t r0 = (int64_t)blockIdx.x * F::kRows + (int)threadIdx.x / LPR;
@@ -71,67 +95,55 @@ __global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void fwd_kernel(co
     seed = (uint64_t)p.drop.rng[0];
     offset = (uint64_t)p.drop.rng[1] + p.drop.site;
   }
-  float w[F::kVecs][VEC], b[F::kVecs][VEC];
+  float w[VECS][VEC], b[VECS][VEC];
 #pragma unroll
-  for (int j = 0; j < F::kVecs; ++j) {
+  for (int j = 0; j < VECS; ++j) {
     const int c = (l + j * LPR) * VEC;
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      w[j][k] = p.weight && c < p.dim ? p.weight[c + k] : 1.0f;
-      b[j][k] = p.bias && c < p.dim ? p.bias[c + k] : 0.0f;
+      w[j][k] = p.weight && c + k < p.dim ? p.weight[c + k] : 1.0f;
+      b[j][k] = p.bias && c + k < p.dim ? p.bias[c + k] : 0.0f;
     }
   }
   // whole blocks stay for the barriers: the rows past the last are empty.  A row
   // is on its way while the one before it is worked on.
   const int64_t rounds = (p.rows + step - 1) / step;
-  RawN<T, VEC> nx[F::kVecs];
-  RawN<TH, VEC> nr[F::kVecs];
+  Raw8<T> nx[VECS];
+  Raw8<TH> nr[VECS];
   auto fetch = [&](int64_t row) {
 #pragma unroll
-    for (int j = 0; j < F::kVecs; ++j) {
-      const int c = (l + j * LPR) * VEC;
-      nx[j] = RawN<T, VEC>{};
-      nr[j] = RawN<TH, VEC>{};
-      if (row < p.rows && c < p.dim) {
-        nx[j].load((const T*)p.x + row * p.dim + c);
-        if (p.residual) nr[j].load((const TH*)p.residual + row * p.dim + c);
-      }
+    for (int j = 0; j < VECS; ++j) {
+      const int c = (l + j * LPR) * VEC, n = row < p.rows ? values_at<EVEN>(c, p.dim) : 0;
+      load<EVEN>(nx[j], (const T*)p.x + row * p.dim + c, n);
+      load<EVEN>(nr[j], (const TH*)p.residual + row * p.dim + c, p.residual ? n : 0);
     }
   };
-  constexpr bool kAhead = VEC > 1;  // (single values take too many registers)
-  if (kAhead) fetch(r0);
+  fetch(r0);
   for (int64_t q = 0; q < rounds; ++q) {
     const int64_t row = r0 + q * step;
     const bool real = row < p.rows;
     const int64_t base = row * p.dim;
-    float v[F::kVecs][VEC], res[F::kVecs][VEC];
+    float v[VECS][VEC], res[VECS][VEC];
     float s = 0.0f, sq = 0.0f;
-    if (!kAhead) fetch(row);
 #pragma unroll
-    for (int j = 0; j < F::kVecs; ++j) {
+    for (int j = 0; j < VECS; ++j) {
       nx[j].get(v[j]);
       nr[j].get(res[j]);
     }
-    if (kAhead) fetch(row + step);
+    fetch(row + step);
 #pragma unroll
-    for (int j = 0; j < F::kVecs; ++j) {
+    for (int j = 0; j < VECS; ++j) {
       const int c = (l + j * LPR) * VEC;
-      if (real && c < p.dim) {
+      if (real && c < p.dim) {  // (elsewhere, and past the row's end, all is zero)
         if (p.drop.rng) {
           float f[VEC];
-          drop_factors<VEC>(p.drop, seed, offset, base + c, f);
+          factors<EVEN>(p, seed, offset, base + c, f);
 #pragma unroll
           for (int k = 0; k < VEC; ++k) v[j][k] = dropped(v[j][k], f[k]);
         }
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          if (p.residual) v[j][k] += res[j][k];
-          v[j][k] = as_stored(v[j][k], (const TH*)nullptr);
-        }
-        if (p.h) store_n<VEC>((TH*)p.h + base + c, v[j]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) v[j][k] = 0.0f;
+        for (int k = 0; k < VEC; ++k) v[j][k] = as_stored(v[j][k] + res[j][k], (const TH*)nullptr);
+        if (p.h) store_8((TH*)p.h + base + c, v[j], values_at<EVEN>(c, p.dim));
       }
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
@@ -147,11 +159,16 @@ __global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void fwd_kernel(co
       float left = 0.0f;
       sq = 0.0f;
 #pragma unroll
-      for (int j = 0; j < F::kVecs; ++j) {
-        const bool in = (l + j * LPR) * VEC < p.dim;
+      for (int j = 0; j < VECS; ++j) {
+        const int n = values_at<EVEN>((l + j * LPR) * VEC, p.dim);
+        const bool in = n > 0;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[j][k] = in ? v[j][k] - mean : 0.0f;
+        if (!EVEN)
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) v[j][k] = k < n ? v[j][k] : 0.0f;
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-          v[j][k] = in ? v[j][k] - mean : 0.0f;
           left += v[j][k];
           sq = fmaf(v[j][k], v[j][k], sq);
         }
@@ -162,19 +179,19 @@ __global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void fwd_kernel(co
       var = var < 0.0f ? 0.0f : var;  // (a NaN stays one)
       mean += left;
 #pragma unroll
-      for (int j = 0; j < F::kVecs; ++j)
+      for (int j = 0; j < VECS; ++j)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) v[j][k] -= left;
     }
     const float rstd = 1.0f / sqrtf(var + p.eps);
 #pragma unroll
-    for (int j = 0; j < F::kVecs; ++j) {
+    for (int j = 0; j < VECS; ++j) {
       const int c = (l + j * LPR) * VEC;
       if (real && c < p.dim) {
         float y[VEC];
 #pragma unroll
         for (int k = 0; k < VEC; ++k) y[k] = fmaf(v[j][k] * rstd, w[j][k], b[j][k]);
-        store_n<VEC>((T*)p.y + base + c, y);
+        store_8((T*)p.y + base + c, y, values_at<EVEN>(c, p.dim));
       }
     }
     if (real && l == 0) {
@@ -185,9 +202,9 @@ __global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void fwd_kernel(co
   }
 }
 
-template <typename T, typename TH, int LPR, int CNT, int VEC>
-__global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void bwd_kernel(const Args p) {
-  typedef Form<LPR, CNT, VEC> F;
+template <typename T, typename TH, int LPR, int VECS, bool EVEN>
+__global__ __launch_bounds__(Form<LPR>::kThreads) void bwd_kernel(const Args p) {
+  typedef Form<LPR> F;
   __shared__ float2 part[2][16];
   const int l = (int)threadIdx.x % LPR;
   const int64_t r0 = (int64_t)blockIdx.x * F::kRows + (int)threadIdx.x / LPR;
@@ -198,13 +215,13 @@ __global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void bwd_kernel(co
     seed = (uint64_t)p.drop.rng[0];
     offset = (uint64_t)p.drop.rng[1] + p.drop.site;
   }
-  float w[F::kVecs][VEC], dw[F::kVecs][VEC], db[F::kVecs][VEC];
+  float w[VECS][VEC], dw[VECS][VEC], db[VECS][VEC];
 #pragma unroll
-  for (int j = 0; j < F::kVecs; ++j) {
+  for (int j = 0; j < VECS; ++j) {
     const int c = (l + j * LPR) * VEC;
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      w[j][k] = p.weight && c < p.dim ? p.weight[c + k] : 1.0f;
+      w[j][k] = p.weight && c + k < p.dim ? p.weight[c + k] : 1.0f;
       dw[j][k] = db[j][k] = 0.0f;
     }
   }
@@ -213,23 +230,24 @@ __global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void bwd_kernel(co
     const int64_t row = r0 + q * step;
     const bool real = row < p.rows;
     const int64_t base = row * p.dim;
-    float xh[F::kVecs][VEC], dy[F::kVecs][VEC], dh[F::kVecs][VEC];
+    constexpr bool kLate = VECS > 1;  // dh loaded where it is needed: registers
+    float xh[VECS][VEC], dy[VECS][VEC];
+    Raw8<TH> rh[VECS];
 #pragma unroll
-    for (int j = 0; j < F::kVecs; ++j) {
-      const int c = (l + j * LPR) * VEC;
-      if (real && c < p.dim) {
-        load_n<VEC>((const TH*)p.h + base + c, xh[j]);
-        load_n<VEC>((const T*)p.dy + base + c, dy[j]);
-        if (p.dh) load_n<VEC>((const TH*)p.dh + base + c, dh[j]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) xh[j][k] = dy[j][k] = 0.0f;
-      }
+    for (int j = 0; j < VECS; ++j) {
+      const int c = (l + j * LPR) * VEC, n = real ? values_at<EVEN>(c, p.dim) : 0;
+      Raw8<TH> a;
+      Raw8<T> b;
+      load<EVEN>(a, (const TH*)p.h + base + c, n);
+      load<EVEN>(b, (const T*)p.dy + base + c, n);
+      if (!kLate) load<EVEN>(rh[j], (const TH*)p.dh + base + c, p.dh ? n : 0);
+      a.get(xh[j]);
+      b.get(dy[j]);
     }
     const float mean = real && !p.rms ? p.mean[row] : 0.0f, rstd = real ? p.rstd[row] : 0.0f;
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-    for (int j = 0; j < F::kVecs; ++j)
+    for (int j = 0; j < VECS; ++j)
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
         xh[j][k] = (xh[j][k] - mean) * rstd;  // past the row's end dy is 0
@@ -243,23 +261,23 @@ __global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void bwd_kernel(co
     s1 = p.rms ? 0.0f : s1 * inv;
     s2 *= inv;
 #pragma unroll
-    for (int j = 0; j < F::kVecs; ++j) {
+    for (int j = 0; j < VECS; ++j) {
       const int c = (l + j * LPR) * VEC;
       if (real && c < p.dim) {
-        float g[VEC];
+        const int n = values_at<EVEN>(c, p.dim);
+        float g[VEC], dh[VEC];
+        if (kLate) load<EVEN>(rh[j], (const TH*)p.dh + base + c, p.dh ? n : 0);
+        rh[j].get(dh);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          g[k] = rstd * (dy[j][k] - s1 - xh[j][k] * s2);
-          if (p.dh) g[k] += dh[j][k];
-        }
-        if (p.dresidual) store_n<VEC>((TH*)p.dresidual + base + c, g);
+        for (int k = 0; k < VEC; ++k) g[k] = rstd * (dy[j][k] - s1 - xh[j][k] * s2) + dh[k];
+        if (p.dresidual) store_8((TH*)p.dresidual + base + c, g, n);
         if (p.drop.rng) {
           float f[VEC];
-          drop_factors<VEC>(p.drop, seed, offset, base + c, f);
+          factors<EVEN>(p, seed, offset, base + c, f);
 #pragma unroll
           for (int k = 0; k < VEC; ++k) g[k] = dropped(g[k], f[k]);
         }
-        store_n<VEC>((T*)p.dx + base + c, g);
+        store_8((T*)p.dx + base + c, g, n);
       }
     }
   }
@@ -267,7 +285,7 @@ __global__ __launch_bounds__((Form<LPR, CNT, VEC>::kThreads)) void bwd_kernel(co
   // the block's rows added in order, then one row of partial sums (dw, db)
   __shared__ float2 sums[F::kThreads];
 #pragma unroll
-  for (int j = 0; j < F::kVecs; ++j)
+  for (int j = 0; j < VECS; ++j)
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
       const int c = (l + j * LPR) * VEC + k;
@@ -346,40 +364,37 @@ struct Call {
   int* blocks;  // how many were launched
 };
 
-template <typename T, typename TH, int LPR, int CNT, int VEC>
+template <typename T, typename TH, int LPR, int VECS, bool EVEN>
 hipError_t launch(const Call& c) {
-  typedef Form<LPR, CNT, VEC> F;
+  typedef Form<LPR> F;
   static_assert(F::kThreads >= 192, "the workspace has room for blocks of 192 threads");
   int64_t n = (c.p.rows + F::kRows - 1) / F::kRows;
   const int64_t most = c.back ? back_most(F::kThreads) : most_blocks(F::kThreads);
   if (n > most) n = most;
   *c.blocks = (int)n;
-  if (c.back) bwd_kernel<T, TH, LPR, CNT, VEC><<<(unsigned)n, F::kThreads, 0, c.s>>>(c.p);
-  else fwd_kernel<T, TH, LPR, CNT, VEC><<<(unsigned)n, F::kThreads, 0, c.s>>>(c.p);
+  if (c.back) bwd_kernel<T, TH, LPR, VECS, EVEN><<<(unsigned)n, F::kThreads, 0, c.s>>>(c.p);
+  else fwd_kernel<T, TH, LPR, VECS, EVEN><<<(unsigned)n, F::kThreads, 0, c.s>>>(c.p);
   return hipGetLastError();
 }
 
+template <typename T, typename TH, bool EVEN>
+hipError_t pick(const Call& c) {
+  const int d = c.p.dim;
+  if (d <= 128) return launch<T, TH, 16, 1, EVEN>(c);
+  if (d <= 256) return launch<T, TH, 32, 1, EVEN>(c);
+  if (d <= 512) return launch<T, TH, 64, 1, EVEN>(c);
+  if (d <= 1024) return launch<T, TH, 128, 1, EVEN>(c);
+  if (d <= 1536) return launch<T, TH, 192, 1, EVEN>(c);
+  if (d <= 2048) return launch<T, TH, 256, 1, EVEN>(c);
+  if (d <= 4096) return launch<T, TH, 512, 1, EVEN>(c);
+  if (d <= 8192) return launch<T, TH, 1024, 1, EVEN>(c);
+  return launch<T, TH, 1024, 2, EVEN>(c);
+}
+// Rows that are no multiple of eight pay for the piece at their end (16384 x
+// 1536: 65 and 86 us, by the kernels for any row 77 and 89).
 template <typename T, typename TH>
 hipError_t pick(const Call& c) {
-  const Args& p = c.p;
-  const uintptr_t all = (uintptr_t)p.x | (uintptr_t)p.residual | (uintptr_t)p.y | (uintptr_t)p.h |
-                        (uintptr_t)p.dy | (uintptr_t)p.dh | (uintptr_t)p.dx | (uintptr_t)p.dresidual;
-  const int d = p.dim;
-  if (all % 16 == 0 && d % 8 == 0) {
-    if (d <= 128) return launch<T, TH, 16, 8, 8>(c);
-    if (d <= 256) return launch<T, TH, 32, 8, 8>(c);
-    if (d <= 512) return launch<T, TH, 64, 8, 8>(c);
-    if (d <= 1024) return launch<T, TH, 128, 8, 8>(c);
-    if (d <= 1536) return launch<T, TH, 192, 8, 8>(c);
-    if (d <= 2048) return launch<T, TH, 256, 8, 8>(c);
-    if (d <= 4096) return launch<T, TH, 512, 8, 8>(c);
-    if (d <= 8192) return launch<T, TH, 1024, 8, 8>(c);
-    return launch<T, TH, 1024, 16, 8>(c);
-  }
-  if (d <= 512) return launch<T, TH, 64, 8, 1>(c);
-  if (d <= 2048) return launch<T, TH, 256, 8, 1>(c);
-  if (d <= 8192) return launch<T, TH, 1024, 8, 1>(c);
-  return launch<T, TH, 1024, 16, 1>(c);
+  return c.p.dim % VEC == 0 ? pick<T, TH, true>(c) : pick<T, TH, false>(c);
 }
 
 hipError_t run(const Call& c, bool x_f32, bool h_f32) {

@@ -989,9 +989,8 @@ void launch_step(const StepArgs& p, hipStream_t s) {
 }
 
 hipError_t step(const StepArgs& p, bool f32, hipStream_t s) {
-  // 16 bytes an access (8 of bf16) where rows and tensors allow it
-  const uintptr_t all = (uintptr_t)p.x | (uintptr_t)p.r | (uintptr_t)p.i | (uintptr_t)p.y;
-  const bool four = p.dim % 4 == 0 && (uintptr_t)p.state % 16 == 0 && all % (f32 ? 16 : 8) == 0;
+  // 16 bytes an access (8 of bf16) where rows allow it
+  const bool four = p.dim % 4 == 0;
   if (f32) four ? launch_step<float, 4>(p, s) : launch_step<float, 1>(p, s);
   else four ? launch_step<bf16_bits, 4>(p, s) : launch_step<bf16_bits, 1>(p, s);
   return hipGetLastError();

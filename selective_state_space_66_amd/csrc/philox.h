@@ -51,24 +51,34 @@ inline Drop drop_of(float p, const int64_t* rng, int64_t site) {
   return d;
 }
 
-// The factors of N values from `at` on (N = 8: at a multiple of 4; N = 1: any).
-template <int N>
+// The factors of eight values from `at` on, a multiple of 4.
 __device__ __forceinline__ void drop_factors(const Drop& d, uint64_t seed, uint64_t offset,
-                                             int64_t at, float (&f)[N]) {
-  static_assert(N == 1 || N % 4 == 0, "whole blocks, or one value");
-  if constexpr (N == 1) {
+                                             int64_t at, float (&f)[8]) {
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
     uint32_t w[4];
-    philox_block(seed, offset, (uint64_t)at >> 2, w);
-    const uint32_t lo = at & 1 ? w[1] : w[0], hi = at & 1 ? w[3] : w[2];
-    f[0] = (at & 2 ? hi : lo) >= d.below ? d.factor : 0.0f;
-  } else {
+    philox_block(seed, offset, ((uint64_t)at >> 2) + b, w);
 #pragma unroll
-    for (int b = 0; b < N / 4; ++b) {
-      uint32_t w[4];
-      philox_block(seed, offset, ((uint64_t)at >> 2) + b, w);
+    for (int k = 0; k < 4; ++k) f[4 * b + k] = w[k] >= d.below ? d.factor : 0.0f;
+  }
+}
+__device__ __forceinline__ uint32_t either(bool second, uint32_t a, uint32_t b) { return second ? b : a; }
+// The same from anywhere: they lie in three blocks.
+__device__ __forceinline__ void drop_factors_any(const Drop& d, uint64_t seed, uint64_t offset,
+                                                 int64_t at, float (&f)[8]) {
+  uint32_t w[12];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) f[4 * b + k] = w[k] >= d.below ? d.factor : 0.0f;
-    }
+  for (int b = 0; b < 3; ++b) {
+    uint32_t t[4];
+    philox_block(seed, offset, ((uint64_t)at >> 2) + b, t);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[4 * b + k] = t[k];
+  }
+  const int s = (int)(at & 3);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t lo = either(s & 1, w[k], w[k + 1]), hi = either(s & 1, w[k + 2], w[k + 3]);
+    f[k] = either(s & 2, lo, hi) >= d.below ? d.factor : 0.0f;
   }
 }
 

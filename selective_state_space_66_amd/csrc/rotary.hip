@@ -145,8 +145,7 @@ hipError_t launch(Args p, hipStream_t s) {
 template <typename T>
 hipError_t pick(const Args& p, hipStream_t s) {
   constexpr int VEC = 16 / sizeof(T);
-  const bool wide = (((uintptr_t)p.q | (uintptr_t)p.k | (uintptr_t)p.qo | (uintptr_t)p.ko) & 15) == 0 &&
-                    p.D % VEC == 0 && (p.interleaved ? 2 * p.pairs : p.pairs) % VEC == 0;
+  const bool wide = p.D % VEC == 0 && (p.interleaved ? 2 * p.pairs : p.pairs) % VEC == 0;
   if (p.interleaved) return wide ? launch<T, VEC, true>(p, s) : launch<T, 1, true>(p, s);
   return wide ? launch<T, VEC, false>(p, s) : launch<T, 1, false>(p, s);
 }
