@@ -67,11 +67,18 @@ __global__ __launch_bounds__(256) void rotary_kernel(const Args p) {
   T* const qo = (T*)p.qo + tok * p.H * p.D + col;
   T* const ko = (T*)p.ko + tok * p.Hk * p.D + col;
   if (!turns) {
-    for (int h = h0; h < h1; ++h) {
-      const int64_t at = (int64_t)(h < p.H ? h : h - p.H) * p.D;
-      float v[VEC];
-      load_n<VEC>((h < p.H ? q : k) + at, v);
-      store_n<VEC>((h < p.H ? qo : ko) + at, v);
+    for (int g0 = h0; g0 < h1; g0 += 4) {
+      float v[4][VEC];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int h = g0 + g;
+        if (h < h1) load_n<VEC>((h < p.H ? q : k) + (int64_t)(h < p.H ? h : h - p.H) * p.D, v[g]);
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int h = g0 + g;
+        if (h < h1) store_n<VEC>((h < p.H ? qo : ko) + (int64_t)(h < p.H ? h : h - p.H) * p.D, v[g]);
+      }
     }
     return;
   }
@@ -144,10 +151,14 @@ hipError_t launch(Args p, hipStream_t s) {
 
 template <typename T>
 hipError_t pick(const Args& p, hipStream_t s) {
+  // 16 bytes an access where the turned and the copied part of a head are whole
+  // multiples of them, else 8, else a value
   constexpr int VEC = 16 / sizeof(T);
-  const bool wide = p.D % VEC == 0 && (p.interleaved ? 2 * p.pairs : p.pairs) % VEC == 0;
-  if (p.interleaved) return wide ? launch<T, VEC, true>(p, s) : launch<T, 1, true>(p, s);
-  return wide ? launch<T, VEC, false>(p, s) : launch<T, 1, false>(p, s);
+  const int turned = p.interleaved ? 2 * p.pairs : p.pairs;
+  const bool wide = p.D % VEC == 0 && turned % VEC == 0, half = p.D % (VEC / 2) == 0 && turned % (VEC / 2) == 0;
+  if (p.interleaved)
+    return wide ? launch<T, VEC, true>(p, s) : half ? launch<T, VEC / 2, true>(p, s) : launch<T, 1, true>(p, s);
+  return wide ? launch<T, VEC, false>(p, s) : half ? launch<T, VEC / 2, false>(p, s) : launch<T, 1, false>(p, s);
 }
 
 }  // namespace

@@ -10,6 +10,7 @@
 namespace ssm66 {
 
 struct __attribute__((packed, aligned(4))) Four32 { float v[4]; };
+struct __attribute__((packed, aligned(4))) Two32 { float v[2]; };
 struct __attribute__((packed, aligned(2))) Four16 { uint32_t w[2]; };
 struct __attribute__((packed, aligned(2))) Eight16 { uint32_t w[4]; };
 
@@ -22,6 +23,10 @@ __device__ __forceinline__ void load_n(const float* p, float (&f)[N]) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) f[4 * q + k] = v.v[k];
     }
+  } else if constexpr (N == 2) {
+    const Two32 v = *(const Two32*)p;
+    f[0] = v.v[0];
+    f[1] = v.v[1];
   } else {
 #pragma unroll
     for (int k = 0; k < N; ++k) f[k] = p[k];
@@ -54,6 +59,8 @@ __device__ __forceinline__ void store_n(float* p, const float (&f)[N]) {
 #pragma unroll
     for (int q = 0; q < N / 4; ++q)
       ((Four32*)p)[q] = Four32{{f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]}};
+  } else if constexpr (N == 2) {
+    *(Two32*)p = Two32{{f[0], f[1]}};
   } else {
 #pragma unroll
     for (int k = 0; k < N; ++k) p[k] = f[k];

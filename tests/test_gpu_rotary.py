@@ -21,7 +21,7 @@ def make(B, L, H, Hk, D, io, seed=1):
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("B,L,H,Hk,D,rot", [
     (1, 1, 1, 1, 2, 2), (2, 5, 3, 1, 7, 4), (1, 9, 2, 2, 16, 16), (2, 33, 4, 4, 40, 10),
-    (2, 70, 6, 2, 64, 64), (1, 300, 8, 1, 96, 48), (3, 65, 5, 5, 128, 32), (64, 1, 24, 8, 128, 128),
+    (2, 70, 6, 2, 64, 64), (2, 21, 3, 2, 40, 20), (1, 50, 9, 4, 96, 24), (2, 6, 2, 1, 36, 12), (1, 300, 8, 1, 96, 48), (3, 65, 5, 5, 128, 32), (64, 1, 24, 8, 128, 128),
     (1, 130, 2, 2, 256, 254), (2, 40, 1, 0, 64, 32)])
 def test_forward_and_gradient(B, L, H, Hk, D, rot, interleaved, io):
     print(f"[rotary] {B} x {L} x {H}/{Hk} x {D} rot {rot} {interleaved} {io}", flush=True)
