@@ -31,7 +31,7 @@
 // kernel at 4.0 TB/s), backwards 94 (352 MB, its kernel 83 at 4.2, the sums of
 // ddecay 4.5); 65536 x 2048 forwards 240 (1074 MB at 4.5).  HBM bounds it, and in
 // front of that a block's waits: for its loads, its number and the words of others
-// it waits 7 of the 14 us of its life; the vector units are 58% busy, 64%
+// it waits 7 of the 14 us of its life; the vector units are 58% busy, 63%
 // backwards.  3 x 1537 x 1000, fp32: 24 and 36 us for 14 and 25 of bytes, one round
 // of blocks whose chain is load, 69 and 114 instructions a value, join, store.
 //
