@@ -6,9 +6,14 @@
 // The gradient is the turn by -t.
 //
 // HBM bounds it: 8 x 2048 tokens, 24 + 8 heads of 128, half of each turned, bf16,
-// 51 us (268 MB, a copy's rate; a head at a time and up to 32 heads a thread, 67).  A thread keeps the cosines and sines of its pairs of one token
-// and goes over the heads of queries and keys with them, 16 bytes an access (the
-// two halves of a pair are two); few tokens are spread over the heads too.
+// 51 us (268 MB, a copy's rate; a head at a time and up to 32 heads a thread, 67).
+// A thread keeps the cosines and sines of its pairs of one token and goes over the
+// heads of queries and keys with them, 16 bytes an access (the two halves of a pair
+// are two); few tokens are spread over the heads too.  A thread's heads are one in
+// so many, so that threads beside each other have heads beside each other:
+// 8 x 2048 tokens, 16 + 16 heads of 40, 20 turned as halves, bf16, 31 us a turn
+// (heads in a row, 36; and 4 bytes an access in the copied part, 41; 2 bytes, 50);
+// heads of 128 as halves lose 1%.
 //
 // Angles: position * freqs / 2 pi in fp64 (2^31 positions leave 6e-8 of a turn),
 // less the nearest quarter turn, then the series of sine and cosine up to an
@@ -42,6 +47,25 @@ __device__ __forceinline__ void turn_of(int position, float freq, float* c, floa
   *s = k >= 2 ? -b : b;
 }
 
+// N elements of each of a thread's heads
+template <typename T, int N>
+__device__ __forceinline__ void copy(const Args& p, const T* q, const T* k, T* qo, T* ko, int split) {
+  const int heads = p.H + p.Hk;
+  for (int g0 = split; g0 < heads; g0 += 4 * p.splits) {
+    float v[4][N];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int h = g0 + g * p.splits;
+      if (h < heads) load_n<N>((h < p.H ? q : k) + (int64_t)(h < p.H ? h : h - p.H) * p.D, v[g]);
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int h = g0 + g * p.splits;
+      if (h < heads) store_n<N>((h < p.H ? qo : ko) + (int64_t)(h < p.H ? h : h - p.H) * p.D, v[g]);
+    }
+  }
+}
+
 // VEC elements an access.  Interleaved: a thread has one access, VEC / 2 pairs
 // (VEC == 1: one pair as two elements).  Halves: two accesses, VEC pairs.  The
 // threads past the pairs copy what is not turned.  N: unsigned of 32 bits where
@@ -58,28 +82,21 @@ __global__ __launch_bounds__(256) void rotary_kernel(const Args p) {
   const int split = (int)(rest - (N)tok * (N)p.splits);
   if (tok >= p.tokens) return;
   const int turning = INTER ? 2 * p.pairs / W : p.pairs / VEC;
-  const int heads = p.H + p.Hk;
-  const int h0 = split * p.each, h1 = h0 + p.each < heads ? h0 + p.each : heads;
+  const int heads = p.H + p.Hk, step = p.splits;
   const bool turns = lane < turning;
-  const int col = turns ? lane * W : 2 * p.pairs + (lane - turning) * VEC;
+  // copied: 16 bytes an access wherever there are as many, the last one overlapping
+  // the one before it (both store the same)
+  constexpr int FULL = 16 / sizeof(T);
+  const int copied = p.D - 2 * p.pairs, piece = lane - turning;
+  int col = lane * W;
+  if (!turns) col = 2 * p.pairs + (copied >= FULL ? min(piece * FULL, copied - FULL) : piece * VEC);
   const T* const q = (const T*)p.q + tok * p.H * p.D + col;
   const T* const k = (const T*)p.k + tok * p.Hk * p.D + col;
   T* const qo = (T*)p.qo + tok * p.H * p.D + col;
   T* const ko = (T*)p.ko + tok * p.Hk * p.D + col;
   if (!turns) {
-    for (int g0 = h0; g0 < h1; g0 += 4) {
-      float v[4][VEC];
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int h = g0 + g;
-        if (h < h1) load_n<VEC>((h < p.H ? q : k) + (int64_t)(h < p.H ? h : h - p.H) * p.D, v[g]);
-      }
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int h = g0 + g;
-        if (h < h1) store_n<VEC>((h < p.H ? qo : ko) + (int64_t)(h < p.H ? h : h - p.H) * p.D, v[g]);
-      }
-    }
+    if (copied >= FULL) copy<T, FULL>(p, q, k, qo, ko, split);
+    else copy<T, VEC>(p, q, k, qo, ko, split);
     return;
   }
   const int position = p.positions ? p.positions[tok] : (int)((N)tok % (N)p.L);
@@ -90,20 +107,20 @@ __global__ __launch_bounds__(256) void rotary_kernel(const Args p) {
     c[j] *= p.mscale;
     s[j] *= p.mscale * p.sign;
   }
-  for (int g0 = h0; g0 < h1; g0 += kAhead) {
+  for (int g0 = split; g0 < heads; g0 += kAhead * step) {
     float a[kAhead][W], b[INTER ? 1 : kAhead][VEC];
 #pragma unroll
     for (int g = 0; g < kAhead; ++g) {
-      const int h = g0 + g;
-      if (h >= h1) break;
+      const int h = g0 + g * step;
+      if (h >= heads) break;
       const T* const in = (h < p.H ? q : k) + (int64_t)(h < p.H ? h : h - p.H) * p.D;
       load_n<W>(in, a[g]);
       if constexpr (!INTER) load_n<VEC>(in + p.pairs, b[g]);
     }
 #pragma unroll
     for (int g = 0; g < kAhead; ++g) {
-      const int h = g0 + g;
-      if (h >= h1) break;
+      const int h = g0 + g * step;
+      if (h >= heads) break;
       T* const out = (h < p.H ? qo : ko) + (int64_t)(h < p.H ? h : h - p.H) * p.D;
       if constexpr (INTER) {
 #pragma unroll
@@ -131,7 +148,10 @@ template <typename T, int VEC, bool INTER>
 hipError_t launch(Args p, hipStream_t s) {
   constexpr int W = INTER ? (VEC == 1 ? 2 : VEC) : VEC;
   const bool in_place = p.q == p.qo && p.k == p.ko;
-  p.lanes = (INTER ? 2 * p.pairs / W : p.pairs / VEC) + (in_place ? 0 : (p.D - 2 * p.pairs) / VEC);
+  constexpr int FULL = 16 / sizeof(T);
+  const int copied = p.D - 2 * p.pairs;
+  p.lanes = INTER ? 2 * p.pairs / W : p.pairs / VEC;
+  if (!in_place) p.lanes += copied >= FULL ? (copied + FULL - 1) / FULL : copied / VEC;
   // a thread takes up to eight heads (the angles cost as much as three), fewer
   // where that leaves less than eight waves a CU
   const int heads = p.H + p.Hk;
@@ -139,8 +159,8 @@ hipError_t launch(Args p, hipStream_t s) {
   int64_t splits = (want + wide - 1) / wide;
   if (splits < (heads + 7) / 8) splits = (heads + 7) / 8;
   if (splits > heads) splits = heads;
-  p.each = (int)((heads + splits - 1) / splits);
-  p.splits = (heads + p.each - 1) / p.each;
+  const int each = (int)((heads + splits - 1) / splits);
+  p.splits = (heads + each - 1) / each;
   const int64_t n = wide * p.splits;
   const Grid g = grid_of((n + 255) / 256, 256);
   const dim3 grid(g.x, g.more);
@@ -149,16 +169,21 @@ hipError_t launch(Args p, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename T, int VEC>
+hipError_t layouts(const Args& p, hipStream_t s) {
+  return p.interleaved ? launch<T, VEC, true>(p, s) : launch<T, VEC, false>(p, s);
+}
+
 template <typename T>
 hipError_t pick(const Args& p, hipStream_t s) {
   // 16 bytes an access where the turned and the copied part of a head are whole
-  // multiples of them, else 8, else a value
+  // multiples of them, else 8, 4 of bf16, a value
   constexpr int VEC = 16 / sizeof(T);
-  const int turned = p.interleaved ? 2 * p.pairs : p.pairs;
-  const bool wide = p.D % VEC == 0 && turned % VEC == 0, half = p.D % (VEC / 2) == 0 && turned % (VEC / 2) == 0;
-  if (p.interleaved)
-    return wide ? launch<T, VEC, true>(p, s) : half ? launch<T, VEC / 2, true>(p, s) : launch<T, 1, true>(p, s);
-  return wide ? launch<T, VEC, false>(p, s) : half ? launch<T, VEC / 2, false>(p, s) : launch<T, 1, false>(p, s);
+  const int parts = p.D | (p.interleaved ? 2 * p.pairs : p.pairs);  // divided by a power of two if both are
+  if (parts % VEC == 0) return layouts<T, VEC>(p, s);
+  if (parts % (VEC / 2) == 0) return layouts<T, VEC / 2>(p, s);
+  if (VEC == 8 && parts % 2 == 0) return layouts<T, VEC / 4>(p, s);
+  return layouts<T, 1>(p, s);
 }
 
 }  // namespace

@@ -17,7 +17,7 @@ struct Args {
   float mscale, sign;        // sign: -1 rotates back
   int interleaved;
   // set by the launch
-  int lanes, splits, each;   // threads of a token along a head, along the heads, heads of a thread
+  int lanes, splits;         // threads of a token along a head, along the heads
 };
 // whether the grid these sizes need exists
 bool fits(int64_t tokens, int heads, int D);

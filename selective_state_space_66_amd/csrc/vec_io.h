@@ -12,6 +12,7 @@ namespace ssm66 {
 struct __attribute__((packed, aligned(4))) Four32 { float v[4]; };
 struct __attribute__((packed, aligned(4))) Two32 { float v[2]; };
 struct __attribute__((packed, aligned(2))) Four16 { uint32_t w[2]; };
+struct __attribute__((packed, aligned(2))) Two16 { uint32_t w; };
 struct __attribute__((packed, aligned(2))) Eight16 { uint32_t w[4]; };
 
 template <int N>
@@ -48,6 +49,10 @@ __device__ __forceinline__ void load_n(const bf16_bits* p, float (&f)[N]) {
       f[2 * q] = __uint_as_float(v.w[q] << 16);
       f[2 * q + 1] = __uint_as_float(v.w[q] & 0xffff0000u);
     }
+  } else if constexpr (N == 2) {
+    const uint32_t w = ((const Two16*)p)->w;
+    f[0] = __uint_as_float(w << 16);
+    f[1] = __uint_as_float(w & 0xffff0000u);
   } else {
 #pragma unroll
     for (int k = 0; k < N; ++k) f[k] = to_f32(p[k]);
@@ -73,6 +78,8 @@ __device__ __forceinline__ void store_n(bf16_bits* p, const float (&f)[N]) {
                             pack_bf16x2(f[6], f[7])}};
   } else if constexpr (N == 4) {
     *(Four16*)p = Four16{{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])}};
+  } else if constexpr (N == 2) {
+    *(Two16*)p = Two16{pack_bf16x2(f[0], f[1])};
   } else {
 #pragma unroll
     for (int k = 0; k < N; ++k) store_io(p + k, f[k]);
