@@ -298,7 +298,7 @@ def add_norm_fwd(x, residual=None, weight=None, bias=None, kind="layer", eps=1e-
         _want(h, "h", x.shape, h_dtype, x.device, index)
     elif not same:
         h = torch.empty_like(x, dtype=h_dtype)
-    elif y is x:
+    elif rows and y.data_ptr() == x.data_ptr():
         raise ValueError("y: may be x only where h is a tensor of its own")
     mean = rstd = None
     if return_stats:

@@ -200,6 +200,19 @@ def test_same_bits_again_and_empty_calls():
     assert not g["dweight"].any() and not g["dbias"].any()
 
 
+def test_a_view_of_x_is_x():
+    x = normal((4, 64), BF16, 1)
+    kept = x.clone()
+    with pytest.raises(ValueError):
+        ssm.add_norm_fwd(x, y=x.view(4, 64))  # h would be x, and overwritten
+    assert torch.equal(x, kept)
+    want = ssm.add_norm_fwd(x)[0]
+    y, h, _, _ = ssm.add_norm_fwd(x, y=x.view(4, 64), h=torch.empty_like(x))
+    assert torch.equal(h, kept) and torch.equal(y, want)
+    none = torch.zeros((0, 64), device=DEV)
+    ssm.add_norm_fwd(none, y=torch.empty_like(none))
+
+
 def test_refusals():
     x = normal((4, 64), BF16, 1)
     with pytest.raises(ValueError):
