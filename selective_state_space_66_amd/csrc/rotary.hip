@@ -47,21 +47,28 @@ __device__ __forceinline__ void turn_of(int position, float freq, float* c, floa
   *s = k >= 2 ? -b : b;
 }
 
+// BYTES of memory as they are, from any address of a value
+template <int BYTES> struct Piece {
+  typedef uint32_t type __attribute__((ext_vector_type(BYTES / 4), aligned(2)));
+};
+template <> struct Piece<4> { typedef uint32_t type __attribute__((aligned(2))); };
+template <> struct Piece<2> { typedef uint16_t type; };
 // N elements of each of a thread's heads
 template <typename T, int N>
 __device__ __forceinline__ void copy(const Args& p, const T* q, const T* k, T* qo, T* ko, int split) {
+  typedef typename Piece<N * sizeof(T)>::type P;
   const int heads = p.H + p.Hk;
   for (int g0 = split; g0 < heads; g0 += 4 * p.splits) {
-    float v[4][N];
+    P v[4];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int h = g0 + g * p.splits;
-      if (h < heads) load_n<N>((h < p.H ? q : k) + (int64_t)(h < p.H ? h : h - p.H) * p.D, v[g]);
+      if (h < heads) v[g] = *(const P*)((h < p.H ? q : k) + (int64_t)(h < p.H ? h : h - p.H) * p.D);
     }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int h = g0 + g * p.splits;
-      if (h < heads) store_n<N>((h < p.H ? qo : ko) + (int64_t)(h < p.H ? h : h - p.H) * p.D, v[g]);
+      if (h < heads) *(P*)((h < p.H ? qo : ko) + (int64_t)(h < p.H ? h : h - p.H) * p.D) = v[g];
     }
   }
 }

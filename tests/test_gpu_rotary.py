@@ -72,6 +72,28 @@ def test_tensors_between_words():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("D,rot", [(64, 32), (36, 12), (40, 20), (11, 8), (9, 2)])
+def test_what_is_copied_is_copied_bit_by_bit(D, rot, io):
+    """Signalling NaNs and subnormal values too, and with the queries in place alone."""
+    bits = torch.int32 if io == F32 else torch.int16
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    info = torch.iinfo(bits)
+    q, k = make(2, 37, 5, 2, D, io)
+    for t in (q, k):
+        t[..., rot:] = torch.randint(info.min, info.max, t[..., rot:].shape, generator=gen, device=DEV,
+                                     dtype=bits).view(io)
+    q[0, 0, :, rot:] = torch.tensor(1, dtype=bits, device=DEV).view(io)
+    freqs, _ = ssm.rotary_freqs(rot, device=DEV)
+    for interleaved in (False, True):
+        a = q.clone()
+        qo, ko = ssm.rotary_fwd(q, k, freqs, interleaved=interleaved)
+        _, kb = ssm.rotary_fwd(a, k, freqs, interleaved=interleaved, q_out=a)
+        for got, x in ((qo, q), (ko, k), (a, q), (kb, k)):
+            assert torch.equal(got[..., rot:].contiguous().view(bits), x[..., rot:].contiguous().view(bits))
+        assert torch.equal(a[..., :rot], qo[..., :rot]) and torch.equal(kb[..., :rot], ko[..., :rot])
+
+
 def test_offsets_past_32_bits():
     L, H, D = 1 << 20, 33, 128
     q = torch.zeros((1, L, H, D), dtype=BF16, device=DEV)
