@@ -38,8 +38,6 @@
 // 1 - a^2 comes from its series where v is small: long memories have v of 1e-3 and
 // less.  fp32 tensors also take h - (1 - a) h instead of a h there (a rounds to
 // 2^-25, which a memory of n tokens adds up n times).
-#include <initializer_list>
-
 #include "gated_scan_launch.h"
 #include "lm_grid.h"
 #include "vec_io.h"
@@ -160,15 +158,16 @@ __device__ __forceinline__ float joint(float V, float W) { return V == kCut || W
 
 // ---- memory -------------------------------------------------------------------
 
-// VEC neighbouring channels as they lie in memory
+// VEC neighbouring channels as they lie in memory: their type there (from any
+// address of a value) and elsewhere
 template <typename T, int VEC> struct Raw;
 template <> struct Raw<float, 1> {
-  typedef float type;
+  typedef float type, mem;
   static __device__ __forceinline__ void get(type r, float (&f)[1]) { f[0] = r; }
   static __device__ __forceinline__ type put(const float (&f)[1]) { return f[0]; }
 };
 template <> struct Raw<bf16_bits, 1> {
-  typedef uint16_t type;
+  typedef uint16_t type, mem;
   static __device__ __forceinline__ void get(type r, float (&f)[1]) { f[0] = to_f32(r); }
   static __device__ __forceinline__ type put(const float (&f)[1]) {
     return __builtin_bit_cast(uint16_t, (__bf16)f[0]);
@@ -176,6 +175,7 @@ template <> struct Raw<bf16_bits, 1> {
 };
 template <> struct Raw<bf16_bits, 2> {
   typedef uint32_t type;
+  typedef uint32_t mem __attribute__((aligned(2)));
   static __device__ __forceinline__ void get(type r, float (&f)[2]) {
     f[0] = __uint_as_float(r << 16);
     f[1] = __uint_as_float(r & 0xffff0000u);
@@ -256,6 +256,9 @@ struct Spot {
     w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     c = ((int)(t.row - (uint32_t)entry * (uint32_t)p.tiles) * 64 + lane) * VEC;
     here = c < p.dim;
+    // an odd number of channels: the last thread has the one before it too, and
+    // what two threads have they compute and store alike
+    if (VEC > 1 && here && c > p.dim - VEC) c = p.dim - VEC;
     t0 = (int64_t)chunk * (TOK * W) + w * TOK;
     int64_t len = p.L;
     if (p.seq_lens) {
@@ -431,9 +434,9 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
   if (MANY || p.L > 0)
 #pragma unroll
     for (int j = 0; j < TOK; ++j) {
-      rr[j] = *(const typename IO::type*)(s.template from<T>(p, p.r) + s.template load_at<T>(p, j));
-      ri[j] = *(const typename IO::type*)(s.template from<T>(p, p.i) + s.template load_at<T>(p, j));
-      rx[j] = *(const typename IO::type*)(s.template from<T>(p, p.x) + s.template load_at<T>(p, j));
+      rr[j] = *(const typename IO::mem*)(s.template from<T>(p, p.r) + s.template load_at<T>(p, j));
+      ri[j] = *(const typename IO::mem*)(s.template from<T>(p, p.i) + s.template load_at<T>(p, j));
+      rx[j] = *(const typename IO::mem*)(s.template from<T>(p, p.x) + s.template load_at<T>(p, j));
     }
   s.read_cuts(p);
   const int64_t row = s.b * p.dim + s.c;
@@ -530,7 +533,7 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
 #pragma unroll
       for (int k = 0; k < VEC; ++k) h[k] = advance<PRECISE>(f[j][k], h[k], u[j][k]);
       if (s.here)
-        *(typename IO::type*)(s.template to<T>(p, p.y) + s.template store_at<T>(p, j)) = IO::put(h);
+        *(typename IO::mem*)(s.template to<T>(p, p.y) + s.template store_at<T>(p, j)) = IO::put(h);
     }
   } else {
 #pragma unroll
@@ -543,7 +546,7 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
         o[k] = j < s.real ? h[k] : 0.0f;
       }
       if (s.here && j < s.inside)
-        *(typename IO::type*)(s.template to<T>(p, p.y) + s.template store_at<T>(p, j)) = IO::put(o);
+        *(typename IO::mem*)(s.template to<T>(p, p.y) + s.template store_at<T>(p, j)) = IO::put(o);
     }
   }
   if (s.w == W - 1 && s.here && p.last_state && s.chunk == p.chunks - 1)
@@ -574,7 +577,7 @@ __device__ __forceinline__ void token_gradients(
     const float (&before)[TOK][VEC], const float (&decay)[VEC], float (&c)[VEC], float (&P)[VEC]) {
   constexpr bool PRECISE = sizeof(T) == 4;
   typedef Raw<T, VEC> IO;
-  typedef typename IO::type R;
+  typedef typename IO::mem R;
 #pragma unroll
   for (int j = TOK - 1; j >= 0; --j) {
     float x[VEC], dy[VEC], dx[VEC], dr[VEC], di[VEC];
@@ -628,10 +631,10 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
   if (MANY || p.L > 0)
 #pragma unroll
     for (int j = 0; j < TOK; ++j) {
-      rr[j] = *(const typename IO::type*)(s.template from<T>(p, p.r) + s.template load_at<T>(p, j));
-      ri[j] = *(const typename IO::type*)(s.template from<T>(p, p.i) + s.template load_at<T>(p, j));
-      rx[j] = *(const typename IO::type*)(s.template from<T>(p, p.x) + s.template load_at<T>(p, j));
-      rd[j] = *(const typename IO::type*)(s.template from<T>(p, p.dy) + s.template load_at<T>(p, j));
+      rr[j] = *(const typename IO::mem*)(s.template from<T>(p, p.r) + s.template load_at<T>(p, j));
+      ri[j] = *(const typename IO::mem*)(s.template from<T>(p, p.i) + s.template load_at<T>(p, j));
+      rx[j] = *(const typename IO::mem*)(s.template from<T>(p, p.x) + s.template load_at<T>(p, j));
+      rd[j] = *(const typename IO::mem*)(s.template from<T>(p, p.dy) + s.template load_at<T>(p, j));
     }
   s.read_cuts(p);
   const int64_t row = s.b * p.dim + s.c;
@@ -929,15 +932,17 @@ hipError_t launch(Args p, hipStream_t s) {
   return hipGetLastError();
 }
 
-bool aligned4(std::initializer_list<const void*> ptrs) {
-  for (const void* q : ptrs)
-    if ((uintptr_t)q % 4) return false;
-  return true;
-}
-
-// two bf16 channels a thread where rows keep their words whole
-bool pairs(int dim, std::initializer_list<const void*> ptrs) {
-  return dim % 2 == 0 && dim > 64 && aligned4(ptrs);
+// Two bf16 channels a thread instead of one: half as many lanes for the recurrence,
+// and a wave's access of 256 bytes instead of 128.  That pays where rows are no whole
+// lines of 128 bytes, so that every access touches one more, where there is work
+// for the fewer blocks, and where the last tile does not waste it.  Forwards and
+// backwards, one channel and two:
+//   8 x 2048 x 1536: 44 + 92, 49 + 95 us;   1 x 32768 x 2048: 123 + 231, 131 + 241;
+//   8 x 2048 x 1535: 66 + 125, 57 + 116;    32 x 1024 x 711: 63 + 121, 55 + 114;
+//   1 x 4096 x 711: 17 + 25, 19 + 29;       1 x 32768 x 257: 38 + 60, 44 + 76.
+bool pairs(const Args& p) {
+  const int64_t tiled = (p.dim + 127) / 128 * (int64_t)128;
+  return p.dim % 64 != 0 && 3 * tiled <= 4 * (int64_t)p.dim && p.batch * p.L * p.dim >= 6 << 20;
 }
 
 }  // namespace
@@ -960,7 +965,7 @@ hipError_t forward(const Args& p, bool f32, hipStream_t s) {
   if (p.L <= kKeep)
     return f32 ? launch<float, 1, 4, 16, false, true>(p, s) : launch<bf16_bits, 1, 4, 16, false, true>(p, s);
   if (f32) return launch<float, 1, 16, 8, false, false>(p, s);
-  if (pairs(p.dim, {p.x, p.r, p.i, p.y})) return launch<bf16_bits, 2, 16, 8, false, false>(p, s);
+  if (pairs(p)) return launch<bf16_bits, 2, 16, 8, false, false>(p, s);
   return launch<bf16_bits, 1, 16, 8, false, false>(p, s);
 }
 
@@ -969,10 +974,11 @@ hipError_t backward(const Args& p, bool f32, hipStream_t s) {
   if (p.batch == 0) {
   } else if (p.L <= kKeep) {
     e = f32 ? launch<float, 1, 4, 16, true, true>(p, s) : launch<bf16_bits, 1, 4, 16, true, true>(p, s);
-  } else if (f32) e = launch<float, 1, 8, 8, true, false>(p, s);
-  else if (pairs(p.dim, {p.x, p.r, p.i, p.dy, p.dx, p.dr, p.di}))
-    e = launch<bf16_bits, 2, 8, 8, true, false>(p, s);
-  else e = launch<bf16_bits, 1, 8, 8, true, false>(p, s);
+  } else if (f32) {
+    e = launch<float, 1, 8, 8, true, false>(p, s);
+  } else {
+    e = pairs(p) ? launch<bf16_bits, 2, 8, 8, true, false>(p, s) : launch<bf16_bits, 1, 8, 8, true, false>(p, s);
+  }
   if (e != hipSuccess || !p.ddecay) return e;
   const Layout a = layout(p.batch, p.L, p.dim, kKeep, true);
   decay_sum_kernel<<<(p.dim + 63) / 64, 1024, 0, s>>>((const float*)((const char*)p.ws + a.part), p.decay,

@@ -223,6 +223,58 @@ def test_tensors_that_start_between_words():
         assert torch.equal(gg[n], gw[n])
 
 
+# small ones, and bf16 of 6.3 million values and more in rows of no whole lines, which threads take
+# two channels of: many chunks, and one (forwards); a last one that two tiles have
+WIDE = [(3, 1100, 1999), (3, 1100, 2002), (50, 100, 1271), (7, 1000, 981), (7, 1000, 1025)]
+
+
+@pytest.mark.parametrize("B,L,dim", [(2, 333, 65), (2, 333, 191), (2, 333, 1537)] + WIDE)
+def test_a_last_channel_of_its_own_is_like_any_other(B, L, dim):
+    """Odd rows of bf16 give the bits of rows with one more channel, and nothing behind them."""
+    print(f"[gated scan] {B} x {L} x {dim} beside one more channel", flush=True)
+    d, h0, dy, dlast, kw = inputs(B, L, dim + 1, torch.bfloat16, 15, True)
+
+    def cut(t):
+        return t[..., :dim].contiguous()
+
+    def room(t):  # for an output, with a mark behind it
+        flat = torch.full((t.numel() + 1,), 7.0, dtype=t.dtype, device=DEV)
+        return flat, flat[:-1].view(t.shape)
+
+    want = ssm.gated_scan_fwd(**d, h0=h0, return_states=True, **kw)
+    odd = {n: cut(t) for n, t in d.items()}
+    flat, y = room(odd["x"])
+    got = ssm.gated_scan_fwd(**odd, h0=cut(h0), return_states=True, y=y, **kw)
+    for a, b in zip(got, want):
+        assert torch.equal(a, cut(b))
+    assert flat[-1] == 7.0
+    gw = ssm.gated_scan_bwd(**d, dy=dy, states=want[2], dlast=dlast, need_dh0=True, **kw)
+    for _ in range(3):
+        gg = ssm.gated_scan_bwd(**odd, dy=cut(dy), states=got[2], dlast=cut(dlast), need_dh0=True, **kw)
+        for n in gw:
+            assert torch.equal(gg[n], cut(gw[n])), n
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("B,L,dim", WIDE)
+def test_two_channels_a_thread(B, L, dim, masked):
+    print(f"[gated scan] {B} x {L} x {dim} masked {masked}", flush=True)
+    d, h0, dy, dlast, kw = inputs(B, L, dim, torch.bfloat16, 16, masked)
+    y, last, states = ssm.gated_scan_fwd(**d, h0=h0, return_states=True, **kw)
+    g = ssm.gated_scan_bwd(**d, dy=dy, states=states, dlast=dlast, need_dh0=True, **kw)
+    torch.cuda.synchronize()
+    f = ref.forward(**d, h0=h0, **kw)
+    ref.check("y", y, f["y"], f["y_bound"], torch.bfloat16)
+    ref.check("last_state", last, f["last_state"], f["last_bound"])
+    assert not y[~f["live"]].any()
+    want = ref.backward(**d, dy=dy, dlast=dlast, h0=h0, **kw)
+    for n in ("dx", "dr", "di"):
+        ref.check(n, g[n], want[n], want[n + "_bound"], torch.bfloat16)
+        assert not g[n][~f["live"]].any()
+    for n in ("dh0", "ddecay"):
+        ref.check(n, g[n], want[n], want[n + "_bound"])
+
+
 def test_empty_calls():
     z = torch.zeros((2, 0, 5), device=DEV)
     decay, h0 = torch.ones(5, device=DEV), torch.randn((2, 5), device=DEV)
