@@ -41,8 +41,8 @@ extern "C" {
  *   last_state : (batch, dim) float32, or NULL; must not overlap h0
  *   states     : (batch, ceil(seqlen / 64), dim) float32, or NULL: the state
  *                before every 64th token, which ssm_gated_scan_bwd takes
- * Tensors are aligned to their element size (bf16 to 4 bytes, with dim even, is
- * fastest); outputs and workspace overlap no input.  dim at most 2^24, batch *
+ * Tensors are aligned to their element size (to 128 bytes, and rows of as many or
+ * a multiple, is fastest); outputs and workspace overlap no input.  dim at most 2^24, batch *
  * ceil(dim / 64) * ceil(seqlen / 64) below 2^31 and seqlen at most 2^31 - 256
  * (else SSM_ERR_UNSUPPORTED).  Zero batch or dim is a no-op; seqlen == 0 copies
  * h0 (or zero) to last_state.

@@ -27,13 +27,13 @@
 // by a kernel before.
 //
 // Measured (a copy reaches 5.1 TB/s), inputs from HBM, with the kernel that clears
-// the words (2 to 3 us): 8 x 2048 x 1536, bf16, forwards 56 us (201 MB once, the
-// kernel at 4.0 TB/s), backwards 94 (352 MB, its kernel 83 at 4.2, the sums of
-// ddecay 4.5); 65536 x 2048 forwards 240 (1074 MB at 4.5).  HBM bounds it, and in
+// the words (2 to 3 us): 8 x 2048 x 1536, bf16, forwards 51 us (201 MB once, the
+// kernel at 4.3 TB/s), backwards 92 (352 MB, its kernel 82 at 4.3, the sums of
+// ddecay 4.5); 65536 x 2048 forwards 235 (1074 MB at 4.6).  HBM bounds it, and in
 // front of that a block's waits: for its loads, its number and the words of others
-// it waits 7 of the 14 us of its life; the vector units are 58% busy, 63%
-// backwards.  3 x 1537 x 1000, fp32: 24 and 36 us for 14 and 25 of bytes, one round
-// of blocks whose chain is load, 69 and 114 instructions a value, join, store.
+// it waits 5 of the 10 us of its life; the vector units are 55% busy.
+// 3 x 1537 x 1000, fp32: 24 and 36 us for 14 and 25 of bytes, one round of blocks
+// whose chain is load, 69 and 114 instructions a value, join, store.
 //
 // 1 - a^2 comes from its series where v is small: long memories have v of 1e-3 and
 // less.  fp32 tensors also take h - (1 - a) h instead of a h there (a rounds to
@@ -849,18 +849,18 @@ int64_t up(int64_t n) { return (n + 255) / 256 * 256; }
 // Chunks of a group.  Few rows wait for the chain from group to group (about a
 // microsecond a link), many for the words that each block reads.  Forwards and
 // backwards of 32768 tokens, bf16, with groups of 4, 8, 16 and 32:
-//   256 channels:  73 + 194, 49 + 112, 39 + 73, 37 + 60 us;
-//   512:           78 + 204, 56 + 121, 51 + 84, 55 + 89;
-//   2048:          132 + 295, 133 + 264, 141 + 275, 156 + 316;
-//   8 x 2048 x 1536: 51 + 101, 53 + 103, 54 + 107, 54 + 119.
-int group_of(int64_t rows, int chunk) {
-  return rows <= 256 ? 32 : rows <= 768 ? 16 : rows <= (chunk > kKeep ? 1536 : 2048) ? 8 : 4;
-}
+//   64 channels:   46 + 90, 27 + 52, 20 + 37, 20 + 31 us;
+//   256:           49 + 90, 34 + 58, 29 + 45, 32 + 50;
+//   512:           56 + 98, 42 + 67, 42 + 66, 47 + 76;
+//   1024:          71 + 143, 66 + 130, 69 + 135, 76 + 146;
+//   2048:          124 + 232, 126 + 236, 130 + 242, 143 + 267;
+//   8 x 2048 x 1536: 45 + 93, 46 + 95, 48 + 101, 48 + 112.
+int group_of(int64_t rows) { return rows <= 128 ? 32 : rows <= 512 ? 16 : rows <= 1536 ? 8 : 4; }
 
 struct Layout { int64_t ticket, sums, groups, part, bytes; };
 // chunk: tokens of a block
 Layout layout(int64_t batch, int64_t L, int64_t dim, int chunk, bool need_part) {
-  const int64_t chunks = pieces_of(L, chunk), rows = batch * dim, group = group_of(rows, chunk);
+  const int64_t chunks = pieces_of(L, chunk), rows = batch * dim, group = group_of(rows);
   Layout a = {};
   int64_t at = 0;
   if (chunks > 1) {
@@ -879,14 +879,14 @@ void place(Args& p, int vec, int chunk) {
   char* const ws = (char*)p.ws;
   p.chunks = (int)pieces_of(p.L, chunk);
   p.kept = (int)pieces_of(p.L, kKeep);
-  p.group = group_of(p.batch * p.dim, chunk);
+  p.group = group_of(p.batch * p.dim);
   p.tiles = (p.dim + 64 * vec - 1) / (64 * vec);
   p.rows = (uint32_t)(p.batch * p.tiles);
   // A counter gives 85 numbers a microsecond.  Blocks that all begin at once (3 x
   // 1537 x 1000, fp32, forwards) take 26 us with a counter for each row, 29 with
   // two and 30 with one; where there are more than run at a time, two keep them
-  // from loading in step (8 x 2048 x 1536, bf16, backwards: 94 us; a counter for
-  // each row 98; 32768 x 2048: 246 and 264).
+  // from loading in step (32768 x 2048, bf16: 125 + 235 us; a counter for each row
+  // 135 + 261).
   const uint32_t most = (int64_t)p.rows * p.chunks <= 1024 ? kCounters : 2;
   // rows of a counter, and as few counters as they need: hardly a block is left over
   const uint32_t each = (p.rows + most - 1) / most;
@@ -954,7 +954,7 @@ bool fits(int64_t batch, int64_t L, int64_t dim) {
 }
 
 size_t workspace_bytes(int64_t batch, int64_t L, int64_t dim, bool backward, bool need_ddecay) {
-  // the forward's chunks are longer and need less, however the groups fall
+  // the forward's chunks are longer and need less
   return (size_t)layout(batch, L, dim, kKeep, backward && need_ddecay).bytes;
 }
 

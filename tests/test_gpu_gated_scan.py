@@ -158,7 +158,7 @@ def test_documents_side_by_side(every, io):
     assert not g["dh0"].any()
 
 
-@pytest.mark.parametrize("rows,dim", [(1, 200), (1, 700), (1, 1500), (2, 1030), (3, 1100)])
+@pytest.mark.parametrize("rows,dim", [(1, 100), (1, 200), (1, 700), (1, 1500), (2, 1030), (3, 1100)])
 def test_groups_of_every_size(rows, dim):
     """Rows for groups of 32, 16, 8 and 4 chunks, forwards and backwards, a few groups long."""
     d, h0, dy, dlast, kw = inputs(rows, 4500, dim, torch.bfloat16, 14, True)
