@@ -42,10 +42,12 @@ extern "C" {
  *   states     : (batch, ceil(seqlen / 64), dim) float32, or NULL: the state
  *                before every 64th token, which ssm_gated_scan_bwd takes
  * Tensors are aligned to their element size (to 128 bytes, and rows of as many or
- * a multiple, is fastest); outputs and workspace overlap no input.  dim at most 2^24, batch *
- * ceil(dim / 64) * ceil(seqlen / 64) below 2^31 and seqlen at most 2^31 - 256
- * (else SSM_ERR_UNSUPPORTED).  Zero batch or dim is a no-op; seqlen == 0 copies
- * h0 (or zero) to last_state.
+ * a multiple, is fastest).  y, last_state, states and the workspace share no
+ * memory with each other or with an input (else SSM_ERR_FLAG; y is not x, r or i:
+ * two blocks may read one channel).  dim at most 2^24, batch * ceil(dim / 64) *
+ * ceil(seqlen / 64) below 2^31 and seqlen at most 2^31 - 256 (else
+ * SSM_ERR_UNSUPPORTED).  Zero batch or dim is a no-op; seqlen == 0 copies h0 (or
+ * zero) to last_state.
  * workspace: ssm_gated_scan_workspace_size(..., 0, 0) bytes, 256-byte aligned,
  * contents not needed before or after (NULL where the size is 0).
  * Values are not checked: a NaN or infinity in a real token reaches the later
@@ -68,8 +70,10 @@ int ssm_gated_scan_fwd(const void* x, const void* r, const void* i, const float*
  *   ddecay     : (dim) float32, or NULL (not a number where decay is 0: the root
  *                has no derivative there)
  *   dh0        : (batch, dim) float32, or NULL; must not overlap dlast
- * Outputs are overwritten.  workspace: ssm_gated_scan_workspace_size(..., 1,
- * ddecay != NULL) bytes.  Alignment and limits as for ssm_gated_scan_fwd; zero
+ * Outputs are overwritten; they and the workspace share no memory with each
+ * other or with an input (else SSM_ERR_FLAG).  workspace:
+ * ssm_gated_scan_workspace_size(..., 1, ddecay != NULL) bytes.  Alignment and
+ * limits as for ssm_gated_scan_fwd; zero
  * batch writes zeros to ddecay.  All sums are taken in a fixed order: repeated
  * calls give identical bits.
  */

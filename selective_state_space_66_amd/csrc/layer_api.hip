@@ -30,6 +30,23 @@ bool product_fits(std::initializer_list<int64_t> f) {
   return true;
 }
 
+// A tensor's memory; NULL has none.
+struct Span { const void* p; size_t bytes; };
+bool meet(const Span& a, const Span& b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+}
+// whether no output shares memory with an input or with another output
+bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span* q = outs.begin(); q != o; ++q)
+      if (meet(*o, *q)) return false;
+    for (const Span& i : ins)
+      if (meet(*o, i)) return false;
+  }
+  return true;
+}
+
 int status(hipError_t e) { return e == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
 
 size_t width(int io_dtype) { return io_dtype == SSM_BF16 ? 2 : 4; }
@@ -38,6 +55,10 @@ int scan_shape(int64_t batch, int64_t seqlen, int64_t dim, int io_dtype) {
   if (batch < 0 || seqlen < 0 || dim < 0) return SSM_ERR_SHAPE;
   if (io_dtype != SSM_F32 && io_dtype != SSM_BF16) return SSM_ERR_DTYPE;
   return product_fits({batch, seqlen, dim}) && product_fits({batch, dim}) ? SSM_OK : SSM_ERR_SHAPE;
+}
+
+size_t kept_states(int64_t seqlen) {
+  return (size_t)(seqlen / ssm66::gated_scan::kKeep + (seqlen % ssm66::gated_scan::kKeep != 0));
 }
 
 ssm66::gated_scan::Args scan_args(const void* x, const void* r, const void* i, const float* decay,
@@ -85,10 +106,15 @@ int ssm_gated_scan_fwd(const void* x, const void* r, const void* i, const float*
   if (!aligned_all(width(io_dtype), {x, r, i, y})) return SSM_ERR_ALIGN;
   if (!aligned_all(4, {decay, h0, seq_lens, last_state, states}) || !aligned(workspace, 256))
     return SSM_ERR_ALIGN;
-  if (h0 && h0 == last_state) return SSM_ERR_FLAG;  // several blocks read h0 on their own
   const size_t need = ssm66::gated_scan::workspace_bytes(batch, seqlen, dim, false, false);
   if (need > 0 && !workspace) return SSM_ERR_NULL;
   if (workspace_bytes < need) return SSM_ERR_SHAPE;
+  // several blocks read h0, and two tiles read the channels that both have
+  const size_t io = (size_t)(batch * seqlen * dim) * width(io_dtype), row = (size_t)(batch * dim) * 4;
+  if (!apart({{y, io}, {last_state, row}, {states, row * kept_states(seqlen)}, {workspace, need}},
+             {{x, io}, {r, io}, {i, io}, {decay, (size_t)dim * 4}, {h0, row},
+              {seq_lens, (size_t)batch * 4}, {reset, (size_t)(batch * seqlen)}}))
+    return SSM_ERR_FLAG;
   ssm66::gated_scan::Args a = scan_args(x, r, i, decay, seq_lens, reset, batch, seqlen, dim, workspace);
   a.h0 = h0; a.y = y; a.last_state = last_state; a.states = seqlen > 0 ? states : nullptr;
   return status(ssm66::gated_scan::forward(a, io_dtype == SSM_F32, (hipStream_t)stream));
@@ -108,11 +134,15 @@ int ssm_gated_scan_bwd(const void* x, const void* r, const void* i, const float*
   if (!aligned_all(width(io_dtype), {x, r, i, dy, dx, dr, di})) return SSM_ERR_ALIGN;
   if (!aligned_all(4, {decay, states, seq_lens, dlast, ddecay, dh0}) || !aligned(workspace, 256))
     return SSM_ERR_ALIGN;
-  if (dh0 && dh0 == dlast) return SSM_ERR_FLAG;  // several blocks read dlast on their own
   const size_t need = batch == 0 ? 0
       : ssm66::gated_scan::workspace_bytes(batch, seqlen, dim, true, ddecay != nullptr);
   if (need > 0 && !workspace) return SSM_ERR_NULL;
   if (workspace_bytes < need) return SSM_ERR_SHAPE;
+  const size_t io = (size_t)(batch * seqlen * dim) * width(io_dtype), row = (size_t)(batch * dim) * 4;
+  if (!apart({{dx, io}, {dr, io}, {di, io}, {ddecay, (size_t)dim * 4}, {dh0, row}, {workspace, need}},
+             {{x, io}, {r, io}, {i, io}, {decay, (size_t)dim * 4}, {states, row * kept_states(seqlen)},
+              {seq_lens, (size_t)batch * 4}, {reset, (size_t)(batch * seqlen)}, {dy, io}, {dlast, row}}))
+    return SSM_ERR_FLAG;
   ssm66::gated_scan::Args a = scan_args(x, r, i, decay, seq_lens, reset, batch, seqlen, dim, workspace);
   a.states = seqlen > 0 ? (float*)states : nullptr;
   a.dy = dy; a.dlast = dlast; a.dx = dx; a.dr = dr; a.di = di; a.ddecay = ddecay; a.dh0 = dh0;

@@ -114,7 +114,8 @@ def gated_scan_fwd(x, r, i, decay, h0=None, seq_lens=None, reset=None, y=None, l
     reset: optional (batch, L) bool or uint8, state zeroed before each flagged token.
     Returns (y like x, last_state (batch, dim) float32 or None, states or None): with
     return_states the state before every 64th token, (batch, ceil(L / 64), dim) float32,
-    which gated_scan_bwd takes.
+    which gated_scan_bwd takes.  y, last_state and workspace may be given; they share no memory
+    with each other or with an input (y is not x, r or i).
     """
     c, torch = _core()
     reset = _flags(torch, reset)

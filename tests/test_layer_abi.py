@@ -179,3 +179,38 @@ def test_binding_refuses_cpu_tensors_and_wrong_arguments(lib):
         ssm.dropout_bwd(x, 0.0, None)
     with pytest.raises(ValueError):
         ssm.rotary_fwd(torch.zeros(1, 2, 1, 8), None, torch.ones(4))
+
+
+def at(k, offset=0):
+    """An address of a gigabyte of its own."""
+    return ctypes.c_void_p((k << 30) + offset)
+
+
+# every tensor in a place of its own: 2 x 300 x 64, bf16
+SCAN_APART = dict(x=at(1), r=at(2), i=at(3), decay=at(4), h0=at(5), lens=at(6), reset=at(7), y=at(8), last=at(9),
+                  states=at(10), ws=at(11))
+BWD_APART = dict(x=at(1), r=at(2), i=at(3), decay=at(4), states=at(5), lens=at(6), reset=at(7), dy=at(8), dlast=at(9),
+                 dx=at(10), dr=at(11), di=at(12), ddecay=at(13), dh0=at(14), ws=at(15))
+
+
+@pytest.mark.parametrize("call,apart,inputs,outputs", [
+    (scan, SCAN_APART, ("x", "r", "i", "decay", "h0", "lens", "reset"), ("y", "last", "states", "ws")),
+    (scan_bwd, BWD_APART, ("x", "r", "i", "decay", "states", "lens", "reset", "dy", "dlast"),
+     ("dx", "dr", "di", "ddecay", "dh0", "ws"))])
+def test_scan_refuses_outputs_in_the_place_of_another_tensor(lib, call, apart, inputs, outputs):
+    """In place, and where only the ends meet: with two channels a thread the last two tiles read
+    one channel, and the blocks of all chunks read h0, so a block may find what another wrote."""
+    n = 2 * 300 * 64
+    size = dict(x=2 * n, r=2 * n, i=2 * n, y=2 * n, dy=2 * n, dx=2 * n, dr=2 * n, di=2 * n, decay=256, ddecay=256,
+                h0=512, last=512, dlast=512, dh0=512, lens=8, reset=600, states=2 * 5 * 64 * 4)
+    backward = call is scan_bwd
+    size["ws"] = lib.ssm_gated_scan_workspace_size(2, 300, 64, backward, backward)
+    for k, out in enumerate(outputs):
+        for other in inputs + outputs[:k]:
+            there = apart[other].value
+            assert call(lib, **{**apart, out: at(0, there)}) == FLAG, (out, other)
+            # the last bytes of the one on the first of the other, and the other way round
+            for address in (there - size[out] // 256 * 256 - (size[out] % 256 > 0) * 256 + 256,
+                            there + (size[other] - 1) // 256 * 256):
+                if abs(address - there) < size[out if address < there else other]:
+                    assert call(lib, **{**apart, out: at(0, address)}) == FLAG, (out, other, address - there)
