@@ -51,8 +51,9 @@ extern "C" {
  * workspace: ssm_gated_scan_workspace_size(..., 0, 0) bytes, 256-byte aligned,
  * contents not needed before or after (NULL where the size is 0).
  * Values are not checked: a NaN or infinity in a real token reaches the later
- * tokens of its document (in float32 calls an infinite state becomes a NaN there),
- * no other document and no other channel.  Repeated calls give identical bits.
+ * tokens of its document (an infinite state stays infinite; a bfloat16 call makes
+ * it a NaN at a token whose v is over 87, where a is 0 in float32), no other
+ * document and no other channel.  Repeated calls give identical bits.
  */
 size_t ssm_gated_scan_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int backward,
                                      int need_ddecay);
