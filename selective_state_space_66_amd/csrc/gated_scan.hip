@@ -102,12 +102,14 @@ __device__ __forceinline__ float one_minus(float v, float a) {
 
 // What a token's gate r does: V is v in the unit of the sums (natural where
 // PRECISE, of log2 else, so that a is one exp2), f the factor of the state, m
-// the root of 1 - a^2.  f is a itself, or (PRECISE, where a is near 1) -b with
-// the sign bit set, which stands for 1 - b.
+// the root of 1 - a^2.  f is a itself, or (LESS, where a is near 1) -b with the
+// sign bit set, which stands for 1 - b: a rounds to 2^-25, which is 1% of b = 1 - a
+// where that is 3e-6, and a state that is handed on from token to token in memory
+// would forget that much too fast or too slowly.
 struct Gate { float V, f, m, s, rest; };
 template <bool PRECISE>
 __device__ __forceinline__ float sum_unit(float decay) { return PRECISE ? decay : decay * kLog2e; }
-template <bool PRECISE>
+template <bool PRECISE, bool LESS>
 __device__ __forceinline__ Gate gate_of(float d, float r) {  // d: sum_unit(decay)
   Gate g;
   sigmoid2<PRECISE>(r, &g.s, &g.rest);
@@ -117,19 +119,31 @@ __device__ __forceinline__ Gate gate_of(float d, float r) {  // d: sum_unit(deca
     g.f = g.V < 0.6931472f ? -b : a;
     g.m = __builtin_amdgcn_sqrtf(b * (2.0f - b));
   } else {
-    // 1 - a^2: four terms of its series below v = 0.05, which leave out 8e-7 of
-    // it; a's rounding is 6e-7 of the difference above
-    g.f = exp2_hw(-g.V);
-    float s = fmaf(g.V, -0.15388844f, 0.44403291f);
-    s = fmaf(g.V, s, -0.96090603f);
-    s = fmaf(g.V, s, 1.38629436f);
-    const float m2 = g.V < 0.07f ? g.V * s : fmaf(-g.f, g.f, 1.0f);
+    // below v = 0.05 four terms of a series, of 1 - a^2 (which leave out 8e-7 of
+    // it) or of 1 - a (5e-8); a's rounding is 6e-7 of the differences above
+    const bool small = g.V < 0.07f;
+    const float a = exp2_hw(-g.V);
+    float s, m2;
+    if (LESS) {
+      s = fmaf(g.V, -0.0096181291f, 0.055504109f);
+      s = fmaf(g.V, s, -0.24022651f);
+      s = fmaf(g.V, -s, -kLn2);  // -b / V
+      const float f = g.V * s;
+      g.f = small ? f : a;
+      m2 = small ? f * (-2.0f - f) : fmaf(-a, a, 1.0f);
+    } else {
+      s = fmaf(g.V, -0.15388844f, 0.44403291f);
+      s = fmaf(g.V, s, -0.96090603f);
+      s = fmaf(g.V, s, 1.38629436f);
+      g.f = a;
+      m2 = small ? g.V * s : fmaf(-a, a, 1.0f);
+    }
     g.m = __builtin_amdgcn_sqrtf(m2);
   }
   return g;
 }
 
-// f h and f h + u; PRECISE: f with the sign bit set stands for 1 + f.  kept() takes
+// f h and f h + u; LESS: f with the sign bit set stands for 1 + f.  kept() takes
 // the product with the finite h nearest to h, and then adds h or what is left of it
 // (0 or an infinity): an infinite state stays one, where -b h + h would make it a
 // NaN (fp32, forwards and backwards, without and with it: 3 x 1537 x 1000 26.4 + 44.1,
@@ -138,13 +152,13 @@ __device__ __forceinline__ float kept(float f, float h, float u) {
   const float fin = __builtin_amdgcn_fmed3f(h, -3.402823466e38f, 3.402823466e38f), t = fmaf(f, fin, u);
   return t + (__float_as_int(f) < 0 ? h : h - fin);
 }
-template <bool PRECISE>
+template <bool LESS>
 __device__ __forceinline__ float times(float f, float h) {
-  return PRECISE ? kept(f, h, 0.0f) : f * h;
+  return LESS ? kept(f, h, 0.0f) : f * h;
 }
-template <bool PRECISE>
+template <bool LESS>
 __device__ __forceinline__ float advance(float f, float h, float u) {
-  return PRECISE ? kept(f, h, u) : fmaf(f, h, u);
+  return LESS ? kept(f, h, u) : fmaf(f, h, u);
 }
 
 // What a stretch of tokens does to a state, its factor instead of V (kCut: a
@@ -466,7 +480,7 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
     IO::get(ri[j], i);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      const Gate g = gate_of<PRECISE>(d[k], r[k]);
+      const Gate g = gate_of<PRECISE, PRECISE>(d[k], r[k]);
       f[j][k] = g.f;
       u[j][k] = g.m * sigmoid1<PRECISE>(i[k]) * x[k];
       V[k] += j < s.real ? g.V : 0.0f;
@@ -666,7 +680,7 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
     IO::get(ri[j], i);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      const Gate g = gate_of<PRECISE>(sum_unit<PRECISE>(decay[k]), r[k]);
+      const Gate g = gate_of<PRECISE, PRECISE>(sum_unit<PRECISE>(decay[k]), r[k]);
       gate.f[j][k] = g.f;
       gate.m[j][k] = g.m;
       gate.r[j][k] = g.s;
@@ -826,7 +840,8 @@ __global__ __launch_bounds__(1024) void decay_sum_kernel(const float* part, cons
 
 // ---- one token ----------------------------------------------------------------
 
-// A thread keeps its channels over the rows it takes.
+// A thread keeps its channels over the rows it takes.  The factor as what it is less
+// than 1, in bf16 calls too (4096 x 5120, bf16: 64.1 us, with a itself 63.9).
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void step_kernel(const StepArgs p) {
   constexpr bool PRECISE = sizeof(T) == 4;
@@ -844,8 +859,8 @@ __global__ __launch_bounds__(256) void step_kernel(const StepArgs p) {
     load_n<VEC>(p.state + at, h);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      const Gate g = gate_of<PRECISE>(d[k], r[k]);
-      h[k] = advance<PRECISE>(g.f, h[k], g.m * sigmoid1<PRECISE>(i[k]) * x[k]);
+      const Gate g = gate_of<PRECISE, true>(d[k], r[k]);
+      h[k] = advance<true>(g.f, h[k], g.m * sigmoid1<PRECISE>(i[k]) * x[k]);
     }
     store_n<VEC>(p.state + at, h);
     store_n<VEC>((T*)p.y + at, h);

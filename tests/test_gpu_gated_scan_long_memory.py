@@ -1,0 +1,79 @@
+"""States of channels that forget little, handed on from call to call: thousands of tokens, one at a
+time, against 64 bits.
+
+The gates r and i are fixed, so that what is wrong about a factor adds up; x is drawn.  With e =
+2^-24 and big the largest state on the way, a channel's state after N tokens is off by
+ - the rounding of the state at each token, half a unit of it at most, 2^-24 big.  Tokens with the
+   same x add the same and may all be rounded the same way; between different x the errors are
+   taken as independent, with mean 0, in an interval of width 2^-23 big.  With n_k tokens of the
+   k-th value, by Hoeffding's inequality their sum passes 2^-23 big sqrt(sum n_k^2 ln(2 C / q) / 2)
+   in one of C channels with probability q (1e-9 here).  Without equal values sum n_k^2 is N; for
+   normal x in bf16 it is 16 N, and that is no slack: the exact recurrence with nothing but its
+   state rounded to fp32 at each token (computed in 64 bits) is 1.9 times off the bound for N
+   independent errors at r = -9, and 0.5 times this one.
+ - the rounding of what a token adds and of what it takes away, 3 e (|u| + b |h|) a token;
+ - the error of m sigmoid(i), the same at each token: (24 + |r| + |i|) e of all that was added;
+ - the rate b = 1 - a, off by (|r| + 8) e of itself, over N tokens.
+A factor a rounded to 2^-25 is off by as much of the state at each token, the same way: at 16384
+tokens twice (bf16) and eight times (fp32) the bound where that rounding is at its largest.
+"""
+import math
+
+import pytest
+import torch
+
+import selective_state_space_66_amd as ssm
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+E = 2.0 ** -24
+N, C = 16384, 512
+R = -6.0  # with decays of 1e-3 to 4e-3: v of 2.5e-6 to 1e-5
+
+
+def problem(io, seed, r=R, slowest=1e-3):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn((1, N, C), generator=gen, device=DEV).to(io)
+    decay = (slowest * 4.0 ** torch.rand((C,), generator=gen, device=DEV)).contiguous()
+    h0 = torch.randn((1, C), generator=gen, device=DEV)
+    gate_r, gate_i = torch.full_like(x, r), torch.zeros_like(x)
+    v = decay.double() / (1.0 + math.exp(-r))
+    a, m = torch.exp(-v), torch.sqrt(-torch.expm1(-2.0 * v)) * 0.5
+    u = m * x[0].double()
+    h, states = h0[0].double(), []
+    for t in range(N):
+        h = a * h + u[t]
+        states.append(h)
+    h = torch.stack(states)
+    big = torch.maximum(h.abs().max(0).values, h0[0].double().abs())
+    b = -torch.expm1(-v)
+    ordered = x[0].float().sort(0).values
+    first = torch.ones((N, C), device=DEV)
+    first[1:] = (ordered[1:] != ordered[:-1]).float()
+    count = torch.zeros((N + 1, C), device=DEV)
+    count.scatter_add_(0, first.cumsum(0).long(), torch.ones((N, C), device=DEV))
+    bound = 2.0 ** -23 * big * (count.double().square().sum(0) * math.log(2 * C / 1e-9) / 2).sqrt()
+    bound = bound + 3 * E * (u.abs().sum(0) + b * N * big)
+    bound = bound + (24 + abs(r)) * E * (h[-1] - torch.exp(-v * N) * h0[0].double()).abs()
+    bound = bound + (abs(r) + 8) * E * N * b * big
+    return x, gate_r, gate_i, decay, h0, h, bound
+
+
+def worst(got, want, bound):
+    return float(((got.double() - want).abs() / bound).max())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("r,slowest", [(R, 1e-3), (-9.0, 1e-3), (1.0, 0.07)])
+def test_steps(r, slowest, io):
+    """v of 2.5e-6 on, of 1.2e-7 on (a is 1 in fp32 for some), and on both sides of 0.05."""
+    print(f"[gated scan] {N} steps, r {r}, {io}", flush=True)
+    x, gr, gi, decay, h0, h, bound = problem(TYPES[io], 1, r, slowest)
+    state = h0.clone()
+    for t in range(N):
+        ssm.gated_scan_step(state, x[:, t], gr[:, t], gi[:, t], decay)
+    assert worst(state[0], h[-1], bound) <= 1.0
+    # the whole sequence in one call, its own error inside the same bound
+    last = ssm.gated_scan_fwd(x, gr, gi, decay, h0=h0)[1]
+    assert worst(last[0], h[-1], bound) <= 1.0
