@@ -77,3 +77,16 @@ def test_steps(r, slowest, io):
     # the whole sequence in one call, its own error inside the same bound
     last = ssm.gated_scan_fwd(x, gr, gi, decay, h0=h0)[1]
     assert worst(last[0], h[-1], bound) <= 1.0
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("piece", [1, 3, 16, 64, 65, 128, 300])
+def test_sequences_piece_by_piece(piece, io):
+    """The same tokens in calls of a few, each from the last one's state."""
+    print(f"[gated scan] {N} tokens in pieces of {piece}, {io}", flush=True)
+    x, gr, gi, decay, h0, h, bound = problem(TYPES[io], 2)
+    state = h0
+    for t in range(0, N, piece):
+        e = min(t + piece, N)
+        state = ssm.gated_scan_fwd(x[:, t:e], gr[:, t:e], gi[:, t:e], decay, h0=state)[1]
+    assert worst(state[0], h[-1], bound) <= 1.0
