@@ -69,21 +69,25 @@ template <bool PRECISE>
 __device__ __forceinline__ float sigmoid1(float z) {
   return rcp_hw(1.0f + exp_f<PRECISE>(PRECISE ? held(-z) : -z));
 }
-// sigmoid(z) and 1 - sigmoid(z).  PRECISE: both to a few units in the last
-// place.  Else the second is a difference, off by 2^-24 at most: half a unit of
-// a bf16 gradient where the gate is within 3e-5 of open, more of smaller ones.
-template <bool PRECISE>
+// sigmoid(z) and 1 - sigmoid(z), both to a few units in the last place.
 __device__ __forceinline__ void sigmoid2(float z, float* s, float* rest) {
-  if (PRECISE) {
-    const float e = exp_f<true>(held(-fabsf(z)));
-    const float r = rcp_hw(1.0f + e), er = e * r;
-    *s = z > 0.0f ? r : er;
-    *rest = z > 0.0f ? er : r;
-  } else {
-    *s = sigmoid1<false>(z);
-    *rest = 1.0f - *s;
-  }
+  const float e = exp_f<true>(held(-fabsf(z)));
+  const float r = rcp_hw(1.0f + e), er = e * r;
+  *s = z > 0.0f ? r : er;
+  *rest = z > 0.0f ? er : r;
 }
+// Both of them in one number, of which the fraction is sigmoid(z) and that of its
+// negative 1 - sigmoid(z): the smaller of the two, with the sign bit set where that
+// is 1 - sigmoid(z).  (That is never 0, the fraction of which is 0 and not 1.)
+struct Open { float s, both; };
+__device__ __forceinline__ Open open_of(float z) {
+  const float e = exp_f<false>(-z), s = rcp_hw(1.0f + e), rest = fmaf(e, s, 1.17549435e-38f);
+  float both = s > 0.5f ? -rest : s;  // (a NaN stays one)
+  asm("" : "+v"(both));  // made here: else s and rest both wait for the gradients, in 16 registers more
+  return Open{s, both};
+}
+__device__ __forceinline__ float open_part(float both) { return __builtin_amdgcn_fractf(both); }
+__device__ __forceinline__ float shut_part(float both) { return __builtin_amdgcn_fractf(-both); }
 
 // 1 - e^-v from v and a = e^-v: the series where it leaves out less than half a
 // unit (its last term), the difference above, where it has lost at most a bit
@@ -106,7 +110,7 @@ __device__ __forceinline__ float one_minus(float v, float a) {
 // sign bit set, which stands for 1 - b: a rounds to 2^-25, which is 1% of b = 1 - a
 // where that is 3e-6, and a state that is handed on from token to token in memory
 // would forget that much too fast or too slowly.
-struct Gate { float V, f, m, s, rest; };
+struct Gate { float V, f, m, s, rest; };  // s, rest: of sigmoid(r); s not PRECISE: both (open_of)
 // -b = 2^-V - 1 for V below 0.07
 __device__ __forceinline__ float minus_b(float V) {
   float s = fmaf(V, -0.0096181291f, 0.055504109f);
@@ -118,15 +122,18 @@ __device__ __forceinline__ float sum_unit(float decay) { return PRECISE ? decay 
 template <bool PRECISE, bool LESS = PRECISE>
 __device__ __forceinline__ Gate gate_of(float d, float r) {  // d: sum_unit(decay)
   Gate g;
-  sigmoid2<PRECISE>(r, &g.s, &g.rest);
-  g.V = d * g.s;
   if (PRECISE) {
+    sigmoid2(r, &g.s, &g.rest);
+    g.V = d * g.s;
     const float a = exp_f<true>(-g.V), b = one_minus(g.V, a);
     g.f = g.V < 0.6931472f ? -b : a;
     g.m = __builtin_amdgcn_sqrtf(b * (2.0f - b));
   } else {
     // below v = 0.05 four terms of a series, of 1 - a^2 (which leave out 8e-7 of
     // it) or of 1 - a (5e-8); a's rounding is 6e-7 of the differences above
+    const Open o = open_of(r);
+    g.s = o.both;
+    g.V = d * o.s;
     const bool small = g.V < 0.07f;
     const float a = exp2_hw(-g.V);
     float m2;
@@ -595,8 +602,8 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
 // again; the adjoint comes from the right as the state does from the left.  The
 // gates stay in registers, x and dy wait in LDS meanwhile.
 
-// What a block keeps of a token's gates: f, m, sigmoid(r), sigmoid(i), and of
-// fp32 also what is left of both to 1.
+// What a block keeps of a token's gates: f, m, sigmoid(r), sigmoid(i) and what is
+// left of both to 1 (bf16: each two of them in one register, open_of).
 template <bool PRECISE, int VEC, int TOK>
 struct Gates {
   float f[TOK][VEC], m[TOK][VEC], r[TOK][VEC], i[TOK][VEC];
@@ -621,9 +628,11 @@ __device__ __forceinline__ void token_gradients(
     const bool real = PLAIN || j < s.real, cut = !PLAIN && (s.cuts >> j & 1);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      const float sr = gate.r[j][k], g = gate.i[j][k], f = gate.f[j][k], m = gate.m[j][k];
-      const float rest_r = PRECISE ? gate.rest_r[PRECISE ? j : 0][k] : 1.0f - sr;
-      const float rest_g = PRECISE ? gate.rest_i[PRECISE ? j : 0][k] : 1.0f - g;
+      const float f = gate.f[j][k], m = gate.m[j][k];
+      const float sr = PRECISE ? gate.r[j][k] : open_part(gate.r[j][k]);
+      const float g = PRECISE ? gate.i[j][k] : open_part(gate.i[j][k]);
+      const float rest_r = PRECISE ? gate.rest_r[PRECISE ? j : 0][k] : shut_part(gate.r[j][k]);
+      const float rest_g = PRECISE ? gate.rest_i[PRECISE ? j : 0][k] : shut_part(gate.i[j][k]);
       const float v = decay[k] * sr, lam = dy[k] + c[k];
       const float al = times<PRECISE>(f, lam);
       const float gx = g * x[k], lm = lam * m;
@@ -695,13 +704,17 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
       gate.f[j][k] = g.f;
       gate.m[j][k] = g.m;
       gate.r[j][k] = g.s;
-      float rest;
-      sigmoid2<PRECISE>(i[k], &gate.i[j][k], &rest);
+      float open;
       if (PRECISE) {
         gate.rest_r[PRECISE ? j : 0][k] = g.rest;
-        gate.rest_i[PRECISE ? j : 0][k] = rest;
+        sigmoid2(i[k], &open, &gate.rest_i[PRECISE ? j : 0][k]);
+        gate.i[j][k] = open;
+      } else {
+        const Open o = open_of(i[k]);
+        gate.i[j][k] = o.both;
+        open = o.s;
       }
-      u[j][k] = g.m * gate.i[j][k] * x[k];
+      u[j][k] = g.m * open * x[k];
       V[k] += j < s.real ? g.V : 0.0f;
     }
   }
