@@ -74,9 +74,8 @@ int ssm_gated_scan_fwd(const void* x, const void* r, const void* i, const float*
  * Outputs are overwritten; they and the workspace share no memory with each
  * other or with an input (else SSM_ERR_FLAG).  workspace:
  * ssm_gated_scan_workspace_size(..., 1, ddecay != NULL) bytes.  Alignment and
- * limits as for ssm_gated_scan_fwd; zero
- * batch writes zeros to ddecay.  All sums are taken in a fixed order: repeated
- * calls give identical bits.
+ * limits as for ssm_gated_scan_fwd; zero batch or seqlen writes zeros to ddecay.
+ * All sums are taken in a fixed order: repeated calls give identical bits.
  */
 int ssm_gated_scan_bwd(const void* x, const void* r, const void* i, const float* decay,
                        const float* states, const int32_t* seq_lens, const uint8_t* reset,

@@ -858,7 +858,7 @@ __global__ __launch_bounds__(1024) void decay_sum_kernel(const float* part, cons
   __syncthreads();
   if (w == 0 && c < dim) {
     for (int q = 1; q < 16; ++q) t += sums[q][lane];
-    ddecay[c] = (float)(t / (double)decay[c]);
+    ddecay[c] = rows > 0 ? (float)(t / (double)decay[c]) : 0.0f;
   }
 }
 
@@ -1031,8 +1031,9 @@ hipError_t backward(const Args& p, bool f32, hipStream_t s) {
   }
   if (e != hipSuccess || !p.ddecay) return e;
   const Layout a = layout(p.batch, p.L, p.dim, kKeep, true);
+  const int64_t rows = p.L > 0 ? pieces_of(p.L, kKeep) * p.batch : 0;  // without tokens the gradient is 0
   decay_sum_kernel<<<(p.dim + 63) / 64, 1024, 0, s>>>((const float*)((const char*)p.ws + a.part), p.decay,
-                                                      p.ddecay, pieces_of(p.L, kKeep) * p.batch, p.dim);
+                                                      p.ddecay, rows, p.dim);
   return hipGetLastError();
 }
 
