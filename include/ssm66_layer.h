@@ -31,7 +31,8 @@ extern "C" {
  *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,   y_t = h_t.
  *   x, r, i, y : (batch, seqlen, dim), io dtype; r and i are the gates before
  *                their sigmoid
- *   decay      : (dim) float32, finite, not negative; 0 keeps the state
+ *   decay      : (dim) float32, 0 to 1e30 (v of 1e38 overflows in its products);
+ *                0 keeps the state
  *   h0         : (batch, dim) float32, the state before token 0, or NULL (zero)
  *   seq_lens   : (batch) int32 or NULL: as for ssm_scan_fwd_ex -- tokens at or
  *                past a length are padding, whatever they hold: y = 0 there and

@@ -108,7 +108,7 @@ def gated_scan_fwd(x, r, i, decay, h0=None, seq_lens=None, reset=None, y=None, l
 
     a_t = exp(-decay sigmoid(r_t)), h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t, y = h.
     x, r, i: (batch, L, dim), all float32 or all bfloat16 (r, i: the gates before their
-    sigmoid); decay: (dim,) float32, not negative;
+    sigmoid); decay: (dim,) float32, 0 to 1e30;
     h0: optional (batch, dim) float32 initial state;
     seq_lens: optional (batch,) int32 real lengths (y = 0 past them, the state kept);
     reset: optional (batch, L) bool or uint8, state zeroed before each flagged token.
