@@ -4,7 +4,9 @@
  * caller-owned device pointers, dense row-major tensors, no allocation, every
  * call asynchronous on the caller's stream (of the current device), arguments
  * checked before any HIP call, the status codes and io dtypes of ssm66.h,
- * float32 states and parameters in every mode.
+ * float32 states and parameters in every mode.  An output shares memory with an
+ * input only where that is said ("may be"), from the first byte to the last, and
+ * with no other output and no workspace: else SSM_ERR_FLAG.
  *
  *   ssm_gated_scan_fwd, ssm_gated_scan_bwd, ssm_gated_scan_step
  *       a recurrence of one state per channel whose decay and input are gated
@@ -43,10 +45,9 @@ extern "C" {
  *   states     : (batch, ceil(seqlen / 64), dim) float32, or NULL: the state
  *                before every 64th token, which ssm_gated_scan_bwd takes
  * Tensors are aligned to their element size (to 128 bytes, and rows of as many or
- * a multiple, is fastest).  y, last_state, states and the workspace share no
- * memory with each other or with an input (else SSM_ERR_FLAG; y is not x, r or i:
- * two blocks may read one channel).  dim at most 2^24, batch * ceil(dim / 64) *
- * ceil(seqlen / 64) below 2^31 and seqlen at most 2^31 - 256 (else
+ * a multiple, is fastest).  No output may be an input (two blocks may read one
+ * channel, and all blocks of a row read h0).  dim at most 2^24, batch * ceil(dim /
+ * 64) * ceil(seqlen / 64) below 2^31 and seqlen at most 2^31 - 256 (else
  * SSM_ERR_UNSUPPORTED).  Zero batch or dim is a no-op; seqlen == 0 copies h0 (or
  * zero) to last_state.
  * workspace: ssm_gated_scan_workspace_size(..., 0, 0) bytes, 256-byte aligned,
@@ -72,8 +73,7 @@ int ssm_gated_scan_fwd(const void* x, const void* r, const void* i, const float*
  *   ddecay     : (dim) float32, or NULL (not a number where decay is 0: the root
  *                has no derivative there)
  *   dh0        : (batch, dim) float32, or NULL; must not overlap dlast
- * Outputs are overwritten; they and the workspace share no memory with each
- * other or with an input (else SSM_ERR_FLAG).  workspace:
+ * Outputs are overwritten; none may be an input.  workspace:
  * ssm_gated_scan_workspace_size(..., 1, ddecay != NULL) bytes.  Alignment and
  * limits as for ssm_gated_scan_fwd; zero batch or seqlen writes zeros to ddecay.
  * All sums are taken in a fixed order: repeated calls give identical bits.
@@ -86,7 +86,7 @@ int ssm_gated_scan_bwd(const void* x, const void* r, const void* i, const float*
 
 /*
  * One token against a state cache (batch, dim) float32, updated in place; x, r,
- * i, y: (batch, dim), io dtype; y may be any of them.  dim at most 2^24.
+ * i, y: (batch, dim), io dtype; y may be any of x, r and i.  dim at most 2^24.
  */
 int ssm_gated_scan_step(float* state, const void* x, const void* r, const void* i,
                         const float* decay, void* y, int64_t batch, int64_t dim, int io_dtype,
@@ -106,7 +106,7 @@ int ssm_gated_scan_step(float* state, const void* x, const void* r, const void* 
  *
  * Dropout: y = dropout(x) + residual (NULL: none).
  *   x           : (n) io_dtype
- *   residual, y : (n) out_dtype; y may be x (of one type) or residual
+ *   residual, y : (n) out_dtype; y may be x (of one type) or residual, or both
  * The gradient of x is ssm_dropout of dy, without a residual, from out_dtype to
  * io_dtype.  Tensors are aligned to their element size (16 bytes is fastest);
  * zero n is a no-op.  A dropped value counts as 0 whatever it is.
@@ -126,7 +126,8 @@ int ssm_dropout(const void* x, const void* residual, const int64_t* rng, int64_t
  * over each row, the variance over the same values (not one less).
  *   x, y         : (rows, dim), io_dtype
  *   residual, h  : (rows, dim), h_dtype, which is io_dtype or SSM_F32; either
- *                  may be NULL (no residual; h not kept).  h may be residual
+ *                  may be NULL (no residual; h not kept).  h may be residual,
+ *                  or x where they are of one type
  *   weight, bias : (dim) float32, or NULL (one, zero)
  *   mean, rstd   : (rows) float32, or NULL: what ssm_add_norm_bwd takes (mean
  *                  is not written by the RMS norm)
@@ -148,11 +149,11 @@ int ssm_add_norm_fwd(const void* x, const void* residual, const float* weight, c
  *   dx             : (rows, dim), io_dtype
  *   dresidual      : (rows, dim), h_dtype, or NULL
  *   dweight, dbias : (dim) float32, or NULL
- * Outputs are overwritten; dx may be dy, dresidual may be dh.  workspace:
- * ssm_add_norm_workspace_size(...) bytes, 256-byte aligned (NULL and 0 where
- * neither dweight nor dbias is asked for).  Zero rows writes zeros to dweight
- * and dbias.  All sums are taken in a fixed order: repeated calls give identical
- * bits.
+ * Outputs are overwritten; dx and dresidual may each be dy or dh, of their type.
+ * workspace: ssm_add_norm_workspace_size(...) bytes, 256-byte aligned (NULL and 0
+ * where neither dweight nor dbias is asked for).  Zero rows writes zeros to
+ * dweight and dbias.  All sums are taken in a fixed order: repeated calls give
+ * identical bits.
  */
 size_t ssm_add_norm_workspace_size(int64_t rows, int64_t dim);
 int ssm_add_norm_bwd(const void* h, const void* dy, const void* dh, const float* weight, int norm,

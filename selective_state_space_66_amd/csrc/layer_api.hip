@@ -47,6 +47,11 @@ bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
   return true;
 }
 
+// whether an output shares no memory with an input, or lies in its place value by value
+bool apart_or_over(const Span& out, const Span& in) {
+  return !meet(out, in) || (out.p == in.p && out.bytes == in.bytes);
+}
+
 int status(hipError_t e) { return e == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
 
 size_t width(int io_dtype) { return io_dtype == SSM_BF16 ? 2 : 4; }
@@ -158,6 +163,11 @@ int ssm_gated_scan_step(float* state, const void* x, const void* r, const void* 
   if (!state || !x || !r || !i || !decay || !y) return SSM_ERR_NULL;
   if (dim > (1 << 24)) return SSM_ERR_UNSUPPORTED;
   if (!aligned_all(width(io_dtype), {x, r, i, y}) || !aligned_all(4, {state, decay})) return SSM_ERR_ALIGN;
+  const size_t io = (size_t)(batch * dim) * width(io_dtype);
+  const Span out = {y, io}, sx = {x, io}, sr = {r, io}, si = {i, io}, sd = {decay, (size_t)dim * 4};
+  if (!apart({{state, (size_t)(batch * dim) * 4}}, {out, sx, sr, si, sd}) || meet(out, sd) ||
+      !apart_or_over(out, sx) || !apart_or_over(out, sr) || !apart_or_over(out, si))
+    return SSM_ERR_FLAG;
   ssm66::gated_scan::StepArgs a;
   a.state = state; a.x = x; a.r = r; a.i = i; a.decay = decay; a.y = y; a.batch = batch; a.dim = (int)dim;
   return status(ssm66::gated_scan::step(a, io_dtype == SSM_F32, (hipStream_t)stream));
@@ -172,7 +182,11 @@ int ssm_dropout(const void* x, const void* residual, const int64_t* rng, int64_t
   if (!x || !y || (p > 0.0f && !rng)) return SSM_ERR_NULL;
   if (!aligned(x, width(io_dtype)) || !aligned_all(width(out_dtype), {residual, y}) || !aligned(rng, 8))
     return SSM_ERR_ALIGN;
-  if (x == y && io_dtype != out_dtype) return SSM_ERR_FLAG;  // written before its neighbours are read
+  // (in place of the other type a value would be written before its neighbours are read)
+  const Span out = {y, (size_t)n * width(out_dtype)};
+  if (!apart_or_over(out, {x, (size_t)n * width(io_dtype)}) || !apart_or_over(out, {residual, out.bytes}) ||
+      meet(out, {rng, 16}))
+    return SSM_ERR_FLAG;
   ssm66::dropout::Args a;
   a.x = x; a.residual = residual; a.y = y; a.n = n; a.drop = ssm66::drop_of(p, rng, site);
   return status(ssm66::dropout::run(a, io_dtype == SSM_F32, out_dtype == SSM_F32, (hipStream_t)stream));
@@ -189,7 +203,13 @@ int ssm_add_norm_fwd(const void* x, const void* residual, const float* weight, c
   if (!aligned_all(width(io_dtype), {x, y}) || !aligned_all(width(h_dtype), {residual, h}) ||
       !aligned_all(4, {weight, bias, mean, rstd}) || !aligned(rng, 8))
     return SSM_ERR_ALIGN;
-  if (h == y || (h == x && io_dtype != h_dtype) || (residual == y && residual)) return SSM_ERR_FLAG;
+  const size_t n = (size_t)(rows * dim), row = (size_t)rows * 4, col = (size_t)dim * 4;
+  const Span sx = {x, n * width(io_dtype)}, sy = {y, sx.bytes}, sres = {residual, n * width(h_dtype)};
+  const Span sh = {h, sres.bytes}, sw = {weight, col}, sb = {bias, col}, sg = {rng, 16};
+  const Span smean = {norm == SSM_NORM_LAYER ? mean : nullptr, row}, srstd = {rstd, row};
+  if (!apart({sy, sh}, {sw, sb, sg}) || !apart({smean, srstd}, {sx, sres, sy, sh, sw, sb, sg}) ||
+      !apart_or_over(sy, sx) || meet(sy, sres) || !apart_or_over(sh, sres) || !apart_or_over(sh, sx))
+    return SSM_ERR_FLAG;
   ssm66::add_norm::Args a = {};
   a.x = x; a.residual = residual; a.weight = weight; a.bias = bias; a.y = y; a.h = h;
   a.mean = mean; a.rstd = rstd; a.drop = ssm66::drop_of(p, rng, site);
@@ -214,13 +234,18 @@ int ssm_add_norm_bwd(const void* h, const void* dy, const void* dh, const float*
   if (!aligned_all(width(io_dtype), {dy, dx}) || !aligned_all(width(h_dtype), {h, dh, dresidual}) ||
       !aligned_all(4, {weight, mean, rstd, dweight, dbias}) || !aligned(rng, 8) || !aligned(workspace, 256))
     return SSM_ERR_ALIGN;
-  if (rows > 0 && (dx == dresidual || dx == h || dresidual == h || (dx == dh && io_dtype != h_dtype) ||
-                   (dresidual == dy && io_dtype != h_dtype)))
-    return SSM_ERR_FLAG;
   const bool sums = dweight || dbias;
   const size_t need = sums ? ssm66::add_norm::workspace_bytes(rows, dim) : 0;
   if (need > 0 && !workspace) return SSM_ERR_NULL;
   if (workspace_bytes < need) return SSM_ERR_SHAPE;
+  const size_t n = (size_t)(rows * dim), row = (size_t)rows * 4, col = (size_t)dim * 4;
+  const Span sh = {h, n * width(h_dtype)}, sdy = {dy, n * width(io_dtype)}, sdh = {dh, sh.bytes};
+  const Span sdx = {dx, sdy.bytes}, sres = {dresidual, sh.bytes};
+  const Span sw = {weight, col}, smean = {norm == SSM_NORM_LAYER ? mean : nullptr, row}, srstd = {rstd, row}, sg = {rng, 16};
+  if (!apart({sdx, sres}, {sh, sw, smean, srstd, sg}) ||
+      !apart({{dweight, col}, {dbias, col}, {workspace, need}}, {sh, sdy, sdh, sdx, sres, sw, smean, srstd, sg}) ||
+      !apart_or_over(sdx, sdy) || !apart_or_over(sdx, sdh) || !apart_or_over(sres, sdy) || !apart_or_over(sres, sdh))
+    return SSM_ERR_FLAG;
   ssm66::add_norm::Args a = {};
   a.h = (void*)h; a.dy = dy; a.dh = dh; a.weight = weight; a.mean = (float*)mean; a.rstd = (float*)rstd;
   a.drop = ssm66::drop_of(p, rng, site); a.dx = dx; a.dresidual = dresidual;
@@ -247,7 +272,12 @@ int ssm_rotary(const void* q, const void* k, const float* freqs, const int32_t* 
     return SSM_ERR_UNSUPPORTED;
   if (!aligned_all(width(io_dtype), {q, k, q_out, k_out}) || !aligned_all(4, {freqs, positions}))
     return SSM_ERR_ALIGN;
-  if (kheads > 0 && (q_out == k || k_out == q || q_out == k_out)) return SSM_ERR_FLAG;
+  const size_t token = (size_t)dim * width(io_dtype), tokens = (size_t)(batch * seqlen);
+  const Span sq = {q, tokens * heads * token}, so = {q_out, sq.bytes};
+  const Span sk = {kheads > 0 ? k : nullptr, tokens * kheads * token}, sko = {kheads > 0 ? k_out : nullptr, sk.bytes};
+  const Span sf = {freqs, (size_t)rot * 2}, sp = {positions, tokens * 4};
+  if (!apart({so, sko}, {sf, sp}) || !apart_or_over(so, sq) || !apart_or_over(sko, sk) || meet(so, sk) || meet(sko, sq))
+    return SSM_ERR_FLAG;
   ssm66::rotary::Args a = {};
   a.q = q; a.k = kheads > 0 ? k : nullptr; a.qo = q_out; a.ko = kheads > 0 ? k_out : nullptr;
   a.freqs = freqs; a.positions = positions; a.tokens = batch * seqlen; a.L = seqlen;

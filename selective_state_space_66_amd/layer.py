@@ -19,6 +19,9 @@ step of the computation runs in the library's HIP kernels.
 rng is a tensor of two int64 on the GPU, seed and offset of a counter-based generator; the
 program moves the offset on from step to step (rng[1] += number of sites), a backward call
 takes its forward's rng and site.
+
+An output that is given shares memory with an input only where its function says so, and then
+is that tensor or a view of all of it; anything else is refused.
 """
 import ctypes
 import functools
@@ -114,8 +117,8 @@ def gated_scan_fwd(x, r, i, decay, h0=None, seq_lens=None, reset=None, y=None, l
     reset: optional (batch, L) bool or uint8, state zeroed before each flagged token.
     Returns (y like x, last_state (batch, dim) float32 or None, states or None): with
     return_states the state before every 64th token, (batch, ceil(L / 64), dim) float32,
-    which gated_scan_bwd takes.  y, last_state and workspace may be given; they share no memory
-    with each other or with an input (y is not x, r or i).
+    which gated_scan_bwd takes.  y, last_state and workspace may be given, but no input may be
+    any of them.
     """
     c, torch = _core()
     reset = _flags(torch, reset)

@@ -1,0 +1,101 @@
+"""Outputs of the layer operators over the inputs they may lie over, and beside them: the bits of
+outputs of their own; views that meet an input elsewhere are refused."""
+import pytest
+import torch
+
+import selective_state_space_66_amd as ssm
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def normal(shape, dtype, seed):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randn(shape, generator=gen, device=DEV).to(dtype)
+
+
+def beside(t):
+    """t, and a tensor like it that begins where t ends."""
+    room = torch.empty((2,) + t.shape, dtype=t.dtype, device=DEV)
+    room[0] = t
+    return room[0], room[1]
+
+
+def shifted(t):
+    """t with a row before it, and the tensor of its shape one row earlier."""
+    room = torch.empty((t.shape[0] + 1,) + t.shape[1:], dtype=t.dtype, device=DEV)
+    room[1:] = t
+    return room[1:], room[:-1]
+
+
+def refused(call, *args, **kw):
+    with pytest.raises(ssm.SsmError) as e:
+        call(*args, **kw)
+    assert e.value.status == 4
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_norm(dtype):
+    x, res, rng = normal((33, 200), dtype, 1), normal((33, 200), dtype, 2), torch.tensor([1, 2], device=DEV)
+    kw = dict(p=0.2, rng=rng)
+    y, h, mean, rstd = ssm.add_norm_fwd(x, residual=res, **kw)
+    a, b = beside(x)
+    assert torch.equal(ssm.add_norm_fwd(a, residual=res, y=b, **kw)[0], y)
+    a = x.clone()
+    got = ssm.add_norm_fwd(a, residual=res, h=a, **kw)  # h over x, of one type
+    assert torch.equal(got[0], y) and torch.equal(a, h)
+    a, b = shifted(x)
+    refused(ssm.add_norm_fwd, a, residual=res, y=b, **kw)
+    refused(ssm.add_norm_fwd, a, residual=res, h=b, **kw)
+    a, b = shifted(res)
+    refused(ssm.add_norm_fwd, x, residual=a, h=b, **kw)
+    refused(ssm.add_norm_fwd, x, residual=res, y=res, **kw)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_dropout(dtype):
+    x, res, rng = normal((33, 200), dtype, 3), normal((33, 200), dtype, 4), torch.tensor([1, 2], device=DEV)
+    want = ssm.dropout_fwd(x, 0.3, rng, residual=res)
+    a, b = beside(x)
+    assert torch.equal(ssm.dropout_fwd(a, 0.3, rng, residual=res, y=b), want)
+    a = x.clone()
+    assert torch.equal(ssm.dropout_fwd(a, 0.3, rng, residual=a, y=a), ssm.dropout_fwd(x, 0.3, rng, residual=x))
+    a, b = shifted(x)
+    refused(ssm.dropout_fwd, a, 0.3, rng, residual=res, y=b)
+    a, b = shifted(res)
+    refused(ssm.dropout_fwd, x, 0.3, rng, residual=a, y=b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rotary(dtype):
+    q, k = normal((2, 9, 4, 40), dtype, 5), normal((2, 9, 2, 40), dtype, 6)
+    freqs, _ = ssm.rotary_freqs(20, device=DEV)
+    want = ssm.rotary_fwd(q, k, freqs)
+    a, b = beside(q)
+    c, d = beside(k)
+    got = ssm.rotary_fwd(a, c, freqs, q_out=b, k_out=d)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    a = k.clone()
+    got = ssm.rotary_fwd(q, a, freqs, k_out=a)
+    assert torch.equal(got[0], want[0]) and torch.equal(a, want[1])
+    a, b = shifted(q)
+    refused(ssm.rotary_fwd, a, k, freqs, q_out=b)
+    a, b = shifted(k)
+    refused(ssm.rotary_fwd, q, a, freqs, k_out=b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_step(dtype):
+    x, r, i = (normal((5, 70), dtype, s) for s in (7, 8, 9))
+    decay, state = torch.rand(70, device=DEV), normal((5, 70), F32, 10)
+    s = state.clone()
+    want = ssm.gated_scan_step(s, x, r, i, decay)
+    for over in (0, 1, 2):
+        t = [v.clone() for v in (x, r, i)]
+        s2 = state.clone()
+        assert torch.equal(ssm.gated_scan_step(s2, *t, decay, y=t[over]), want) and torch.equal(s2, s)
+    a, b = shifted(x)
+    refused(ssm.gated_scan_step, state, a, r, i, decay, y=b)
+    if dtype == F32:
+        refused(ssm.gated_scan_step, state, x, r, i, decay, y=state)

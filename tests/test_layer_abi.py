@@ -214,3 +214,57 @@ def test_scan_refuses_outputs_in_the_place_of_another_tensor(lib, call, apart, i
                             there + (size[other] - 1) // 256 * 256):
                 if abs(address - there) < size[out if address < there else other]:
                     assert call(lib, **{**apart, out: at(0, address)}) == FLAG, (out, other, address - there)
+
+
+# each operator's tensors in places of their own, their bytes, and which outputs may lie over which inputs
+MEMORY = {
+    "step": (step, dict(state=at(1), x=at(2), r=at(3), i=at(4), decay=at(5), y=at(6), batch=4, dim=64, io=1),
+             dict(state=1024, x=512, r=512, i=512, decay=256, y=512), ("state", "y"),
+             {("y", "x"), ("y", "r"), ("y", "i")}),
+    "dropout": (drop, dict(x=at(1), residual=at(2), rng=at(3), y=at(4), n=1000, io=0, out=0),
+                dict(x=4000, residual=4000, rng=16, y=4000), ("y",), {("y", "x"), ("y", "residual")}),
+    "dropout to f32": (drop, dict(x=at(1), residual=at(2), rng=at(3), y=at(4), n=1000, io=1, out=0),
+                       dict(x=2000, residual=4000, rng=16, y=4000), ("y",), {("y", "residual")}),
+    "norm": (norm, dict(x=at(1), residual=at(2), weight=at(3), bias=at(4), p=0.5, rng=at(5), y=at(6), h=at(7),
+                        mean=at(8), rstd=at(9), rows=40, dim=64, io=0, ht=0),
+             dict(x=10240, residual=10240, weight=256, bias=256, rng=16, y=10240, h=10240, mean=160, rstd=160),
+             ("y", "h", "mean", "rstd"), {("y", "x"), ("h", "residual"), ("h", "x")}),
+    "norm, f32 stream": (norm, dict(x=at(1), residual=at(2), weight=at(3), bias=at(4), p=0.5, rng=at(5), y=at(6),
+                                    h=at(7), mean=at(8), rstd=at(9), rows=40, dim=64, io=1, ht=0),
+                         dict(x=5120, residual=10240, weight=256, bias=256, rng=16, y=5120, h=10240, mean=160, rstd=160),
+                         ("y", "h", "mean", "rstd"), {("y", "x"), ("h", "residual")}),
+    "norm_bwd": (norm_bwd, dict(h=at(1), dy=at(2), dh=at(3), weight=at(4), mean=at(5), rstd=at(6), p=0.5, rng=at(7),
+                                dx=at(8), dresidual=at(9), dweight=at(10), dbias=at(11), ws=at(12), rows=40, dim=64,
+                                io=0, ht=0),
+                 dict(h=10240, dy=10240, dh=10240, weight=256, mean=160, rstd=160, rng=16, dx=10240, dresidual=10240,
+                      dweight=256, dbias=256, ws=20480), ("dx", "dresidual", "dweight", "dbias", "ws"),
+                 {("dx", "dy"), ("dx", "dh"), ("dresidual", "dy"), ("dresidual", "dh")}),
+    "norm_bwd, f32 stream": (norm_bwd, dict(h=at(1), dy=at(2), dh=at(3), weight=at(4), mean=at(5), rstd=at(6), p=0.5,
+                                            rng=at(7), dx=at(8), dresidual=at(9), dweight=at(10), dbias=at(11),
+                                            ws=at(12), rows=40, dim=64, io=1, ht=0),
+                             dict(h=10240, dy=5120, dh=10240, weight=256, mean=160, rstd=160, rng=16, dx=5120,
+                                  dresidual=10240, dweight=256, dbias=256, ws=20480),
+                             ("dx", "dresidual", "dweight", "dbias", "ws"), {("dx", "dy"), ("dresidual", "dh")}),
+    "rotary": (rotary, dict(q=at(1), k=at(2), freqs=at(3), positions=at(4), qo=at(5), ko=at(6), batch=2, L=10, heads=4,
+                            kheads=2, dim=64, rot=32, io=1),
+               dict(q=10240, k=5120, freqs=64, positions=80, qo=10240, ko=5120), ("qo", "ko"),
+               {("qo", "q"), ("ko", "k")}),
+}
+
+
+@pytest.mark.parametrize("name", list(MEMORY))
+def test_outputs_that_meet_another_tensor_are_refused(lib, name):
+    """By a byte range: in its place (but where it may lie there), and shifted so that the ends meet."""
+    call, args, size, outputs, over = MEMORY[name]
+    for out in outputs:
+        for other in size:
+            if other == out:
+                continue
+            there = args[other].value
+            # 256 bytes further or before, where that still meets; in its place
+            for address in (there, there + 256, there - 256):
+                if not (address < there + size[other] and there < address + size[out]):
+                    continue
+                if address == there and (out, other) in over:
+                    continue
+                assert call(lib, **{**args, out: at(0, address)}) == FLAG, (out, other, address - there)
