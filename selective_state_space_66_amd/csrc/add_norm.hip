@@ -27,10 +27,11 @@ namespace {
 
 constexpr int VEC = 8;
 
+constexpr int threads_of(int lanes) { return lanes > 128 ? lanes : 256; }
 // LPR lanes hold a row, VECS times eight neighbouring values each.
 template <int LPR>
 struct Form {
-  static constexpr int kThreads = LPR > 128 ? LPR : 256;
+  static constexpr int kThreads = threads_of(LPR);
   static constexpr int kRows = kThreads / LPR;  // of a block at a time
 };
 
@@ -357,38 +358,44 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float2* part, fl
 constexpr int64_t most_blocks(int threads) { return 256 * (1024 / threads); }
 constexpr int64_t back_most(int threads) { return 256 * (threads > 256 ? 1024 / threads : 4); }
 
+// Lanes of a row; past 8192 each holds twice eight values.
+constexpr int lanes_of(int64_t dim) {
+  return dim <= 128 ? 16 : dim <= 256 ? 32 : dim <= 512 ? 64 : dim <= 1024 ? 128 : dim <= 1536 ? 192
+       : dim <= 2048 ? 256 : dim <= 4096 ? 512 : 1024;
+}
+// The blocks of a launch, which the backward's workspace is sized by too.
+constexpr int64_t blocks_of(int64_t rows, int lanes, bool back) {
+  const int threads = threads_of(lanes), at_once = threads / lanes;
+  const int64_t n = rows / at_once + (rows % at_once != 0), most = back ? back_most(threads) : most_blocks(threads);
+  return n < most ? n : most;
+}
+
 struct Call {
   Args p;
   bool back;
   hipStream_t s;
-  int* blocks;  // how many were launched
 };
 
 template <typename T, typename TH, int LPR, int VECS, bool EVEN>
 hipError_t launch(const Call& c) {
-  typedef Form<LPR> F;
-  static_assert(F::kThreads >= 192, "the workspace has room for blocks of 192 threads");
-  int64_t n = (c.p.rows + F::kRows - 1) / F::kRows;
-  const int64_t most = c.back ? back_most(F::kThreads) : most_blocks(F::kThreads);
-  if (n > most) n = most;
-  *c.blocks = (int)n;
-  if (c.back) bwd_kernel<T, TH, LPR, VECS, EVEN><<<(unsigned)n, F::kThreads, 0, c.s>>>(c.p);
-  else fwd_kernel<T, TH, LPR, VECS, EVEN><<<(unsigned)n, F::kThreads, 0, c.s>>>(c.p);
+  const unsigned n = (unsigned)blocks_of(c.p.rows, LPR, c.back);
+  if (c.back) bwd_kernel<T, TH, LPR, VECS, EVEN><<<n, threads_of(LPR), 0, c.s>>>(c.p);
+  else fwd_kernel<T, TH, LPR, VECS, EVEN><<<n, threads_of(LPR), 0, c.s>>>(c.p);
   return hipGetLastError();
 }
 
 template <typename T, typename TH, bool EVEN>
 hipError_t pick(const Call& c) {
-  const int d = c.p.dim;
-  if (d <= 128) return launch<T, TH, 16, 1, EVEN>(c);
-  if (d <= 256) return launch<T, TH, 32, 1, EVEN>(c);
-  if (d <= 512) return launch<T, TH, 64, 1, EVEN>(c);
-  if (d <= 1024) return launch<T, TH, 128, 1, EVEN>(c);
-  if (d <= 1536) return launch<T, TH, 192, 1, EVEN>(c);
-  if (d <= 2048) return launch<T, TH, 256, 1, EVEN>(c);
-  if (d <= 4096) return launch<T, TH, 512, 1, EVEN>(c);
-  if (d <= 8192) return launch<T, TH, 1024, 1, EVEN>(c);
-  return launch<T, TH, 1024, 2, EVEN>(c);
+  switch (lanes_of(c.p.dim)) {
+    case 16: return launch<T, TH, 16, 1, EVEN>(c);
+    case 32: return launch<T, TH, 32, 1, EVEN>(c);
+    case 64: return launch<T, TH, 64, 1, EVEN>(c);
+    case 128: return launch<T, TH, 128, 1, EVEN>(c);
+    case 192: return launch<T, TH, 192, 1, EVEN>(c);
+    case 256: return launch<T, TH, 256, 1, EVEN>(c);
+    case 512: return launch<T, TH, 512, 1, EVEN>(c);
+    default: return c.p.dim <= 8192 ? launch<T, TH, 1024, 1, EVEN>(c) : launch<T, TH, 1024, 2, EVEN>(c);
+  }
 }
 // Rows that are no multiple of eight pay for the piece at their end (16384 x
 // 1536: 65 and 86 us, by the kernels for any row 77 and 89).
@@ -405,23 +412,20 @@ hipError_t run(const Call& c, bool x_f32, bool h_f32) {
 }  // namespace
 
 size_t workspace_bytes(int64_t rows, int64_t dim) {
-  // a block takes a row at least, and 192 threads
-  const int64_t most = back_most(192), n = rows < most ? rows : most;
-  return (size_t)((n * dim * 8 + 255) / 256 * 256);
+  return (size_t)((blocks_of(rows, lanes_of(dim), true) * dim * 8 + 255) / 256 * 256);
 }
 
 hipError_t forward(const Args& p, bool x_f32, bool h_f32, hipStream_t s) {
-  int blocks;
-  return run(Call{p, false, s, &blocks}, x_f32, h_f32);
+  return run(Call{p, false, s}, x_f32, h_f32);
 }
 
 hipError_t backward(const Args& p, bool x_f32, bool h_f32, hipStream_t s) {
-  int blocks = 0;
   if (p.rows > 0) {
-    const hipError_t e = run(Call{p, true, s, &blocks}, x_f32, h_f32);
+    const hipError_t e = run(Call{p, true, s}, x_f32, h_f32);
     if (e != hipSuccess) return e;
   }
   if (!p.dweight && !p.dbias) return hipSuccess;
+  const int blocks = (int)blocks_of(p.rows, lanes_of(p.dim), true);
   column_sum_kernel<<<(p.dim + 15) / 16, 1024, 0, s>>>(p.part, p.dweight, p.dbias, blocks, p.dim);
   return hipGetLastError();
 }

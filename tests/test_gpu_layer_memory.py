@@ -99,3 +99,22 @@ def test_step(dtype):
     refused(ssm.gated_scan_step, state, a, r, i, decay, y=b)
     if dtype == F32:
         refused(ssm.gated_scan_step, state, x, r, i, decay, y=state)
+
+
+# a form of the norm each, with more rows than its blocks take at a time and with few
+@pytest.mark.parametrize("rows,dim", [(20000, 64), (9, 64), (9000, 256), (5000, 512), (3000, 1000), (1500, 1536),
+                                      (1500, 2048), (700, 4096), (300, 8192), (300, 16384), (3, 16384)])
+def test_norm_gradients_stay_inside_their_workspace(rows, dim):
+    print(f"[add norm] workspace {rows} x {dim}", flush=True)
+    x, dy = normal((rows, dim), BF16, 11), normal((rows, dim), BF16, 12)
+    _, h, mean, rstd = ssm.add_norm_fwd(x)
+    need = ssm.add_norm_workspace_size(rows, dim)
+    room = torch.full((need + 65536,), 0x5A, dtype=torch.uint8, device=DEV)
+    g = ssm.add_norm_bwd(h, dy, mean, rstd, need_dweight=True, need_dbias=True, workspace=room[:need])
+    assert (room[need:] == 0x5A).all()
+    want = ssm.add_norm_bwd(h, dy, mean, rstd, need_dweight=True, need_dbias=True)
+    for n in ("dx", "dweight", "dbias"):
+        assert torch.equal(g[n], want[n])
+    # dbias is a plain sum: off by the roundings of its terms, as many as a thread and its block add up
+    exact = dy.double().sum(0)
+    assert ((g["dbias"].double() - exact).abs() <= (rows / 256 + 20) * 2.0 ** -24 * dy.double().abs().sum(0)).all()

@@ -268,3 +268,15 @@ def test_outputs_that_meet_another_tensor_are_refused(lib, name):
                 if address == there and (out, other) in over:
                     continue
                 assert call(lib, **{**args, out: at(0, address)}) == FLAG, (out, other, address - there)
+
+
+def test_norm_workspace_is_what_its_blocks_fill(lib):
+    """A row of (dw, db) for each block: at most 1024 blocks of 256 threads or less, 512 of 512, 256 of 1024."""
+    size = lib.ssm_add_norm_workspace_size
+    for dim, most in ((64, 1024), (1536, 1024), (2048, 1024), (2056, 512), (4096, 512), (4104, 256), (8192, 256),
+                      (16384, 256)):
+        assert size(1 << 20, dim) == most * dim * 8, dim
+        assert size(1, dim) == (dim * 8 + 255) // 256 * 256
+    assert size(40, 64) == 3 * 64 * 8   # sixteen rows a block
+    assert size(0, 64) == 0
+    assert norm_bwd(lib, rows=1 << 20, dim=16384, size=256 * 16384 * 8 - 1) == SHAPE
