@@ -118,3 +118,48 @@ def test_norm_gradients_stay_inside_their_workspace(rows, dim):
     # dbias is a plain sum: off by the roundings of its terms, as many as a thread and its block add up
     exact = dy.double().sum(0)
     assert ((g["dbias"].double() - exact).abs() <= (rows / 256 + 20) * 2.0 ** -24 * dy.double().abs().sum(0)).all()
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("dim", [97, 256, 1536])
+def test_the_norm_of_tensors_between_words_has_the_same_bits(dim, types):
+    """Nothing depends on an address: tensors one value off, outputs too."""
+    xt, ht = types
+    x, res, dy, dh = (normal((17, dim), t, s) for t, s in ((xt, 13), (ht, 14), (xt, 15), (ht, 16)))
+    w, rng = normal((dim,), F32, 17), torch.tensor([1, 2], device=DEV)
+    kw = dict(weight=w, p=0.3, rng=rng)
+
+    def off(t):
+        room = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)
+        room[1:] = t.reshape(-1)
+        return room[1:].view(t.shape)
+
+    want = ssm.add_norm_fwd(x, residual=res, **kw)
+    got = ssm.add_norm_fwd(off(x), residual=off(res), y=off(x), h=off(res), **kw)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    y, h, mean, rstd = want
+    want = ssm.add_norm_bwd(h, dy, mean, rstd, dh=dh, need_dbias=True, **kw)
+    got = ssm.add_norm_bwd(off(h), off(dy), mean, rstd, dh=off(dh), need_dbias=True, **kw)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_with_more_threads_than_32_bits(interleaved):
+    """2^32 tokens and more of one head of two values: a thread each, numbered in 64 bits."""
+    B, L = 3, 1_431_700_000
+    print(f"[rotary] {B} x {L} x 1 x 2", flush=True)
+    q = torch.ones((B, L, 1, 2), dtype=BF16, device=DEV)
+    freqs = torch.tensor([1e-3], device=DEV)
+    at = [0, 1, 12345, 1 << 20, L - 2, L - 1]
+    few = normal((B, len(at), 1, 2), BF16, 18)
+    q[:, at] = few
+    positions = torch.tensor([at], dtype=torch.int32, device=DEV).expand(B, -1).contiguous()
+    want = ssm.rotary_fwd(few, None, freqs, positions=positions, interleaved=interleaved)[0]
+    one = ssm.rotary_fwd(torch.ones((1, 1000, 1, 2), dtype=BF16, device=DEV), None, freqs, interleaved=interleaved,
+                         positions=torch.arange(L // 2, L // 2 + 1000, dtype=torch.int32, device=DEV)[None])[0]
+    out = ssm.rotary_fwd(q, None, freqs, interleaved=interleaved, q_out=q)[0]
+    assert torch.equal(out[:, at], want)
+    for b in range(B):
+        assert torch.equal(out[b, L // 2:L // 2 + 1000], one[0])
