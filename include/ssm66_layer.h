@@ -51,7 +51,9 @@ extern "C" {
  * SSM_ERR_UNSUPPORTED).  Zero batch or dim is a no-op; seqlen == 0 copies h0 (or
  * zero) to last_state.
  * workspace: ssm_gated_scan_workspace_size(..., 0, 0) bytes, 256-byte aligned,
- * contents not needed before or after (NULL where the size is 0).
+ * contents not needed before or after (NULL where the size is 0).  It serves one
+ * call at a time: its blocks wait for one another through it, and two calls that
+ * run at once on one workspace could wait for ever.
  * Values are not checked: a NaN or infinity in a real token reaches the later
  * tokens of its document (an infinite state stays infinite; a bfloat16 call makes
  * it a NaN at a token whose v is over 87, where a is 0 in float32), no other
@@ -131,7 +133,8 @@ int ssm_dropout(const void* x, const void* residual, const int64_t* rng, int64_t
  *   weight, bias : (dim) float32, or NULL (one, zero)
  *   mean, rstd   : (rows) float32, or NULL: what ssm_add_norm_bwd takes (mean
  *                  is not written by the RMS norm)
- * y may be x.  dim at most 16384 (else SSM_ERR_UNSUPPORTED).  Tensors are
+ * y may be x.  dim at most 16384 (else SSM_ERR_UNSUPPORTED).  Squares are summed
+ * in float32: values stay below 1e17 (a sum past 3e38 makes rstd 0).  Tensors are
  * aligned to their element size (to 16 bytes, and with dim a multiple of 8, is
  * fastest).  Zero rows is a no-op.
  */

@@ -9,8 +9,8 @@
 //   dresidual = dH,  dx = dropout's map of dH,  dw = sum dy xh,  db = sum dy.
 //
 // HBM bounds all of it: 16384 x 1536, bf16 with an fp32 stream and dropout,
-// forwards 64 us (302 MB, 4.7 TB/s; a copy 5.1), backwards 80 (403 MB, 5.0) and 5 for
-// the column sums.  A row is read once and held by 16 to 64 lanes or by two
+// forwards 59 us (302 MB, at a copy's 5.1 TB/s; 65 in a training step, behind a
+// backward call), backwards 80 (403 MB, 5.0) and 5 for the column sums.  A row is read once and held by 16 to 64 lanes or by two
 // to sixteen waves, eight neighbouring values a lane (sixteen past 8192); the
 // sums go over the lanes by shuffles and over the waves through LDS.  A thread
 // keeps its columns over all the rows it takes, so the backward adds dw and db
@@ -358,7 +358,12 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float2* part, fl
 constexpr int64_t most_blocks(int threads) { return 256 * (1024 / threads); }
 constexpr int64_t back_most(int threads) { return 256 * (threads > 256 ? 1024 / threads : 4); }
 
-// Lanes of a row; past 8192 each holds twice eight values.
+// Lanes of a row, eight values each: the next power of two, and three waves; past
+// 8192 each holds twice eight values.  Forwards and backwards, bf16 with fp32 h and
+// dropout, three waves and four: 16384 x 1536 59 + 85 us, 64 + 86; 1280: 50 + 72, 55 +
+// 73; 1032: 47 + 58, 52 + 58.  Five or ten waves are forwards faster alone, five
+// slower backwards: 8192 x 2560 50 + 79, with 512 lanes 61 + 72; 4096 x 5120 62 + 73,
+// with 1024 lanes 72 + 72.
 constexpr int lanes_of(int64_t dim) {
   return dim <= 128 ? 16 : dim <= 256 ? 32 : dim <= 512 ? 64 : dim <= 1024 ? 128 : dim <= 1536 ? 192
        : dim <= 2048 ? 256 : dim <= 4096 ? 512 : 1024;

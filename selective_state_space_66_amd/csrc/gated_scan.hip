@@ -26,18 +26,23 @@
 // chip before they end.  The words are cleared to a pattern that no block writes
 // by a kernel before.
 //
-// Measured (a copy reaches 5.1 TB/s), inputs from HBM, with the kernel that clears
-// the words (2 to 3 us): 8 x 2048 x 1536, bf16, forwards 51 us (201 MB once, the
-// kernel at 4.3 TB/s), backwards 92 (352 MB, its kernel 82 at 4.3, the sums of
-// ddecay 4.5); 65536 x 2048 forwards 235 (1074 MB at 4.6).  HBM bounds it, and in
+// Measured (a copy reaches 5.1 TB/s), calls with inputs from HBM and the kernel that
+// clears the words (2 to 3 us): 8 x 2048 x 1536, bf16, forwards 51 us (201 MB once,
+// the kernel at 4.3 TB/s), backwards 93 (352 MB, its kernel at 4.2, the sums of
+// ddecay 4.5); 65536 x 2048 forwards 233 (1074 MB at 4.6).  HBM bounds it, and in
 // front of that a block's waits: for its loads, its number and the words of others
-// it waits 5 of the 10 us of its life; the vector units are 55% busy.
-// 3 x 1537 x 1000, fp32: 24 and 36 us for 14 and 25 of bytes, one round of blocks
-// whose chain is load, 69 and 114 instructions a value, join, store.
+// it waits 5 of the 10 us of its life; the vector units are busy for 55% of the
+// time forwards and 60% backwards.
+// 3 x 1537 x 1000, fp32: the kernels 25 and 38 us for 14 and 25 of bytes.  Their
+// blocks' chain is load, 72 and 121 instructions a value, join, store; forwards 624
+// blocks are one round (768 run at a time), backwards 1200 are more than two (512).
 //
 // 1 - a^2 comes from its series where v is small: long memories have v of 1e-3 and
 // less.  fp32 tensors also take h - (1 - a) h instead of a h there (a rounds to
-// 2^-25, which a memory of n tokens adds up n times).
+// 2^-25, which a memory of n tokens adds up n times), and so do the state after a
+// sequence and that of the step for bf16 tensors: 16384 tokens of fixed gates with v
+// of 2.5e-6 to 1e-5 leave a state of relative error 3.5e-6 as steps (with a h
+// 2.8e-4), 4.0e-7 as calls of 64 (1.9e-5) and 2.3e-7 as one call.
 #include "gated_scan_launch.h"
 #include "lm_grid.h"
 #include "vec_io.h"
@@ -898,13 +903,13 @@ int64_t up(int64_t n) { return (n + 255) / 256 * 256; }
 
 // Chunks of a group.  Few rows wait for the chain from group to group (about a
 // microsecond a link), many for the words that each block reads.  Forwards and
-// backwards of 32768 tokens, bf16, with groups of 4, 8, 16 and 32:
-//   64 channels:   46 + 90, 27 + 52, 20 + 37, 20 + 31 us;
-//   256:           49 + 90, 34 + 58, 29 + 45, 32 + 50;
-//   512:           56 + 98, 42 + 67, 42 + 66, 47 + 76;
-//   1024:          71 + 143, 66 + 130, 69 + 135, 76 + 146;
-//   2048:          124 + 232, 126 + 236, 130 + 242, 143 + 267;
-//   8 x 2048 x 1536: 45 + 93, 46 + 95, 48 + 101, 48 + 112.
+// backwards of 32768 tokens, bf16, inputs from HBM, groups of 4, 8, 16 and 32:
+//   64 channels:   44 + 88, 27 + 53, 21 + 37, 19 + 31 us;
+//   256:           50 + 91, 36 + 64, 31 + 52, 34 + 55;
+//   512:           60 + 107, 46 + 80, 46 + 76, 51 + 85;
+//   1024:          75 + 141, 71 + 131, 73 + 135, 80 + 146;
+//   2048:          124 + 242, 126 + 245, 129 + 250, 142 + 275;
+//   8 x 2048 x 1536: 50 + 92, 51 + 95, 54 + 99, 53 + 110.
 int group_of(int64_t rows) { return rows <= 128 ? 32 : rows <= 512 ? 16 : rows <= 1536 ? 8 : 4; }
 
 struct Layout { int64_t ticket, sums, groups, part, bytes; };
@@ -932,11 +937,14 @@ void place(Args& p, int vec, int chunk) {
   p.group = group_of(p.batch * p.dim);
   p.tiles = (p.dim + 64 * vec - 1) / (64 * vec);
   p.rows = (uint32_t)(p.batch * p.tiles);
-  // A counter gives 85 numbers a microsecond.  Blocks that all begin at once (3 x
-  // 1537 x 1000, fp32, forwards) take 26 us with a counter for each row, 29 with
-  // two and 30 with one; where there are more than run at a time, two keep them
-  // from loading in step (32768 x 2048, bf16: 125 + 235 us; a counter for each row
-  // 135 + 261).
+  // A counter gives 85 numbers a microsecond.  Calls of as many blocks as run at a
+  // time and a little more (768 of the fp32 forward kernel, 1024 of the bf16 one, 512
+  // and 768 of the backward ones) take a counter for each row: all begin at once, and
+  // wait for their numbers (3 x 1537 x 1000, fp32, 624 blocks: 27 us, with two
+  // counters 29.5, with one 31).  More blocks take two counters, which keep them from
+  // loading in step (32768 x 2048, bf16: 123 + 234 us, a counter for each row 135 +
+  // 257; 8 x 2048 x 1536: 50 + 92, 50 + 96; fp32 3 x 1537 x 1000 backwards, 1200
+  // blocks: 45.6, 45.2).
   const uint32_t most = (int64_t)p.rows * p.chunks <= 1024 ? kCounters : 2;
   // rows of a counter, and as few counters as they need: hardly a block is left over
   const uint32_t each = (p.rows + most - 1) / most;
@@ -986,10 +994,10 @@ hipError_t launch(Args p, hipStream_t s) {
 // and a wave's access of 256 bytes instead of 128.  That pays where rows are no whole
 // lines of 128 bytes, so that every access touches one more, where there is work
 // for the fewer blocks, and where the last tile does not waste it.  Forwards and
-// backwards, one channel and two:
-//   8 x 2048 x 1536: 44 + 92, 49 + 95 us;   1 x 32768 x 2048: 123 + 231, 131 + 241;
-//   8 x 2048 x 1535: 66 + 125, 57 + 116;    32 x 1024 x 711: 63 + 121, 55 + 114;
-//   1 x 4096 x 711: 17 + 25, 19 + 29;       1 x 32768 x 257: 38 + 60, 44 + 76.
+// backwards, inputs from HBM, one channel and two:
+//   8 x 2048 x 1536: 51 + 93, 56 + 97 us;   1 x 32768 x 2048: 124 + 236, 133 + 267;
+//   8 x 2048 x 1535: 66 + 124, 62 + 116;    32 x 1024 x 711: 63 + 123, 59 + 113;
+//   1 x 4096 x 711: 17 + 25, 19 + 31;       1 x 32768 x 257: 39 + 66, 48 + 86.
 bool pairs(const Args& p) {
   const int64_t tiled = (p.dim + 127) / 128 * (int64_t)128;
   return p.dim % 64 != 0 && 3 * tiled <= 4 * (int64_t)p.dim && p.batch * p.L * p.dim >= 6 << 20;
@@ -1009,8 +1017,8 @@ size_t workspace_bytes(int64_t batch, int64_t L, int64_t dim, bool backward, boo
 }
 
 // Up to kKeep tokens: one chunk, and a kernel of few instructions, which are most
-// of what such a call waits for (33 tokens of 256 channels: 4.9 us, by the kernel
-// for longer rows 8.0; 64 x 64 x 1024, bf16: 13.3 and 16.1).
+// of what such a call waits for (33 tokens of 256 channels: 4.7 us, by the kernel
+// for longer rows 8.0; calls of 64 x 64 x 1024, bf16: 13.8 and 16.1).
 hipError_t forward(const Args& p, bool f32, hipStream_t s) {
   if (p.L <= kKeep)
     return f32 ? launch<float, 1, 4, 16, false, true>(p, s) : launch<bf16_bits, 1, 4, 16, false, true>(p, s);

@@ -20,6 +20,9 @@ rng is a tensor of two int64 on the GPU, seed and offset of a counter-based gene
 program moves the offset on from step to step (rng[1] += number of sites), a backward call
 takes its forward's rng and site.
 
+A workspace that is given serves one call at a time: calls that may run at once, on two streams
+or in two graphs, take one each (each call makes its own where none is given).
+
 An output that is given shares memory with an input only where its function says so, and then
 is that tensor or a view of all of it; anything else is refused.
 """
