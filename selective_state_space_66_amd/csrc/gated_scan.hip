@@ -186,9 +186,10 @@ __device__ __forceinline__ float stretch_factor(float V) {
     const float a = exp_f<true>(-V);
     return V < 0.6931472f && V > 0.0f ? -one_minus(V, a) : a;
   }
-  // never 0, which would make an infinite state a NaN (of a V that is a NaN the
-  // stretch's H is one too)
-  const float a = fmaxf(exp2_hw(-V), 1.17549435e-38f);
+  // never 0, which would make an infinite state a NaN: the least number there is,
+  // which leaves 5e-7 of the largest finite state (of a V that is a NaN the stretch's
+  // H is one too)
+  const float a = fmaxf(exp2_hw(-V), 1.4e-45f);
   return LESS && V < 0.07f && V > 0.0f ? minus_b(V) : a;
 }
 template <bool LESS>

@@ -83,3 +83,21 @@ def test_an_infinite_state_stays_in_steps(io):
         assert torch.equal(y, state.to(io)) and torch.isfinite(state[:, 4:]).all()
         assert (state[:, 0] == INF).all() and (state[:, 1] == -INF).all()
         assert (state[:, 2] == INF).all() == (t >= 4) and (state[:, 3] == -INF).all() == (t >= 4)
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("L", [64, 128, 700, 9000])
+def test_the_largest_finite_state_is_forgotten(L, io):
+    """A state of 3e38 that nothing is left of after a while: less than 2^-149 of it is, so no more
+    than 3e38 2^-149 = 4e-7 stays where a factor is held in 32 bits, and that is forgotten too."""
+    d, h0, gen = inputs(2, L, 6, io, 4)
+    d["decay"].fill_(12.0)
+    d["r"] = d["r"].abs()  # v of 6 and more: 2^-149 after 18 tokens
+    h0[:, 0], h0[:, 1] = 3e38, -3e38
+    clean = ssm.gated_scan_fwd(**d, h0=torch.zeros_like(h0))
+    y, last, _ = ssm.gated_scan_fwd(**d, h0=h0)
+    for got, want in ((y[:, 20:], clean[0][:, 20:]), (last, clean[1])):
+        err = (got.double() - want.double()).abs()
+        # each side's rounding to its type, and sums of a few terms in another order
+        assert (err <= 1e-6 + (torch.finfo(got.dtype).eps + 16 * 2.0 ** -24) * want.double().abs()).all()
+    assert torch.equal(y[:, 64:], clean[0][:, 64:])
