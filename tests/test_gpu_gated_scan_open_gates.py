@@ -1,5 +1,12 @@
 """Gradients of gates that are nearly open or shut: what is left of a gate to 1, or the gate itself, is
-2e-9 there and still a bf16 number, so dr and di have their relative accuracy."""
+2e-9 there and still a bf16 number, so dr and di have their relative accuracy.
+
+What the bounds of gated_scan_ref have to hold, by the kernels' chunks and groups: ddecay's partial
+sums add the 8 tokens of a thread and 8 waves (calls of 64 tokens at most: 4 and 16), 20 roundings at
+most of the 24 it counts.  A state passes up to 31 joins before a block in a group of 32 chunks and one
+with the group's state: these cover 31 chunks of 64 tokens and more, for each token of which the bound
+adds 5.5 e, so that a join of 5.5 e is less than one token's share of a chunk.  The joins inside a block
+(8 waves, 16 in short calls) and its first state are in the 64 e it adds once."""
 import pytest
 import torch
 
