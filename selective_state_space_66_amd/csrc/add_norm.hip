@@ -10,13 +10,13 @@
 //
 // HBM bounds all of it: 16384 x 1536, bf16 with an fp32 stream and dropout,
 // forwards 59 us (302 MB, at a copy's 5.1 TB/s; 65 in a training step, behind a
-// backward call), backwards 80 (403 MB, 5.0) and 5 for the column sums.  A row is read once and held by 16 to 64 lanes or by two
-// to sixteen waves, eight neighbouring values a lane (sixteen past 8192); the
-// sums go over the lanes by shuffles and over the waves through LDS.  A thread
-// keeps its columns over all the rows it takes, so the backward adds dw and db
-// in registers; a block leaves one row of partial sums, added up in a fixed
-// order by a kernel of its own.  All sums are fp32, those over the rows' blocks
-// fp64.
+// backward call), backwards 80 (403 MB, 5.0) and 5 for the column sums.  A row is
+// read once and held by 16 to 64 lanes or by two to sixteen waves, eight
+// neighbouring values a lane (sixteen past 8192); the sums go over the lanes by
+// shuffles and over the waves through LDS.  A thread keeps its columns over all the
+// rows it takes, so the backward adds dw and db in registers; a block leaves one
+// row of partial sums, added up in a fixed order by a kernel of its own.  All sums
+// are fp32, those over the rows' blocks fp64.
 #include "add_norm_launch.h"
 #include "vec_io.h"
 

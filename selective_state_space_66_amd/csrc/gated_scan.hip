@@ -83,7 +83,8 @@ __device__ __forceinline__ void sigmoid2(float z, float* s, float* rest) {
 }
 // Both of them in one number, of which the fraction is sigmoid(z) and that of its
 // negative 1 - sigmoid(z): the smaller of the two, with the sign bit set where that
-// is 1 - sigmoid(z).  (That is never 0, the fraction of which is 0 and not 1.)
+// is 1 - sigmoid(z).  The fraction of 0 is 0 and not 1, so 1 - sigmoid(z) is never 0;
+// a gate of 0 (z below -88) has 0 for both, and everything they multiply is 0 there.
 struct Open { float s, both; };
 __device__ __forceinline__ Open open_of(float z) {
   const float e = exp_f<false>(-z), s = rcp_hw(1.0f + e), rest = fmaf(e, s, 1.17549435e-38f);
