@@ -39,8 +39,8 @@
 //
 // 1 - a^2 comes from its series where v is small: long memories have v of 1e-3 and
 // less.  fp32 tensors also take h - (1 - a) h instead of a h there (a rounds to
-// 2^-25, which a memory of n tokens adds up n times), and so do the state after a
-// sequence and that of the step for bf16 tensors: 16384 tokens of fixed gates with v
+// 2^-25, which a memory of n tokens adds up n times), and so do for bf16 tensors the
+// step, the state after a sequence and the gradient of that before it: 16384 tokens of fixed gates with v
 // of 2.5e-6 to 1e-5 leave a state of relative error 3.5e-6 as steps (with a h
 // 2.8e-4), 4.0e-7 as calls of 64 (1.9e-5) and 2.3e-7 as one call.
 #include "gated_scan_launch.h"
@@ -533,24 +533,20 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
 #pragma unroll
     for (int k = 0; k < VEC; ++k) h[k] = begin[k] = s.here && p.h0 ? p.h0[row + k] : 0.0f;
     const bool ends = MANY && ends_group(p, s.at);
-    // the state after the last chunk: bf16 calls join it from the chunk's own pair, its
-    // factor as what that is less than 1, for the tokens' rounded factors would add
-    // up in a state that is handed on from call to call, and a call of one token is a
-    // step (64 x 64 x 1024: 13.6 -> 13.8 us; with all factors so, 16.9)
-    const bool closes = !PRECISE && p.last_state && s.chunk == p.chunks - 1;
-    float Vb[VEC], fb[VEC], Hb[VEC];
+    float fb[VEC], Hb[VEC];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) Vb[k] = fb[k] = Hb[k] = 0.0f;
-    if (ends || closes)
+    for (int k = 0; k < VEC; ++k) fb[k] = Hb[k] = 0.0f;
+    if (ends)
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
+        float Vb = 0.0f;
 #pragma unroll 2
         for (int q = 0; q < W; ++q) {
           const float2 e = pair[q][slot + k];
           Hb[k] = over<PRECISE>(stretch_factor<PRECISE>(e.x), Hb[k], e.y);
-          Vb[k] = joint(Vb[k], e.x);
+          Vb = joint(Vb, e.x);
         }
-        fb[k] = stretch_factor<PRECISE>(Vb[k]);
+        fb[k] = stretch_factor<PRECISE>(Vb);
       }
     if (s.here) {
       if (MANY) state_before<PRECISE, VEC>(p, s.at, row, begin, h);
@@ -559,9 +555,24 @@ __global__ __launch_bounds__(64 * W, 4) void fwd_kernel(const Args p) {
         if (ends)
           publish(p.groups + (int64_t)(s.at / p.group) * (p.batch * p.dim) + row + k, 0.0f,
                   over<PRECISE>(fb[k], h[k], Hb[k]));
-        if (closes) p.last_state[row + k] = over<true>(stretch_factor<PRECISE, true>(Vb[k]), h[k], Hb[k]);
         start[slot + k] = h[k];
       }
+      // the state after the last chunk: bf16 calls join it from the chunk's own pair, its
+      // factor as what that is less than 1, for the tokens' rounded factors would add
+      // up in a state that is handed on from call to call, and a call of one token is a
+      // step (64 x 64 x 1024: 13.5 us as before; with all factors so, 16.9)
+      if (!PRECISE && p.last_state && s.chunk == p.chunks - 1)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          float V = 0.0f, H = 0.0f;
+#pragma unroll
+          for (int q = 0; q < W; ++q) {
+            const float2 e = pair[q][slot + k];
+            H = over<PRECISE>(stretch_factor<PRECISE>(e.x), H, e.y);
+            V = joint(V, e.x);
+          }
+          p.last_state[row + k] = over<true>(stretch_factor<PRECISE, true>(V), h[k], H);
+        }
     }
   }
   lds_barrier();
@@ -803,6 +814,20 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
                   over<PRECISE>(fb[k], c[k], Db[k]));
         start[slot + k] = c[k];
       }
+      // the gradient of the first state, handed on from call to call as the last state
+      // is (not unrolled: 26 registers more in short calls, 64 x 64 x 1024 22.5 -> 27.4 us)
+      if (!PRECISE && p.dh0 && s.chunk == 0)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          float V = 0.0f, D = 0.0f;
+#pragma unroll 1
+          for (int q = W - 1; q >= 0; --q) {
+            const float Vq = pair[q][slot + k].x;
+            D = over<PRECISE>(stretch_factor<PRECISE>(Vq), D, back[q][slot + k]);
+            V = joint(V, Vq);
+          }
+          p.dh0[row + k] = over<true>(stretch_factor<PRECISE, true>(V), c[k], D);
+        }
     }
   }
   lds_barrier();
@@ -824,7 +849,7 @@ __global__ __launch_bounds__(64 * W, 4) void bwd_kernel(const Args p) {
     states_before<PRECISE, false>(s.real, s.cuts, gate.f, u, h);
     token_gradients<T, false>(p, s, stash, gate, u, decay, c, P);
   }
-  if (s.w == 0 && s.here && p.dh0 && s.chunk == 0)
+  if (PRECISE && s.w == 0 && s.here && p.dh0 && s.chunk == 0)
 #pragma unroll
     for (int k = 0; k < VEC; ++k) p.dh0[row + k] = c[k];
   if (p.part) {

@@ -90,3 +90,34 @@ def test_sequences_piece_by_piece(piece, io):
         e = min(t + piece, N)
         state = ssm.gated_scan_fwd(x[:, t:e], gr[:, t:e], gi[:, t:e], decay, h0=state)[1]
     assert worst(state[0], h[-1], bound) <= 1.0
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("piece", [1, 64, 300])
+def test_gradients_piece_by_piece(piece, io):
+    """The gradient of the state from call to call, from the end: c = a (dy + c).  Its roundings are those
+    of the state, in fp32 calls also that of dy + c: twice the bound.  What a token adds is dy itself,
+    off by the rounding of a dy and of a: 3 e |dy|."""
+    print(f"[gated scan] gradients of {N} tokens in pieces of {piece}, {io}", flush=True)
+    dy, gr, gi, decay, c, _, _ = problem(TYPES[io], 3)
+    v = decay.double() / (1.0 + math.exp(-R))
+    a, b = torch.exp(-v), -torch.expm1(-v)
+    want, big = c[0].double(), c[0].double().abs()
+    for t in range(N - 1, -1, -1):
+        want = a * (dy[0, t].double() + want)
+        big = torch.maximum(big, want.abs() + dy[0, t].double().abs())
+    ordered = dy[0].float().sort(0).values
+    first = torch.ones((N, C), device=DEV)
+    first[1:] = (ordered[1:] != ordered[:-1]).float()
+    count = torch.zeros((N + 1, C), device=DEV)
+    count.scatter_add_(0, first.cumsum(0).long(), torch.ones((N, C), device=DEV))
+    bound = 2.0 ** -23 * big * (count.double().square().sum(0) * math.log(2 * C / 1e-9) / 2).sqrt()
+    bound = bound * (2 if io == "f32" else 1) + 3 * E * (dy[0].double().abs().sum(0) + b * N * big)
+    bound = bound + (abs(R) + 8) * E * N * b * big
+    x = torch.zeros_like(dy)
+    for e in range(N, 0, -piece):
+        t = max(e - piece, 0)
+        part = (x[:, t:e].contiguous(), gr[:, t:e].contiguous(), gi[:, t:e].contiguous(), decay)
+        states = torch.zeros((1, (e - t + 63) // 64, C), device=DEV)
+        c = ssm.gated_scan_bwd(*part, dy[:, t:e].contiguous(), states, dlast=c, need_ddecay=False, need_dh0=True)["dh0"]
+    assert worst(c[0], want, bound) <= 1.0
